@@ -344,6 +344,37 @@ GRPO_API int grpo_logprob_loss_fwd_bwd_host(const void* logits_host, int32_t dty
                                             void* staging, int64_t block_rows, void* stream,
                                             void* copy_stream);
 
+/* ---- scoring and distillation over logits --------------------------------------------------- */
+
+#define GRPO_TOPK_MAX 256  /* largest K of the top-K calls below */
+
+/* Scores logits rows: per row t, with tau = temperature and p = softmax(z / tau),
+ *   logp_tok    = log p_y of the given token y
+ *   entropy_tok = -sum_v p_v log p_v
+ *   top_idx, top_logp = the K most probable tokens, most probable first, equal logits by ascending
+ *                 index, and their log-probs
+ * in one pass over the logits. A teacher's top_idx / top_logp are what the distillation calls
+ * below take.
+ *  logits    device [T, ld] GRPO_DTYPE_F32 or _BF16, row-major, V <= ld, any alignment of the rows
+ *  tok_src   device int64 [T] or NULL: the index of row t in target, mask and the outputs (a
+ *            negative one marks a padding row, which is skipped); NULL means t
+ *  target    device int32, required with logp_tok; outside [0, V): log-prob NaN
+ *  mask      device uint8 or NULL (every row counts). A masked row is not read: its log-prob and
+ *            entropy are 0, its top_idx -1 and its top_logp -inf
+ *  K         0 <= K <= min(V, GRPO_TOPK_MAX); 0: no alternatives, top_idx and top_logp unused
+ *  logp_tok, entropy_tok  device float or NULL
+ *  top_idx   device int32, row stride ld_top >= K; top_logp device float, the same stride, or NULL
+ * -inf logits (and logits whose z log2(e)/tau lies below the float32 range) have probability 0;
+ * where fewer than K are left they fill up the list with log-prob -inf. A row with a NaN or +inf
+ * logit, or none with mass, has no distribution: float outputs NaN, top_idx -1.
+ * Errors: GRPO_ERR_INVALID (sizes, K, a temperature that is not positive and finite, NULL required
+ * pointer, logits not aligned to their element), GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CUDA. */
+GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V,
+                                      int64_t ld, const int64_t* tok_src, const int32_t* target,
+                                      const uint8_t* mask, float temperature, int32_t K,
+                                      float* logp_tok, float* entropy_tok, int32_t* top_idx,
+                                      float* top_logp, int64_t ld_top, void* stream);
+
 /* ---- step finish ------------------------------------------------------------------------- */
 
 /* Close one optimizer step ("Sizing mini-batches and micro-batches", "The hard part:

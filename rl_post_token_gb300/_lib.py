@@ -37,6 +37,7 @@ AGG_SEQ_MEAN_TOKEN_MEAN = 2
 KL_NONE = 0
 KL_K1 = 1
 KL_K3 = 2
+TOPK_MAX = 256  # largest K of the top-K calls
 ACC_BYTES = 128
 
 _i32p = C.POINTER(C.c_int32)
@@ -146,6 +147,9 @@ def _lib() -> C.CDLL:
     lib.grpo_lmhead_forward_noalloc.restype = C.c_int
     lib.grpo_lmhead_forward_noalloc_max_scratch.argtypes = []
     lib.grpo_lmhead_forward_noalloc_max_scratch.restype = C.c_size_t
+    lib.grpo_token_topk_logprobs.argtypes = [vp, C.c_int32, C.c_int64, C.c_int64, C.c_int64, vp, vp, vp, C.c_float,
+                                             C.c_int32, vp, vp, vp, vp, C.c_int64, vp]
+    lib.grpo_token_topk_logprobs.restype = C.c_int
     lib.grpo_window_init.argtypes = [C.POINTER(grpo_window), C.c_int32]
     lib.grpo_window_chunk.argtypes = [C.POINTER(grpo_window), C.c_int32, C.c_double, C.c_int64,
                                       C.POINTER(C.c_int32), C.POINTER(C.c_double)]
@@ -397,6 +401,64 @@ def grpo_logprob_loss_fwd_bwd_host(logits_host, target, old_logp, adv_tok, mask,
                                                int(block_rows), st, st if copy_stream is None else _stream(copy_stream))
     if rc != OK:
         raise GrpoError(rc, "grpo_logprob_loss_fwd_bwd_host")
+
+
+def _device_args(device, **tensors):
+    """Raise unless every given tensor (None passes) is on `device`, the current CUDA device: a
+    launch goes to the current device, and another device's memory would fault there. Each value
+    is (tensor, dtype, least element count); 1-D tensors must be contiguous."""
+    import torch
+
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors must be on the current CUDA device, not on {device}")
+    for name, (t, dtype, n) in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, not on {t.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        if t.numel() < n or not (t.dim() == 2 or t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous with at least {n} elements")
+
+
+def _rows2d(t, name: str, cols: int, rows: int):
+    """Row stride in elements of a 2-D tensor with unit inner stride and the given extent."""
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols:
+        raise ValueError(f"{name} must be 2-D with at least {rows} rows and {cols} columns")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have a unit inner stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def grpo_token_topk_logprobs(logits, K: int, target=None, logp_tok=None, entropy_tok=None, top_idx=None,
+                             top_logp=None, temperature: float = 1.0, mask=None, tok_src=None,
+                             V: Optional[int] = None, stream=None) -> None:
+    """logits [T, ld] (float32 or bfloat16) on the device -> the log-prob of each row's target, its
+    entropy and its K most probable tokens (top_idx int32 and top_logp float32, [rows, >= K]);
+    outputs left None are not computed. With tok_src, target, mask and the outputs are indexed
+    through it. See grpo.h."""
+    import torch
+
+    T = logits.shape[0]
+    V = logits.shape[1] if V is None else V
+    ld = _rows2d(logits, "logits", V, 0)
+    dt = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}[logits.dtype]
+    n = 0 if tok_src is not None else T
+    f32, i32 = torch.float32, torch.int32
+    _device_args(logits.device, target=(target, i32, n), mask=(mask, torch.uint8, n), tok_src=(tok_src, torch.int64, T),
+                 logp_tok=(logp_tok, f32, n), entropy_tok=(entropy_tok, f32, n), top_idx=(top_idx, i32, n * K),
+                 top_logp=(top_logp, f32, n * K))
+    ld_top = K
+    if K > 0 and top_idx is not None:
+        ld_top = _rows2d(top_idx, "top_idx", K, n)
+        if top_logp is not None and _rows2d(top_logp, "top_logp", K, n) != ld_top:
+            raise ValueError("top_logp must have top_idx's row stride")
+    rc = _lib().grpo_token_topk_logprobs(_ptr(logits), dt, T, V, ld, _ptr(tok_src), _ptr(target), _ptr(mask),
+                                         float(temperature), int(K), _ptr(logp_tok), _ptr(entropy_tok), _ptr(top_idx),
+                                         _ptr(top_logp), ld_top, _stream(stream))
+    if rc != OK:
+        raise GrpoError(rc, "grpo_token_topk_logprobs")
 
 
 def _grad_arrays(grad_bufs):

@@ -136,3 +136,42 @@ def test_lmhead_workspace_sizes():
     for bad in [(0, 8, 64), (8, 0, 64), (8, 8, 0), (-1, 8, 64)]:
         assert _lib.grpo_lmhead_workspace_size(*bad) == 0
     assert _lib.lib().grpo_lmhead_forward_noalloc_max_scratch() == 16 << 20
+
+
+def _score(dtype=_lib.DTYPE_BF16, T=8, V=64, ld=64, logits=P, target=P, mask=None, temperature=1.0, K=4, logp=P,
+           entropy=P, idx=P, top=P, ld_top=4):
+    return _lib.lib().grpo_token_topk_logprobs(logits, dtype, T, V, ld, None, target, mask, temperature, K, logp,
+                                               entropy, idx, top, ld_top, None)
+
+
+@pytest.mark.parametrize("kw, code", [
+    (dict(dtype=7), _lib.ERR_UNSUPPORTED),
+    (dict(T=-1), _lib.ERR_INVALID),
+    (dict(T=2 ** 31), _lib.ERR_INVALID),
+    (dict(V=0), _lib.ERR_INVALID),
+    (dict(V=2 ** 31, ld=2 ** 31), _lib.ERR_INVALID),
+    (dict(ld=63), _lib.ERR_INVALID),
+    (dict(K=-1), _lib.ERR_INVALID),
+    (dict(K=65, ld_top=65), _lib.ERR_INVALID),  # more than the row holds
+    (dict(K=257, V=1024, ld=1024, ld_top=257), _lib.ERR_INVALID),
+    (dict(ld_top=3), _lib.ERR_INVALID),
+    (dict(temperature=0.0), _lib.ERR_INVALID),
+    (dict(temperature=-1.0), _lib.ERR_INVALID),
+    (dict(temperature=math.nan), _lib.ERR_INVALID),
+    (dict(temperature=math.inf), _lib.ERR_INVALID),
+    (dict(temperature=1e-39), _lib.ERR_INVALID),  # log2(e)/tau overflows
+    (dict(logits=None), _lib.ERR_INVALID),
+    (dict(logits=P + 1), _lib.ERR_INVALID),  # not aligned to its element
+    (dict(target=None), _lib.ERR_INVALID),
+    (dict(idx=None), _lib.ERR_INVALID),
+    (dict(T=0), _lib.OK),
+    (dict(T=0, logits=None, target=None, idx=None), _lib.OK),
+])
+def test_score_argument_checks(kw, code):
+    assert _score(**kw) == code
+
+
+def test_score_binding_refuses_host_tensors():
+    import torch
+    with pytest.raises(ValueError):
+        _lib.grpo_token_topk_logprobs(torch.zeros(2, 8), 2, top_idx=torch.zeros((2, 2), dtype=torch.int32))
