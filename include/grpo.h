@@ -375,6 +375,47 @@ GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t
                                       float* logp_tok, float* entropy_tok, int32_t* top_idx,
                                       float* top_logp, int64_t ld_top, void* stream);
 
+/* Distillation from a teacher's top tokens, loss and gradient of each student row in one call. Per
+ * token, with p = softmax(z / tau), the teacher's list of tokens i_k and log-probs log q_k (as
+ * grpo_token_topk_logprobs writes them at the same temperature), Q = sum q_k, q_R = 1 - Q and p_R
+ * the student's mass outside the list:
+ *   FORWARD_TOPK  L = sum_k (q_k/Q) (log(q_k/Q) - log p_k)     the list renormalised (log q_k may
+ *                                                              then carry any constant: top logits)
+ *   FORWARD_TAIL  L = sum_k q_k (log q_k - log p_k) + q_R (log q_R - log p_R)
+ *   REVERSE_TAIL  L = sum_k p_k (log p_k - log q_k) + p_R (log p_R - log q_R)
+ *   dlogits_t = grad_scale w_t m_t dL/dz (the 1/tau of dL/dz included, no tau^2 factor)
+ * The tail kinds treat every other token as one; where the list holds the whole vocabulary there
+ * is no such term. A q_R below 2^-24 (what float32 log-probs cannot resolve) counts as 0 in
+ * FORWARD_TAIL and as 2^-24 in REVERSE_TAIL's logarithm.
+ *  logits    device [T, ld], dtype, tok_src, mask, loss_tok, acc: as grpo_logprob_loss_fwd_bwd (the
+ *            rows may start at any multiple of their element)
+ *  top_idx, top_logp  device int32 / float, row t's list at t (or tok_src[t]) * ld_top; entries with
+ *            token -1 are unused, in any place. 1 <= K <= GRPO_TOPK_MAX, K <= ld_top. A row whose
+ *            list is empty (FORWARD_TOPK: or has no mass) has loss and gradient 0
+ *  w_tok     device float per token, indexed like mask, or NULL: a weight on grad_scale (see
+ *            grpo_loss_terms); loss_tok stays unweighted
+ *  dlogits   device [T, ld_out], same dtype, or NULL (loss only); it must not overlap logits. Masked
+ *            rows are written as zeros, and masked tokens get loss 0
+ * loss_tok and acc go to grpo_finish_step as those of the policy loss (no token counts as clipped).
+ * A token whose list holds a token twice or outside [0, V), or a NaN or +inf log-prob, or whose row
+ * has a NaN or +inf logit or no mass, has loss and gradient NaN; it and a token with an infinite
+ * loss (a listed token the student cannot produce; for REVERSE_TAIL one the teacher cannot) count as
+ * non-finite. Logits below the float32 range after the scaling have no mass, as in
+ * grpo_token_topk_logprobs.
+ * Errors: GRPO_ERR_INVALID (sizes, kind, temperature, a non-finite grad_scale, NULL required
+ * pointer, alignment, overlap), GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CUDA. */
+#define GRPO_DISTILL_FORWARD_TOPK 0
+#define GRPO_DISTILL_FORWARD_TAIL 1
+#define GRPO_DISTILL_REVERSE_TAIL 2
+
+GRPO_API int grpo_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_t T, int64_t V,
+                                       int64_t ld, const int64_t* tok_src, const int32_t* top_idx,
+                                       const float* top_logp, int64_t ld_top, int32_t K,
+                                       const uint8_t* mask, int32_t kind, float temperature,
+                                       const float* w_tok, float grad_scale, void* dlogits,
+                                       int64_t ld_out, float* loss_tok, grpo_step_acc* acc,
+                                       void* stream);
+
 /* ---- step finish ------------------------------------------------------------------------- */
 
 /* Close one optimizer step ("Sizing mini-batches and micro-batches", "The hard part:

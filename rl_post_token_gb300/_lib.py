@@ -37,6 +37,10 @@ AGG_SEQ_MEAN_TOKEN_MEAN = 2
 KL_NONE = 0
 KL_K1 = 1
 KL_K3 = 2
+# GRPO_DISTILL_*: the distillation objectives
+DISTILL_FORWARD_TOPK = 0
+DISTILL_FORWARD_TAIL = 1
+DISTILL_REVERSE_TAIL = 2
 TOPK_MAX = 256  # largest K of the top-K calls
 ACC_BYTES = 128
 
@@ -150,6 +154,10 @@ def _lib() -> C.CDLL:
     lib.grpo_token_topk_logprobs.argtypes = [vp, C.c_int32, C.c_int64, C.c_int64, C.c_int64, vp, vp, vp, C.c_float,
                                              C.c_int32, vp, vp, vp, vp, C.c_int64, vp]
     lib.grpo_token_topk_logprobs.restype = C.c_int
+    lib.grpo_distill_topk_fwd_bwd.argtypes = [vp, C.c_int32, C.c_int64, C.c_int64, C.c_int64, vp, vp, vp, C.c_int64,
+                                              C.c_int32, vp, C.c_int32, C.c_float, vp, C.c_float, vp, C.c_int64, vp,
+                                              vp, vp]
+    lib.grpo_distill_topk_fwd_bwd.restype = C.c_int
     lib.grpo_window_init.argtypes = [C.POINTER(grpo_window), C.c_int32]
     lib.grpo_window_chunk.argtypes = [C.POINTER(grpo_window), C.c_int32, C.c_double, C.c_int64,
                                       C.POINTER(C.c_int32), C.POINTER(C.c_double)]
@@ -459,6 +467,42 @@ def grpo_token_topk_logprobs(logits, K: int, target=None, logp_tok=None, entropy
                                          _ptr(top_logp), ld_top, _stream(stream))
     if rc != OK:
         raise GrpoError(rc, "grpo_token_topk_logprobs")
+
+
+def _teacher_list(top_idx, top_logp, rows: int):
+    """(K, row stride) of a teacher's list, [rows, K] with a unit inner stride in both tensors."""
+    K = top_idx.shape[1] if top_idx.dim() == 2 else 0
+    ld_top = _rows2d(top_idx, "top_idx", K, rows)
+    if top_logp.shape != top_idx.shape or _rows2d(top_logp, "top_logp", K, rows) != ld_top:
+        raise ValueError("top_logp must have top_idx's shape and row stride")
+    return K, ld_top
+
+
+def grpo_distill_topk_fwd_bwd(logits, top_idx, top_logp, mask, kind: int, grad_scale: float, dlogits, loss_tok, acc,
+                              temperature: float = 1.0, w_tok=None, tok_src=None, V: Optional[int] = None,
+                              stream=None) -> None:
+    """logits [T, ld] (float32 or bfloat16) on the device and the teacher's list top_idx (int32) /
+    top_logp (float32) [rows, K] -> loss_tok, dlogits (None: loss only); kind is DISTILL_*. See
+    grpo.h."""
+    import torch
+
+    T = logits.shape[0]
+    V = logits.shape[1] if V is None else V
+    ld = _rows2d(logits, "logits", V, 0)
+    dt = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}[logits.dtype]
+    n = 0 if tok_src is not None else T
+    f32 = torch.float32
+    _device_args(logits.device, top_idx=(top_idx, torch.int32, 0), top_logp=(top_logp, f32, 0),
+                 mask=(mask, torch.uint8, n), w_tok=(w_tok, f32, n), tok_src=(tok_src, torch.int64, T),
+                 dlogits=(dlogits, logits.dtype, 0), loss_tok=(loss_tok, f32, n), acc=(acc, torch.uint8, ACC_BYTES))
+    K, ld_top = _teacher_list(top_idx, top_logp, n)
+    ld_out = 0 if dlogits is None else _rows2d(dlogits, "dlogits", V, T)
+    rc = _lib().grpo_distill_topk_fwd_bwd(_ptr(logits), dt, T, V, ld, _ptr(tok_src), _ptr(top_idx), _ptr(top_logp),
+                                          ld_top, K, _ptr(mask), int(kind), float(temperature), _ptr(w_tok),
+                                          float(grad_scale), _ptr(dlogits), ld_out, _ptr(loss_tok), _ptr(acc),
+                                          _stream(stream))
+    if rc != OK:
+        raise GrpoError(rc, "grpo_distill_topk_fwd_bwd")
 
 
 def _grad_arrays(grad_bufs):

@@ -24,7 +24,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgrpo.so")
 
 SOURCES = ["grpo_plan.cpp", "grpo_window.cpp", "grpo_rowpass.cu", "grpo_step.cu", "grpo_lmhead.cu",
-           "grpo_score.cu"]
+           "grpo_score.cu", "grpo_distill.cu"]
 LINK: list = []  # every kernel is the library's own: no CUDA library beyond the static runtime
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

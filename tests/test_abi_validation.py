@@ -175,3 +175,51 @@ def test_score_binding_refuses_host_tensors():
     import torch
     with pytest.raises(ValueError):
         _lib.grpo_token_topk_logprobs(torch.zeros(2, 8), 2, top_idx=torch.zeros((2, 2), dtype=torch.int32))
+
+
+def _distill(dtype=_lib.DTYPE_BF16, T=8, V=64, ld=64, logits=P, idx=P, lq=P, ld_top=4, K=4, mask=P, kind=0,
+             temperature=1.0, scale=1.0, dl=None, ld_out=0, loss=P, acc=P):
+    return _lib.lib().grpo_distill_topk_fwd_bwd(logits, dtype, T, V, ld, None, idx, lq, ld_top, K, mask, kind,
+                                                temperature, None, scale, dl, ld_out, loss, acc, None)
+
+
+@pytest.mark.parametrize("kw, code", [
+    (dict(dtype=7), _lib.ERR_UNSUPPORTED),
+    (dict(kind=3), _lib.ERR_INVALID),
+    (dict(kind=-1), _lib.ERR_INVALID),
+    (dict(T=-1), _lib.ERR_INVALID),
+    (dict(T=2 ** 31), _lib.ERR_INVALID),
+    (dict(V=0), _lib.ERR_INVALID),
+    (dict(V=2 ** 31, ld=2 ** 31), _lib.ERR_INVALID),
+    (dict(ld=63), _lib.ERR_INVALID),
+    (dict(K=0), _lib.ERR_INVALID),
+    (dict(K=257, ld_top=257), _lib.ERR_INVALID),
+    (dict(ld_top=3), _lib.ERR_INVALID),
+    (dict(temperature=0.0), _lib.ERR_INVALID),
+    (dict(temperature=math.nan), _lib.ERR_INVALID),
+    (dict(temperature=1e-39), _lib.ERR_INVALID),
+    (dict(scale=math.inf), _lib.ERR_INVALID),
+    (dict(acc=None), _lib.ERR_INVALID),
+    (dict(logits=None), _lib.ERR_INVALID),
+    (dict(logits=P + 1), _lib.ERR_INVALID),
+    (dict(idx=None), _lib.ERR_INVALID),
+    (dict(lq=None), _lib.ERR_INVALID),
+    (dict(mask=None), _lib.ERR_INVALID),
+    (dict(loss=None), _lib.ERR_INVALID),
+    (dict(dl=P + (1 << 20), ld_out=63), _lib.ERR_INVALID),
+    (dict(dl=P + (1 << 20) + 1, ld_out=64), _lib.ERR_INVALID),
+    (dict(dl=P, ld_out=64), _lib.ERR_INVALID),  # in place
+    (dict(dl=P + 7 * 128 + 126, ld_out=64), _lib.ERR_INVALID),  # the last logit's bytes
+    (dict(T=0), _lib.OK),
+    (dict(T=0, logits=None, idx=None, lq=None, mask=None, loss=None), _lib.OK),
+])
+def test_distill_argument_checks(kw, code):
+    assert _distill(**kw) == code
+
+
+def test_distill_binding_refuses_host_tensors():
+    import torch
+    f, i = torch.zeros(2), torch.zeros((2, 2), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        _lib.grpo_distill_topk_fwd_bwd(torch.zeros(2, 8), i, torch.zeros(2, 2), torch.ones(2, dtype=torch.uint8), 0, 1.0,
+                                       None, f, _lib.new_step_acc("cpu"))
