@@ -599,6 +599,27 @@ GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W, int64_t T
                                          grpo_step_acc* acc, void* workspace, size_t workspace_bytes,
                                          void* stream);
 
+/* Bytes of device workspace grpo_lmhead_distill_topk_fwd_bwd needs: grpo_lmhead_workspace_size's,
+ * and per token an int32 and K floats (each part rounded up to 256 bytes). 0 on bad sizes. */
+GRPO_API size_t grpo_lmhead_distill_workspace_size(int64_t T, int64_t V, int64_t H, int64_t K);
+
+/* grpo_distill_topk_fwd_bwd's FORWARD_TOPK loss (temperature 1) from hidden states: z = h W^T is
+ * formed tile by tile and never stored, as in grpo_lmhead_loss_fwd_bwd, whose h, W, d_h, dW, flags,
+ * loss_tok, acc and workspace rules hold (workspace: grpo_lmhead_distill_workspace_size(T, V, H, K)
+ * bytes); H at most 16384. top_idx, top_logp, ld_top, K, w_tok as in grpo_distill_topk_fwd_bwd.
+ * The logits of the listed tokens are formed once more as float32 dot products of h and W's rows.
+ * The tail kinds have no LM-head form: the student's mass outside the list would have to be formed
+ * as a difference. A token whose |LSE| is above 4096 counts as non-finite.
+ * Errors: those of grpo_lmhead_loss_fwd_bwd, and GRPO_ERR_INVALID for a bad K, ld_top, H or
+ * grad_scale. */
+GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const void* W, int64_t T, int64_t V, int64_t H,
+                                              const int32_t* top_idx, const float* top_logp,
+                                              int64_t ld_top, int32_t K, const uint8_t* mask,
+                                              const float* w_tok, float grad_scale, float* d_h,
+                                              float* dW, uint32_t flags, float* loss_tok,
+                                              grpo_step_acc* acc, void* workspace,
+                                              size_t workspace_bytes, void* stream);
+
 /* Allocation-free forward pass of the fused LM-head variant. The pages have no counterpart:
  * this entry point exists for callers that cannot allocate device memory when they need the
  * loss -- a serving or scoring process whose device memory is all handed to its own pool (a

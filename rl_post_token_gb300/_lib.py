@@ -158,6 +158,12 @@ def _lib() -> C.CDLL:
                                               C.c_int32, vp, C.c_int32, C.c_float, vp, C.c_float, vp, C.c_int64, vp,
                                               vp, vp]
     lib.grpo_distill_topk_fwd_bwd.restype = C.c_int
+    lib.grpo_lmhead_distill_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, C.c_int64]
+    lib.grpo_lmhead_distill_workspace_size.restype = C.c_size_t
+    lib.grpo_lmhead_distill_topk_fwd_bwd.argtypes = [vp, vp, C.c_int64, C.c_int64, C.c_int64, vp, vp, C.c_int64,
+                                                     C.c_int32, vp, vp, C.c_float, vp, vp, C.c_uint32, vp, vp, vp,
+                                                     C.c_size_t, vp]
+    lib.grpo_lmhead_distill_topk_fwd_bwd.restype = C.c_int
     lib.grpo_window_init.argtypes = [C.POINTER(grpo_window), C.c_int32]
     lib.grpo_window_chunk.argtypes = [C.POINTER(grpo_window), C.c_int32, C.c_double, C.c_int64,
                                       C.POINTER(C.c_int32), C.POINTER(C.c_double)]
@@ -589,6 +595,39 @@ def grpo_lmhead_loss_fwd_bwd(h, W, target, old_logp, adv_tok, mask, clip_eps: fl
                                          _stream(stream))
     if rc != OK:
         raise GrpoError(rc, "grpo_lmhead_loss_fwd_bwd")
+
+
+def grpo_lmhead_distill_workspace_size(T: int, V: int, H: int, K: int) -> int:
+    return int(_lib().grpo_lmhead_distill_workspace_size(T, V, H, K))
+
+
+def grpo_lmhead_distill_topk_fwd_bwd(h, W, top_idx, top_logp, mask, grad_scale: float, d_h, dW, loss_tok, acc,
+                                     workspace, w_tok=None, dw_accumulate: bool = False, skip_masked: bool = False,
+                                     stream=None) -> None:
+    """h [T, H] and W [V, H] bf16 device tensors and the teacher's list top_idx (int32) / top_logp
+    (float32) [T, K] -> loss_tok, d_h and dW (float32, or None); dw_accumulate and skip_masked as
+    for grpo_lmhead_loss_fwd_bwd; see grpo.h."""
+    import torch
+
+    if h.dim() != 2 or W.dim() != 2 or h.shape[1] != W.shape[1] or not (h.is_contiguous() and W.is_contiguous()):
+        raise ValueError("h [T, H] and W [V, H] must be contiguous with one H")
+    T, H = h.shape
+    V = W.shape[0]
+    f32, bf16 = torch.float32, torch.bfloat16
+    _device_args(h.device, h=(h, bf16, 0), W=(W, bf16, 0), top_idx=(top_idx, torch.int32, 0), top_logp=(top_logp, f32, 0),
+                 mask=(mask, torch.uint8, T), w_tok=(w_tok, f32, T), d_h=(d_h, f32, T * H), dW=(dW, f32, V * H),
+                 loss_tok=(loss_tok, f32, T), acc=(acc, torch.uint8, ACC_BYTES))
+    for name, t in (("d_h", d_h), ("dW", dW), ("workspace", workspace)):
+        if t is not None and (t.device != h.device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous on {h.device}")
+    K, ld_top = _teacher_list(top_idx, top_logp, T)
+    flags = (LMHEAD_DW_ACCUMULATE if dw_accumulate else 0) | (LMHEAD_SKIP_MASKED if skip_masked else 0)
+    rc = _lib().grpo_lmhead_distill_topk_fwd_bwd(_ptr(h), _ptr(W), T, V, H, _ptr(top_idx), _ptr(top_logp), ld_top, K,
+                                                 _ptr(mask), _ptr(w_tok), float(grad_scale), _ptr(d_h), _ptr(dW),
+                                                 flags, _ptr(loss_tok), _ptr(acc), _ptr(workspace),
+                                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != OK:
+        raise GrpoError(rc, "grpo_lmhead_distill_topk_fwd_bwd")
 
 
 def grpo_lmhead_forward_noalloc(h, W, target, old_logp, adv_tok, mask, clip_eps: float,

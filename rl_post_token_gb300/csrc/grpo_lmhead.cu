@@ -29,6 +29,7 @@
 #include <cstdlib>
 #include <mutex>
 
+#include "grpo_lmhead_distill.cuh"
 #include "grpo_lmhead_gemm.cuh"
 
 namespace grpo {
@@ -449,13 +450,11 @@ int check_args(const void* h, const void* W, int64_t T, int64_t V, int64_t H, co
   return GRPO_OK;
 }
 
-// Pass A and the per-token reduce: loss_tok, logp_tok, the step counters, and each token's
-// LSE and gradient coefficient in the scratch.
-int forward(int cg, const void* h, const void* W, int64_t T, int64_t V, int64_t H, const int32_t* target,
-            const float* old_logp, const float* adv_tok, const uint8_t* mask, float clip_eps, float grad_scale,
-            float* loss_tok, float* logp_tok, const grpo_loss_terms* terms, grpo_step_acc* acc,
-            const WsLayout& ws, const Scratch& sc, cudaStream_t st, bool skip_masked = false) {
-  const bool ent = wants_entropy(terms);
+// Pass A: the softmax partials of every token's vocabulary tiles in the scratch (epi:
+// EPI_PARTIALS or EPI_PARTIALS_ENT).
+int pass_a(int cg, int epi, const void* h, const void* W, int64_t T, int64_t V, int64_t H, const int32_t* target,
+           const uint8_t* mask, grpo_step_acc* acc, const WsLayout& ws, const Scratch& sc, cudaStream_t st,
+           bool skip_masked) {
   GemmArgs g{};
   g.target = target;
   g.part_m = sc.part_m;
@@ -480,8 +479,19 @@ int forward(int cg, const void* h, const void* W, int64_t T, int64_t V, int64_t 
     g.row_idx = sc.idx;
     g.live_mode = LIVE_ROWS;
   }
-  const int rc = ent ? logits_gemm<EPI_PARTIALS_ENT>(cg, a_src, W, T, V, H, g, st)
-                     : logits_gemm<EPI_PARTIALS>(cg, a_src, W, T, V, H, g, st);
+  return epi == EPI_PARTIALS_ENT ? logits_gemm<EPI_PARTIALS_ENT>(cg, a_src, W, T, V, H, g, st)
+                                 : logits_gemm<EPI_PARTIALS>(cg, a_src, W, T, V, H, g, st);
+}
+
+// Pass A and the per-token reduce: loss_tok, logp_tok, the step counters, and each token's
+// LSE and gradient coefficient in the scratch.
+int forward(int cg, const void* h, const void* W, int64_t T, int64_t V, int64_t H, const int32_t* target,
+            const float* old_logp, const float* adv_tok, const uint8_t* mask, float clip_eps, float grad_scale,
+            float* loss_tok, float* logp_tok, const grpo_loss_terms* terms, grpo_step_acc* acc,
+            const WsLayout& ws, const Scratch& sc, cudaStream_t st, bool skip_masked = false) {
+  const bool ent = wants_entropy(terms);
+  const int rc =
+      pass_a(cg, ent ? EPI_PARTIALS_ENT : EPI_PARTIALS, h, W, T, V, H, target, mask, acc, ws, sc, st, skip_masked);
   if (rc != GRPO_OK) return rc;
   ReduceArgs r{};
   r.T = T;
@@ -569,46 +579,17 @@ Overlap* overlap_state(std::unique_lock<std::mutex>& lock) {
   return &o;
 }
 
-}  // namespace
-
-extern "C" GRPO_API size_t grpo_lmhead_workspace_size(int64_t T, int64_t V, int64_t H) {
-  if (T <= 0 || V <= 0 || H <= 0) return 0;
-  return ws_layout(T, V, H).total;
-}
-
-extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W, int64_t T, int64_t V,
-                                                    int64_t H, const int32_t* target, const float* old_logp,
-                                                    const float* adv_tok, const uint8_t* mask, float clip_eps,
-                                                    float grad_scale, float* d_h, float* dW, uint32_t flags,
-                                                    float* loss_tok, float* logp_tok,
-                                                    const grpo_loss_terms* terms, grpo_step_acc* acc,
-                                                    void* workspace, size_t workspace_bytes, void* stream) {
-  if (terms) {
-    if (terms->kl_kind != GRPO_KL_NONE && terms->kl_kind != GRPO_KL_K1 && terms->kl_kind != GRPO_KL_K3)
-      return GRPO_ERR_INVALID;
-    if (terms->kl_kind != GRPO_KL_NONE && !terms->ref_logp) return GRPO_ERR_INVALID;
-    if (!isfinite(terms->kl_coef) || !isfinite(terms->ent_coef)) return GRPO_ERR_INVALID;
-  }
-  const int arc = check_args(h, W, T, V, H, target, adv_tok, mask, loss_tok, acc);
-  if (arc != GRPO_OK || T == 0) return arc;
-  if (flags & ~(uint32_t)(GRPO_LMHEAD_DW_ACCUMULATE | GRPO_LMHEAD_SKIP_MASKED)) return GRPO_ERR_INVALID;
-  if (!workspace || ((uintptr_t)workspace & 255u)) return GRPO_ERR_INVALID;
-  if (((uintptr_t)d_h | (uintptr_t)dW) & 15u) return GRPO_ERR_INVALID;  // 16-byte row stores
-  const WsLayout ws = ws_layout(T, V, H);
-  if (workspace_bytes < ws.total) return GRPO_ERR_CAPACITY;
-  const cudaStream_t st = as_stream(stream);
-  const Scratch sc = carve(workspace, ws, true);
-  const int cg = cta_group();
-  int rc = forward(cg, h, W, T, V, H, target, old_logp, adv_tok, mask, clip_eps, grad_scale, loss_tok, logp_tok,
-                   terms, acc, ws, sc, st, (flags & GRPO_LMHEAD_SKIP_MASKED) != 0);
-  if (rc != GRPO_OK || (!d_h && !dW)) return rc;
-  // the dlogits take the entropy form p (ea + eb z) when the bonus has a coefficient
-  const bool ent_grad = terms && terms->ent_coef != 0.f;
-
-  // Per vocabulary chunk c: the recompute writes the chunk's dlogits into buffer c % 2 on the
-  // caller's stream; d_h and dW read it on the second stream, so the next chunk's recompute
-  // runs beside them. d_h's launches stay in chunk order on one stream (its accumulation
-  // order), and a buffer is rewritten only after the launches reading it two chunks before.
+// The gradients, from each token's LSE and coefficient in the scratch: partition, gather, and per
+// vocabulary chunk c: the recompute writes the chunk's dlogits into buffer c % 2 on the caller's
+// stream (after_dz then completes them there); d_h and dW read it on the second stream, so the next
+// chunk's recompute runs beside them. d_h's launches stay in chunk order on one stream (its
+// accumulation order), and a buffer is rewritten only after the launches reading it two chunks before.
+// ent_grad: the dlogits take the entropy form p (ea + eb z).
+template <typename AfterDz>
+int backward(int cg, const void* h, const void* W, int64_t T, int64_t V, int64_t H, const int32_t* target,
+             bool ent_grad, float* d_h, float* dW, uint32_t flags, grpo_step_acc* acc, const WsLayout& ws,
+             const Scratch& sc, cudaStream_t st, AfterDz after_dz) {
+  int rc = GRPO_OK;
   const int n_chunks = (ws.n_col_tiles + ws.chunk_tiles - 1) / ws.chunk_tiles;
   std::unique_lock<std::mutex> ov_lock;
   Overlap* ov = (overlap_on() && n_chunks > 1) ? overlap_state(ov_lock) : nullptr;
@@ -625,7 +606,7 @@ extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W
                                                     sc.h_live, d_h);
     GRPO_CUDA_TRY(cudaGetLastError());
   }
-  auto backward = [&]() -> int {
+  auto chunks = [&]() -> int {
   for (int ct0 = 0, c = 0; ct0 < ws.n_col_tiles; ct0 += ws.chunk_tiles, ++c) {
     const int nct = std::min(ws.chunk_tiles, ws.n_col_tiles - ct0);
     const int64_t v0 = (int64_t)ct0 * BN;
@@ -651,6 +632,8 @@ extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W
     g.row_idx = sc.idx;
     g.live_mode = LIVE_ROWS_PADDED;
     rc = logits_gemm<EPI_DLOGITS>(cg, sc.h_live, W, T, V, H, g, st, vc);
+    if (rc != GRPO_OK) return rc;
+    rc = after_dz(dzb, v0, vc);
     if (rc != GRPO_OK) return rc;
     if (ov) {
       GRPO_CUDA_TRY(cudaEventRecord(ov->dz_ready, st));
@@ -699,7 +682,7 @@ extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W
   }
   return GRPO_OK;
   };
-  rc = backward();
+  rc = chunks();
   if (ov) {  // the caller's stream continues after every launch of the call (also after an error)
     const bool joined = cudaEventRecord(ov->joined, bst) == cudaSuccess &&
                         cudaStreamWaitEvent(st, ov->joined, 0) == cudaSuccess;
@@ -711,6 +694,43 @@ extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W
   return rc;
 }
 
+}  // namespace
+
+extern "C" GRPO_API size_t grpo_lmhead_workspace_size(int64_t T, int64_t V, int64_t H) {
+  if (T <= 0 || V <= 0 || H <= 0) return 0;
+  return ws_layout(T, V, H).total;
+}
+
+extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W, int64_t T, int64_t V,
+                                                    int64_t H, const int32_t* target, const float* old_logp,
+                                                    const float* adv_tok, const uint8_t* mask, float clip_eps,
+                                                    float grad_scale, float* d_h, float* dW, uint32_t flags,
+                                                    float* loss_tok, float* logp_tok,
+                                                    const grpo_loss_terms* terms, grpo_step_acc* acc,
+                                                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (terms) {
+    if (terms->kl_kind != GRPO_KL_NONE && terms->kl_kind != GRPO_KL_K1 && terms->kl_kind != GRPO_KL_K3)
+      return GRPO_ERR_INVALID;
+    if (terms->kl_kind != GRPO_KL_NONE && !terms->ref_logp) return GRPO_ERR_INVALID;
+    if (!isfinite(terms->kl_coef) || !isfinite(terms->ent_coef)) return GRPO_ERR_INVALID;
+  }
+  const int arc = check_args(h, W, T, V, H, target, adv_tok, mask, loss_tok, acc);
+  if (arc != GRPO_OK || T == 0) return arc;
+  if (flags & ~(uint32_t)(GRPO_LMHEAD_DW_ACCUMULATE | GRPO_LMHEAD_SKIP_MASKED)) return GRPO_ERR_INVALID;
+  if (!workspace || ((uintptr_t)workspace & 255u)) return GRPO_ERR_INVALID;
+  if (((uintptr_t)d_h | (uintptr_t)dW) & 15u) return GRPO_ERR_INVALID;  // 16-byte row stores
+  const WsLayout ws = ws_layout(T, V, H);
+  if (workspace_bytes < ws.total) return GRPO_ERR_CAPACITY;
+  const cudaStream_t st = as_stream(stream);
+  const Scratch sc = carve(workspace, ws, true);
+  const int cg = cta_group();
+  int rc = forward(cg, h, W, T, V, H, target, old_logp, adv_tok, mask, clip_eps, grad_scale, loss_tok, logp_tok,
+                   terms, acc, ws, sc, st, (flags & GRPO_LMHEAD_SKIP_MASKED) != 0);
+  if (rc != GRPO_OK || (!d_h && !dW)) return rc;
+  return backward(cg, h, W, T, V, H, target, terms && terms->ent_coef != 0.f, d_h, dW, flags, acc, ws, sc, st,
+                  [](__nv_bfloat16*, int64_t, int64_t) -> int { return GRPO_OK; });
+}
+
 extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd(const void* h, const void* W, int64_t T, int64_t V, int64_t H,
                                                  const int32_t* target, const float* old_logp,
                                                  const float* adv_tok, const uint8_t* mask, float clip_eps,
@@ -719,6 +739,98 @@ extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd(const void* h, const void* W, i
                                                  void* workspace, size_t workspace_bytes, void* stream) {
   return grpo_lmhead_loss_fwd_bwd_ex(h, W, T, V, H, target, old_logp, adv_tok, mask, clip_eps, grad_scale, d_h, dW,
                                      flags, loss_tok, logp_tok, nullptr, acc, workspace, workspace_bytes, stream);
+}
+
+// ---- distillation from a teacher's top tokens --------------------------------------------------
+
+namespace {
+
+// The loss's workspace layout, then a target array without targets and the list entries' dlogits.
+struct DistillLayout {
+  WsLayout base;
+  size_t target, corr, total;
+};
+
+DistillLayout distill_layout(int64_t T, int64_t V, int64_t H, int64_t K) {
+  DistillLayout d{};
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  d.base = ws_layout(T, V, H);
+  d.target = up(d.base.total);
+  d.corr = d.target + up((size_t)T * 4);
+  d.total = d.corr + up((size_t)T * K * 4);
+  return d;
+}
+
+}  // namespace
+
+extern "C" GRPO_API size_t grpo_lmhead_distill_workspace_size(int64_t T, int64_t V, int64_t H, int64_t K) {
+  if (T <= 0 || V <= 0 || H <= 0 || K <= 0) return 0;
+  return distill_layout(T, V, H, K).total;
+}
+
+extern "C" GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const void* W, int64_t T, int64_t V, int64_t H,
+                                                         const int32_t* top_idx, const float* top_logp,
+                                                         int64_t ld_top, int32_t K, const uint8_t* mask,
+                                                         const float* w_tok, float grad_scale, float* d_h, float* dW,
+                                                         uint32_t flags, float* loss_tok, grpo_step_acc* acc,
+                                                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (K < 1 || K > GRPO_TOPK_MAX || ld_top < K || !isfinite(grad_scale)) return GRPO_ERR_INVALID;
+  const int arc = check_args(h, W, T, V, H, top_idx, top_logp, mask, loss_tok, acc);
+  if (arc != GRPO_OK || T == 0) return arc;
+  if (flags & ~(uint32_t)(GRPO_LMHEAD_DW_ACCUMULATE | GRPO_LMHEAD_SKIP_MASKED)) return GRPO_ERR_INVALID;
+  if (!workspace || ((uintptr_t)workspace & 255u)) return GRPO_ERR_INVALID;
+  if (((uintptr_t)d_h | (uintptr_t)dW) & 15u) return GRPO_ERR_INVALID;
+  const size_t list_smem = (size_t)H * 2;  // a hidden state in shared memory
+  if (list_smem > 32 * 1024) return GRPO_ERR_INVALID;
+  const DistillLayout dl = distill_layout(T, V, H, K);
+  if (workspace_bytes < dl.total) return GRPO_ERR_CAPACITY;
+  const cudaStream_t st = as_stream(stream);
+  const WsLayout& ws = dl.base;
+  const Scratch sc = carve(workspace, ws, true);
+  int32_t* target = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + dl.target);
+  float* corr = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dl.corr);
+  const int cg = cta_group();
+  const bool skip = (flags & GRPO_LMHEAD_SKIP_MASKED) != 0;
+  // no target: pass A picks up no target logit, the recompute's dlogits are the dense coef p_v
+  GRPO_CUDA_TRY(cudaMemsetAsync(target, 0xFF, (size_t)T * 4, st));
+  int rc = pass_a(cg, EPI_PARTIALS, h, W, T, V, H, target, mask, acc, ws, sc, st, skip);
+  if (rc != GRPO_OK) return rc;
+  // the token's shift and sum in ea and eb (the entropy bonus's, unused here)
+  lse_kernel<<<(unsigned)((T + 31) / 32), kLseWarps * 32, 0, st>>>(T, ws.n_col_tiles, sc.part_m, sc.part_s,
+                                                                   skip ? sc.idx : nullptr, skip ? sc.live_n : nullptr,
+                                                                   sc.ea, sc.eb);
+  GRPO_CUDA_TRY(cudaGetLastError());
+  ListArgs a{};
+  a.T = T;
+  a.V = V;
+  a.H = (int)H;
+  a.h = static_cast<const __nv_bfloat16*>(h);
+  a.W = static_cast<const __nv_bfloat16*>(W);
+  a.top_idx = top_idx;
+  a.top_logp = top_logp;
+  a.ld_top = ld_top;
+  a.K = K;
+  a.mask = mask;
+  a.w_tok = w_tok;
+  a.scale = grad_scale;
+  a.m = sc.ea;
+  a.s = sc.eb;
+  a.lse2 = sc.lse2;
+  a.coef = sc.coef;
+  a.corr = corr;
+  a.loss_tok = loss_tok;
+  a.acc = acc;
+  list_kernel<<<(unsigned)T, kListThreads, list_smem, st>>>(a);
+  GRPO_CUDA_TRY(cudaGetLastError());
+  if (!d_h && !dW) return GRPO_OK;
+  const unsigned fix_blocks = (unsigned)std::min<int64_t>((T * K + 255) / 256, (int64_t)sm_count() * 16);
+  return backward(cg, h, W, T, V, H, target, false, d_h, dW, flags, acc, ws, sc, st,
+                  [&](__nv_bfloat16* dz, int64_t v0, int64_t vc) -> int {
+                    fix_kernel<<<fix_blocks, 256, 0, st>>>(sc.live_n, sc.idx, top_idx, ld_top, K, corr, dz, ws.vchunk,
+                                                           v0, vc);
+                    GRPO_CUDA_TRY(cudaGetLastError());
+                    return GRPO_OK;
+                  });
 }
 
 // ---- allocation-free forward entry point -----------------------------------------------------

@@ -223,3 +223,45 @@ def test_distill_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         _lib.grpo_distill_topk_fwd_bwd(torch.zeros(2, 8), i, torch.zeros(2, 2), torch.ones(2, dtype=torch.uint8), 0, 1.0,
                                        None, f, _lib.new_step_acc("cpu"))
+
+
+def _lm_distill(T=256, V=1024, H=128, h=P, W=P, idx=P, lq=P, ld_top=8, K=8, mask=P, scale=1.0, ws=P, ws_bytes=1 << 30,
+                acc=P, loss=P, flags=0, d_h=P, dW=P):
+    return _lib.lib().grpo_lmhead_distill_topk_fwd_bwd(h, W, T, V, H, idx, lq, ld_top, K, mask, None, scale, d_h, dW,
+                                                       flags, loss, acc, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw, code", [
+    (dict(H=100), _lib.ERR_INVALID),
+    (dict(H=16448), _lib.ERR_INVALID),
+    (dict(K=0), _lib.ERR_INVALID),
+    (dict(K=257, ld_top=257), _lib.ERR_INVALID),
+    (dict(ld_top=7), _lib.ERR_INVALID),
+    (dict(flags=4), _lib.ERR_INVALID),
+    (dict(scale=math.nan), _lib.ERR_INVALID),
+    (dict(V=0), _lib.ERR_INVALID),
+    (dict(T=-1), _lib.ERR_INVALID),
+    (dict(h=P + 8), _lib.ERR_INVALID),
+    (dict(ws=P + 16), _lib.ERR_INVALID),
+    (dict(ws=None), _lib.ERR_INVALID),
+    (dict(idx=None), _lib.ERR_INVALID),
+    (dict(lq=None), _lib.ERR_INVALID),
+    (dict(mask=None), _lib.ERR_INVALID),
+    (dict(loss=None), _lib.ERR_INVALID),
+    (dict(acc=None), _lib.ERR_INVALID),
+    (dict(d_h=P + 4), _lib.ERR_INVALID),
+    (dict(dW=P + 8), _lib.ERR_INVALID),
+    (dict(T=0), _lib.OK),
+])
+def test_lmhead_distill_argument_checks(kw, code):
+    assert _lm_distill(**kw) == code
+
+
+def test_lmhead_distill_workspace():
+    up = lambda x: (x + 255) // 256 * 256
+    for T, V, H, K in [(1, 5, 64, 5), (300, 40000, 512, 33)]:
+        n = _lib.grpo_lmhead_distill_workspace_size(T, V, H, K)
+        assert n == up(_lib.grpo_lmhead_workspace_size(T, V, H)) + up(4 * T) + up(4 * T * K)
+        assert _lm_distill(T=T, V=V, H=H, K=K, ld_top=K, ws_bytes=n - 1) == _lib.ERR_CAPACITY
+    for bad in [(0, 8, 64, 1), (8, 0, 64, 1), (8, 8, 0, 1), (8, 8, 64, 0)]:
+        assert _lib.grpo_lmhead_distill_workspace_size(*bad) == 0
