@@ -196,7 +196,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object (10 us of a small call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -417,32 +418,48 @@ def grpo_logprob_loss_fwd_bwd_host(logits_host, target, old_logp, adv_tok, mask,
         raise GrpoError(rc, "grpo_logprob_loss_fwd_bwd_host")
 
 
-def _device_args(device, **tensors):
-    """Raise unless every given tensor (None passes) is on `device`, the current CUDA device: a
-    launch goes to the current device, and another device's memory would fault there. Each value
-    is (tensor, dtype, least element count); 1-D tensors must be contiguous."""
+def _device_args(logits, *tensors) -> None:
+    """Raise unless `logits` and every given tensor, (name, tensor or None, dtype, least element
+    count), is on the current CUDA device: a launch goes to the current device, and another
+    device's memory would fault there. 1-D tensors must be contiguous."""
     import torch
 
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors must be on the current CUDA device, not on {device}")
-    for name, (t, dtype, n) in tensors.items():
+    dev = logits.get_device() if logits.is_cuda else -1
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors must be on the current CUDA device, not on {logits.device}")
+    for name, t, dtype, n in tensors:
         if t is None:
             continue
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, not on {t.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-        if t.numel() < n or not (t.dim() == 2 or t.is_contiguous()):
+        if t.dtype is not dtype or t.get_device() != dev:
+            raise ValueError(f"{name} must be {dtype} on {logits.device}, not {t.dtype} on {t.device}")
+        if t.numel() < n or (t.dim() == 1 and n > 1 and t.stride(0) != 1):
             raise ValueError(f"{name} must be contiguous with at least {n} elements")
 
 
-def _rows2d(t, name: str, cols: int, rows: int):
+def _rows2d(t, name: str, cols: int, rows: int) -> int:
     """Row stride in elements of a 2-D tensor with unit inner stride and the given extent."""
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] < cols:
         raise ValueError(f"{name} must be 2-D with at least {rows} rows and {cols} columns")
-    if cols > 1 and t.stride(1) != 1:
+    st = t.stride()
+    if cols > 1 and st[1] != 1:
         raise ValueError(f"{name} must have a unit inner stride")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return st[0] if shape[0] > 1 else max(shape[1], 1)
+
+
+def _same_rows(a, b) -> bool:
+    """Whether b's rows lie as a's do (a has passed _rows2d)."""
+    return b.dim() == 2 and (b.shape[1] < 2 or b.stride(1) == 1) and (b.shape[0] < 2 or b.stride(0) == a.stride(0))
+
+
+def _logits_dtype(t) -> int:
+    import torch
+
+    if t.dtype is torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype is torch.float32:
+        return DTYPE_F32
+    raise ValueError(f"logits must be float32 or bfloat16, not {t.dtype}")
 
 
 def grpo_token_topk_logprobs(logits, K: int, target=None, logp_tok=None, entropy_tok=None, top_idx=None,
@@ -454,20 +471,20 @@ def grpo_token_topk_logprobs(logits, K: int, target=None, logp_tok=None, entropy
     through it. See grpo.h."""
     import torch
 
-    T = logits.shape[0]
-    V = logits.shape[1] if V is None else V
+    T, cols = logits.shape
+    V = cols if V is None else V
     ld = _rows2d(logits, "logits", V, 0)
-    dt = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}[logits.dtype]
+    dt = _logits_dtype(logits)
     n = 0 if tok_src is not None else T
     f32, i32 = torch.float32, torch.int32
-    _device_args(logits.device, target=(target, i32, n), mask=(mask, torch.uint8, n), tok_src=(tok_src, torch.int64, T),
-                 logp_tok=(logp_tok, f32, n), entropy_tok=(entropy_tok, f32, n), top_idx=(top_idx, i32, n * K),
-                 top_logp=(top_logp, f32, n * K))
+    _device_args(logits, ("target", target, i32, n), ("mask", mask, torch.uint8, n), ("tok_src", tok_src, torch.int64, T),
+                 ("logp_tok", logp_tok, f32, n), ("entropy_tok", entropy_tok, f32, n), ("top_idx", top_idx, i32, n * K),
+                 ("top_logp", top_logp, f32, n * K))
     ld_top = K
     if K > 0 and top_idx is not None:
         ld_top = _rows2d(top_idx, "top_idx", K, n)
-        if top_logp is not None and _rows2d(top_logp, "top_logp", K, n) != ld_top:
-            raise ValueError("top_logp must have top_idx's row stride")
+        if top_logp is not None and (top_logp.shape != top_idx.shape or not _same_rows(top_idx, top_logp)):
+            raise ValueError("top_logp must have top_idx's shape and strides")
     rc = _lib().grpo_token_topk_logprobs(_ptr(logits), dt, T, V, ld, _ptr(tok_src), _ptr(target), _ptr(mask),
                                          float(temperature), int(K), _ptr(logp_tok), _ptr(entropy_tok), _ptr(top_idx),
                                          _ptr(top_logp), ld_top, _stream(stream))
@@ -477,10 +494,10 @@ def grpo_token_topk_logprobs(logits, K: int, target=None, logp_tok=None, entropy
 
 def _teacher_list(top_idx, top_logp, rows: int):
     """(K, row stride) of a teacher's list, [rows, K] with a unit inner stride in both tensors."""
-    K = top_idx.shape[1] if top_idx.dim() == 2 else 0
+    K = top_idx.shape[-1]
     ld_top = _rows2d(top_idx, "top_idx", K, rows)
-    if top_logp.shape != top_idx.shape or _rows2d(top_logp, "top_logp", K, rows) != ld_top:
-        raise ValueError("top_logp must have top_idx's shape and row stride")
+    if top_logp.shape != top_idx.shape or not _same_rows(top_idx, top_logp):
+        raise ValueError("top_logp must have top_idx's shape and strides")
     return K, ld_top
 
 
@@ -492,15 +509,15 @@ def grpo_distill_topk_fwd_bwd(logits, top_idx, top_logp, mask, kind: int, grad_s
     grpo.h."""
     import torch
 
-    T = logits.shape[0]
-    V = logits.shape[1] if V is None else V
+    T, cols = logits.shape
+    V = cols if V is None else V
     ld = _rows2d(logits, "logits", V, 0)
-    dt = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}[logits.dtype]
+    dt = _logits_dtype(logits)
     n = 0 if tok_src is not None else T
-    f32 = torch.float32
-    _device_args(logits.device, top_idx=(top_idx, torch.int32, 0), top_logp=(top_logp, f32, 0),
-                 mask=(mask, torch.uint8, n), w_tok=(w_tok, f32, n), tok_src=(tok_src, torch.int64, T),
-                 dlogits=(dlogits, logits.dtype, 0), loss_tok=(loss_tok, f32, n), acc=(acc, torch.uint8, ACC_BYTES))
+    f32, u8 = torch.float32, torch.uint8
+    _device_args(logits, ("top_idx", top_idx, torch.int32, 0), ("top_logp", top_logp, f32, 0), ("mask", mask, u8, n),
+                 ("w_tok", w_tok, f32, n), ("tok_src", tok_src, torch.int64, T), ("dlogits", dlogits, logits.dtype, 0),
+                 ("loss_tok", loss_tok, f32, n), ("acc", acc, u8, ACC_BYTES))
     K, ld_top = _teacher_list(top_idx, top_logp, n)
     ld_out = 0 if dlogits is None else _rows2d(dlogits, "dlogits", V, T)
     rc = _lib().grpo_distill_topk_fwd_bwd(_ptr(logits), dt, T, V, ld, _ptr(tok_src), _ptr(top_idx), _ptr(top_logp),
@@ -614,9 +631,11 @@ def grpo_lmhead_distill_topk_fwd_bwd(h, W, top_idx, top_logp, mask, grad_scale: 
     T, H = h.shape
     V = W.shape[0]
     f32, bf16 = torch.float32, torch.bfloat16
-    _device_args(h.device, h=(h, bf16, 0), W=(W, bf16, 0), top_idx=(top_idx, torch.int32, 0), top_logp=(top_logp, f32, 0),
-                 mask=(mask, torch.uint8, T), w_tok=(w_tok, f32, T), d_h=(d_h, f32, T * H), dW=(dW, f32, V * H),
-                 loss_tok=(loss_tok, f32, T), acc=(acc, torch.uint8, ACC_BYTES))
+    u8 = torch.uint8
+    _device_args(h, ("h", h, bf16, 0), ("W", W, bf16, 0), ("top_idx", top_idx, torch.int32, 0),
+                 ("top_logp", top_logp, f32, 0), ("mask", mask, u8, T), ("w_tok", w_tok, f32, T),
+                 ("d_h", d_h, f32, T * H), ("dW", dW, f32, V * H), ("loss_tok", loss_tok, f32, T),
+                 ("acc", acc, u8, ACC_BYTES))
     for name, t in (("d_h", d_h), ("dW", dW), ("workspace", workspace)):
         if t is not None and (t.device != h.device or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous on {h.device}")

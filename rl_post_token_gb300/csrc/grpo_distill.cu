@@ -85,8 +85,9 @@ __device__ __forceinline__ uint64_t listed_bits(const int32_t* sorted, int n, in
   for (; lo < n; ++lo) {
     const int64_t d = (int64_t)sorted[lo] - e0;
     if (d >= TE) break;
-    const int j = (int)d / E;  // vector of the tile
-    if ((j & 31) == lane) bits |= 1ull << ((j >> 5) * E + (int)d % E);
+    const int j = (int)d / E;  // vector of the tile: lane and u as tile_vec has them
+    const int l = (j >> 2) & 31, u = (j >> 7) * 4 + ((j - (l >> 1)) & 3);
+    if (l == lane) bits |= 1ull << (u * E + (int)d % E);
   }
   return bits;
 }
@@ -201,10 +202,12 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(Args a) {
           const int64_t tile = (int64_t)b * a.fold + f;
           if (tile * tile_elems<T>() >= V) break;
           uint4 x[kTileVecs];
-          load_tile<T, ALIGNED>(row, tile, V, lane, x);
-          const float lm = tile_lane_max<T>(x);
+#pragma unroll
+          for (int u = 0; u < kTileVecs; ++u)
+            x[u] = load_vec<T, ALIGNED>(row, tile * (32 * kTileVecs) + tile_vec(lane, u), V);
+          const float tm = warp_max_nan(tile_lane_max<T>(x)) * a.c;
           if (TAIL) drop_listed<T>(x, row_bad ? 0ull : listed_bits<T>(sh.sorted, n_listed, tile, lane));
-          const Part tp = tile_part<T, false>(x, lm, a.c);
+          const Part tp = tile_part<T, false>(x, tm, a.c);
           p = f == 0 ? tp : part_join(p, tp);
         }
         if (lane == 0) {

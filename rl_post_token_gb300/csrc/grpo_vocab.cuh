@@ -1,23 +1,26 @@
 #pragma once
 // Vocabulary rows read in warp tiles, for the scoring and distillation kernels.
 //
-// A row of V logits is cut into tiles of kTileVecs 16-byte vectors per lane (a warp reads a tile
-// of 4 KB: 2048 bf16 or 1024 float32 logits, lane l holding vectors l, l + 32, ...). A tile's
-// softmax partial is taken against the tile's own maximum,
+// A row of V logits is cut into tiles of 4 KB (2048 bf16 or 1024 float32 logits), one warp's work: 8
+// vectors of 16 bytes a lane. A tile's softmax partial is taken against its own maximum,
 //     m = max z log2(e)/tau,   s = sum 2^t,   q = sum 2^t t,   t = z log2(e)/tau - m,
-// and the row's from its tiles' in tile order. Element -> lane -> tile depends on V alone, so a
-// row's sums are the same bits however many CTAs, and whichever of them, read its tiles and
-// however the row is aligned in memory.
-#include <type_traits>
-
+// and the row's from its tiles'. Element -> lane -> tile depends on V alone, so a row's sums are the
+// same bits however many CTAs, and whichever of them, read its tiles and however the row is aligned
+// in memory.
+//
+// Tiles go through shared memory (bulk copies, one mbarrier per slot): the loads in flight cost no
+// registers, and a row that does not start on a 16-byte boundary is fetched by the aligned vectors it
+// touches and shifted into place when it is read from its slot.
 #include "grpo_common.cuh"
 
 namespace grpo {
 
-constexpr int kTileVecs = 8;
+constexpr int kTileVecs = 8;                       // vectors per lane
+constexpr int kTileBytes = 32 * kTileVecs * 16;    // 4 KB
+constexpr int kSlotBytes = kTileBytes + 128;       // and the vector an unaligned tile reaches into
 
 template <typename T>
-__host__ __device__ constexpr int tile_elems() { return 32 * kTileVecs * (16 / (int)sizeof(T)); }
+__host__ __device__ constexpr int tile_elems() { return kTileBytes / (int)sizeof(T); }
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -38,10 +41,6 @@ __device__ __forceinline__ float warp_max_nan(float x) {
   return r;
 }
 
-// -inf in every element of a 32-bit word of T.
-template <typename T>
-__host__ __device__ constexpr uint32_t neg_inf_word() { return sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u; }
-
 template <typename T>
 __device__ __forceinline__ float elem_f32(const T* p) {
   if constexpr (sizeof(T) == 2)
@@ -50,38 +49,134 @@ __device__ __forceinline__ float elem_f32(const T* p) {
     return *p;
 }
 
-// Vector j (E elements from E j) of a row of V elements, -inf past its end. ALIGNED: the row
-// starts on a 16-byte boundary; else its elements are read one by one.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ uint4 load_vec(const T* row, int64_t j, int64_t V) {
+// 16 bytes of a row from element e0 (which may lie before it), -inf outside [0, V); read element by
+// element.
+template <typename T>
+__device__ __forceinline__ uint4 edge_vec(const T* row, int64_t e0, int64_t V) {
   constexpr int E = 16 / (int)sizeof(T);
-  const int64_t e0 = j * E;
-  if (ALIGNED && e0 + E <= V) return __ldg(reinterpret_cast<const uint4*>(row) + j);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = neg_inf_word<T>();
-  if (e0 < V) {
-    if constexpr (sizeof(T) == 2) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + e0;
+  for (int i = 0; i < 4; ++i) w[i] = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (e0 + i < V) w[i / 2] = i & 1 ? (w[i / 2] & 0x0000FFFFu) | ((uint32_t)p[i] << 16) : (w[i / 2] & 0xFFFF0000u) | p[i];
-    } else {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + e0;
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (e0 + i < V) w[i] = p[i];
+  for (int i = 0; i < E; ++i)
+    if (e0 + i >= 0 && e0 + i < V) {
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t h = reinterpret_cast<const uint16_t*>(row)[e0 + i];
+        w[i / 2] = i & 1 ? (w[i / 2] & 0x0000FFFFu) | (h << 16) : (w[i / 2] & 0xFFFF0000u) | h;
+      } else {
+        w[i] = reinterpret_cast<const uint32_t*>(row)[e0 + i];
+      }
     }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Bytes by which a row's start (and with it every tile's) lies past a 16-byte boundary.
+__device__ __forceinline__ int row_off(const void* row) { return (int)(reinterpret_cast<uintptr_t>(row) & 15u); }
+
+// The part of fetch_tile at a row's ends: the slot's vectors [v0, v1) are wholly inside the row, the
+// others up to `all` are filled in here. (Out of line: few tiles come here, and the streaming loops
+// are short of instruction cache.)
+template <typename T>
+__device__ __noinline__ int2 fetch_edges(uint8_t* slot, const T* row, int off, int tile, int64_t V, int lane, int all) {
+  constexpr int E = 16 / (int)sizeof(T);
+  int v0 = 0, v1 = all;
+  const int64_t to_end = V * (int64_t)sizeof(T) - (int64_t)tile * kTileBytes + off;  // from the slot's start
+  if (to_end < (int64_t)v1 * 16) v1 = (int)(to_end / 16);
+  if (tile == 0 && off) v0 = 1;
+  const int64_t e0 = ((int64_t)tile * kTileBytes - off) / (int64_t)sizeof(T);
+  if (v0 && lane == 0) reinterpret_cast<uint4*>(slot)[0] = edge_vec(row, e0, V);
+  for (int v = (v1 > v0 ? v1 : v0) + lane; v < all; v += 32)
+    reinterpret_cast<uint4*>(slot)[v] = edge_vec(row, e0 + (int64_t)v * E, V);
+  return make_int2(v0, v1);
+}
+
+// Starts the fetch of a tile into a slot; every lane of the warp calls it. The slot receives the
+// aligned vectors that hold the tile, so the tile starts `off` bytes into it. Those wholly inside the
+// row come by one bulk copy, which completes on `bar`; what the row's ends cut is filled in by the
+// lanes (no byte outside the row is read), -inf where there is no element. A reader must be separated
+// from these stores by a barrier of the warp beside waiting for `bar`.
+template <typename T>
+__device__ __forceinline__ void fetch_tile(uint8_t* slot, const T* row, int off, int tile, int n_tiles, int64_t V,
+                                           int lane, uint64_t* bar) {
+  int2 v = make_int2(0, kTileVecs * 32 + (off ? 1 : 0));
+  // (the last vector of the last tile but one may be cut, too)
+  if ((tile == 0 && off) || tile + 1 >= n_tiles - 1) v = fetch_edges(slot, row, off, tile, V, lane, v.y);
+  if (lane == 0) {
+    const uint32_t bytes = v.y > v.x ? (uint32_t)(v.y - v.x) * 16u : 0u;
+    mbar_arrive_expect_tx(bar, bytes);
+    if (bytes)
+      bulk_g2s(slot + v.x * 16, reinterpret_cast<const uint8_t*>(row) + (int64_t)tile * kTileBytes - off + v.x * 16, bytes,
+               bar);
+  }
+}
+
+// Vector of a tile held by (lane, u): a lane's 8 vectors are two runs of 64 bytes. u rotates within a
+// run so that the 8 lanes of a shared-memory phase touch different banks.
+__device__ __forceinline__ int tile_vec(int lane, int u) {
+  return (u >> 2) * 128 + lane * 4 + ((u + (lane >> 1)) & 3);
+}
+
+// 16 bytes from `off` bytes (uniform over the warp) into the pair of vectors a, b.
+template <typename T>
+__device__ __forceinline__ uint4 shift_vec(const uint4& a, const uint4& b, int off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (off & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (sizeof(T) == 2 && (off & 2)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// This lane's vectors of a tile.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void load_tile(const T* row, int64_t tile, int64_t V, int lane, uint4 (&x)[kTileVecs]) {
-  const int64_t j0 = tile * (32 * kTileVecs) + lane;
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// Byte offsets of this lane's vectors 0..3 in a tile (4..7 follow 2048 bytes on).
+struct LaneOffsets {
+  uint32_t o[4];
+  __device__ explicit LaneOffsets(int lane) {
 #pragma unroll
-  for (int u = 0; u < kTileVecs; ++u) x[u] = load_vec<T, ALIGNED>(row, j0 + 32 * u, V);
+    for (int u = 0; u < 4; ++u) o[u] = (uint32_t)tile_vec(lane, u) * 16u;
+  }
+};
+
+// This lane's vectors of the tile in the slot at a shared-memory address.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void read_tile(uint32_t slot, int off, const LaneOffsets& lo, uint4 (&x)[kTileVecs]) {
+#pragma unroll
+  for (int u = 0; u < kTileVecs; ++u) {
+    const uint32_t at = slot + lo.o[u & 3] + (u >> 2) * 2048u;
+    x[u] = lds128(at);
+    if (!ALIGNED && off != 0) x[u] = shift_vec<T>(x[u], lds128(at + 16), off);
+  }
+}
+
+// Vector j of a row straight from global memory, -inf past its end. ALIGNED: the row starts on a
+// 16-byte boundary.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ uint4 load_vec(const T* row, int64_t j, int64_t V) {
+  constexpr int E = 16 / (int)sizeof(T);
+  if (ALIGNED && (j + 1) * E <= V) return __ldg(reinterpret_cast<const uint4*>(row) + j);
+  return edge_vec(row, j * E, V);
+}
+
+// Element i of a vector (a run-time index).
+template <typename T>
+__device__ __forceinline__ float vec_elem(const uint4& v, int i) {
+  const int k = sizeof(T) == 2 ? i >> 1 : i;
+  const uint32_t w = k & 2 ? (k & 1 ? v.w : v.z) : (k & 1 ? v.y : v.x);
+  if constexpr (sizeof(T) == 2) return i & 1 ? bf16_hi(w) : bf16_lo(w);
+  return __uint_as_float(w);
 }
 
 // Maximum of a vector's elements; NaN if one is.
@@ -126,7 +221,7 @@ __device__ __forceinline__ void vec_floats(const uint4& v, float (&f)[16 / sizeo
   }
 }
 
-// A softmax partial: (m, s, q) as above. s = 0 where nothing has mass (m is then -inf).
+// A softmax partial: (m, s, q) as above. m = -inf where nothing has mass.
 struct Part {
   float m, s, q;
 };
@@ -152,16 +247,23 @@ __device__ __forceinline__ Part warp_part(Part v) {
   return v;
 }
 
-// A tile's partial from its vectors and the lanes' maxima, c = log2(e)/tau. The sums run in
-// packed pairs over the lane's vectors, then by a fixed tree over the lanes; every lane gets
-// them. A NaN or +inf in the tile makes s NaN. Logits that c z takes below the float32 range
-// (the type's lowest value as a mask) have no mass, like -inf.
+// A row's partial from its blocks' in shared memory: lane l joins blocks l, l + 32, ... in order, the
+// lanes by a fixed tree.
+__device__ __forceinline__ Part row_part(const float* m, const float* s, const float* q, int n, int lane) {
+  Part r{-INFINITY, 0.f, 0.f};
+  for (int i = lane; i < n; i += 32) r = part_join(r, Part{m[i], s[i], q ? q[i] : 0.f});
+  return warp_part(r);
+}
+
+// A tile's partial from its vectors, m its maximum in log2 units, c = log2(e)/tau. The sums run in
+// packed pairs over the lane's vectors, then by a fixed tree over the lanes; every lane gets them. A
+// NaN or +inf in the tile makes s NaN or inf. Logits that c z takes below the float32 range (the type's
+// lowest value as a mask) have no mass, like -inf.
 template <typename T, bool Q>
-__device__ __forceinline__ Part tile_part(const uint4 (&x)[kTileVecs], float lane_max, float c) {
+__device__ __forceinline__ Part tile_part(const uint4 (&x)[kTileVecs], float m, float c) {
   constexpr int E = 16 / (int)sizeof(T);
-  const float m = warp_max_nan(lane_max) * c;
-  if (m == -INFINITY) return {m, 0.f, 0.f};
-  const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+  const float shift = m == -INFINITY ? 0.f : m;
+  const float2 c2 = make_float2(c, c), m2 = make_float2(-shift, -shift);
   float2 s[2] = {{0.f, 0.f}, {0.f, 0.f}}, q[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
   for (int u = 0; u < kTileVecs; ++u) {
@@ -181,13 +283,17 @@ __device__ __forceinline__ Part tile_part(const uint4 (&x)[kTileVecs], float lan
     qq = (q[0].x + q[1].x) + (q[0].y + q[1].y);
     if (qq != qq) {  // 0 * -inf of an element without mass (or a NaN row): once more without them
       qq = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < kTileVecs; ++i) {
+        uint4 v = x[0];
 #pragma unroll
-      for (int u = 0; u < kTileVecs; ++u) {
+        for (int u = 1; u < kTileVecs; ++u)
+          if (u == i) v = x[u];
         float f[E];
-        vec_floats<T>(x[u], f);
+        vec_floats<T>(v, f);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float t = fmaf(f[i], c, -m), e = ex2(t);
+        for (int k = 0; k < E; ++k) {
+          const float t = fmaf(f[k], c, -shift), e = ex2(t);
           if (e != 0.f) qq = fmaf(e, t, qq);
         }
       }

@@ -203,17 +203,45 @@ def test_targets_outside_the_vocabulary_and_left_out_outputs():
     _lib.grpo_token_topk_logprobs(z[:0], 5, top_idx=idx[:0])
 
 
-def test_results_do_not_depend_on_how_many_rows_share_the_call():
-    z = _logits(300, 151936, "bf16", 3.0, 21)
-    y = torch.arange(300, dtype=torch.int32, device=DEV) * 500
-    whole = _call(z, 20, y)
-    for a, b in [(0, 1), (1, 3), (3, 12), (12, 40), (40, 140), (140, 300)]:
-        part = _call(z[a:b], 20, y[a:b])
+@pytest.mark.parametrize("V, dtype, pad", [(151936, "bf16", 0), (50257, "bf16", 0), (35001, "f32", 0),
+                                           (35000, "f32", 0), (40000, "bf16", 8), (163840, "bf16", 3)])
+@pytest.mark.parametrize("K", [0, 1, 20, 256])
+def test_results_do_not_depend_on_how_many_rows_share_the_call(V, dtype, pad, K):
+    # a few rows, or a few dozen, go to other kernels than many rows: the bits are the same, with
+    # masked rows, padding rows and a shuffled order
+    T = 460
+    z = _logits(40, V, dtype, 3.0, 21, pad).repeat(12, 1)[:T]
+    if pad:
+        buf = torch.zeros((T, V + pad), dtype=DT[dtype], device=DEV)
+        buf[:, :V] = z
+        z = buf[:, :V]
+    z[7, 3:400] = float("-inf")
+    z[11, 5] = float("nan")
+    y = torch.arange(T, dtype=torch.int32, device=DEV) * 70
+    rng = np.random.default_rng(K)
+    mask = torch.from_numpy((rng.random(T) < 0.8).astype(np.uint8)).to(DEV)
+    src = rng.permutation(T)
+    src[rng.choice(T, 9, replace=False)] = -3
+    src = torch.from_numpy(src).to(DEV)
+    same = lambda a, b: torch.equal(a.view(torch.int32), b.view(torch.int32))
+    whole = _call(z, K, y)
+    for a, b in [(0, 1), (1, 3), (3, 12), (12, 40), (40, 140), (140, 460)]:
+        part = _call(z[a:b], K, y[a:b])
         for k in part:
-            assert torch.equal(part[k], whole[k][a:b]), (k, a, b)
+            assert same(part[k], whole[k][a:b]), (k, a, b)
     zh = W.logits_to_host(z[:2])
     for r in range(2):
-        _check_row(whole, r, zh[r], int(y[r]), 20, 1.0)
+        _check_row(whole, r, zh[r], int(y[r]), K, 1.0)
+    full = _call(z, K, y, mask=mask, tok_src=src)
+    at = src.clamp(min=0)
+    parts = _call(z[:1], K, y, mask=mask, tok_src=src[:1], rows=T)
+    for a in range(1, T, 50):
+        o = _call(z[a:a + 50], K, y, mask=mask, tok_src=src[a:a + 50], rows=T)
+        for k in o:
+            rows = src[a:a + 50][src[a:a + 50] >= 0]
+            parts[k][rows] = o[k][rows]
+    for k in full:
+        assert same(full[k][at], parts[k][at]), k
 
 
 def test_captured_into_a_graph_and_on_another_stream():
