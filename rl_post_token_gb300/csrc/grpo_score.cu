@@ -14,7 +14,7 @@
 // the bound.
 //
 // Two kernels, chosen by the number and length of the rows (launch rule at the end of the file):
-//  * stream_kernel  many long rows: one persistent CTA per SM whose 16 streaming warps never stop,
+//  * stream_kernel  many long rows: one persistent CTA per SM whose 12 streaming warps never stop,
 //                   while 8 others finish (LSE, bound, ranking) the rows before
 //  * row_kernel     few or short rows: one CTA per row, or a cluster that shares its reading
 #include <algorithm>
@@ -532,27 +532,28 @@ int launch_row(const Args& a, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------------
-// Many long rows: a persistent CTA per SM. Warps 0..15 stream: the blocks (two tiles) of the CTA's
+// Many long rows: a persistent CTA per SM. Warps 0..11 stream: the blocks (two tiles) of the CTA's
 // rows, in row order, go round-robin over them; each warp fetches its next block with bulk copies
 // while it reduces this one (rows that are not 16-byte aligned: into registers, one tile ahead). A
-// row's results go to one of a.slots row states. Every streaming warp passes every row: before it
-// enters a row it waits until the row's state was handed back as often as rows used it before, and it
-// counts the rows it has left, also those where none of the tiles is its own. The other warps
-// finish rows, kFinishGroups groups in turn, each once every streaming warp has left its row, and
-// hand the state back. So the loads never wait for a row's end. Masked and padding rows are skipped by
-// every warp alike. (The counts only grow, so a late reader cannot mistake a round for another, as
-// it could with a barrier's phase bit.)
+// row's results go to one of a.slots row states. Every streaming warp passes every row, also where
+// none of the tiles is its own: before it enters a row it waits until the row's state was handed back
+// (mbarrier freed), and it arrives on the state's other mbarrier (done) when it leaves it. So rows
+// are done in order, and both barriers' phases follow the rows one by one: a phase bit is never a
+// whole round off as long as there are at least as many states as finishing groups. The other warps
+// finish rows, kFinishGroups groups in turn, and hand the state back. So the loads never wait for a
+// row's end. Masked and padding rows are skipped by every warp alike.
 // ------------------------------------------------------------------------------------------
-constexpr int kStreamWarps = 16;
+constexpr int kStreamWarps = 12;
 constexpr int kFinishThreads = 128;
 constexpr int kFinishGroups = 2;
 constexpr int kStreamThreads = kStreamWarps * 32 + kFinishGroups * kFinishThreads;
 constexpr int kMinSlots = 3, kMaxSlots = 8;
+static_assert(kFinishGroups <= kMinSlots, "the phases' order");
 struct StreamShared {
   Finish<kFinishThreads> fin[kFinishGroups];
   uint64_t full[kStreamWarps][2];  // the copy of a tile of the block has landed
-  int left[32];                    // rows each streaming warp has left
-  int freed[kMaxSlots];            // times the row state was handed back
+  uint64_t done[kMaxSlots];        // every streaming warp has left the row
+  uint64_t freed[kMaxSlots];       // the row state may be rewritten
   int abort;
 };
 
@@ -562,26 +563,6 @@ __host__ __device__ constexpr int state_floats(int n_blocks) { return 4 * n_bloc
 __device__ __forceinline__ RowState row_state(float* base, int slot, int n_blocks) {
   float* p = base + (size_t)slot * state_floats(n_blocks);
   return {reinterpret_cast<float4*>(p), p + 4 * n_blocks, p + 4 * n_blocks + (n_blocks + 3) / 4 * 4};
-}
-
-// Bounded wait until a count that other warps of the CTA raise has reached n: about a second, as the
-// mbarrier waits. Every lane calls it; the result is the warp's.
-__device__ __noinline__ bool wait_count(const volatile int* count, int n, volatile int* abort) {
-  bool ok = *count >= n;
-  if (!__all_sync(0xffffffffu, ok)) {
-    const uint64_t t0 = global_timer_ns();
-    do {
-      __nanosleep(400);
-      ok = *count >= n;
-      if (*abort || global_timer_ns() - t0 > 1000000000ull) {
-        *abort = 1;
-        break;
-      }
-    } while (!ok);
-    ok = __all_sync(0xffffffffu, ok);
-  }
-  __threadfence_block();
-  return ok;
 }
 
 __host__ __device__ constexpr size_t stream_head_bytes() { return (sizeof(StreamShared) + 127) / 128 * 128; }
@@ -647,8 +628,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Args a) {
   if (tid == 0) {
     for (int w = 0; w < kStreamWarps; ++w)
       for (int s = 0; s < 2; ++s) mbar_init(&sh.full[w][s], 1);
-    for (int w = 0; w < kStreamWarps; ++w) sh.left[w] = 0;
-    for (int s = 0; s < kMaxSlots; ++s) sh.freed[s] = 0;
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(&sh.done[s], kStreamWarps);
+      mbar_init(&sh.freed[s], 1);
+    }
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -700,17 +683,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Args a) {
     auto pass_to = [&](int n, bool end) {  // on to read row n (end: there is none)
       while (at < n && ok) {
         __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.done[at_slot]);
         ++at;
-        if (lane == 0) {
-          __threadfence_block();  // the row's results before the count
-          *static_cast<volatile int*>(&sh.left[warp]) = at;
-        }
         if (++at_slot == a.slots) {
           at_slot = 0;
           ++at_round;
         }
-        if (!(end && at == n)) ok = wait_count(&sh.freed[at_slot], at_round, s_abort);
+        if (at_round > 0 && !(end && at == n))
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.freed[at_slot], (uint32_t)(at_round - 1) & 1u, s_abort));
       }
+      if (__any_sync(0xffffffffu, *s_abort)) ok = false;
       st = row_state(states, at_slot, a.n_blocks);
     };
     Flight cur = fetch(0), nxt = fetch(1);
@@ -785,8 +767,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Args a) {
     while (cur.row < a.T) {
       finish_reset(fin, gt);
       const int slot = cur.k % a.slots;
-      if (gt < 32) {  // the group's first warp waits (lanes past the streaming warps watch warp 0's count)
-        const bool ok = wait_count(&sh.left[lane < kStreamWarps ? lane : 0], cur.k + 1, s_abort);
+      if (gt < 32) {  // the group's first warp waits, the others at the barrier
+        const bool ok = mbar_wait_bounded(&sh.done[slot], (uint32_t)(cur.k / a.slots) & 1u, s_abort);
         if (gt == 0) fin.broken = !ok || *s_abort;
       }
       const Ahead nxt = look();
@@ -798,10 +780,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Args a) {
         const RowState st = row_state(states, slot, a.n_blocks);
         finish_row<T, ALIGNED, kFinishThreads>(a, row, cur.out, cur.zy,
                                                cur.y >= 0 && (int64_t)cur.y < V, st, fin, gt, bar, [&] {
-                                                 if (gt == 0) {  // one group at a time holds the state
-                                                   __threadfence_block();
-                                                   *static_cast<volatile int*>(&sh.freed[slot]) = cur.k / a.slots + 1;
-                                                 }
+                                                 if (gt == 0) mbar_arrive(&sh.freed[slot]);
                                                });
       }
       named_bar_sync(bar, kFinishThreads);  // the scratch is rewritten for the group's next row
