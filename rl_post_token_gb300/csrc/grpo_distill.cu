@@ -1,23 +1,23 @@
 // Distillation of a student's logits rows from a teacher's top tokens, loss and dlogits in one
-// call (formulas in grpo_distill.cuh).
+// call (formulas in grpo_distill.cuh). Per row: the softmax sums over its tiles (grpo_vocab.cuh; the
+// tail kinds leave the listed tokens out of them and add them singly), the list's arithmetic by one
+// warp, and dlogits over the tiles again.
 //
-// One CTA takes a row: it sorts the teacher's list by token, reads the row once for its softmax
-// sums (warp tiles, grpo_vocab.cuh; the tail kinds leave the listed tokens out of the tiles' sums
-// and add them singly), forms the token's loss with one thread per list entry, and reads the
-// row again, from L2, to write dlogits. 304 KB x 152 rows in flight fit L2.
+// Two kernels with the same bits, chosen by the row length:
+//  * cluster_kernel  rows of 16 to 384 tiles: the row stays in the shared memory of a cluster of 1 to 8
+//                    CTAs between its two readings, so HBM sees one read and one write of it
+//  * row_kernel      shorter and longer rows: one CTA per row, the second reading from L2
 #include <algorithm>
 #include <cmath>
 #include <mutex>
 
 #include "grpo_distill.cuh"
-#include "grpo_vocab.cuh"
 
 namespace grpo {
-namespace distill {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBlocks = 160;  // softmax partials kept per row
+size_t max_smem_optin();
+
+namespace distill {
 
 struct Args {
   const void* logits;
@@ -35,71 +35,56 @@ struct Args {
   int64_t ld_out;
   float* loss_tok;
   grpo_step_acc* acc;
-  int32_t n_blocks, fold;  // `fold` consecutive tiles per kept partial (a function of V)
+  int32_t n_tiles;
+  int32_t slots;           // cluster_kernel: tile slots per CTA
+  int32_t n_blocks, fold;  // row_kernel: `fold` consecutive tiles per kept partial
 };
 
-struct Shared {
-  int32_t sorted[GRPO_TOPK_MAX];  // the listed tokens in ascending order
-  float pm[kMaxBlocks], ps[kMaxBlocks];
-  double red[2][kWarps];
-  int bad, n_listed;
+// What the list's warp leaves for the others.
+struct Stats {
+  float shift, mult;  // dlogits = mult 2^(z c - shift) outside the list
 };
 
-// Sum of a value over the block (fixed tree); every thread gets it. Calls alternate `buf`.
-__device__ __forceinline__ double block_sum(double v, double* red, int lane, int warp) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) s += red[w];
-  return s;
+__device__ __forceinline__ float grad_scale_of(const Args& a, int64_t src) {
+  return a.w_tok ? a.scale * a.w_tok[src] : a.scale;
 }
 
-__device__ __forceinline__ float block_max(float v, double* red, int lane, int warp) {
-  v = warp_max_f32(v);
-  if (lane == 0) red[warp] = (double)v;
-  __syncthreads();
-  double m = red[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) m = fmax(m, red[w]);
-  return (float)m;
+__device__ __forceinline__ void count(grpo_step_acc* acc, unsigned long long tokens, unsigned long long valid,
+                                      unsigned long long nonfinite) {
+  if (tokens) atomicAdd(reinterpret_cast<unsigned long long*>(&acc->n_tokens), tokens);
+  if (valid) atomicAdd(reinterpret_cast<unsigned long long*>(&acc->n_valid), valid);
+  if (nonfinite) atomicAdd(reinterpret_cast<unsigned long long*>(&acc->n_nonfinite), nonfinite);
 }
 
-// The elements of this lane's tile vectors that are on the sorted list, as a bit mask (bit
-// u E + i: element i of vector u).
-template <typename T>
-__device__ __forceinline__ uint64_t listed_bits(const int32_t* sorted, int n, int64_t tile, int lane) {
-  constexpr int E = 16 / (int)sizeof(T), TE = tile_elems<T>();
-  const int64_t e0 = tile * TE;
-  int lo = 0, hi = n;
-  while (lo < hi) {  // first entry at or after the tile's start
-    const int mid = (lo + hi) / 2;
-    if ((int64_t)sorted[mid] < e0)
-      lo = mid + 1;
-    else
-      hi = mid;
+// Calls f(d, k) in every lane for each listed token of the tile, d its element of the tile and k its
+// place in the list: the warp looks at 32 entries at a time.
+template <typename T, typename F>
+__device__ __forceinline__ void for_listed(const int32_t* sh_tok, int K, int tile, int lane, F f) {
+  const int64_t e0 = (int64_t)tile * tile_elems<T>();
+#pragma unroll 1
+  for (int k0 = 0; k0 < K; k0 += 32) {
+    const int64_t d = (int64_t)sh_tok[k0 + lane] - e0;
+    unsigned hits = __ballot_sync(0xffffffffu, d >= 0 && d < tile_elems<T>());
+    for (; hits; hits &= hits - 1) {
+      const int l = __ffs(hits) - 1;
+      f(__shfl_sync(0xffffffffu, (int)d, l), k0 + l);
+    }
   }
-  uint64_t bits = 0;
-  for (; lo < n; ++lo) {
-    const int64_t d = (int64_t)sorted[lo] - e0;
-    if (d >= TE) break;
-    const int j = (int)d / E;  // vector of the tile: lane and u as tile_vec has them
-    const int l = (j >> 2) & 31, u = (j >> 7) * 4 + ((j - (l >> 1)) & 3);
-    if (l == lane) bits |= 1ull << (u * E + (int)d % E);
-  }
-  return bits;
 }
 
-// The listed elements of the vectors set to -inf.
+// The listed elements of this lane's vectors set to -inf (vectors as tile_vec has them).
 template <typename T>
-__device__ __forceinline__ void drop_listed(uint4 (&x)[kTileVecs], uint64_t bits) {
+__device__ __forceinline__ void drop_listed(uint4 (&x)[kTileVecs], const int32_t* sh_tok, int K, int tile, int lane) {
   constexpr int E = 16 / (int)sizeof(T);
+  uint64_t bits = 0;  // bit u E + i: element i of vector u
+  for_listed<T>(sh_tok, K, tile, lane, [&](int d, int) {
+    const int j = d / E, l = (j >> 2) & 31, u = (j >> 7) * 4 + ((j - (l >> 1)) & 3);
+    if (l == lane) bits |= 1ull << (u * E + d % E);
+  });
+  if (__any_sync(0xffffffffu, bits != 0)) {
 #pragma unroll
-  for (int u = 0; u < kTileVecs; ++u) {
-    const uint32_t b = (uint32_t)(bits >> (u * E)) & ((1u << E) - 1u);
-    if (b) {
+    for (int u = 0; u < kTileVecs; ++u) {
+      const uint32_t b = (uint32_t)(bits >> (u * E)) & ((1u << E) - 1u);
       uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
       for (int i = 0; i < E; ++i)
@@ -122,200 +107,497 @@ __device__ __forceinline__ void put_elem(T* p, float v) {
     *p = v;
 }
 
-template <typename T, int KIND, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) distill_kernel(Args a) {
-  __shared__ Shared sh;
+// The dlogits of a vector.
+template <typename T>
+__device__ __forceinline__ uint4 grad_vec(const uint4& v, float c, const Stats& s) {
   constexpr int E = 16 / (int)sizeof(T);
+  float f[E];
+  vec_floats<T>(v, f);
+  const float2 c2 = make_float2(c, c), m2 = make_float2(-s.shift, -s.shift), g2 = make_float2(s.mult, s.mult);
+#pragma unroll
+  for (int i = 0; i < E; i += 2) {
+    const float2 t = __ffma2_rn(make_float2(f[i], f[i + 1]), c2, m2);
+    const float2 e = __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), g2);
+    f[i] = e.x;
+    f[i + 1] = e.y;
+  }
+  if constexpr (sizeof(T) == 2)
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  else
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+// The first n elements of a vector, one by one.
+template <typename T>
+__device__ __noinline__ void store_elems(T* p, uint4 v, int n) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 16 / (int)sizeof(T); ++i)
+    if (i < n) {
+      if constexpr (sizeof(T) == 2)
+        reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+      else
+        reinterpret_cast<uint32_t*>(p)[i] = w[i];
+    }
+}
+
+// A vector stored to a row at elements e0.. (cut at the row's end). `align`: the row's alignment in
+// bytes. bf16 rows on odd elements (align 2) have their own way below.
+template <typename T>
+__device__ __forceinline__ void store_vec(T* row, int64_t e0, int64_t V, int align, const uint4& v) {
+  constexpr int E = 16 / (int)sizeof(T);
+  T* p = row + e0;
+  if (e0 + E > V || align < 4) {
+    if (e0 < V) store_elems(p, v, (int)min((int64_t)E, V - e0));
+  } else if (align == 16) {
+    *reinterpret_cast<uint4*>(p) = v;
+  } else if (align == 8) {
+    reinterpret_cast<uint2*>(p)[0] = make_uint2(v.x, v.y);
+    reinterpret_cast<uint2*>(p)[1] = make_uint2(v.z, v.w);
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
+}
+
+__device__ __forceinline__ int row_align(const void* row) {
+  const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(row);
+  return (a & 15u) == 0 ? 16 : (a & 7u) == 0 ? 8 : (a & 3u) == 0 ? 4 : 2;
+}
+
+// One vector of each lane (lane l: vector j0 + l of the row, wholly inside it in every lane) to a bf16
+// row on an odd element: in aligned words, each lane taking its successor's first element.
+__device__ __forceinline__ void store_odd(__nv_bfloat16* row, int64_t j0, int lane, const uint4& v) {
+  uint16_t* p = reinterpret_cast<uint16_t*>(row) + (j0 + lane) * 8;
+  const uint32_t nx = __shfl_down_sync(0xffffffffu, v.x, 1);
+  if (lane == 0) p[0] = (uint16_t)v.x;
+  uint32_t* w = reinterpret_cast<uint32_t*>(p + 1);
+  w[0] = __funnelshift_r(v.x, v.y, 16);
+  w[1] = __funnelshift_r(v.y, v.z, 16);
+  w[2] = __funnelshift_r(v.z, v.w, 16);
+  if (lane < 31)
+    w[3] = __funnelshift_r(v.w, nx, 16);
+  else
+    p[7] = (uint16_t)(v.w >> 16);
+}
+
+// ------------------------------------------------------------------------------------------
+// Rows outside the cluster kernel's range: one CTA per row.
+// ------------------------------------------------------------------------------------------
+constexpr int kMaxBlocks = 160;  // softmax partials kept per row
+
+template <typename T, int KIND, bool ALIGNED, int NT>
+__global__ void __launch_bounds__(NT) row_kernel(Args a) {
+  __shared__ int32_t sh_tok[GRPO_TOPK_MAX];
+  __shared__ float sh_corr[GRPO_TOPK_MAX], pm[kMaxBlocks], ps[kMaxBlocks];
+  __shared__ Stats stats;
+  constexpr int E = 16 / (int)sizeof(T), NW = NT / 32;
+  constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t V = a.V, nvec = (V + E - 1) / E;
+  unsigned long long c_tok = 0, c_val = 0, c_bad = 0;
   for (int64_t row_i = blockIdx.x; row_i < a.T; row_i += gridDim.x) {
     const int64_t src = a.tok_src ? a.tok_src[row_i] : row_i;
     const T* row = static_cast<const T*>(a.logits) + row_i * a.ld;
     T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + row_i * a.ld_out : nullptr;
+    const int align = dz ? row_align(dz) : 16;
     const bool valid = src >= 0 && a.mask[src] != 0;
-    float mult = 0.f, M = 0.f;   // dz_v = mult 2^(z_v c - M) outside the list
-    float corr = 0.f;            // dz of this thread's list entry
-    int32_t tok = -1;            // its token
-    if (tid == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&a.acc->n_tokens), 1ull);
+    ++c_tok;
     if (!valid) {
       if (tid == 0 && src >= 0) a.loss_tok[src] = 0.f;
-    } else {
-      // ---- the teacher's list: one thread per entry ----
-      float tlp = -INFINITY, z = -INFINITY;
-      if (tid < a.K) {
-        tok = a.top_idx[src * a.ld_top + tid];
-        if (tok != -1) tlp = a.top_logp[src * a.ld_top + tid];
-      }
-      if (tid == 0) sh.bad = sh.n_listed = 0;
-      if (tid < GRPO_TOPK_MAX) sh.sorted[tid] = tok;
-      __syncthreads();
-      const bool listed = tok != -1;
-      bool bad = listed && (tok < 0 || (int64_t)tok >= V || tlp != tlp || tlp == INFINITY);
-      int rank = 0;
-      if (listed)
-        for (int k = 0; k < a.K; ++k) {
-          const int32_t o = sh.sorted[k];
-          bad |= o == tok && k != tid;  // a token listed twice
-          rank += o != -1 && o < tok;
-        }
-      if (listed && !bad) z = elem_f32(row + tok);
-      const unsigned nl = __popc(__ballot_sync(0xffffffffu, listed));
-      if (lane == 0 && nl) atomicAdd(&sh.n_listed, (int)nl);
-      if (bad) atomicOr(&sh.bad, 1);
-      __syncthreads();
-      if (listed && !bad) sh.sorted[rank] = tok;
-      const bool row_bad = sh.bad != 0;
-      const int n_listed = sh.n_listed;
-      Teacher te{0.f, 0.f, 0.f};
-      float q = 0.f;
-      {
-        // the list's mass: in 64 bits, as q_R = 1 - Q cancels
-        const bool use = listed && !row_bad;
-        float mx = 0.f;  // FORWARD_TOPK takes the list up to a constant
-        if (KIND == GRPO_DISTILL_FORWARD_TOPK) {
-          mx = block_max(use ? tlp : -INFINITY, sh.red[1], lane, warp);
-          if (mx == -INFINITY) mx = 0.f;
-        }
-        const double qd = use ? exp((double)tlp - (double)mx) : 0.0;
-        const double Q = block_sum(qd, sh.red[0], lane, warp);
-        if (KIND == GRPO_DISTILL_FORWARD_TOPK) {
-          te.log_norm = (float)((double)mx + log(Q));
-          q = Q > 0.0 ? (float)(qd / Q) : 0.f;
-          te.q_all = Q > 0.0 ? 1.f : 0.f;
-        } else {
-          const double qr = 1.0 - Q;
-          q = (float)qd;
-          const bool none = n_listed >= V;
-          if (KIND == GRPO_DISTILL_FORWARD_TAIL)
-            te.q_rest = qr < kTailMin || none ? 0.f : (float)qr;
-          else
-            te.q_rest = (float)fmax(qr, kTailMin);
-          te.q_all = (float)(Q + (double)te.q_rest);
-        }
-      }
-
-      // ---- the row's softmax sums ----
-      constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
-      for (int b = warp; b < a.n_blocks; b += kWarps) {
-        Part p{-INFINITY, 0.f, 0.f};
-        for (int f = 0; f < a.fold; ++f) {
-          const int64_t tile = (int64_t)b * a.fold + f;
-          if (tile * tile_elems<T>() >= V) break;
-          uint4 x[kTileVecs];
-#pragma unroll
-          for (int u = 0; u < kTileVecs; ++u)
-            x[u] = load_vec<T, ALIGNED>(row, tile * (32 * kTileVecs) + tile_vec(lane, u), V);
-          const float tm = warp_max_nan(tile_lane_max<T>(x)) * a.c;
-          if (TAIL) drop_listed<T>(x, row_bad ? 0ull : listed_bits<T>(sh.sorted, n_listed, tile, lane));
-          const Part tp = tile_part<T, false>(x, tm, a.c);
-          p = f == 0 ? tp : part_join(p, tp);
-        }
-        if (lane == 0) {
-          sh.pm[b] = p.m;
-          sh.ps[b] = p.s;
-        }
-      }
-      __syncthreads();
+      if (dz)
+        for (int64_t j = tid; j < nvec; j += NT) store_vec(dz, j * E, V, align, make_uint4(0, 0, 0, 0));
+      continue;
+    }
+    ++c_val;
+    List<T, KIND> list;
+    if (warp == 0) list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, row, V, sh_tok, lane);
+    if (TAIL) __syncthreads();
+    for (int b = warp; b < a.n_blocks; b += NW) {
       Part p{-INFINITY, 0.f, 0.f};
-      for (int b = lane; b < a.n_blocks; b += 32) p = part_join(p, Part{sh.pm[b], sh.ps[b], 0.f});
-      p = warp_part(p);
-      M = p.m;
-
-      // ---- the token's loss and gradient coefficients ----
-      const float t = fmaf(z, a.c, -M);  // log2 of the entry's share before normalisation
-      const bool in = listed && !bad;
-      const float e = in ? ex2(t) : 0.f;
-      const float S = TAIL ? p.s + (float)block_sum((double)e, sh.red[1], lane, warp) : p.s;
-      const bool ok = !row_bad && fabsf(M) < INFINITY && S > 0.f && S < INFINITY;
-      const float l2s = log2f(S), inv = 1.f / S;
-      const float lp = in ? (t - l2s) * kLn2 : 0.f;
-      const float pk = e * inv;
-      const float pr = TAIL ? p.s * inv : 0.f;
-      float term = 0.f;
-      if (KIND == GRPO_DISTILL_REVERSE_TAIL)
-        term = in && pk > 0.f ? pk * (lp - tlp) : 0.f;
-      else
-        term = in && q > 0.f ? q * ((tlp - te.log_norm) - lp) : 0.f;
-      float loss = (float)block_sum((double)term, sh.red[0], lane, warp);
-      float alpha;
-      if (KIND == GRPO_DISTILL_FORWARD_TOPK) {
-        alpha = te.q_all;
-        corr = te.q_all != 0.f ? pk - q : 0.f;
-      } else if (KIND == GRPO_DISTILL_FORWARD_TAIL) {
-        const float ratio = te.q_rest > 0.f ? te.q_rest / pr : 0.f;
-        if (te.q_rest > 0.f) loss += te.q_rest * logf(ratio);
-        alpha = te.q_all - ratio;
-        corr = fmaf(te.q_all, pk, -q);
-      } else {
-        const bool tail = pr > 0.f && n_listed < V;
-        const float fr = tail ? logf(pr / te.q_rest) : 0.f;
-        if (tail) loss = fmaf(pr, fr, loss);
-        alpha = tail ? fr - loss : 0.f;
-        corr = pk > 0.f ? pk * ((lp - tlp) - loss) : 0.f;
+      for (int f = 0; f < a.fold; ++f) {
+        const int tile = b * a.fold + f;
+        if (tile >= a.n_tiles) break;
+        uint4 x[kTileVecs];
+#pragma unroll
+        for (int u = 0; u < kTileVecs; ++u)
+          x[u] = load_vec<T, ALIGNED>(row, (int64_t)tile * (32 * kTileVecs) + tile_vec(lane, u), V);
+        const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
+        if (TAIL) drop_listed<T>(x, sh_tok, a.K, tile, lane);
+        const Part tp = tile_part<T, false>(x, m, a.c);
+        p = f == 0 ? tp : part_join(p, tp);
       }
-      if (!ok) loss = alpha = corr = __int_as_float(0x7fc00000);
-      const float g = a.w_tok ? a.scale * a.w_tok[src] : a.scale;
-      corr *= g;
-      mult = alpha * g * inv;
-      if (!ok) M = 0.f;
-      if (tid == 0) {
-        a.loss_tok[src] = loss;
-        atomicAdd(reinterpret_cast<unsigned long long*>(&a.acc->n_valid), 1ull);
-        if (!isfinite(loss) || !isfinite(alpha * g))
-          atomicAdd(reinterpret_cast<unsigned long long*>(&a.acc->n_nonfinite), 1ull);
+      if (lane == 0) {
+        pm[b] = p.m;
+        ps[b] = p.s;
       }
-      if (bad) tok = -1;
     }
+    __syncthreads();
+    if (warp == 0) {
+      float loss;
+      Stats st;
+      bool finite;
+      list.finish(row_part(pm, ps, nullptr, a.n_blocks, lane), a.c, grad_scale_of(a, src), V, a.K, sh_corr, lane, loss,
+                  st.shift, st.mult, finite);
+      if (lane == 0) {
+        a.loss_tok[src] = loss;
+        stats = st;
+        if (!finite) ++c_bad;
+      }
+    }
+    __syncthreads();
     if (dz) {
-      // ---- dlogits: the dense part, then the list's entries over it ----
-      for (int64_t j = tid; j < nvec; j += kThreads) {
-        float f[E];
-        if (mult == 0.f) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) f[i] = 0.f;
-        } else {
-          vec_floats<T>(load_vec<T, ALIGNED>(row, j, V), f);
-#pragma unroll
-          for (int i = 0; i < E; ++i) f[i] = mult * ex2(fmaf(f[i], a.c, -M));
-        }
-        if (ALIGNED && (j + 1) * E <= V) {
-          if constexpr (sizeof(T) == 2)
-            __stcs(reinterpret_cast<uint4*>(dz) + j,
-                   make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                              pack_bf16x2(f[6], f[7])));
-          else
-            __stcs(reinterpret_cast<float4*>(dz) + j, make_float4(f[0], f[1], f[2], f[3]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (j * E + i < V) put_elem(dz + j * E + i, f[i]);
-        }
+      const Stats st = stats;
+      for (int64_t j = tid; j < nvec; j += NT) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (st.mult != 0.f) v = grad_vec<T>(load_vec<T, ALIGNED>(row, j, V), a.c, st);
+        store_vec(dz, j * E, V, align, v);
       }
       __syncthreads();
-      if (tok >= 0) put_elem(dz + tok, corr);
+      for (int k = tid; k < a.K; k += NT)
+        if (sh_tok[k] >= 0) put_elem(dz + sh_tok[k], sh_corr[k]);
     }
-    __syncthreads();  // sh is rewritten by the next row
+    __syncthreads();  // the shared arrays are rewritten by the next row
   }
+  if (tid == 0) count(a.acc, c_tok, c_val, c_bad);
 }
 
-template <typename T, int KIND, bool ALIGNED>
-int launch(const Args& a, cudaStream_t st) {
-  const int64_t grid = std::min<int64_t>(a.T, (int64_t)sm_count() * 2);
-  distill_kernel<T, KIND, ALIGNED><<<(unsigned)grid, kThreads, 0, st>>>(a);
+template <typename T, int KIND, bool ALIGNED, int NT>
+int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
+  const int64_t grid = std::min<int64_t>(a.T, (int64_t)sm_count() * per_sm);
+  row_kernel<T, KIND, ALIGNED, NT><<<(unsigned)grid, NT, 0, st>>>(a);
   GRPO_CUDA_TRY(cudaGetLastError());
   return GRPO_OK;
 }
 
-template <typename T, int KIND>
-int launch_aligned(const Args& a, bool aligned, cudaStream_t st) {
-  return aligned ? launch<T, KIND, true>(a, st) : launch<T, KIND, false>(a, st);
+// ------------------------------------------------------------------------------------------
+// The cluster kernel: persistent clusters of C CTAs, one CTA per SM; CTA r of a cluster has the tiles
+// [r tpc, (r + 1) tpc) of its rows. Warps of a CTA:
+//   0       producer: fetches the CTA's tiles, row after row, into a ring of slots; slots beyond a
+//           row's tiles hold the first tiles of the next row already
+//   1, 2    the rows' lists, in turn: loads a list (and the listed logits) a row ahead; joins the
+//           row's partials once all have arrived; writes the loss and what pass 2 needs
+//   3..18   the tiles, tile i of the CTA by warp 3 + i % 16. Pass 1: the tile's partial, sent to every
+//           CTA of the cluster (st.async, counted by the row's mbarrier there, so nobody waits for a
+//           cluster barrier). Pass 2: dlogits from the same slot, the listed tokens' over them;
+//           then the slot is free.
+// Two buffers (rows alternate) hold partials, lists and stats. Barriers per buffer: parts (the
+// partials have landed), taken (every CTA's list warp has read them: they may be sent again), listed
+// (the tokens are in shared memory), ready (stats and corrections are), over (pass 2 is done with
+// them). Masked and padding rows are skipped by all but the tile warps, which write their zeros.
+// ------------------------------------------------------------------------------------------
+constexpr int kTileWarps = 16;
+constexpr int kFirstTileWarp = 3;
+constexpr int kClusterThreads = (kFirstTileWarp + kTileWarps) * 32;
+constexpr int kMaxTiles = 384;
+constexpr int kMaxSlots = 56;
+constexpr int kMinTiles = 16;
+
+struct ClusterShared {
+  float2 part[2][kMaxTiles];  // (m, s) of every tile of the row
+  alignas(16) int32_t tok[2][GRPO_TOPK_MAX];
+  float corr[2][GRPO_TOPK_MAX];
+  Stats stats[2];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t parts[2], taken[2], listed[2], ready[2], over[2];
+  int abort;
+};
+
+__host__ __device__ constexpr size_t cluster_head_bytes() { return (sizeof(ClusterShared) + 127) / 128 * 128; }
+
+template <typename T, int KIND, bool ALIGNED>
+__global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int C) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  ClusterShared& sh = *reinterpret_cast<ClusterShared*>(smem_raw);
+  uint8_t* ring = smem_raw + cluster_head_bytes();
+  constexpr int E = 16 / (int)sizeof(T);
+  constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster_ctarank();
+  const int64_t first = blockIdx.x / C, stride = gridDim.x / C;
+  const int64_t V = a.V;
+  const int S = a.slots;
+  const int tpc = (a.n_tiles + C - 1) / C, t0 = rank * tpc;
+  const int mine = max(0, min(tpc, a.n_tiles - t0));  // tiles of this CTA
+  volatile int* s_abort = &sh.abort;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.parts[b], 1);
+      mbar_init(&sh.taken[b], (uint32_t)C);
+      mbar_init(&sh.listed[b], 1);
+      mbar_init(&sh.ready[b], 1);
+      mbar_init(&sh.over[b], kTileWarps);
+    }
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  cluster_sync_all();  // every CTA's barriers exist
+
+  const T* base = static_cast<const T*>(a.logits);
+  auto src_of = [&](int64_t r) -> int64_t { return a.tok_src ? a.tok_src[r] : r; };
+  auto is_read = [&](int64_t src) { return src >= 0 && a.mask[src] != 0; };
+
+  if (warp == 0) {
+    // ---- producer ----
+    int slot = 0;
+    uint32_t round = 0;  // times the ring went round
+    bool ok = true;
+    int64_t nsrc = first < a.T ? src_of(first) : -1;
+    bool nread = first < a.T && is_read(nsrc);
+    for (int64_t r = first; r < a.T && ok; r += stride) {
+      const bool read = nread;
+      if (r + stride < a.T) {  // the next row's index and mask while this row's tiles are issued
+        nsrc = src_of(r + stride);
+        nread = is_read(nsrc);
+      }
+      if (!read) continue;
+      const T* row = base + r * a.ld;
+      const int off = ALIGNED ? 0 : row_off(row);
+      for (int i = 0; i < mine; ++i) {
+        if (round > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort))) {
+          ok = false;
+          break;
+        }
+        fetch_tile<T>(ring + (size_t)slot * kSlotBytes, row, off, t0 + i, a.n_tiles, V, lane, &sh.full[slot]);
+        if (++slot == S) {
+          slot = 0;
+          ++round;
+        }
+      }
+    }
+    // a wait gave up: let the copies in flight land before the CTA's memory goes away (bounded)
+    if (!ok || *s_abort) {
+      const uint64_t begin = global_timer_ns();
+      for (int s = lane; s < S; s += 32) {
+        const uint32_t filled = round + (s < slot ? 1u : 0u);  // fills of the slot so far
+        while (filled > 0 && !mbar_try_wait(&sh.full[s], (filled - 1) & 1u) && global_timer_ns() - begin < 1000000000ull) {}
+      }
+    }
+  } else if (warp < kFirstTileWarp) {
+    // ---- the lists of every other read row ----
+    const int me = warp - 1;
+    unsigned long long c_val = 0, c_bad = 0;
+    int64_t v = 0;  // read rows so far
+    for (int64_t r = first; r < a.T; r += stride) {
+      const int64_t src = src_of(r);
+      if (!is_read(src)) continue;
+      const int64_t k = v++;
+      if ((int)(k & 1) != me) continue;
+      const uint32_t use = (uint32_t)(k >> 1), ph = use & 1u;  // the buffer's use, its phase
+      // the partials of all C CTAs will be counted: 8 bytes a tile
+      if (lane == 0) mbar_arrive_expect_tx_relaxed(&sh.parts[me], 8u * (uint32_t)a.n_tiles);
+      if (use > 0) mbar_wait_bounded(&sh.over[me], ph ^ 1u, s_abort);
+      List<T, KIND> list;
+      list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, base + r * a.ld, V, sh.tok[me], lane);
+      const float g = grad_scale_of(a, src);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.listed[me]);
+      mbar_wait_bounded(&sh.parts[me], ph, s_abort);
+      Part p{-INFINITY, 0.f, 0.f};
+      for (int i = lane; i < a.n_tiles; i += 32) {
+        const float2 q = sh.part[me][i];
+        p = part_join(p, Part{q.x, q.y, 0.f});
+      }
+      p = warp_part(p);
+      // (the partials were consumed by the shuffles: the signal needs no fence)
+      if (lane < C) mbar_arrive_remote_relaxed(mapa_u32(smem_u32(&sh.taken[me]), (uint32_t)lane));
+      float loss;
+      Stats st;
+      bool finite;
+      list.finish(p, a.c, g, V, a.K, sh.corr[me], lane, loss, st.shift, st.mult, finite);
+      if (lane == 0) sh.stats[me] = st;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.ready[me]);
+        if (rank == 0) a.loss_tok[src] = loss;
+      }
+      ++c_val;
+      if (!finite) ++c_bad;
+    }
+    if (rank == 0 && lane == 0) count(a.acc, 0, c_val, c_bad);
+  } else {
+    // ---- tiles ----
+    const int w = warp - kFirstTileWarp;
+    const LaneOffsets lo4(lane);
+    const uint32_t ring32 = smem_u32(ring);
+    int slot0 = 0;         // slot of the row's first tile
+    uint32_t round0 = 0;   // times the ring had gone round there
+    unsigned long long c_tok = 0;
+    uint32_t k = 0;  // read rows so far
+    int64_t nsrc = first < a.T ? src_of(first) : -1;
+    bool nread = first < a.T && is_read(nsrc);
+    for (int64_t r = first; r < a.T; r += stride) {
+      const int64_t src = nsrc;
+      const bool read = nread;
+      if (r + stride < a.T) {
+        nsrc = src_of(r + stride);
+        nread = is_read(nsrc);
+      }
+      ++c_tok;
+      T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ld_out : nullptr;
+      const int align = dz ? row_align(dz) : 16;
+      if (!read) {
+        if (rank == 0 && w == 0 && lane == 0 && src >= 0) a.loss_tok[src] = 0.f;
+        if (dz)
+          for (int i = w; i < mine; i += kTileWarps)
+            for (int u = 0; u < kTileVecs; ++u)
+              store_vec(dz, ((int64_t)(t0 + i) * (32 * kTileVecs) + u * 32 + lane) * E, V, align, make_uint4(0, 0, 0, 0));
+        continue;
+      }
+      const int buf = (int)(k & 1u);
+      const uint32_t use = k >> 1, ph = use & 1u;
+      ++k;
+      const int off = ALIGNED ? 0 : row_off(base + r * a.ld);
+      // pass 1
+      if (use > 0) mbar_wait_bounded(&sh.taken[buf], ph ^ 1u, s_abort);
+      if (TAIL) mbar_wait_bounded(&sh.listed[buf], ph, s_abort);
+      for (int i = w; i < mine; i += kTileWarps) {
+        int slot = slot0 + i;
+        uint32_t round = round0;
+        if (slot >= S) {
+          slot -= S;
+          ++round;
+        }
+        mbar_wait_bounded(&sh.full[slot], round & 1u, s_abort);
+        uint4 x[kTileVecs];
+        read_tile<T, ALIGNED>(ring32 + (uint32_t)slot * kSlotBytes, off, lo4, x);
+        const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
+        if (TAIL) drop_listed<T>(x, sh.tok[buf], a.K, t0 + i, lane);
+        const Part p = tile_part<T, false>(x, m, a.c);
+        if (lane < C)
+          st_async_v2f32(mapa_u32(smem_u32(&sh.part[buf][t0 + i]), (uint32_t)lane), p.m, p.s,
+                         mapa_u32(smem_u32(&sh.parts[buf]), (uint32_t)lane));
+      }
+      // pass 2
+      mbar_wait_bounded(&sh.ready[buf], ph, s_abort);
+      const Stats st = sh.stats[buf];
+      for (int i = w; i < mine; i += kTileWarps) {
+        int slot = slot0 + i;
+        if (slot >= S) slot -= S;
+        if (dz) {
+          const int tile = t0 + i;
+          const bool inside = (int64_t)(tile + 1) * tile_elems<T>() <= V;
+          const uint32_t at = ring32 + (uint32_t)slot * kSlotBytes + (uint32_t)lane * 16u;
+          const int64_t j0 = (int64_t)tile * (32 * kTileVecs);
+#pragma unroll
+          for (int u = 0; u < kTileVecs; ++u) {
+            uint4 v = lds128(at + (uint32_t)u * 512u);
+            if (!ALIGNED && off != 0) v = shift_vec<T>(v, lds128(at + (uint32_t)u * 512u + 16u), off);
+            v = st.mult != 0.f ? grad_vec<T>(v, a.c, st) : make_uint4(0, 0, 0, 0);
+            if constexpr (ALIGNED) {
+              if (inside)
+                reinterpret_cast<uint4*>(dz)[j0 + u * 32 + lane] = v;
+              else
+                store_vec(dz, (j0 + u * 32 + lane) * E, V, 16, v);
+            } else if (sizeof(T) == 2 && align == 2 && inside) {
+              store_odd(reinterpret_cast<__nv_bfloat16*>(dz), j0 + u * 32, lane, v);
+            } else {
+              store_vec(dz, (j0 + u * 32 + lane) * E, V, align, v);
+            }
+          }
+          __syncwarp();  // the listed tokens' over what other lanes have stored
+          for_listed<T>(sh.tok[buf], a.K, tile, lane, [&](int d, int e) {
+            if (lane == 0) put_elem(dz + (int64_t)tile * tile_elems<T>() + d, sh.corr[buf][e]);
+          });
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[slot]);
+      }
+      if (lane == 0) mbar_arrive(&sh.over[buf]);
+      slot0 += mine;
+      if (slot0 >= S) {
+        slot0 -= S;
+        ++round0;
+      }
+    }
+    if (rank == 0 && w == 0 && lane == 0) count(a.acc, c_tok, 0, 0);
+  }
+  __syncthreads();
+  if (*s_abort && tid == 0) atomicOr(&a.acc->flags, kFlagWaitTimeout);
+  cluster_sync_all();  // no CTA leaves while a peer may still store into or arrive on its memory
+}
+
+// CTAs per row: as many as its tiles need, and up to 8 where the call has too few rows for the SMs.
+int cluster_size(int64_t T, int n_tiles, int slots, int sms) {
+  int C = 1;
+  while (C * slots < n_tiles) C *= 2;
+  while (C < 8 && 2 * C * T <= sms && 2 * C * 2 <= n_tiles) C *= 2;
+  return C;
+}
+
+int cluster_slots() {
+  const size_t optin = max_smem_optin();
+  return optin > cluster_head_bytes() ? (int)std::min<size_t>(kMaxSlots, (optin - cluster_head_bytes()) / kSlotBytes) : 0;
+}
+
+template <typename T, int KIND, bool ALIGNED>
+int launch_cluster(Args a, int C, cudaStream_t st) {
+  auto kern = cluster_kernel<T, KIND, ALIGNED>;
+  const size_t smem = cluster_head_bytes() + (size_t)a.slots * kSlotBytes;
+  int dev = 0, n_clusters = 0;
+  GRPO_CUDA_TRY(cudaGetDevice(&dev));
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kClusterThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  {
+    static std::mutex mu;
+    static bool ready[64] = {};
+    static int fit[64][4] = {};  // clusters that run at once, by log2 C
+    const int lc = C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3;
+    std::lock_guard<std::mutex> lock(mu);
+    const bool known = dev >= 0 && dev < 64;
+    if (!known || !ready[dev]) {
+      GRPO_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      if (known) ready[dev] = true;
+    }
+    if (known) n_clusters = fit[dev][lc];
+    if (n_clusters == 0) {
+      cfg.gridDim = dim3((unsigned)(C * 1024), 1, 1);
+      GRPO_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n_clusters, kern, &cfg));
+      if (n_clusters < 1) return GRPO_ERR_UNSUPPORTED;
+      if (known) fit[dev][lc] = n_clusters;
+    }
+  }
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(a.T, n_clusters) * C), 1, 1);
+  GRPO_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, a, C));
+  return GRPO_OK;
+}
+
+template <typename T, int KIND, bool ALIGNED>
+int launch(Args a, cudaStream_t st) {
+  a.slots = cluster_slots();
+  if (a.n_tiles >= kMinTiles && a.n_tiles <= kMaxTiles && 8 * a.slots >= a.n_tiles)
+    return launch_cluster<T, KIND, ALIGNED>(a, cluster_size(a.T, a.n_tiles, a.slots, sm_count()), st);
+  a.fold = (a.n_tiles + kMaxBlocks - 1) / kMaxBlocks;
+  a.n_blocks = (a.n_tiles + a.fold - 1) / a.fold;
+  // short rows: small blocks, several rows in flight on an SM
+  if (a.n_tiles < kMinTiles) return launch_row_nt<T, KIND, ALIGNED, 128>(a, 8, st);
+  return launch_row_nt<T, KIND, ALIGNED, 512>(a, 2, st);
 }
 
 template <typename T>
 int dispatch(const Args& a, int32_t kind, bool aligned, cudaStream_t st) {
-  if (kind == GRPO_DISTILL_FORWARD_TOPK) return launch_aligned<T, GRPO_DISTILL_FORWARD_TOPK>(a, aligned, st);
-  if (kind == GRPO_DISTILL_FORWARD_TAIL) return launch_aligned<T, GRPO_DISTILL_FORWARD_TAIL>(a, aligned, st);
-  return launch_aligned<T, GRPO_DISTILL_REVERSE_TAIL>(a, aligned, st);
+  if (kind == GRPO_DISTILL_FORWARD_TOPK)
+    return aligned ? launch<T, GRPO_DISTILL_FORWARD_TOPK, true>(a, st) : launch<T, GRPO_DISTILL_FORWARD_TOPK, false>(a, st);
+  if (kind == GRPO_DISTILL_FORWARD_TAIL)
+    return aligned ? launch<T, GRPO_DISTILL_FORWARD_TAIL, true>(a, st) : launch<T, GRPO_DISTILL_FORWARD_TAIL, false>(a, st);
+  return aligned ? launch<T, GRPO_DISTILL_REVERSE_TAIL, true>(a, st) : launch<T, GRPO_DISTILL_REVERSE_TAIL, false>(a, st);
 }
 
 }  // namespace distill
@@ -364,9 +646,7 @@ extern "C" GRPO_API int grpo_distill_topk_fwd_bwd(const void* logits, int32_t dt
   a.ld_out = ld_out;
   a.loss_tok = loss_tok;
   a.acc = acc;
-  const int64_t tiles = (V * (int64_t)es + 4095) / 4096;
-  a.fold = (int32_t)((tiles + distill::kMaxBlocks - 1) / distill::kMaxBlocks);
-  a.n_blocks = (int32_t)((tiles + a.fold - 1) / a.fold);
+  a.n_tiles = (int32_t)((V * (int64_t)es + kTileBytes - 1) / kTileBytes);
   const bool aligned = ((in | out) & 15u) == 0 && (ld * es) % 16 == 0 && (!dlogits || (ld_out * es) % 16 == 0);
   const cudaStream_t st = as_stream(stream);
   return dtype == GRPO_DTYPE_BF16 ? distill::dispatch<__nv_bfloat16>(a, kind, aligned, st)

@@ -1,7 +1,7 @@
 #pragma once
-// Distillation from a teacher's top tokens: the arithmetic of one token, shared by the row kernel
-// and the LM-head variant. With the student's p = softmax(z/tau), the teacher's list S of
-// (token i_k, log q_k), Q = sum q_k, P = sum_S p, q_R = 1 - Q and p_R = 1 - P:
+// Distillation from a teacher's top tokens: the arithmetic of one token's list. With the student's
+// p = softmax(z/tau), the teacher's list S of (token i_k, log q_k), Q = sum q_k, P = sum_S p,
+// q_R = 1 - Q and p_R = 1 - P:
 //
 //   FORWARD_TOPK  L = sum_k qh_k (log qh_k - log p_k), qh = q/Q
 //   FORWARD_TAIL  L = sum_k q_k (log q_k - log p_k) + q_R (log q_R - log p_R)
@@ -15,7 +15,7 @@
 //
 // p_R is summed over the tokens outside S, never formed as 1 - P: a confident student leaves a
 // remainder that 1 - P would round away.
-#include "grpo_common.cuh"
+#include "grpo_vocab.cuh"
 
 namespace grpo {
 namespace distill {
@@ -24,11 +24,165 @@ namespace distill {
 // FORWARD_TAIL counts it as none, REVERSE_TAIL takes this value in its logarithm.
 constexpr double kTailMin = 5.9604644775390625e-08;
 
-// What the slots of one token need of the teacher's whole list.
-struct Teacher {
-  float log_norm;  // FORWARD_TOPK: log Q; 0 otherwise
+constexpr int kPerLane = GRPO_TOPK_MAX / 32;  // list entries a lane of the list's warp holds
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// One token's list, entry 32 j + lane in slot j of the lane. The warp holds it from the loads to the
+// gradients.
+template <typename T, int KIND>
+struct List {
+  int32_t tok[kPerLane];  // -1: unused
+  float tlp[kPerLane], z[kPerLane], q[kPerLane];
+  float log_norm;  // FORWARD_TOPK: log Q
   float q_rest;    // q_R (tail kinds), floored as above; 0 where nothing lies outside the list
-  float q_all;     // FORWARD_TAIL: Q + q_R
+  float q_all;     // FORWARD_TOPK: 1, or 0 without a list; FORWARD_TAIL: Q + q_R
+  int n;           // tokens listed
+  bool bad;        // a token twice or outside the vocabulary, a NaN or +inf log-prob
+
+  // Loads the list and the listed logits and writes the tokens to sh_tok [GRPO_TOPK_MAX] (unused
+  // entries -1; all of them if the list is bad).
+  __device__ __forceinline__ void load(const int32_t* top_idx, const float* top_logp, int K, const T* row, int64_t V,
+                                       int32_t* sh_tok, int lane) {
+    bool b = false;
+    n = 0;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      const int k = 32 * j + lane;
+      tok[j] = k < K ? top_idx[k] : -1;
+      tlp[j] = k < K && tok[j] != -1 ? top_logp[k] : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      const bool in = tok[j] >= 0 && (int64_t)tok[j] < V;
+      z[j] = in ? elem_f32(row + tok[j]) : -INFINITY;
+      b |= tok[j] != -1 && (!in || tlp[j] != tlp[j] || tlp[j] == INFINITY);
+      n += __popc(__ballot_sync(0xffffffffu, tok[j] != -1));
+      sh_tok[32 * j + lane] = tok[j];
+    }
+    __syncwarp();
+    // every entry against the entries before it
+#pragma unroll 1
+    for (int k0 = 0; k0 < K; k0 += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(sh_tok + k0);
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) {
+        const int k = 32 * j + lane;
+        b |= tok[j] != -1 && ((o.x == tok[j] && k0 < k) || (o.y == tok[j] && k0 + 1 < k) ||
+                              (o.z == tok[j] && k0 + 2 < k) || (o.w == tok[j] && k0 + 3 < k));
+      }
+    }
+    bad = __any_sync(0xffffffffu, b);
+    __syncwarp();
+    if (bad) {
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) sh_tok[32 * j + lane] = tok[j] = -1;
+      __syncwarp();
+    }
+    // the list's mass: in 64 bits, as q_R = 1 - Q cancels
+    float mx = -INFINITY;
+    if (KIND == GRPO_DISTILL_FORWARD_TOPK) {  // takes the list up to a constant
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) mx = fmaxf(mx, tok[j] != -1 ? tlp[j] : -INFINITY);
+      mx = warp_max_f32(mx);
+    }
+    const double shift = mx == -INFINITY ? 0.0 : (double)mx;
+    double qd[kPerLane], sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      qd[j] = 0.0;
+      if (32 * j < K) {  // warp-uniform
+        qd[j] = tok[j] != -1 ? exp((double)tlp[j] - shift) : 0.0;
+        sum += qd[j];
+      }
+    }
+    const double Q = warp_sum(sum);
+    log_norm = q_rest = 0.f;
+    if (KIND == GRPO_DISTILL_FORWARD_TOPK) {
+      log_norm = (float)(shift + log(Q));
+      q_all = Q > 0.0 ? 1.f : 0.f;
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) q[j] = qd[j] > 0.0 ? (float)(qd[j] / Q) : 0.f;
+    } else {
+      const double qr = 1.0 - Q;
+      if (KIND == GRPO_DISTILL_FORWARD_TAIL)
+        q_rest = qr < kTailMin || n >= V ? 0.f : (float)qr;
+      else
+        q_rest = (float)fmax(qr, kTailMin);
+      q_all = (float)(Q + (double)q_rest);
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) q[j] = (float)qd[j];
+    }
+  }
+
+  // The token's loss and gradients from the row's partial p (the tail kinds': without the listed
+  // tokens). dlogits are mult 2^(z c - shift) outside the list and sh_corr on it; g: the gradient
+  // scale. A row without a distribution or with a bad list has NaN for all of them.
+  __device__ __forceinline__ void finish(Part p, float c, float g, int64_t V, int K, float* sh_corr, int lane,
+                                         float& loss, float& shift, float& mult, bool& finite) {
+    constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
+    float t[kPerLane], e[kPerLane];
+    double se = 0.0;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      t[j] = fmaf(z[j], c, -p.m);
+      e[j] = tok[j] != -1 ? ex2(t[j]) : 0.f;
+      se += (double)e[j];
+    }
+    const float S = TAIL ? p.s + (float)warp_sum(se) : p.s;
+    const bool ok = !bad && fabsf(p.m) < INFINITY && S > 0.f && S < INFINITY;
+    const float l2s = log2f(S), inv = 1.f / S, pr = TAIL ? p.s * inv : 0.f;
+    double sum = 0.0;
+    float f[kPerLane];  // REVERSE_TAIL: log p - log q
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+      const float lp = (t[j] - l2s) * kLn2, pk = e[j] * inv;
+      float term;
+      if (KIND == GRPO_DISTILL_REVERSE_TAIL) {
+        f[j] = pk > 0.f ? lp - tlp[j] : 0.f;
+        term = pk > 0.f ? pk * f[j] : 0.f;
+      } else {
+        term = tok[j] != -1 && q[j] > 0.f ? q[j] * ((tlp[j] - log_norm) - lp) : 0.f;
+      }
+      sum += (double)term;
+    }
+    loss = (float)warp_sum(sum);
+    float alpha;
+    if (KIND == GRPO_DISTILL_FORWARD_TOPK) {
+      alpha = q_all;
+    } else if (KIND == GRPO_DISTILL_FORWARD_TAIL) {
+      const float ratio = q_rest > 0.f ? q_rest / pr : 0.f;
+      if (q_rest > 0.f) loss += q_rest * logf(ratio);
+      alpha = q_all - ratio;
+    } else {
+      const bool tail = pr > 0.f && n < V;
+      const float fr = tail ? logf(pr / q_rest) : 0.f;
+      if (tail) loss = fmaf(pr, fr, loss);
+      alpha = tail ? fr - loss : 0.f;
+    }
+    const float nan = __int_as_float(0x7fc00000);
+    if (!ok) loss = alpha = nan;
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j)
+      if (32 * j < K) {
+        const float pk = e[j] * inv;
+        float corr;
+        if (KIND == GRPO_DISTILL_FORWARD_TOPK)
+          corr = q_all != 0.f ? pk - q[j] : 0.f;
+        else if (KIND == GRPO_DISTILL_FORWARD_TAIL)
+          corr = fmaf(q_all, pk, -q[j]);
+        else
+          corr = pk > 0.f ? pk * (f[j] - loss) : 0.f;
+        sh_corr[32 * j + lane] = ok ? corr * g : nan;
+      }
+    shift = ok ? p.m : 0.f;
+    mult = ok ? alpha * g * inv : nan;
+    finite = isfinite(loss) && isfinite(alpha * g);
+  }
 };
 
 }  // namespace distill

@@ -87,14 +87,15 @@ __device__ __noinline__ int2 fetch_edges(uint8_t* slot, const T* row, int off, i
   if (v0 && lane == 0) reinterpret_cast<uint4*>(slot)[0] = edge_vec(row, e0, V);
   for (int v = (v1 > v0 ? v1 : v0) + lane; v < all; v += 32)
     reinterpret_cast<uint4*>(slot)[v] = edge_vec(row, e0 + (int64_t)v * E, V);
+  __syncwarp();  // before lane 0's arrive on the slot's barrier
   return make_int2(v0, v1);
 }
 
 // Starts the fetch of a tile into a slot; every lane of the warp calls it. The slot receives the
 // aligned vectors that hold the tile, so the tile starts `off` bytes into it. Those wholly inside the
 // row come by one bulk copy, which completes on `bar`; what the row's ends cut is filled in by the
-// lanes (no byte outside the row is read), -inf where there is no element. A reader must be separated
-// from these stores by a barrier of the warp beside waiting for `bar`.
+// lanes (no byte outside the row is read), -inf where there is no element, before lane 0 arrives on
+// `bar`. (A lane that waits on `bar` sees both.)
 template <typename T>
 __device__ __forceinline__ void fetch_tile(uint8_t* slot, const T* row, int off, int tile, int n_tiles, int64_t V,
                                            int lane, uint64_t* bar) {
