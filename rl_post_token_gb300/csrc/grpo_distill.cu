@@ -191,7 +191,7 @@ constexpr int kMaxBlocks = 160;  // softmax partials kept per row
 
 template <typename T, int KIND, bool ALIGNED, int NT>
 __global__ void __launch_bounds__(NT) row_kernel(Args a) {
-  __shared__ int32_t sh_tok[GRPO_TOPK_MAX];
+  __shared__ alignas(16) int32_t sh_tok[GRPO_TOPK_MAX];
   __shared__ float sh_corr[GRPO_TOPK_MAX], pm[kMaxBlocks], ps[kMaxBlocks];
   __shared__ Stats stats;
   constexpr int E = 16 / (int)sizeof(T), NW = NT / 32;
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
       float loss;
       Stats st;
       bool finite;
-      list.finish(row_part(pm, ps, nullptr, a.n_blocks, lane), a.c, grad_scale_of(a, src), V, a.K, sh_corr, lane, loss,
+      list.finish(join_blocks(a.n_blocks, lane, [&](int i) { return make_float2(pm[i], ps[i]); }), a.c, grad_scale_of(a, src), V, a.K, sh_corr, lane, loss,
                   st.shift, st.mult, finite);
       if (lane == 0) {
         a.loss_tok[src] = loss;
@@ -284,10 +284,13 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 //           CTA of the cluster (st.async, counted by the row's mbarrier there, so nobody waits for a
 //           cluster barrier). Pass 2: dlogits from the same slot, the listed tokens' over them;
 //           then the slot is free.
-// Two buffers (rows alternate) hold partials, lists and stats. Barriers per buffer: parts (the
-// partials have landed), taken (every CTA's list warp has read them: they may be sent again), listed
-// (the tokens are in shared memory), ready (stats and corrections are), over (pass 2 is done with
-// them). Masked and padding rows are skipped by all but the tile warps, which write their zeros.
+// Two buffers (rows alternate) hold partials, corrections and stats, four the tokens, which are
+// written while the tile warps may still be in pass 2 of the row before last. Barriers per buffer:
+// parts (the partials have landed), taken (every CTA's list warp has read them: they may be sent
+// again), listed (the tokens are in shared memory), ready (stats and corrections are). A tile warp with
+// tiles in a row cannot fall behind by a round of them, as the row's partials need its own; one
+// without (fewer than 16 tiles in the CTA) waits for none. Masked and padding rows are skipped by all
+// but the tile warps, which write their zeros.
 // ------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 16;
 constexpr int kFirstTileWarp = 3;
@@ -298,11 +301,11 @@ constexpr int kMinTiles = 16;
 
 struct ClusterShared {
   float2 part[2][kMaxTiles];  // (m, s) of every tile of the row
-  alignas(16) int32_t tok[2][GRPO_TOPK_MAX];
+  alignas(16) int32_t tok[4][GRPO_TOPK_MAX];
   float corr[2][GRPO_TOPK_MAX];
   Stats stats[2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t parts[2], taken[2], listed[2], ready[2], over[2];
+  uint64_t parts[2], taken[2], listed[2], ready[2];
   int abort;
 };
 
@@ -333,7 +336,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       mbar_init(&sh.taken[b], (uint32_t)C);
       mbar_init(&sh.listed[b], 1);
       mbar_init(&sh.ready[b], 1);
-      mbar_init(&sh.over[b], kTileWarps);
     }
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -394,19 +396,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       const uint32_t use = (uint32_t)(k >> 1), ph = use & 1u;  // the buffer's use, its phase
       // the partials of all C CTAs will be counted: 8 bytes a tile
       if (lane == 0) mbar_arrive_expect_tx_relaxed(&sh.parts[me], 8u * (uint32_t)a.n_tiles);
-      if (use > 0) mbar_wait_bounded(&sh.over[me], ph ^ 1u, s_abort);
       List<T, KIND> list;
-      list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, base + r * a.ld, V, sh.tok[me], lane);
+      list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, base + r * a.ld, V, sh.tok[k & 3], lane);
       const float g = grad_scale_of(a, src);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.listed[me]);
       mbar_wait_bounded(&sh.parts[me], ph, s_abort);
-      Part p{-INFINITY, 0.f, 0.f};
-      for (int i = lane; i < a.n_tiles; i += 32) {
-        const float2 q = sh.part[me][i];
-        p = part_join(p, Part{q.x, q.y, 0.f});
-      }
-      p = warp_part(p);
+      const Part p = join_blocks(a.n_tiles, lane, [&](int i) { return sh.part[me][i]; });
       // (the partials were consumed by the shuffles: the signal needs no fence)
       if (lane < C) mbar_arrive_remote_relaxed(mapa_u32(smem_u32(&sh.taken[me]), (uint32_t)lane));
       float loss;
@@ -456,6 +452,15 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       const uint32_t use = k >> 1, ph = use & 1u;
       ++k;
       const int off = ALIGNED ? 0 : row_off(base + r * a.ld);
+      const int32_t* tok = sh.tok[(k - 1) & 3u];
+      if (w >= mine) {
+        slot0 += mine;
+        if (slot0 >= S) {
+          slot0 -= S;
+          ++round0;
+        }
+        continue;
+      }
       // pass 1
       if (use > 0) mbar_wait_bounded(&sh.taken[buf], ph ^ 1u, s_abort);
       if (TAIL) mbar_wait_bounded(&sh.listed[buf], ph, s_abort);
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         uint4 x[kTileVecs];
         read_tile<T, ALIGNED>(ring32 + (uint32_t)slot * kSlotBytes, off, lo4, x);
         const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
-        if (TAIL) drop_listed<T>(x, sh.tok[buf], a.K, t0 + i, lane);
+        if (TAIL) drop_listed<T>(x, tok, a.K, t0 + i, lane);
         const Part p = tile_part<T, false>(x, m, a.c);
         if (lane < C)
           st_async_v2f32(mapa_u32(smem_u32(&sh.part[buf][t0 + i]), (uint32_t)lane), p.m, p.s,
@@ -504,14 +509,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
             }
           }
           __syncwarp();  // the listed tokens' over what other lanes have stored
-          for_listed<T>(sh.tok[buf], a.K, tile, lane, [&](int d, int e) {
+          for_listed<T>(tok, a.K, tile, lane, [&](int d, int e) {
             if (lane == 0) put_elem(dz + (int64_t)tile * tile_elems<T>() + d, sh.corr[buf][e]);
           });
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[slot]);
       }
-      if (lane == 0) mbar_arrive(&sh.over[buf]);
       slot0 += mine;
       if (slot0 >= S) {
         slot0 -= S;

@@ -26,10 +26,26 @@ constexpr double kTailMin = 5.9604644775390625e-08;
 
 constexpr int kPerLane = GRPO_TOPK_MAX / 32;  // list entries a lane of the list's warp holds
 
-__device__ __forceinline__ double warp_sum(double v) {
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// The row's partial (without q) from those of its blocks: get(i) gives block i's (m, s). Lane l joins
+// blocks l, l + 32, ... in order.
+template <typename G>
+__device__ __forceinline__ Part join_blocks(int n, int lane, G get) {
+  float m = -INFINITY, s = 0.f;
+  for (int i = lane; i < n; i += 32) {
+    const float2 b = get(i);
+    const float M = fmaxf(m, b.x);
+    // (where nothing has mass yet the sums are added as they are: 0, or the NaN of a NaN block)
+    s = M == -INFINITY ? s + b.y : fmaf(s, ex2(m - M), b.y * ex2(b.x - M));
+    m = M;
+  }
+  return warp_part<false>(Part{m, s, 0.f});
 }
 
 // One token's list, entry 32 j + lane in slot j of the lane. The warp holds it from the loads to the
@@ -38,7 +54,7 @@ template <typename T, int KIND>
 struct List {
   int32_t tok[kPerLane];  // -1: unused
   float tlp[kPerLane], z[kPerLane], q[kPerLane];
-  float log_norm;  // FORWARD_TOPK: log Q
+  float log_norm;  // FORWARD_TOPK: log of the list's mass, its log-probs taken from their largest
   float q_rest;    // q_R (tail kinds), floored as above; 0 where nothing lies outside the list
   float q_all;     // FORWARD_TOPK: 1, or 0 without a list; FORWARD_TAIL: Q + q_R
   int n;           // tokens listed
@@ -52,30 +68,37 @@ struct List {
     n = 0;
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      const int k = 32 * j + lane;
-      tok[j] = k < K ? top_idx[k] : -1;
-      tlp[j] = k < K && tok[j] != -1 ? top_logp[k] : -INFINITY;
+      tok[j] = -1;
+      tlp[j] = z[j] = -INFINITY;
+      if (32 * j < K && 32 * j + lane < K) {
+        tok[j] = top_idx[32 * j + lane];
+        tlp[j] = top_logp[32 * j + lane];
+      }
     }
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      const bool in = tok[j] >= 0 && (int64_t)tok[j] < V;
-      z[j] = in ? elem_f32(row + tok[j]) : -INFINITY;
-      b |= tok[j] != -1 && (!in || tlp[j] != tlp[j] || tlp[j] == INFINITY);
-      n += __popc(__ballot_sync(0xffffffffu, tok[j] != -1));
+      if (32 * j < K) {  // warp-uniform, here and below
+        const bool in = tok[j] >= 0 && (int64_t)tok[j] < V;
+        if (in) z[j] = elem_f32(row + tok[j]);
+        if (tok[j] == -1) tlp[j] = -INFINITY;
+        b |= tok[j] != -1 && (!in || tlp[j] != tlp[j] || tlp[j] == INFINITY);
+        n += __popc(__ballot_sync(0xffffffffu, tok[j] != -1));
+      }
       sh_tok[32 * j + lane] = tok[j];
     }
     __syncwarp();
     // every entry against the entries before it
-#pragma unroll 1
-    for (int k0 = 0; k0 < K; k0 += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(sh_tok + k0);
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j) {
+    for (int j = 0; j < kPerLane; ++j)
+      if (32 * j < K) {
         const int k = 32 * j + lane;
-        b |= tok[j] != -1 && ((o.x == tok[j] && k0 < k) || (o.y == tok[j] && k0 + 1 < k) ||
-                              (o.z == tok[j] && k0 + 2 < k) || (o.w == tok[j] && k0 + 3 < k));
+#pragma unroll 2
+        for (int k0 = 0; k0 < 32 * j + 32; k0 += 4) {
+          const int4 o = *reinterpret_cast<const int4*>(sh_tok + k0);
+          b |= tok[j] != -1 && ((o.x == tok[j] && k0 < k) || (o.y == tok[j] && k0 + 1 < k) ||
+                                (o.z == tok[j] && k0 + 2 < k) || (o.w == tok[j] && k0 + 3 < k));
+        }
       }
-    }
     bad = __any_sync(0xffffffffu, b);
     __syncwarp();
     if (bad) {
@@ -83,39 +106,49 @@ struct List {
       for (int j = 0; j < kPerLane; ++j) sh_tok[32 * j + lane] = tok[j] = -1;
       __syncwarp();
     }
-    // the list's mass: in 64 bits, as q_R = 1 - Q cancels
-    float mx = -INFINITY;
-    if (KIND == GRPO_DISTILL_FORWARD_TOPK) {  // takes the list up to a constant
+    log_norm = q_rest = 0.f;
+    if constexpr (KIND == GRPO_DISTILL_FORWARD_TOPK) {  // takes the list up to a constant
+      float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < kPerLane; ++j) mx = fmaxf(mx, tok[j] != -1 ? tlp[j] : -INFINITY);
       mx = warp_max_f32(mx);
-    }
-    const double shift = mx == -INFINITY ? 0.0 : (double)mx;
-    double qd[kPerLane], sum = 0.0;
+      const float shift = mx == -INFINITY ? 0.f : mx;
+      float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-      qd[j] = 0.0;
-      if (32 * j < K) {  // warp-uniform
-        qd[j] = tok[j] != -1 ? exp((double)tlp[j] - shift) : 0.0;
-        sum += qd[j];
+      for (int j = 0; j < kPerLane; ++j) {
+        q[j] = 0.f;
+        if (32 * j < K) {
+          q[j] = tok[j] != -1 ? expf(tlp[j] - shift) : 0.f;
+          sum += q[j];
+        }
       }
-    }
-    const double Q = warp_sum(sum);
-    log_norm = q_rest = 0.f;
-    if (KIND == GRPO_DISTILL_FORWARD_TOPK) {
-      log_norm = (float)(shift + log(Q));
-      q_all = Q > 0.0 ? 1.f : 0.f;
+      const float Q = warp_sum(sum), inv = Q > 0.f ? 1.f / Q : 0.f;
+      // log(q/Q) is formed as (log q - shift) - log Q: exact differences of the list's values
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j) q[j] = qd[j] > 0.0 ? (float)(qd[j] / Q) : 0.f;
+      for (int j = 0; j < kPerLane; ++j) {
+        q[j] *= inv;
+        tlp[j] -= shift;
+      }
+      log_norm = logf(Q);
+      q_all = Q > 0.f ? 1.f : 0.f;
     } else {
-      const double qr = 1.0 - Q;
+      // the list's mass in 64 bits, as q_R = 1 - Q cancels
+      double sum = 0.0;
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) {
+        q[j] = 0.f;
+        if (32 * j < K) {
+          const double qd = tok[j] != -1 ? exp((double)tlp[j]) : 0.0;
+          sum += qd;
+          q[j] = (float)qd;
+        }
+      }
+      const double Q = warp_sum(sum), qr = 1.0 - Q;
       if (KIND == GRPO_DISTILL_FORWARD_TAIL)
         q_rest = qr < kTailMin || n >= V ? 0.f : (float)qr;
       else
         q_rest = (float)fmax(qr, kTailMin);
       q_all = (float)(Q + (double)q_rest);
-#pragma unroll
-      for (int j = 0; j < kPerLane; ++j) q[j] = (float)qd[j];
     }
   }
 
@@ -126,20 +159,25 @@ struct List {
                                          float& loss, float& shift, float& mult, bool& finite) {
     constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
     float t[kPerLane], e[kPerLane];
-    double se = 0.0;
+    float se = 0.f;
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
-      t[j] = fmaf(z[j], c, -p.m);
-      e[j] = tok[j] != -1 ? ex2(t[j]) : 0.f;
-      se += (double)e[j];
+      t[j] = e[j] = 0.f;
+      if (32 * j < K) {
+        t[j] = fmaf(z[j], c, -p.m);
+        e[j] = tok[j] != -1 ? ex2(t[j]) : 0.f;
+        if (TAIL) se += e[j];
+      }
     }
-    const float S = TAIL ? p.s + (float)warp_sum(se) : p.s;
+    const float S = TAIL ? p.s + warp_sum(se) : p.s;
     const bool ok = !bad && fabsf(p.m) < INFINITY && S > 0.f && S < INFINITY;
     const float l2s = log2f(S), inv = 1.f / S, pr = TAIL ? p.s * inv : 0.f;
-    double sum = 0.0;
+    float sum = 0.f;
     float f[kPerLane];  // REVERSE_TAIL: log p - log q
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) {
+      f[j] = 0.f;
+      if (32 * j >= K) continue;
       const float lp = (t[j] - l2s) * kLn2, pk = e[j] * inv;
       float term;
       if (KIND == GRPO_DISTILL_REVERSE_TAIL) {
@@ -148,9 +186,9 @@ struct List {
       } else {
         term = tok[j] != -1 && q[j] > 0.f ? q[j] * ((tlp[j] - log_norm) - lp) : 0.f;
       }
-      sum += (double)term;
+      sum += term;
     }
-    loss = (float)warp_sum(sum);
+    loss = warp_sum(sum);
     float alpha;
     if (KIND == GRPO_DISTILL_FORWARD_TOPK) {
       alpha = q_all;

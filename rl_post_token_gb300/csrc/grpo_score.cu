@@ -183,7 +183,7 @@ __device__ __forceinline__ void finish_row(const Args& a, const T* row, int64_t 
     // ---- the row's log-sum-exp, entropy and target ----
     Part r{-INFINITY, 0.f, 0.f};
     for (int i = lane; i < a.n_blocks; i += 32) r = part_join(r, Part{st.part[i].x, st.part[i].y, st.part[i].z});
-    r = warp_part(r);
+    r = warp_part<true>(r);
     if (lane == 0) {
       // no distribution: a NaN or +inf logit, or no mass at all
       const bool ok = fabsf(r.m) < INFINITY && r.s > 0.f && r.s < INFINITY;

@@ -237,23 +237,20 @@ __device__ __forceinline__ Part part_join(Part a, Part b) {
   return {M, fmaf(fa, a.s, fb * b.s), qa + qb};
 }
 
-// The warp's partials joined by a fixed tree (every lane gets the result).
+// The warp's partials joined (every lane gets the result): all rescaled to the largest shift, the sums
+// by a fixed tree.
+template <bool Q>
 __device__ __forceinline__ Part warp_part(Part v) {
+  const float M = warp_max_nan(v.m);
+  if (M == -INFINITY) return {M, 0.f, 0.f};
+  const float d = v.m - M, f = ex2(d);
+  float q = Q && f != 0.f ? f * fmaf(d, v.s, v.q) : 0.f, s = f * v.s;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const Part w{__shfl_xor_sync(0xffffffffu, v.m, o), __shfl_xor_sync(0xffffffffu, v.s, o),
-                 __shfl_xor_sync(0xffffffffu, v.q, o)};
-    v = part_join(v, w);
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (Q) q += __shfl_xor_sync(0xffffffffu, q, o);
   }
-  return v;
-}
-
-// A row's partial from its blocks' in shared memory: lane l joins blocks l, l + 32, ... in order, the
-// lanes by a fixed tree.
-__device__ __forceinline__ Part row_part(const float* m, const float* s, const float* q, int n, int lane) {
-  Part r{-INFINITY, 0.f, 0.f};
-  for (int i = lane; i < n; i += 32) r = part_join(r, Part{m[i], s[i], q ? q[i] : 0.f});
-  return warp_part(r);
+  return {M, s, q};
 }
 
 // A tile's partial from its vectors, m its maximum in log2 units, c = log2(e)/tau. The sums run in

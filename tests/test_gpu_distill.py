@@ -1,13 +1,14 @@
 """GPU parity of the distillation call against the float64 oracle, every element of dlogits.
 
 Tolerances, from the arithmetic (t = (z - max) log2(e)/tau, E over the student's distribution):
-  dS = 2^-22 + 40 2^-24 + 2^-23 ln2 E|t|    relative error of a sum of exponentials (ex2 within
-       2^-22; at most 16 additions in a lane, 2 + 5 over the tile and 16 joins over the tiles, and one
-       to add the list's part, itself summed in 64 bits)
+  dS = 2^-22 + 50 2^-24 + 2^-23 ln2 E|t|    relative error of a sum of exponentials (ex2 within
+       2^-22; at most 16 additions in a lane, 2 + 5 over the tile, 12 joins and 5 additions over the
+       tiles, 8 + 5 over the list, one to add its part, and the joins' rescaling)
   dlp = dS + 2^-24 |log S| + 2^-23 (|z - max|/tau + |log p|)     of a log-prob (natural units)
   dp  = dS + 2^-22 + 2^-23 |t| ln2 + 4 2^-24                     relative, of a probability
        = what 2^t carries, the reciprocal of S and three products
-Loss: each term's parts with their errors. dlogits: |alpha p| (relative error of p) + p d(alpha), on
+Loss: each term's parts with their errors, and 8 + 5 additions over the list: 13 2^-24 of the terms'
+magnitudes; FORWARD_TOPK's q/Q is within 2^-22 (expf within 2^-22 at these arguments, the sum, the reciprocal). dlogits: |alpha p| (relative error of p) + p d(alpha), on
 the list p dp + q 2^-22 (FORWARD), p (dp |f - L| + d(f) + dL) (REVERSE); the grad scale adds three
 roundings. The output type adds half a step: 2^-8 (bf16) or 2^-24 (float32) of the value, and results
 below 2^-126 of the multiplier may be flushed."""
@@ -41,7 +42,7 @@ def _bars(z, idx, lq, kind, tau, g, parts, loss):
     S, lq = idx[on], lq[on].astype(np.float64)
     p, lp, pr, q, alpha = parts["p"], parts["lp"], parts["pr"], parts["q"], parts["alpha"]
     d = np.where(p > 0, (parts["m"] - z) / tau, 0.0)  # |t| ln2
-    dS = 2.0 ** -22 + 40 * U + 2 * U * float((p * d).sum())
+    dS = 2.0 ** -22 + 50 * U + 2 * U * float((p * d).sum())
     safe_lp = np.where(p > 0, lp, 0.0)
     dlp = dS + U * abs(np.log(parts["tot"])) + 2 * U * (d + np.abs(safe_lp))
     dp = dS + 2.0 ** -22 + 2 * U * d + 6 * U
@@ -52,16 +53,18 @@ def _bars(z, idx, lq, kind, tau, g, parts, loss):
     if kind == OD.FORWARD_TOPK:
         norm = abs(np.log(np.exp(lq - np.max(lq)).sum()) + np.max(lq)) if np.any(lq > -np.inf) else 0.0
         lqn = np.where(q > 0, np.log(np.where(q > 0, q, 1.0)), 0.0)
-        bl = np.sum(q * (dlp[S] + U * (2 * norm + 2 * np.abs(lq0) + 2 * np.abs(lqn)) + 3 * U * np.abs(lqn - lpS)))
+        dq = 8 * U + 13 * U
+        bl = np.sum(q * (dlp[S] + dq + U * (2 * norm + 2 * np.abs(lq0) + 2 * np.abs(lqn))
+                         + (3 * U + dq + 13 * U) * np.abs(lqn - lpS)))
         da = 0.0
         dz[:] = abs(alpha) * p * dp
-        dz[S] = pS * dp[S] + 3 * U * q + U * np.abs(pS - q)
+        dz[S] = pS * dp[S] + (dq + 3 * U) * q + U * np.abs(pS - q)
         if alpha == 0.0:
             dz[:] = 0.0
     elif kind == OD.FORWARD_TAIL:
         qr = parts["qr"]
         r = qr / pr if qr > 0 else 0.0
-        bl = np.sum(q * (dlp[S] + 3 * U * np.abs(lq0 - lpS) + U * (np.abs(lq0) + np.abs(lpS))))
+        bl = np.sum(q * (dlp[S] + 16 * U * np.abs(lq0 - lpS) + U * (np.abs(lq0) + np.abs(lpS))))
         bl += qr * (dpr + 3 * U + 3 * U * abs(np.log(r))) if qr > 0 else 0.0
         da = r * (dpr + 3 * U) + 3 * U * (q.sum() + qr)
         dz[:] = abs(alpha) * p * dp + p * da
@@ -70,7 +73,7 @@ def _bars(z, idx, lq, kind, tau, g, parts, loss):
         f, fr, qr = parts["f"], parts["fr"], parts["qr"]
         df = dlp[S] + 2 * U * np.abs(f) + U * (np.abs(lq0) + np.abs(lpS))
         dfr = dpr + 3 * U + 3 * U * abs(fr)
-        bl = np.sum(pS * (df + (dp[S] + 3 * U) * np.abs(f))) + pr * (dfr + (dpr + 3 * U) * abs(fr))
+        bl = np.sum(pS * (df + (dp[S] + 16 * U) * np.abs(f))) + pr * (dfr + (dpr + 3 * U) * abs(fr))
         da = dfr + bl + 3 * U * (abs(fr) + abs(loss))
         dz[:] = np.abs(alpha) * p * dp + p * da
         dz[S] = pS * ((dp[S] + 3 * U) * np.abs(f - loss) + df + bl + 3 * U * (np.abs(f) + abs(loss)))
