@@ -274,38 +274,51 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------------
-// The cluster kernel: persistent clusters of C CTAs, one CTA per SM; CTA r of a cluster has the tiles
-// [r tpc, (r + 1) tpc) of its rows. Warps of a CTA:
-//   0       producer: fetches the CTA's tiles, row after row, into a ring of slots; slots beyond a
-//           row's tiles hold the first tiles of the next row already
-//   1, 2    the rows' lists, in turn: loads a list (and the listed logits) a row ahead; joins the
-//           row's partials once all have arrived; writes the loss and what pass 2 needs
-//   3..18   the tiles, tile i of the CTA by warp 3 + i % 16. Pass 1: the tile's partial, sent to every
-//           CTA of the cluster (st.async, counted by the row's mbarrier there, so nobody waits for a
-//           cluster barrier). Pass 2: dlogits from the same slot, the listed tokens' over them;
-//           then the slot is free.
-// Two buffers (rows alternate) hold partials, corrections and stats, four the tokens, which are
-// written while the tile warps may still be in pass 2 of the row before last. Barriers per buffer:
-// parts (the partials have landed), taken (every CTA's list warp has read them: they may be sent
-// again), listed (the tokens are in shared memory), ready (stats and corrections are). A tile warp with
-// tiles in a row cannot fall behind by a round of them, as the row's partials need its own; one
-// without (fewer than 16 tiles in the CTA) waits for none. Masked and padding rows are skipped by all
-// but the tile warps, which write their zeros.
+// The cluster kernel: persistent clusters of C CTAs, one CTA per SM; the tiles of a row are split
+// evenly over the CTAs. Read row k (masked and padding rows are not read) is owned by CTA k % C, which
+// does its list's arithmetic. Warps of a CTA:
+//   0       producer: fetches the CTA's tiles, row after row, into a ring of slots
+//   1       tokens: puts every row's listed tokens into shared memory
+//   2, 3    lists of the rows this CTA owns, in turn: loads a list and the listed logits ahead of time,
+//           joins the row's partials once all have arrived, and sends what pass 2 needs (stats, the
+//           listed tokens' dlogits) to every CTA
+//   4..19   the tiles, tile i of the CTA by warp 4 + i % 16. Pass 1: the tile's partial, sent to the
+//           row's owner. Pass 2: dlogits from the same slot, the listed tokens' over them; then the
+//           slot is free.
+// Everything sent goes by asynchronous stores that an mbarrier of the receiver counts, so nobody waits
+// for a cluster barrier. Where two rows fit the ring, pass 1 of a row comes before pass 2 of the row
+// before it: the exchange and the list's arithmetic of one row run beside the tiles of the next. Each
+// row's arithmetic by every CTA of the cluster (no owner) took 1.9x at C = 4: one list is about 14,000
+// cycles of latency, a row 6,300 of bandwidth.
+//
+// Barriers: full/empty of the slots; listed[k & 1] (the tokens are in shared
+// memory; the tail kinds, which need them in pass 1); parts (owner, per
+// list warp: the row's partials are in); ready[k & 1] (stats and dlogits of the list are in, and the
+// tokens). Why no
+// buffer is rewritten too early: parts of row k are complete only when every tile warp of the cluster
+// is through pass 1 of row k, hence through pass 2 of row k - 2; so what is sent to ready[k & 1] then
+// finds row k - 2's done with, in every CTA, and a phase of ready, listed or parts is never overtaken
+// by a round. Tokens have four buffers: they are written two rows ahead of that. Warps without a tile
+// in the CTA wait for nothing.
 // ------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 16;
-constexpr int kFirstTileWarp = 3;
+constexpr int kListWarps = 2;  // (20 warps: five per scheduler, 96 registers a thread)
+constexpr int kFirstListWarp = 2;
+constexpr int kFirstTileWarp = kFirstListWarp + kListWarps;
 constexpr int kClusterThreads = (kFirstTileWarp + kTileWarps) * 32;
 constexpr int kMaxTiles = 384;
 constexpr int kMaxSlots = 56;
 constexpr int kMinTiles = 16;
 
 struct ClusterShared {
-  float2 part[2][kMaxTiles];  // (m, s) of every tile of the row
+  float2 part[kListWarps][kMaxTiles];  // (m, s) of every tile of an owned row
   alignas(16) int32_t tok[4][GRPO_TOPK_MAX];
+  alignas(16) int32_t list_tok[kListWarps][GRPO_TOPK_MAX];
+  float list_corr[kListWarps][GRPO_TOPK_MAX];
   float corr[2][GRPO_TOPK_MAX];
   Stats stats[2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t parts[2], taken[2], listed[2], ready[2];
+  uint64_t parts[kListWarps], listed[2], ready[2];
   int abort;
 };
 
@@ -323,17 +336,17 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
   const int64_t first = blockIdx.x / C, stride = gridDim.x / C;
   const int64_t V = a.V;
   const int S = a.slots;
-  const int tpc = (a.n_tiles + C - 1) / C, t0 = rank * tpc;
-  const int mine = max(0, min(tpc, a.n_tiles - t0));  // tiles of this CTA
+  const int t0 = rank * a.n_tiles / C, mine = (rank + 1) * a.n_tiles / C - t0;  // tiles of this CTA
+  const int most = (a.n_tiles + C - 1) / C;                                    // of any CTA
+  const int list_slots = (a.K + 31) / 32;
   volatile int* s_abort = &sh.abort;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], 1);
     }
+    for (int b = 0; b < kListWarps; ++b) mbar_init(&sh.parts[b], 1);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&sh.parts[b], 1);
-      mbar_init(&sh.taken[b], (uint32_t)C);
       mbar_init(&sh.listed[b], 1);
       mbar_init(&sh.ready[b], 1);
     }
@@ -383,49 +396,146 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         while (filled > 0 && !mbar_try_wait(&sh.full[s], (filled - 1) & 1u) && global_timer_ns() - begin < 1000000000ull) {}
       }
     }
-  } else if (warp < kFirstTileWarp) {
-    // ---- the lists of every other read row ----
-    const int me = warp - 1;
-    unsigned long long c_val = 0, c_bad = 0;
-    int64_t v = 0;  // read rows so far
+  } else if (warp == 1) {
+    // ---- tokens ----
+    uint32_t k = 0;
     for (int64_t r = first; r < a.T; r += stride) {
       const int64_t src = src_of(r);
       if (!is_read(src)) continue;
-      const int64_t k = v++;
-      if ((int)(k & 1) != me) continue;
-      const uint32_t use = (uint32_t)(k >> 1), ph = use & 1u;  // the buffer's use, its phase
-      // the partials of all C CTAs will be counted: 8 bytes a tile
+      int32_t tok[kPerLane];
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j) {
+        tok[j] = -1;
+        if (32 * j + lane < a.K) tok[j] = a.top_idx[src * a.ld_top + 32 * j + lane];
+        if (tok[j] < 0 || (int64_t)tok[j] >= V) tok[j] = -1;
+      }
+      const int buf = (int)(k & 1u);
+      if (k >= 2) mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
+#pragma unroll
+      for (int j = 0; j < kPerLane; ++j)
+        if (j < list_slots) sh.tok[k & 3u][32 * j + lane] = tok[j];
+      __syncwarp();
+      if (lane == 0) {
+        if (TAIL) mbar_arrive(&sh.listed[buf]);
+        // the row's stats and its list's dlogits will be counted (and the tokens are published)
+        mbar_arrive_expect_tx(&sh.ready[buf], 8u + 128u * (uint32_t)list_slots);
+      }
+      ++k;
+    }
+  } else if (warp < kFirstTileWarp) {
+    // ---- the lists of the rows this CTA owns ----
+    const int me = warp - kFirstListWarp;
+    unsigned long long c_val = 0, c_bad = 0;
+    uint32_t k = 0, own = 0;  // read rows, owned rows so far
+    for (int64_t r = first; r < a.T; r += stride) {
+      const int64_t src = src_of(r);
+      if (!is_read(src)) continue;
+      const uint32_t row_k = k++;
+      if ((int)(row_k % (uint32_t)C) != rank) continue;
+      const uint32_t j_own = own++;
+      if ((int)(j_own % kListWarps) != me) continue;
+      const uint32_t use = j_own / kListWarps;
+      // the partials of all tiles will be counted: 8 bytes each
       if (lane == 0) mbar_arrive_expect_tx_relaxed(&sh.parts[me], 8u * (uint32_t)a.n_tiles);
       List<T, KIND> list;
-      list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, base + r * a.ld, V, sh.tok[k & 3], lane);
+      list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, base + r * a.ld, V, sh.list_tok[me], lane);
       const float g = grad_scale_of(a, src);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.listed[me]);
-      mbar_wait_bounded(&sh.parts[me], ph, s_abort);
+      mbar_wait_bounded(&sh.parts[me], use & 1u, s_abort);
       const Part p = join_blocks(a.n_tiles, lane, [&](int i) { return sh.part[me][i]; });
-      // (the partials were consumed by the shuffles: the signal needs no fence)
-      if (lane < C) mbar_arrive_remote_relaxed(mapa_u32(smem_u32(&sh.taken[me]), (uint32_t)lane));
       float loss;
       Stats st;
       bool finite;
-      list.finish(p, a.c, g, V, a.K, sh.corr[me], lane, loss, st.shift, st.mult, finite);
-      if (lane == 0) sh.stats[me] = st;
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh.ready[me]);
-        if (rank == 0) a.loss_tok[src] = loss;
+      list.finish(p, a.c, g, V, a.K, sh.list_corr[me], lane, loss, st.shift, st.mult, finite);
+      const int buf = (int)(row_k & 1u);
+      if (lane < C)
+        st_async_v2f32(mapa_u32(smem_u32(&sh.stats[buf]), (uint32_t)lane), st.shift, st.mult,
+                       mapa_u32(smem_u32(&sh.ready[buf]), (uint32_t)lane));
+      for (int c = 0; c < C; ++c) {
+        const uint32_t bar = mapa_u32(smem_u32(&sh.ready[buf]), (uint32_t)c);
+        const uint32_t dst = mapa_u32(smem_u32(&sh.corr[buf][lane]), (uint32_t)c);
+        for (int j = 0; j < list_slots; ++j) st_async_f32(dst + 128u * (uint32_t)j, sh.list_corr[me][32 * j + lane], bar);
       }
+      if (lane == 0) a.loss_tok[src] = loss;
       ++c_val;
       if (!finite) ++c_bad;
     }
-    if (rank == 0 && lane == 0) count(a.acc, 0, c_val, c_bad);
+    if (lane == 0) count(a.acc, 0, c_val, c_bad);
   } else {
     // ---- tiles ----
     const int w = warp - kFirstTileWarp;
     const LaneOffsets lo4(lane);
     const uint32_t ring32 = smem_u32(ring);
-    int slot0 = 0;         // slot of the row's first tile
-    uint32_t round0 = 0;   // times the ring had gone round there
+    // a read row on its way: where its tiles are (slot of the first, rounds of the ring there), its number
+    struct Row {
+      T* dz;
+      int off, align, slot0;
+      uint32_t round0, k;
+    };
+    auto pass1 = [&](const Row& q) {
+      if (w >= mine) return;
+      if (TAIL) mbar_wait_bounded(&sh.listed[q.k & 1u], (q.k >> 1) & 1u, s_abort);
+      // the row's owner and the list warp there that takes its partials
+      const uint32_t owner = q.k % (uint32_t)C, box = (q.k / (uint32_t)C) % kListWarps;
+      const uint32_t part = mapa_u32(smem_u32(&sh.part[box][t0]), owner), bar = mapa_u32(smem_u32(&sh.parts[box]), owner);
+      for (int i = w; i < mine; i += kTileWarps) {
+        int slot = q.slot0 + i;
+        uint32_t round = q.round0;
+        if (slot >= S) {
+          slot -= S;
+          ++round;
+        }
+        mbar_wait_bounded(&sh.full[slot], round & 1u, s_abort);
+        uint4 x[kTileVecs];
+        read_tile<T, ALIGNED>(ring32 + (uint32_t)slot * kSlotBytes, q.off, lo4, x);
+        const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
+        if (TAIL) drop_listed<T>(x, sh.tok[q.k & 3u], a.K, t0 + i, lane);
+        const Part p = tile_part<T, false>(x, m, a.c);
+        if (lane == 0) st_async_v2f32(part + 8u * (uint32_t)i, p.m, p.s, bar);
+      }
+    };
+    auto pass2 = [&](const Row& q) {
+      if (w >= mine) return;
+      const int buf = (int)(q.k & 1u);
+      mbar_wait_bounded(&sh.ready[buf], (q.k >> 1) & 1u, s_abort);
+      const Stats st = sh.stats[buf];
+      for (int i = w; i < mine; i += kTileWarps) {
+        int slot = q.slot0 + i;
+        if (slot >= S) slot -= S;
+        if (q.dz) {
+          const int tile = t0 + i;
+          const bool inside = (int64_t)(tile + 1) * tile_elems<T>() <= V;
+          const uint32_t at = ring32 + (uint32_t)slot * kSlotBytes + (uint32_t)lane * 16u;
+          const int64_t j0 = (int64_t)tile * (32 * kTileVecs);
+#pragma unroll
+          for (int u = 0; u < kTileVecs; ++u) {
+            uint4 v = lds128(at + (uint32_t)u * 512u);
+            if (!ALIGNED && q.off != 0) v = shift_vec<T>(v, lds128(at + (uint32_t)u * 512u + 16u), q.off);
+            v = st.mult != 0.f ? grad_vec<T>(v, a.c, st) : make_uint4(0, 0, 0, 0);
+            if constexpr (ALIGNED) {
+              if (inside)
+                reinterpret_cast<uint4*>(q.dz)[j0 + u * 32 + lane] = v;
+              else
+                store_vec(q.dz, (j0 + u * 32 + lane) * E, V, 16, v);
+            } else if (sizeof(T) == 2 && q.align == 2 && inside) {
+              store_odd(reinterpret_cast<__nv_bfloat16*>(q.dz), j0 + u * 32, lane, v);
+            } else {
+              store_vec(q.dz, (j0 + u * 32 + lane) * E, V, q.align, v);
+            }
+          }
+          __syncwarp();  // the listed tokens' over what other lanes have stored
+          for_listed<T>(sh.tok[q.k & 3u], a.K, tile, lane, [&](int d, int e) {
+            if (lane == 0) put_elem(q.dz + (int64_t)tile * tile_elems<T>() + d, sh.corr[buf][e]);
+          });
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[slot]);
+      }
+    };
+    const bool ahead = 2 * most <= S;  // (the same in every CTA)
+    Row prev{};
+    bool pending = false;
+    int slot0 = 0;        // slot of the next row's first tile
+    uint32_t round0 = 0;  // times the ring had gone round there
     unsigned long long c_tok = 0;
     uint32_t k = 0;  // read rows so far
     int64_t nsrc = first < a.T ? src_of(first) : -1;
@@ -448,80 +558,22 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
               store_vec(dz, ((int64_t)(t0 + i) * (32 * kTileVecs) + u * 32 + lane) * E, V, align, make_uint4(0, 0, 0, 0));
         continue;
       }
-      const int buf = (int)(k & 1u);
-      const uint32_t use = k >> 1, ph = use & 1u;
-      ++k;
-      const int off = ALIGNED ? 0 : row_off(base + r * a.ld);
-      const int32_t* tok = sh.tok[(k - 1) & 3u];
-      if (w >= mine) {
-        slot0 += mine;
-        if (slot0 >= S) {
-          slot0 -= S;
-          ++round0;
-        }
-        continue;
-      }
-      // pass 1
-      if (use > 0) mbar_wait_bounded(&sh.taken[buf], ph ^ 1u, s_abort);
-      if (TAIL) mbar_wait_bounded(&sh.listed[buf], ph, s_abort);
-      for (int i = w; i < mine; i += kTileWarps) {
-        int slot = slot0 + i;
-        uint32_t round = round0;
-        if (slot >= S) {
-          slot -= S;
-          ++round;
-        }
-        mbar_wait_bounded(&sh.full[slot], round & 1u, s_abort);
-        uint4 x[kTileVecs];
-        read_tile<T, ALIGNED>(ring32 + (uint32_t)slot * kSlotBytes, off, lo4, x);
-        const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
-        if (TAIL) drop_listed<T>(x, tok, a.K, t0 + i, lane);
-        const Part p = tile_part<T, false>(x, m, a.c);
-        if (lane < C)
-          st_async_v2f32(mapa_u32(smem_u32(&sh.part[buf][t0 + i]), (uint32_t)lane), p.m, p.s,
-                         mapa_u32(smem_u32(&sh.parts[buf]), (uint32_t)lane));
-      }
-      // pass 2
-      mbar_wait_bounded(&sh.ready[buf], ph, s_abort);
-      const Stats st = sh.stats[buf];
-      for (int i = w; i < mine; i += kTileWarps) {
-        int slot = slot0 + i;
-        if (slot >= S) slot -= S;
-        if (dz) {
-          const int tile = t0 + i;
-          const bool inside = (int64_t)(tile + 1) * tile_elems<T>() <= V;
-          const uint32_t at = ring32 + (uint32_t)slot * kSlotBytes + (uint32_t)lane * 16u;
-          const int64_t j0 = (int64_t)tile * (32 * kTileVecs);
-#pragma unroll
-          for (int u = 0; u < kTileVecs; ++u) {
-            uint4 v = lds128(at + (uint32_t)u * 512u);
-            if (!ALIGNED && off != 0) v = shift_vec<T>(v, lds128(at + (uint32_t)u * 512u + 16u), off);
-            v = st.mult != 0.f ? grad_vec<T>(v, a.c, st) : make_uint4(0, 0, 0, 0);
-            if constexpr (ALIGNED) {
-              if (inside)
-                reinterpret_cast<uint4*>(dz)[j0 + u * 32 + lane] = v;
-              else
-                store_vec(dz, (j0 + u * 32 + lane) * E, V, 16, v);
-            } else if (sizeof(T) == 2 && align == 2 && inside) {
-              store_odd(reinterpret_cast<__nv_bfloat16*>(dz), j0 + u * 32, lane, v);
-            } else {
-              store_vec(dz, (j0 + u * 32 + lane) * E, V, align, v);
-            }
-          }
-          __syncwarp();  // the listed tokens' over what other lanes have stored
-          for_listed<T>(tok, a.K, tile, lane, [&](int d, int e) {
-            if (lane == 0) put_elem(dz + (int64_t)tile * tile_elems<T>() + d, sh.corr[buf][e]);
-          });
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[slot]);
-      }
+      const Row cur{dz, ALIGNED ? 0 : row_off(base + r * a.ld), align, slot0, round0, k++};
       slot0 += mine;
       if (slot0 >= S) {
         slot0 -= S;
         ++round0;
       }
+      pass1(cur);
+      if (!ahead) {
+        pass2(cur);
+      } else {
+        if (pending) pass2(prev);
+        prev = cur;
+        pending = true;
+      }
     }
+    if (pending) pass2(prev);
     if (rank == 0 && w == 0 && lane == 0) count(a.acc, c_tok, 0, 0);
   }
   __syncthreads();
@@ -529,10 +581,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
   cluster_sync_all();  // no CTA leaves while a peer may still store into or arrive on its memory
 }
 
+constexpr int kPipeC = 4;
+
 // CTAs per row: as many as its tiles need, and up to 8 where the call has too few rows for the SMs.
 int cluster_size(int64_t T, int n_tiles, int slots, int sms) {
   int C = 1;
   while (C * slots < n_tiles) C *= 2;
+  while (C < kPipeC && 2 * ((n_tiles + C - 1) / C) + 4 > slots) C *= 2;
   while (C < 8 && 2 * C * T <= sms && 2 * C * 2 <= n_tiles) C *= 2;
   return C;
 }

@@ -84,9 +84,12 @@ __device__ __noinline__ int2 fetch_edges(uint8_t* slot, const T* row, int off, i
   if (to_end < (int64_t)v1 * 16) v1 = (int)(to_end / 16);
   if (tile == 0 && off) v0 = 1;
   const int64_t e0 = ((int64_t)tile * kTileBytes - off) / (int64_t)sizeof(T);
+  // at most one vector at either end holds elements of the row and others: read element by element
   if (v0 && lane == 0) reinterpret_cast<uint4*>(slot)[0] = edge_vec(row, e0, V);
-  for (int v = (v1 > v0 ? v1 : v0) + lane; v < all; v += 32)
-    reinterpret_cast<uint4*>(slot)[v] = edge_vec(row, e0 + (int64_t)v * E, V);
+  const int cut = v1 > v0 ? v1 : v0;
+  if (lane == 0 && cut < all) reinterpret_cast<uint4*>(slot)[cut] = edge_vec(row, e0 + (int64_t)cut * E, V);
+  const uint32_t ninf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+  for (int v = cut + 1 + lane; v < all; v += 32) reinterpret_cast<uint4*>(slot)[v] = make_uint4(ninf, ninf, ninf, ninf);
   __syncwarp();  // before lane 0's arrive on the slot's barrier
   return make_int2(v0, v1);
 }
