@@ -76,27 +76,22 @@ __device__ __forceinline__ void for_listed(const int32_t* sh_tok, int K, int til
 template <typename T>
 __device__ __forceinline__ void drop_listed(uint4 (&x)[kTileVecs], const int32_t* sh_tok, int K, int tile, int lane) {
   constexpr int E = 16 / (int)sizeof(T);
-  uint64_t bits = 0;  // bit u E + i: element i of vector u
   for_listed<T>(sh_tok, K, tile, lane, [&](int d, int) {
     const int j = d / E, l = (j >> 2) & 31, u = (j >> 7) * 4 + ((j - (l >> 1)) & 3);
-    if (l == lane) bits |= 1ull << (u * E + d % E);
-  });
-  if (__any_sync(0xffffffffu, bits != 0)) {
+    if (l == lane) {
+      // word of the lane's 32, and what of it stays
+      const int at = u * 4 + (sizeof(T) == 2 ? (d % E) >> 1 : d % E);
+      const uint32_t keep = sizeof(T) == 2 ? (d & 1 ? 0x0000FFFFu : 0xFFFF0000u) : 0u;
+      const uint32_t ninf = (sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u) & ~keep;
 #pragma unroll
-    for (int u = 0; u < kTileVecs; ++u) {
-      const uint32_t b = (uint32_t)(bits >> (u * E)) & ((1u << E) - 1u);
-      uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (b >> i & 1u) {
-          if constexpr (sizeof(T) == 2)
-            w[i / 2] = i & 1 ? (w[i / 2] & 0x0000FFFFu) | 0xFF800000u : (w[i / 2] & 0xFFFF0000u) | 0x0000FF80u;
-          else
-            w[i] = 0xFF800000u;
-        }
-      x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int v = 0; v < kTileVecs; ++v) {
+        if (at == 4 * v) x[v].x = (x[v].x & keep) | ninf;
+        if (at == 4 * v + 1) x[v].y = (x[v].y & keep) | ninf;
+        if (at == 4 * v + 2) x[v].z = (x[v].z & keep) | ninf;
+        if (at == 4 * v + 3) x[v].w = (x[v].w & keep) | ninf;
+      }
     }
-  }
+  });
 }
 
 template <typename T>
@@ -189,7 +184,7 @@ __device__ __forceinline__ void store_odd(__nv_bfloat16* row, int64_t j0, int la
 // ------------------------------------------------------------------------------------------
 constexpr int kMaxBlocks = 160;  // softmax partials kept per row
 
-template <typename T, int KIND, bool ALIGNED, int NT>
+template <typename T, int KIND, bool ALIGNED, int J, int NT>
 __global__ void __launch_bounds__(NT) row_kernel(Args a) {
   __shared__ alignas(16) int32_t sh_tok[GRPO_TOPK_MAX];
   __shared__ float sh_corr[GRPO_TOPK_MAX], pm[kMaxBlocks], ps[kMaxBlocks];
@@ -213,7 +208,7 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
       continue;
     }
     ++c_val;
-    List<T, KIND> list;
+    List<T, KIND, J> list;
     if (warp == 0) list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, row, V, sh_tok, lane);
     if (TAIL) __syncthreads();
     for (int b = warp; b < a.n_blocks; b += NW) {
@@ -237,11 +232,15 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
     }
     __syncthreads();
     if (warp == 0) {
-      float loss;
       Stats st;
       bool finite;
-      list.finish(join_blocks(a.n_blocks, lane, [&](int i) { return make_float2(pm[i], ps[i]); }), a.c, grad_scale_of(a, src), V, a.K, sh_corr, lane, loss,
-                  st.shift, st.mult, finite);
+      const float g = grad_scale_of(a, src);
+      list.stats(join_blocks(a.n_blocks, lane, [&](int i) { return make_float2(pm[i], ps[i]); }), a.c, g, V, a.K, st.shift,
+                 st.mult);
+      const float loss = list.token_loss(V, a.K, g, finite);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (32 * j < a.K) sh_corr[32 * j + lane] = list.entry_grad(j, g);
       if (lane == 0) {
         a.loss_tok[src] = loss;
         stats = st;
@@ -265,10 +264,10 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
   if (tid == 0) count(a.acc, c_tok, c_val, c_bad);
 }
 
-template <typename T, int KIND, bool ALIGNED, int NT>
+template <typename T, int KIND, bool ALIGNED, int J, int NT>
 int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
   const int64_t grid = std::min<int64_t>(a.T, (int64_t)sm_count() * per_sm);
-  row_kernel<T, KIND, ALIGNED, NT><<<(unsigned)grid, NT, 0, st>>>(a);
+  row_kernel<T, KIND, ALIGNED, J, NT><<<(unsigned)grid, NT, 0, st>>>(a);
   GRPO_CUDA_TRY(cudaGetLastError());
   return GRPO_OK;
 }
@@ -293,12 +292,12 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 //
 // Barriers: full/empty of the slots; listed[k & 1] (the tokens are in shared
 // memory; the tail kinds, which need them in pass 1); parts (owner, per
-// list warp: the row's partials are in); ready[k & 1] (stats and dlogits of the list are in, and the
-// tokens). Why no
+// list warp: the row's partials are in); ready[k & 1] (the stats are in, and the tokens);
+// grads[k & 1] (the list's dlogits are in). Why no
 // buffer is rewritten too early: parts of row k are complete only when every tile warp of the cluster
-// is through pass 1 of row k, hence through pass 2 of row k - 2; so what is sent to ready[k & 1] then
-// finds row k - 2's done with, in every CTA, and a phase of ready, listed or parts is never overtaken
-// by a round. Tokens have four buffers: they are written two rows ahead of that. Warps without a tile
+// is through pass 1 of row k, hence through pass 2 of row k - 2; so what is sent to ready[k & 1] and
+// grads[k & 1] then finds row k - 2's done with, in every CTA, and a phase of ready, grads, listed or parts is never
+// overtaken by a round. Tokens have four buffers: they are written two rows ahead of that. Warps without a tile
 // in the CTA wait for nothing.
 // ------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 16;
@@ -314,17 +313,16 @@ struct ClusterShared {
   float2 part[kListWarps][kMaxTiles];  // (m, s) of every tile of an owned row
   alignas(16) int32_t tok[4][GRPO_TOPK_MAX];
   alignas(16) int32_t list_tok[kListWarps][GRPO_TOPK_MAX];
-  float list_corr[kListWarps][GRPO_TOPK_MAX];
   float corr[2][GRPO_TOPK_MAX];
   Stats stats[2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t parts[kListWarps], listed[2], ready[2];
+  uint64_t parts[kListWarps], listed[2], ready[2], grads[2];
   int abort;
 };
 
 __host__ __device__ constexpr size_t cluster_head_bytes() { return (sizeof(ClusterShared) + 127) / 128 * 128; }
 
-template <typename T, int KIND, bool ALIGNED>
+template <typename T, int KIND, bool ALIGNED, int J>
 __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int C) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   ClusterShared& sh = *reinterpret_cast<ClusterShared*>(smem_raw);
@@ -338,7 +336,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
   const int S = a.slots;
   const int t0 = rank * a.n_tiles / C, mine = (rank + 1) * a.n_tiles / C - t0;  // tiles of this CTA
   const int most = (a.n_tiles + C - 1) / C;                                    // of any CTA
-  const int list_slots = (a.K + 31) / 32;
+  const int list_slots = a.dlogits ? (a.K + 31) / 32 : 0;  // entries a lane whose dlogits are sent
   volatile int* s_abort = &sh.abort;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -349,6 +347,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.listed[b], 1);
       mbar_init(&sh.ready[b], 1);
+      mbar_init(&sh.grads[b], 1);
     }
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -362,8 +361,11 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
 
   if (warp == 0) {
     // ---- producer ----
-    int slot = 0;
-    uint32_t round = 0;  // times the ring went round
+    // A lane per tile: the lanes' waits and copies overlap (one lane issuing tile after tile took 500
+    // cycles each, longer than a row's share of the bandwidth). Tiles at a row's ends, which the whole
+    // warp fills up, come after the others.
+    int slot0 = 0;         // slot of the row's first tile
+    uint32_t round0 = 0;   // times the ring had gone round there
     bool ok = true;
     int64_t nsrc = first < a.T ? src_of(first) : -1;
     bool nread = first < a.T && is_read(nsrc);
@@ -376,23 +378,54 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       if (!read) continue;
       const T* row = base + r * a.ld;
       const int off = ALIGNED ? 0 : row_off(row);
-      for (int i = 0; i < mine; ++i) {
-        if (round > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort))) {
-          ok = false;
-          break;
-        }
-        fetch_tile<T>(ring + (size_t)slot * kSlotBytes, row, off, t0 + i, a.n_tiles, V, lane, &sh.full[slot]);
-        if (++slot == S) {
-          slot = 0;
+      const uint32_t bytes = kTileBytes + (off ? 16u : 0u);
+      auto at = [&](int i, int& slot, uint32_t& round) {
+        slot = slot0 + i;
+        round = round0;
+        if (slot >= S) {
+          slot -= S;
           ++round;
         }
+      };
+      auto edge = [&](int i) { return (t0 + i == 0 && off) || t0 + i >= a.n_tiles - 2; };
+      for (int i0 = 0; i0 < mine; i0 += 32) {
+        const int i = i0 + lane;
+        if (i < mine && !edge(i)) {
+          int slot;
+          uint32_t round;
+          at(i, slot, round);
+          if (round == 0 || mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort)) {
+            mbar_arrive_expect_tx(&sh.full[slot], bytes);
+            bulk_g2s(ring + (size_t)slot * kSlotBytes,
+                     reinterpret_cast<const uint8_t*>(row) + (int64_t)(t0 + i) * kTileBytes - off, bytes, &sh.full[slot]);
+          }
+        }
+        __syncwarp();
+      }
+      for (int i = 0; i < mine && ok; ++i) {
+        if (!edge(i)) {
+          if (t0 + i < a.n_tiles - 3) i = max(i, min(mine, a.n_tiles - 2 - t0) - 1);  // on to the last tiles
+          continue;
+        }
+        int slot;
+        uint32_t round;
+        at(i, slot, round);
+        ok = round == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort));
+        if (ok) fetch_tile<T>(ring + (size_t)slot * kSlotBytes, row, off, t0 + i, a.n_tiles, V, lane, &sh.full[slot]);
+      }
+      ok = !__any_sync(0xffffffffu, *s_abort);
+      slot0 += mine;
+      if (slot0 >= S) {
+        slot0 -= S;
+        ++round0;
       }
     }
-    // a wait gave up: let the copies in flight land before the CTA's memory goes away (bounded)
+    // a wait gave up: let the copies in flight land before the CTA's memory goes away (bounded; a slot
+    // whose copy was not issued runs into the limit)
     if (!ok || *s_abort) {
       const uint64_t begin = global_timer_ns();
       for (int s = lane; s < S; s += 32) {
-        const uint32_t filled = round + (s < slot ? 1u : 0u);  // fills of the slot so far
+        const uint32_t filled = round0 + (s < slot0 ? 1u : 0u);  // fills of the slot so far
         while (filled > 0 && !mbar_try_wait(&sh.full[s], (filled - 1) & 1u) && global_timer_ns() - begin < 1000000000ull) {}
       }
     }
@@ -402,23 +435,27 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
     for (int64_t r = first; r < a.T; r += stride) {
       const int64_t src = src_of(r);
       if (!is_read(src)) continue;
-      int32_t tok[kPerLane];
+      int32_t tok[J];
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j) {
+      for (int j = 0; j < J; ++j) {
         tok[j] = -1;
         if (32 * j + lane < a.K) tok[j] = a.top_idx[src * a.ld_top + 32 * j + lane];
         if (tok[j] < 0 || (int64_t)tok[j] >= V) tok[j] = -1;
       }
       const int buf = (int)(k & 1u);
-      if (k >= 2) mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
+      if (k >= 2) {
+        mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
+        if (list_slots) mbar_wait_bounded(&sh.grads[buf], ((k >> 1) - 1u) & 1u, s_abort);
+      }
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j)
-        if (j < list_slots) sh.tok[k & 3u][32 * j + lane] = tok[j];
+      for (int j = 0; j < J; ++j)
+        if (32 * j < a.K) sh.tok[k & 3u][32 * j + lane] = tok[j];
       __syncwarp();
       if (lane == 0) {
         if (TAIL) mbar_arrive(&sh.listed[buf]);
         // the row's stats and its list's dlogits will be counted (and the tokens are published)
-        mbar_arrive_expect_tx(&sh.ready[buf], 8u + 128u * (uint32_t)list_slots);
+        mbar_arrive_expect_tx(&sh.ready[buf], 8u);
+        if (list_slots) mbar_arrive_expect_tx(&sh.grads[buf], 128u * (uint32_t)list_slots);
       }
       ++k;
     }
@@ -437,23 +474,27 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       const uint32_t use = j_own / kListWarps;
       // the partials of all tiles will be counted: 8 bytes each
       if (lane == 0) mbar_arrive_expect_tx_relaxed(&sh.parts[me], 8u * (uint32_t)a.n_tiles);
-      List<T, KIND> list;
+      List<T, KIND, J> list;
       list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, base + r * a.ld, V, sh.list_tok[me], lane);
       const float g = grad_scale_of(a, src);
       mbar_wait_bounded(&sh.parts[me], use & 1u, s_abort);
       const Part p = join_blocks(a.n_tiles, lane, [&](int i) { return sh.part[me][i]; });
-      float loss;
       Stats st;
       bool finite;
-      list.finish(p, a.c, g, V, a.K, sh.list_corr[me], lane, loss, st.shift, st.mult, finite);
+      list.stats(p, a.c, g, V, a.K, st.shift, st.mult);
       const int buf = (int)(row_k & 1u);
       if (lane < C)
         st_async_v2f32(mapa_u32(smem_u32(&sh.stats[buf]), (uint32_t)lane), st.shift, st.mult,
                        mapa_u32(smem_u32(&sh.ready[buf]), (uint32_t)lane));
-      for (int c = 0; c < C; ++c) {
-        const uint32_t bar = mapa_u32(smem_u32(&sh.ready[buf]), (uint32_t)c);
-        const uint32_t dst = mapa_u32(smem_u32(&sh.corr[buf][lane]), (uint32_t)c);
-        for (int j = 0; j < list_slots; ++j) st_async_f32(dst + 128u * (uint32_t)j, sh.list_corr[me][32 * j + lane], bar);
+      const float loss = list.token_loss(V, a.K, g, finite);
+      if (list_slots) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (32 * j < a.K) {
+            const float d = list.entry_grad(j, g);
+            const uint32_t dst = smem_u32(&sh.corr[buf][32 * j + lane]), bar = smem_u32(&sh.grads[buf]);
+            for (int c = 0; c < C; ++c) st_async_f32(mapa_u32(dst, (uint32_t)c), d, mapa_u32(bar, (uint32_t)c));
+          }
       }
       if (lane == 0) a.loss_tok[src] = loss;
       ++c_val;
@@ -506,30 +547,34 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
           const bool inside = (int64_t)(tile + 1) * tile_elems<T>() <= V;
           const uint32_t at = ring32 + (uint32_t)slot * kSlotBytes + (uint32_t)lane * 16u;
           const int64_t j0 = (int64_t)tile * (32 * kTileVecs);
-#pragma unroll
-          for (int u = 0; u < kTileVecs; ++u) {
+          auto vec = [&](int u) -> uint4 {
             uint4 v = lds128(at + (uint32_t)u * 512u);
             if (!ALIGNED && q.off != 0) v = shift_vec<T>(v, lds128(at + (uint32_t)u * 512u + 16u), q.off);
-            v = st.mult != 0.f ? grad_vec<T>(v, a.c, st) : make_uint4(0, 0, 0, 0);
-            if constexpr (ALIGNED) {
-              if (inside)
-                reinterpret_cast<uint4*>(q.dz)[j0 + u * 32 + lane] = v;
-              else
-                store_vec(q.dz, (j0 + u * 32 + lane) * E, V, 16, v);
-            } else if (sizeof(T) == 2 && q.align == 2 && inside) {
-              store_odd(reinterpret_cast<__nv_bfloat16*>(q.dz), j0 + u * 32, lane, v);
-            } else {
-              store_vec(q.dz, (j0 + u * 32 + lane) * E, V, q.align, v);
-            }
+            v = grad_vec<T>(v, a.c, st);
+            return st.mult != 0.f ? v : make_uint4(0, 0, 0, 0);
+          };
+          if (inside && (ALIGNED || q.align == 16)) {
+#pragma unroll
+            for (int u = 0; u < kTileVecs; ++u) reinterpret_cast<uint4*>(q.dz)[j0 + u * 32 + lane] = vec(u);
+          } else if (!ALIGNED && sizeof(T) == 2 && inside && q.align == 2) {
+#pragma unroll
+            for (int u = 0; u < kTileVecs; ++u)
+              store_odd(reinterpret_cast<__nv_bfloat16*>(q.dz), j0 + u * 32, lane, vec(u));
+          } else {
+#pragma unroll 1
+            for (int u = 0; u < kTileVecs; ++u) store_vec(q.dz, (j0 + u * 32 + lane) * E, V, q.align, vec(u));
           }
-          __syncwarp();  // the listed tokens' over what other lanes have stored
-          for_listed<T>(sh.tok[q.k & 3u], a.K, tile, lane, [&](int d, int e) {
-            if (lane == 0) put_elem(q.dz + (int64_t)tile * tile_elems<T>() + d, sh.corr[buf][e]);
-          });
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[slot]);
       }
+      if (!q.dz) return;
+      // the listed tokens' over what other lanes have stored (the barriers of the warp above order them)
+      mbar_wait_bounded(&sh.grads[buf], (q.k >> 1) & 1u, s_abort);
+      for (int i = w; i < mine; i += kTileWarps)
+        for_listed<T>(sh.tok[q.k & 3u], a.K, t0 + i, lane, [&](int d, int e) {
+          if (lane == 0) put_elem(q.dz + (int64_t)(t0 + i) * tile_elems<T>() + d, sh.corr[buf][e]);
+        });
     };
     const bool ahead = 2 * most <= S;  // (the same in every CTA)
     Row prev{};
@@ -597,9 +642,9 @@ int cluster_slots() {
   return optin > cluster_head_bytes() ? (int)std::min<size_t>(kMaxSlots, (optin - cluster_head_bytes()) / kSlotBytes) : 0;
 }
 
-template <typename T, int KIND, bool ALIGNED>
+template <typename T, int KIND, bool ALIGNED, int J>
 int launch_cluster(Args a, int C, cudaStream_t st) {
-  auto kern = cluster_kernel<T, KIND, ALIGNED>;
+  auto kern = cluster_kernel<T, KIND, ALIGNED, J>;
   const size_t smem = cluster_head_bytes() + (size_t)a.slots * kSlotBytes;
   int dev = 0, n_clusters = 0;
   GRPO_CUDA_TRY(cudaGetDevice(&dev));
@@ -638,16 +683,21 @@ int launch_cluster(Args a, int C, cudaStream_t st) {
   return GRPO_OK;
 }
 
-template <typename T, int KIND, bool ALIGNED>
-int launch(Args a, cudaStream_t st) {
+template <typename T, int KIND, bool ALIGNED, int J>
+int launch_j(Args a, cudaStream_t st) {
   a.slots = cluster_slots();
   if (a.n_tiles >= kMinTiles && a.n_tiles <= kMaxTiles && 8 * a.slots >= a.n_tiles)
-    return launch_cluster<T, KIND, ALIGNED>(a, cluster_size(a.T, a.n_tiles, a.slots, sm_count()), st);
+    return launch_cluster<T, KIND, ALIGNED, J>(a, cluster_size(a.T, a.n_tiles, a.slots, sm_count()), st);
   a.fold = (a.n_tiles + kMaxBlocks - 1) / kMaxBlocks;
   a.n_blocks = (a.n_tiles + a.fold - 1) / a.fold;
   // short rows: small blocks, several rows in flight on an SM
-  if (a.n_tiles < kMinTiles) return launch_row_nt<T, KIND, ALIGNED, 128>(a, 8, st);
-  return launch_row_nt<T, KIND, ALIGNED, 512>(a, 2, st);
+  if (a.n_tiles < kMinTiles) return launch_row_nt<T, KIND, ALIGNED, J, 128>(a, 8, st);
+  return launch_row_nt<T, KIND, ALIGNED, J, 512>(a, 2, st);
+}
+
+template <typename T, int KIND, bool ALIGNED>
+int launch(const Args& a, cudaStream_t st) {
+  return a.K <= 64 ? launch_j<T, KIND, ALIGNED, 2>(a, st) : launch_j<T, KIND, ALIGNED, 8>(a, st);
 }
 
 template <typename T>
