@@ -184,9 +184,9 @@ __device__ __forceinline__ void store_odd(__nv_bfloat16* row, int64_t j0, int la
 // ------------------------------------------------------------------------------------------
 constexpr int kMaxBlocks = 160;  // softmax partials kept per row
 
-template <typename T, int KIND, bool ALIGNED, int J, int NT>
+template <typename T, int KIND, bool ALIGNED, int NT>
 __global__ void __launch_bounds__(NT) row_kernel(Args a) {
-  __shared__ alignas(16) int32_t sh_tok[GRPO_TOPK_MAX];
+  __shared__ Entries entries;
   __shared__ float sh_corr[GRPO_TOPK_MAX], pm[kMaxBlocks], ps[kMaxBlocks];
   __shared__ Stats stats;
   constexpr int E = 16 / (int)sizeof(T), NW = NT / 32;
@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
       continue;
     }
     ++c_val;
-    List<T, KIND, J> list;
-    if (warp == 0) list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, row, V, sh_tok, lane);
+    List<T, KIND> list(entries, a.K, V, lane);
+    if (warp == 0) list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, row);
     if (TAIL) __syncthreads();
     for (int b = warp; b < a.n_blocks; b += NW) {
       Part p{-INFINITY, 0.f, 0.f};
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
         for (int u = 0; u < kTileVecs; ++u)
           x[u] = load_vec<T, ALIGNED>(row, (int64_t)tile * (32 * kTileVecs) + tile_vec(lane, u), V);
         const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
-        if (TAIL) drop_listed<T>(x, sh_tok, a.K, tile, lane);
+        if (TAIL) drop_listed<T>(x, entries.tok, a.K, tile, lane);
         const Part tp = tile_part<T, false>(x, m, a.c);
         p = f == 0 ? tp : part_join(p, tp);
       }
@@ -235,12 +235,9 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
       Stats st;
       bool finite;
       const float g = grad_scale_of(a, src);
-      list.stats(join_blocks(a.n_blocks, lane, [&](int i) { return make_float2(pm[i], ps[i]); }), a.c, g, V, a.K, st.shift,
-                 st.mult);
-      const float loss = list.token_loss(V, a.K, g, finite);
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (32 * j < a.K) sh_corr[32 * j + lane] = list.entry_grad(j, g);
+      list.stats(join_blocks(a.n_blocks, lane, [&](int i) { return make_float2(pm[i], ps[i]); }), a.c, g, st.shift, st.mult);
+      const float loss = list.token_loss(g, finite);
+      for (int k = lane; k < list.padded; k += 32) sh_corr[k] = list.entry_grad(k, g);
       if (lane == 0) {
         a.loss_tok[src] = loss;
         stats = st;
@@ -257,17 +254,17 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
       }
       __syncthreads();
       for (int k = tid; k < a.K; k += NT)
-        if (sh_tok[k] >= 0) put_elem(dz + sh_tok[k], sh_corr[k]);
+        if (entries.tok[k] >= 0) put_elem(dz + entries.tok[k], sh_corr[k]);
     }
     __syncthreads();  // the shared arrays are rewritten by the next row
   }
   if (tid == 0) count(a.acc, c_tok, c_val, c_bad);
 }
 
-template <typename T, int KIND, bool ALIGNED, int J, int NT>
+template <typename T, int KIND, bool ALIGNED, int NT>
 int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
   const int64_t grid = std::min<int64_t>(a.T, (int64_t)sm_count() * per_sm);
-  row_kernel<T, KIND, ALIGNED, J, NT><<<(unsigned)grid, NT, 0, st>>>(a);
+  row_kernel<T, KIND, ALIGNED, NT><<<(unsigned)grid, NT, 0, st>>>(a);
   GRPO_CUDA_TRY(cudaGetLastError());
   return GRPO_OK;
 }
@@ -312,7 +309,7 @@ constexpr int kMinTiles = 16;
 struct ClusterShared {
   float2 part[kListWarps][kMaxTiles];  // (m, s) of every tile of an owned row
   alignas(16) int32_t tok[4][GRPO_TOPK_MAX];
-  alignas(16) int32_t list_tok[kListWarps][GRPO_TOPK_MAX];
+  Entries entries[kListWarps];
   float corr[2][GRPO_TOPK_MAX];
   Stats stats[2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
@@ -322,7 +319,7 @@ struct ClusterShared {
 
 __host__ __device__ constexpr size_t cluster_head_bytes() { return (sizeof(ClusterShared) + 127) / 128 * 128; }
 
-template <typename T, int KIND, bool ALIGNED, int J>
+template <typename T, int KIND, bool ALIGNED>
 __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int C) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   ClusterShared& sh = *reinterpret_cast<ClusterShared*>(smem_raw);
@@ -435,9 +432,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
     for (int64_t r = first; r < a.T; r += stride) {
       const int64_t src = src_of(r);
       if (!is_read(src)) continue;
-      int32_t tok[J];
+      int32_t tok[GRPO_TOPK_MAX / 32];
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
+      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j) {
         tok[j] = -1;
         if (32 * j + lane < a.K) tok[j] = a.top_idx[src * a.ld_top + 32 * j + lane];
         if (tok[j] < 0 || (int64_t)tok[j] >= V) tok[j] = -1;
@@ -448,7 +445,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         if (list_slots) mbar_wait_bounded(&sh.grads[buf], ((k >> 1) - 1u) & 1u, s_abort);
       }
 #pragma unroll
-      for (int j = 0; j < J; ++j)
+      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j)
         if (32 * j < a.K) sh.tok[k & 3u][32 * j + lane] = tok[j];
       __syncwarp();
       if (lane == 0) {
@@ -474,28 +471,26 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       const uint32_t use = j_own / kListWarps;
       // the partials of all tiles will be counted: 8 bytes each
       if (lane == 0) mbar_arrive_expect_tx_relaxed(&sh.parts[me], 8u * (uint32_t)a.n_tiles);
-      List<T, KIND, J> list;
-      list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, a.K, base + r * a.ld, V, sh.list_tok[me], lane);
+      List<T, KIND> list(sh.entries[me], a.K, V, lane);
+      list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, base + r * a.ld);
       const float g = grad_scale_of(a, src);
       mbar_wait_bounded(&sh.parts[me], use & 1u, s_abort);
       const Part p = join_blocks(a.n_tiles, lane, [&](int i) { return sh.part[me][i]; });
       Stats st;
       bool finite;
-      list.stats(p, a.c, g, V, a.K, st.shift, st.mult);
+      list.stats(p, a.c, g, st.shift, st.mult);
       const int buf = (int)(row_k & 1u);
       if (lane < C)
         st_async_v2f32(mapa_u32(smem_u32(&sh.stats[buf]), (uint32_t)lane), st.shift, st.mult,
                        mapa_u32(smem_u32(&sh.ready[buf]), (uint32_t)lane));
-      const float loss = list.token_loss(V, a.K, g, finite);
-      if (list_slots) {
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          if (32 * j < a.K) {
-            const float d = list.entry_grad(j, g);
-            const uint32_t dst = smem_u32(&sh.corr[buf][32 * j + lane]), bar = smem_u32(&sh.grads[buf]);
-            for (int c = 0; c < C; ++c) st_async_f32(mapa_u32(dst, (uint32_t)c), d, mapa_u32(bar, (uint32_t)c));
-          }
-      }
+      const float loss = list.token_loss(g, finite);
+      if (list_slots)
+        for (int k = lane; k < list.padded; k += 32) {
+          const float d = list.entry_grad(k, g);
+          const uint32_t dst = smem_u32(&sh.corr[buf][k]), bar = smem_u32(&sh.grads[buf]);
+          for (int c = 0; c < C; ++c) st_async_f32(mapa_u32(dst, (uint32_t)c), d, mapa_u32(bar, (uint32_t)c));
+        }
+      __syncwarp();  // the entries are rewritten by the next list
       if (lane == 0) a.loss_tok[src] = loss;
       ++c_val;
       if (!finite) ++c_bad;
@@ -626,13 +621,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
   cluster_sync_all();  // no CTA leaves while a peer may still store into or arrive on its memory
 }
 
-constexpr int kPipeC = 4;
-
-// CTAs per row: as many as its tiles need, and up to 8 where the call has too few rows for the SMs.
+// CTAs per row: as few as hold its tiles, and up to 8 where the call has too few rows for the SMs.
 int cluster_size(int64_t T, int n_tiles, int slots, int sms) {
   int C = 1;
   while (C * slots < n_tiles) C *= 2;
-  while (C < kPipeC && 2 * ((n_tiles + C - 1) / C) + 4 > slots) C *= 2;
   while (C < 8 && 2 * C * T <= sms && 2 * C * 2 <= n_tiles) C *= 2;
   return C;
 }
@@ -642,9 +634,9 @@ int cluster_slots() {
   return optin > cluster_head_bytes() ? (int)std::min<size_t>(kMaxSlots, (optin - cluster_head_bytes()) / kSlotBytes) : 0;
 }
 
-template <typename T, int KIND, bool ALIGNED, int J>
+template <typename T, int KIND, bool ALIGNED>
 int launch_cluster(Args a, int C, cudaStream_t st) {
-  auto kern = cluster_kernel<T, KIND, ALIGNED, J>;
+  auto kern = cluster_kernel<T, KIND, ALIGNED>;
   const size_t smem = cluster_head_bytes() + (size_t)a.slots * kSlotBytes;
   int dev = 0, n_clusters = 0;
   GRPO_CUDA_TRY(cudaGetDevice(&dev));
@@ -683,21 +675,16 @@ int launch_cluster(Args a, int C, cudaStream_t st) {
   return GRPO_OK;
 }
 
-template <typename T, int KIND, bool ALIGNED, int J>
-int launch_j(Args a, cudaStream_t st) {
+template <typename T, int KIND, bool ALIGNED>
+int launch(Args a, cudaStream_t st) {
   a.slots = cluster_slots();
   if (a.n_tiles >= kMinTiles && a.n_tiles <= kMaxTiles && 8 * a.slots >= a.n_tiles)
-    return launch_cluster<T, KIND, ALIGNED, J>(a, cluster_size(a.T, a.n_tiles, a.slots, sm_count()), st);
+    return launch_cluster<T, KIND, ALIGNED>(a, cluster_size(a.T, a.n_tiles, a.slots, sm_count()), st);
   a.fold = (a.n_tiles + kMaxBlocks - 1) / kMaxBlocks;
   a.n_blocks = (a.n_tiles + a.fold - 1) / a.fold;
   // short rows: small blocks, several rows in flight on an SM
-  if (a.n_tiles < kMinTiles) return launch_row_nt<T, KIND, ALIGNED, J, 128>(a, 8, st);
-  return launch_row_nt<T, KIND, ALIGNED, J, 512>(a, 2, st);
-}
-
-template <typename T, int KIND, bool ALIGNED>
-int launch(const Args& a, cudaStream_t st) {
-  return a.K <= 64 ? launch_j<T, KIND, ALIGNED, 2>(a, st) : launch_j<T, KIND, ALIGNED, 8>(a, st);
+  if (a.n_tiles < kMinTiles) return launch_row_nt<T, KIND, ALIGNED, 128>(a, 8, st);
+  return launch_row_nt<T, KIND, ALIGNED, 512>(a, 2, st);
 }
 
 template <typename T>

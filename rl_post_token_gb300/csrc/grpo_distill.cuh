@@ -53,101 +53,96 @@ __device__ __forceinline__ Part join_blocks(int n, int lane, G get) {
   return {m, warp_sum(s), 0.f};
 }
 
-// One token's list, entry 32 j + lane in slot j < J of the lane (K <= 32 J). The warp holds it from the
-// loads to the gradients. Instances of J = 2 and 8 slots: the small one keeps a list of up to 64
-// tokens without spilling.
-template <typename T, int KIND, int J>
+// A list's entries in shared memory, unused ones with token -1.
+struct alignas(16) Entries {
+  int32_t tok[GRPO_TOPK_MAX];
+  float tlp[GRPO_TOPK_MAX];  // log q
+  float z[GRPO_TOPK_MAX];    // the student's logit; from stats on z c - shift, log2 of its share
+  float q[GRPO_TOPK_MAX];    // the teacher's probability (FORWARD_TOPK: of the renormalised list)
+};
+
+// One token's list, held by one warp from the loads to the gradients. The entries stay in shared memory,
+// lane l working on entries l, l + 32, ... (in registers, 8 a lane spilled and 2 a lane were no faster).
+template <typename T, int KIND>
 struct List {
-  int32_t tok[J];  // -1: unused
-  float tlp[J], z[J], q[J];
+  Entries& en;
+  const int K, padded, lane;  // padded: K rounded up to whole warps
+  const int64_t V;
   float log_norm;  // FORWARD_TOPK: log of the list's mass, its log-probs taken from their largest
   float q_rest;    // q_R (tail kinds), floored as above; 0 where nothing lies outside the list
   float q_all;     // FORWARD_TOPK: 1, or 0 without a list; FORWARD_TAIL: Q + q_R
   int n;           // tokens listed
   bool bad;        // a token twice or outside the vocabulary, a NaN or +inf log-prob
+  float l2s, inv, pr, alpha, loss;  // from stats on
+  bool ok;
 
-  // Loads the list and the listed logits and writes the tokens to sh_tok [32 J] (unused entries
-  // -1; all of them if the list is bad).
-  __device__ __forceinline__ void load(const int32_t* top_idx, const float* top_logp, int K, const T* row, int64_t V,
-                                       int32_t* sh_tok, int lane) {
+  static constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
+
+  __device__ List(Entries& entries, int k, int64_t v, int l) : en(entries), K(k), padded((k + 31) & ~31), lane(l), V(v) {}
+
+  // Loads the list and the listed logits. A bad list is left without tokens.
+  __device__ __forceinline__ void load(const int32_t* top_idx, const float* top_logp, const T* row) {
     bool b = false;
     n = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      tok[j] = -1;
-      tlp[j] = z[j] = -INFINITY;
-      if (32 * j < K && 32 * j + lane < K) {
-        tok[j] = top_idx[32 * j + lane];
-        tlp[j] = top_logp[32 * j + lane];
+    float mx = -INFINITY;
+#pragma unroll 2
+    for (int k = lane; k < padded; k += 32) {
+      int32_t tok = -1;
+      float tlp = -INFINITY, z = -INFINITY;
+      if (k < K) {
+        tok = top_idx[k];
+        tlp = top_logp[k];
       }
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (32 * j < K) {  // warp-uniform, here and below
-        const bool in = tok[j] >= 0 && (int64_t)tok[j] < V;
-        if (in) z[j] = elem_f32(row + tok[j]);
-        if (tok[j] == -1) tlp[j] = -INFINITY;
-        b |= tok[j] != -1 && (!in || tlp[j] != tlp[j] || tlp[j] == INFINITY);
-        n += __popc(__ballot_sync(0xffffffffu, tok[j] != -1));
-      }
-      sh_tok[32 * j + lane] = tok[j];
+      const bool in = tok >= 0 && (int64_t)tok < V;
+      if (in) z = elem_f32(row + tok);
+      if (tok == -1) tlp = -INFINITY;
+      b |= tok != -1 && (!in || tlp != tlp || tlp == INFINITY);
+      n += __popc(__ballot_sync(0xffffffffu, tok != -1));
+      mx = fmaxf(mx, tlp);
+      en.tok[k] = tok;
+      en.tlp[k] = tlp;
+      en.z[k] = z;
     }
     __syncwarp();
     // every entry against the entries before it
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (32 * j < K) {
-        const int k = 32 * j + lane;
-#pragma unroll 2
-        for (int k0 = 0; k0 < 32 * j + 32; k0 += 4) {
-          const int4 o = *reinterpret_cast<const int4*>(sh_tok + k0);
-          b |= tok[j] != -1 && ((o.x == tok[j] && k0 < k) || (o.y == tok[j] && k0 + 1 < k) ||
-                                (o.z == tok[j] && k0 + 2 < k) || (o.w == tok[j] && k0 + 3 < k));
-        }
+#pragma unroll 1
+    for (int k = lane; k < padded; k += 32) {
+      const int32_t tok = en.tok[k];
+#pragma unroll 4
+      for (int k0 = 0; k0 < (k & ~31) + 32; k0 += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(en.tok + k0);
+        b |= tok != -1 && ((o.x == tok && k0 < k) || (o.y == tok && k0 + 1 < k) || (o.z == tok && k0 + 2 < k) ||
+                           (o.w == tok && k0 + 3 < k));
       }
+    }
     bad = __any_sync(0xffffffffu, b);
     __syncwarp();
-    if (bad) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) sh_tok[32 * j + lane] = tok[j] = -1;
-      __syncwarp();
-    }
     log_norm = q_rest = 0.f;
-    if constexpr (KIND == GRPO_DISTILL_FORWARD_TOPK) {  // takes the list up to a constant
-      float mx = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < J; ++j) mx = fmaxf(mx, tok[j] != -1 ? tlp[j] : -INFINITY);
-      mx = warp_max_f32(mx);
+    if constexpr (!TAIL) {  // takes the list up to a constant
+      mx = warp_max_f32(bad ? -INFINITY : mx);
       const float shift = mx == -INFINITY ? 0.f : mx;
       float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        q[j] = 0.f;
-        if (32 * j < K) {
-          q[j] = tok[j] != -1 ? expf(tlp[j] - shift) : 0.f;
-          sum += q[j];
-        }
+      for (int k = lane; k < padded; k += 32) {
+        if (bad) en.tok[k] = -1;
+        // log(q/Q) will be formed as (log q - shift) - log Q: exact differences of the list's values
+        const float d = en.tlp[k] - shift, q = en.tok[k] != -1 ? expf(d) : 0.f;
+        en.tlp[k] = d;
+        en.q[k] = q;
+        sum += q;
       }
-      const float Q = warp_sum(sum), inv = Q > 0.f ? 1.f / Q : 0.f;
-      // log(q/Q) is formed as (log q - shift) - log Q: exact differences of the list's values
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        q[j] *= inv;
-        tlp[j] -= shift;
-      }
+      const float Q = warp_sum(sum), scale = Q > 0.f ? 1.f / Q : 0.f;
+      for (int k = lane; k < padded; k += 32) en.q[k] *= scale;
       log_norm = logf(Q);
       q_all = Q > 0.f ? 1.f : 0.f;
     } else {
       // the list's mass in 64 bits, as q_R = 1 - Q cancels
       double sum = 0.0;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        q[j] = 0.f;
-        if (32 * j < K) {
-          const double qd = tok[j] != -1 ? exp((double)tlp[j]) : 0.0;
-          sum += qd;
-          q[j] = (float)qd;
-        }
+#pragma unroll 1
+      for (int k = lane; k < padded; k += 32) {
+        if (bad) en.tok[k] = -1;
+        const double q = en.tok[k] != -1 ? exp((double)en.tlp[k]) : 0.0;
+        en.q[k] = (float)q;
+        sum += q;
       }
       const double Q = warp_sum(sum), qr = 1.0 - Q;
       if (KIND == GRPO_DISTILL_FORWARD_TAIL)
@@ -158,22 +153,15 @@ struct List {
     }
   }
 
-  // From stats on z holds t = z c - shift (log2 of the entry's share before the normalisation).
-  float l2s, inv, pr, alpha, loss;
-  bool ok;
-
   // The row's part of dlogits from its partial p (the tail kinds': without the listed tokens):
   // dlogits are mult 2^(z c - shift) outside the list. g: the gradient scale. A row without a
   // distribution or with a bad list has NaN throughout.
-  __device__ __forceinline__ void stats(Part p, float c, float g, int64_t V, int K, float& out_shift, float& out_mult) {
-    constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
+  __device__ __forceinline__ void stats(Part p, float c, float g, float& shift, float& mult) {
     float se = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (32 * j < K) {
-        z[j] = fmaf(z[j], c, -p.m);
-        if (TAIL && tok[j] != -1) se += ex2(z[j]);
-      }
+    for (int k = lane; k < padded; k += 32) {
+      const float t = fmaf(en.z[k], c, -p.m);
+      en.z[k] = t;
+      if (TAIL && en.tok[k] != -1) se += ex2(t);
     }
     const float S = TAIL ? p.s + warp_sum(se) : p.s;
     ok = !bad && fabsf(p.m) < INFINITY && S > 0.f && S < INFINITY;
@@ -185,39 +173,40 @@ struct List {
     } else if constexpr (KIND == GRPO_DISTILL_FORWARD_TAIL) {
       alpha = q_all - (q_rest > 0.f ? q_rest / pr : 0.f);
     } else {
-      sum_loss(V, K);
+      sum_loss();
       const bool tail = pr > 0.f && n < V;
       const float fr = tail ? logf(pr / q_rest) : 0.f;
       if (tail) loss = fmaf(pr, fr, loss);
       alpha = tail ? fr - loss : 0.f;
     }
     if (!ok) alpha = __int_as_float(0x7fc00000);
-    out_shift = ok ? p.m : 0.f;
-    out_mult = ok ? alpha * g * inv : alpha;
+    shift = ok ? p.m : 0.f;
+    mult = ok ? alpha * g * inv : alpha;
   }
 
-  // The student's probability of the entry in slot j.
-  __device__ __forceinline__ float share(int j) const { return tok[j] != -1 ? ex2(z[j]) * inv : 0.f; }
+  // The student's probability of entry k.
+  __device__ __forceinline__ float share(int k) const { return en.tok[k] != -1 ? ex2(en.z[k]) * inv : 0.f; }
 
   // The list's terms of the loss.
-  __device__ __forceinline__ void sum_loss(int64_t V, int K) {
+  __device__ __forceinline__ void sum_loss() {
     float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (32 * j >= K) continue;
-      const float lp = (z[j] - l2s) * kLn2, pk = share(j);
-      if (KIND == GRPO_DISTILL_REVERSE_TAIL)
-        sum += pk > 0.f ? pk * (lp - tlp[j]) : 0.f;
-      else
-        sum += tok[j] != -1 && q[j] > 0.f ? q[j] * ((tlp[j] - log_norm) - lp) : 0.f;
+    for (int k = lane; k < padded; k += 32) {
+      const float lp = (en.z[k] - l2s) * kLn2;
+      if (KIND == GRPO_DISTILL_REVERSE_TAIL) {
+        const float pk = share(k);
+        sum += pk > 0.f ? pk * (lp - en.tlp[k]) : 0.f;
+      } else {
+        const float q = en.q[k];
+        sum += q > 0.f ? q * ((en.tlp[k] - log_norm) - lp) : 0.f;  // (q = 0 without a token)
+      }
     }
     loss = warp_sum(sum);
   }
 
   // The token's loss (after stats).
-  __device__ __forceinline__ float token_loss(int64_t V, int K, float g, bool& finite) {
+  __device__ __forceinline__ float token_loss(float g, bool& finite) {
     if constexpr (KIND != GRPO_DISTILL_REVERSE_TAIL) {
-      sum_loss(V, K);
+      sum_loss();
       if (KIND == GRPO_DISTILL_FORWARD_TAIL && q_rest > 0.f) loss += q_rest * logf(q_rest / pr);
     }
     if (!ok) loss = __int_as_float(0x7fc00000);
@@ -225,16 +214,16 @@ struct List {
     return loss;
   }
 
-  // dlogits of the entry in slot j (after stats and, for REVERSE_TAIL, which needs the loss, too).
-  __device__ __forceinline__ float entry_grad(int j, float g) const {
-    const float pk = share(j);
+  // dlogits of entry k (after stats).
+  __device__ __forceinline__ float entry_grad(int k, float g) const {
+    const float pk = share(k);
     float corr;
     if (KIND == GRPO_DISTILL_FORWARD_TOPK)
-      corr = q_all != 0.f ? pk - q[j] : 0.f;
+      corr = q_all != 0.f ? pk - en.q[k] : 0.f;
     else if (KIND == GRPO_DISTILL_FORWARD_TAIL)
-      corr = fmaf(q_all, pk, -q[j]);
+      corr = fmaf(q_all, pk, -en.q[k]);
     else
-      corr = pk > 0.f ? pk * (((z[j] - l2s) * kLn2 - tlp[j]) - loss) : 0.f;
+      corr = pk > 0.f ? pk * (((en.z[k] - l2s) * kLn2 - en.tlp[k]) - loss) : 0.f;
     return ok ? corr * g : __int_as_float(0x7fc00000);
   }
 };
