@@ -59,12 +59,12 @@ __device__ __forceinline__ void count(grpo_step_acc* acc, unsigned long long tok
 // Calls f(d, k) in every lane for each listed token of the tile, d its element of the tile and k its
 // place in the list: the warp looks at 32 entries at a time.
 template <typename T, typename F>
-__device__ __forceinline__ void for_listed(const int32_t* sh_tok, int K, int tile, int lane, F f) {
-  const int64_t e0 = (int64_t)tile * tile_elems<T>();
+__device__ __forceinline__ void for_listed(const int32_t* sh_tok, int K, int64_t e0, int64_t n, F f) {
+  const int lane = (int)(threadIdx.x & 31);
 #pragma unroll 1
   for (int k0 = 0; k0 < K; k0 += 32) {
-    const int64_t d = (int64_t)sh_tok[k0 + lane] - e0;
-    unsigned hits = __ballot_sync(0xffffffffu, d >= 0 && d < tile_elems<T>());
+    const int64_t tok = sh_tok[k0 + lane], d = tok - e0;
+    unsigned hits = __ballot_sync(0xffffffffu, tok >= 0 && d >= 0 && d < n);
     for (; hits; hits &= hits - 1) {
       const int l = __ffs(hits) - 1;
       f(__shfl_sync(0xffffffffu, (int)d, l), k0 + l);
@@ -76,7 +76,7 @@ __device__ __forceinline__ void for_listed(const int32_t* sh_tok, int K, int til
 template <typename T>
 __device__ __forceinline__ void drop_listed(uint4 (&x)[kTileVecs], const int32_t* sh_tok, int K, int tile, int lane) {
   constexpr int E = 16 / (int)sizeof(T);
-  for_listed<T>(sh_tok, K, tile, lane, [&](int d, int) {
+  for_listed<T>(sh_tok, K, (int64_t)tile * tile_elems<T>(), tile_elems<T>(), [&](int d, int) {
     const int j = d / E, l = (j >> 2) & 31, u = (j >> 7) * 4 + ((j - (l >> 1)) & 3);
     if (l == lane) {
       // word of the lane's 32, and what of it stays
@@ -122,13 +122,13 @@ __device__ __forceinline__ uint4 grad_vec(const uint4& v, float c, const Stats& 
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
-// The first n elements of a vector, one by one.
+// Elements [i0, i1) of a vector to p[i0].., one by one.
 template <typename T>
-__device__ __noinline__ void store_elems(T* p, uint4 v, int n) {
+__device__ __noinline__ void store_elems(T* p, uint4 v, int i0, int i1) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 16 / (int)sizeof(T); ++i)
-    if (i < n) {
+    if (i >= i0 && i < i1) {
       if constexpr (sizeof(T) == 2)
         reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
       else
@@ -136,47 +136,24 @@ __device__ __noinline__ void store_elems(T* p, uint4 v, int n) {
     }
 }
 
-// A vector stored to a row at elements e0.. (cut at the row's end). `align`: the row's alignment in
-// bytes. bf16 rows on odd elements (align 2) have their own way below.
+// A vector stored to a row from element e0 on (cut at the row's end), a row of any alignment. Only rows
+// of dlogits that lie otherwise in their 16 bytes than their logits come here.
 template <typename T>
-__device__ __forceinline__ void store_vec(T* row, int64_t e0, int64_t V, int align, const uint4& v) {
+__device__ __forceinline__ void store_vec(T* row, int64_t e0, int64_t V, const uint4& v) {
+  if (e0 < V) store_elems(row + e0, v, 0, (int)min((int64_t)(16 / (int)sizeof(T)), V - e0));
+}
+
+// Aligned vector j of those that hold a row, `off` the row's bytes past a 16-byte boundary; what the
+// vector holds outside the row stays as it is.
+template <typename T>
+__device__ __forceinline__ void store_cover(T* row, int64_t j, int off, int64_t V, const uint4& v) {
   constexpr int E = 16 / (int)sizeof(T);
-  T* p = row + e0;
-  if (e0 + E > V || align < 4) {
-    if (e0 < V) store_elems(p, v, (int)min((int64_t)E, V - e0));
-  } else if (align == 16) {
+  T* p = reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(row) + j * 16 - off);
+  const int64_t e0 = (j * 16 - off) / (int64_t)sizeof(T);  // (a multiple of the element, also below 0)
+  if (e0 >= 0 && e0 + E <= V)
     *reinterpret_cast<uint4*>(p) = v;
-  } else if (align == 8) {
-    reinterpret_cast<uint2*>(p)[0] = make_uint2(v.x, v.y);
-    reinterpret_cast<uint2*>(p)[1] = make_uint2(v.z, v.w);
-  } else {
-    uint32_t* w = reinterpret_cast<uint32_t*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-  }
-}
-
-__device__ __forceinline__ int row_align(const void* row) {
-  const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(row);
-  return (a & 15u) == 0 ? 16 : (a & 7u) == 0 ? 8 : (a & 3u) == 0 ? 4 : 2;
-}
-
-// One vector of each lane (lane l: vector j0 + l of the row, wholly inside it in every lane) to a bf16
-// row on an odd element: in aligned words, each lane taking its successor's first element.
-__device__ __forceinline__ void store_odd(__nv_bfloat16* row, int64_t j0, int lane, const uint4& v) {
-  uint16_t* p = reinterpret_cast<uint16_t*>(row) + (j0 + lane) * 8;
-  const uint32_t nx = __shfl_down_sync(0xffffffffu, v.x, 1);
-  if (lane == 0) p[0] = (uint16_t)v.x;
-  uint32_t* w = reinterpret_cast<uint32_t*>(p + 1);
-  w[0] = __funnelshift_r(v.x, v.y, 16);
-  w[1] = __funnelshift_r(v.y, v.z, 16);
-  w[2] = __funnelshift_r(v.z, v.w, 16);
-  if (lane < 31)
-    w[3] = __funnelshift_r(v.w, nx, 16);
-  else
-    p[7] = (uint16_t)(v.w >> 16);
+  else if (e0 < V)
+    store_elems(p, v, e0 < 0 ? (int)-e0 : 0, (int)min((int64_t)E, V - e0));
 }
 
 // ------------------------------------------------------------------------------------------
@@ -185,26 +162,27 @@ __device__ __forceinline__ void store_odd(__nv_bfloat16* row, int64_t j0, int la
 constexpr int kMaxBlocks = 160;  // softmax partials kept per row
 
 template <typename T, int KIND, bool ALIGNED, int NT>
-__global__ void __launch_bounds__(NT) row_kernel(Args a) {
-  __shared__ Entries entries;
+__global__ void __launch_bounds__(NT, NT == 128 ? 8 : 1) row_kernel(Args a) {
+  __shared__ alignas(16) float sh_list[Entries::kWords * GRPO_TOPK_MAX];
   __shared__ float sh_corr[GRPO_TOPK_MAX], pm[kMaxBlocks], ps[kMaxBlocks];
   __shared__ Stats stats;
   constexpr int E = 16 / (int)sizeof(T), NW = NT / 32;
   constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Entries entries(sh_list, padded_list(a.K));
   const int64_t V = a.V, nvec = (V + E - 1) / E;
   unsigned long long c_tok = 0, c_val = 0, c_bad = 0;
   for (int64_t row_i = blockIdx.x; row_i < a.T; row_i += gridDim.x) {
     const int64_t src = a.tok_src ? a.tok_src[row_i] : row_i;
     const T* row = static_cast<const T*>(a.logits) + row_i * a.ld;
     T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + row_i * a.ld_out : nullptr;
-    const int align = dz ? row_align(dz) : 16;
+    const int off = dz ? row_off(dz) : 0;
     const bool valid = src >= 0 && a.mask[src] != 0;
     ++c_tok;
     if (!valid) {
       if (tid == 0 && src >= 0) a.loss_tok[src] = 0.f;
       if (dz)
-        for (int64_t j = tid; j < nvec; j += NT) store_vec(dz, j * E, V, align, make_uint4(0, 0, 0, 0));
+        for (int64_t j = tid; j <= nvec; j += NT) store_cover(dz, j, off, V, make_uint4(0, 0, 0, 0));
       continue;
     }
     ++c_val;
@@ -247,10 +225,18 @@ __global__ void __launch_bounds__(NT) row_kernel(Args a) {
     __syncthreads();
     if (dz) {
       const Stats st = stats;
-      for (int64_t j = tid; j < nvec; j += NT) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (st.mult != 0.f) v = grad_vec<T>(load_vec<T, ALIGNED>(row, j, V), a.c, st);
-        store_vec(dz, j * E, V, align, v);
+      if (ALIGNED || off == row_off(row)) {
+        for (int64_t j = tid; j <= nvec; j += NT) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (st.mult != 0.f) v = grad_vec<T>(load_cover<T, ALIGNED>(row, j, off, V), a.c, st);
+          store_cover(dz, j, off, V, v);
+        }
+      } else {
+        for (int64_t j = tid; j < nvec; j += NT) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (st.mult != 0.f) v = grad_vec<T>(load_vec<T, ALIGNED>(row, j, V), a.c, st);
+          store_vec(dz, j * E, V, v);
+        }
       }
       __syncthreads();
       for (int k = tid; k < a.K; k += NT)
@@ -273,33 +259,32 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 // The cluster kernel: persistent clusters of C CTAs, one CTA per SM; the tiles of a row are split
 // evenly over the CTAs. Read row k (masked and padding rows are not read) is owned by CTA k % C, which
 // does its list's arithmetic. Warps of a CTA:
-//   0       producer: fetches the CTA's tiles, row after row, into a ring of slots
-//   1       tokens: puts every row's listed tokens into shared memory
-//   2, 3    lists of the rows this CTA owns, in turn: loads a list and the listed logits ahead of time,
+//   0       producer: fetches the CTA's tiles, row after row, into a ring of slots, as far ahead as
+//           there are free ones, and puts every row's listed tokens into shared memory
+//   1, 2    lists of the rows this CTA owns, in turn: loads a list and the listed logits ahead of time,
 //           joins the row's partials once all have arrived, and sends what pass 2 needs (stats, the
 //           listed tokens' dlogits) to every CTA
-//   4..19   the tiles, tile i of the CTA by warp 4 + i % 16. Pass 1: the tile's partial, sent to the
+//   3..18   the tiles, tile i of the CTA by warp 3 + i % 16. Pass 1: the tile's partial, sent to the
 //           row's owner. Pass 2: dlogits from the same slot, the listed tokens' over them; then the
 //           slot is free.
 // Everything sent goes by asynchronous stores that an mbarrier of the receiver counts, so nobody waits
-// for a cluster barrier. Where two rows fit the ring, pass 1 of a row comes before pass 2 of the row
-// before it: the exchange and the list's arithmetic of one row run beside the tiles of the next. Each
-// row's arithmetic by every CTA of the cluster (no owner) took 1.9x at C = 4: one list is about 14,000
-// cycles of latency, a row 6,300 of bandwidth.
+// for a cluster barrier. The list's arithmetic by every CTA of the cluster (no owner) took 1.9x at C = 4,
+// as one list is about 14,000 cycles of latency and a row 6,300 of bandwidth. Pass 1 of a row before
+// pass 2 of the row before it hid the exchange but left no free slots: 8192 x 50257 bf16 499 against
+// 398 us.
 //
-// Barriers: full/empty of the slots; listed[k & 1] (the tokens are in shared
-// memory; the tail kinds, which need them in pass 1); parts (owner, per
-// list warp: the row's partials are in); ready[k & 1] (the stats are in, and the tokens);
-// grads[k & 1] (the list's dlogits are in). Why no
-// buffer is rewritten too early: parts of row k are complete only when every tile warp of the cluster
-// is through pass 1 of row k, hence through pass 2 of row k - 2; so what is sent to ready[k & 1] and
-// grads[k & 1] then finds row k - 2's done with, in every CTA, and a phase of ready, grads, listed or parts is never
-// overtaken by a round. Tokens have four buffers: they are written two rows ahead of that. Warps without a tile
-// in the CTA wait for nothing.
+// Barriers: full/empty of the slots; listed[k & 1] (the tokens are in shared memory; the tail kinds,
+// which need them in pass 1); parts (owner, per list warp: the row's partials are in); ready[k & 1] (the
+// stats are in, and the tokens); grads[k & 1] (the list's dlogits are in). Why no buffer is rewritten too
+// early: the partials of row k are complete only when every tile warp of the cluster is through pass 1 of
+// row k, hence through pass 2 of row k - 1. So what is sent to ready[k & 1] and grads[k & 1] then finds row
+// k - 2 done with in every CTA, and no phase of ready, grads, listed or parts is overtaken by a round. The
+// tokens of row k are written when the stats of row k - 2 have come, with which row k - 3 is done with:
+// they have four buffers. Warps without a tile in the CTA wait for nothing.
 // ------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 16;
-constexpr int kListWarps = 2;  // (20 warps: five per scheduler, 96 registers a thread)
-constexpr int kFirstListWarp = 2;
+constexpr int kListWarps = 2;  // (3: 4% slower at 152K and 10% at 50K, issue slots)
+constexpr int kFirstListWarp = 1;
 constexpr int kFirstTileWarp = kFirstListWarp + kListWarps;
 constexpr int kClusterThreads = (kFirstTileWarp + kTileWarps) * 32;
 constexpr int kMaxTiles = 384;
@@ -307,23 +292,36 @@ constexpr int kMaxSlots = 56;
 constexpr int kMinTiles = 16;
 
 struct ClusterShared {
-  float2 part[kListWarps][kMaxTiles];  // (m, s) of every tile of an owned row
-  alignas(16) int32_t tok[4][GRPO_TOPK_MAX];
-  Entries entries[kListWarps];
-  float corr[2][GRPO_TOPK_MAX];
   Stats stats[2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t parts[kListWarps], listed[2], ready[2], grads[2];
   int abort;
 };
 
-__host__ __device__ constexpr size_t cluster_head_bytes() { return (sizeof(ClusterShared) + 127) / 128 * 128; }
+// Behind it, sized by the call: entries[kListWarps] (Entries), tok[4] and corr[2] (lists), part[kListWarps]
+// ((m, s) of every tile of an owned row), and on the next 128 bytes the ring.
+struct ClusterLayout {
+  int padded;
+  uint32_t entries, tok, corr, part, ring;  // byte offsets
+  __host__ __device__ ClusterLayout(int K, int n_tiles) : padded(padded_list(K)) {
+    entries = (uint32_t)(sizeof(ClusterShared) + 15) / 16 * 16;
+    tok = entries + 4u * kListWarps * Entries::kWords * padded;
+    corr = tok + 4u * 4 * padded;
+    part = corr + 4u * 2 * padded;
+    ring = (part + 8u * kListWarps * n_tiles + 127) / 128 * 128;
+  }
+};
 
 template <typename T, int KIND, bool ALIGNED>
 __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int C) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   ClusterShared& sh = *reinterpret_cast<ClusterShared*>(smem_raw);
-  uint8_t* ring = smem_raw + cluster_head_bytes();
+  const ClusterLayout at(a.K, a.n_tiles);
+  uint8_t* ring = smem_raw + at.ring;
+  int32_t* sh_tok = reinterpret_cast<int32_t*>(smem_raw + at.tok);
+  float* sh_corr = reinterpret_cast<float*>(smem_raw + at.corr);
+  float2* sh_part = reinterpret_cast<float2*>(smem_raw + at.part);
+  const int padded = at.padded;
   constexpr int E = 16 / (int)sizeof(T);
   constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -332,8 +330,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
   const int64_t V = a.V;
   const int S = a.slots;
   const int t0 = rank * a.n_tiles / C, mine = (rank + 1) * a.n_tiles / C - t0;  // tiles of this CTA
-  const int most = (a.n_tiles + C - 1) / C;                                    // of any CTA
-  const int list_slots = a.dlogits ? (a.K + 31) / 32 : 0;  // entries a lane whose dlogits are sent
   volatile int* s_abort = &sh.abort;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -366,17 +362,33 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
     bool ok = true;
     int64_t nsrc = first < a.T ? src_of(first) : -1;
     bool nread = first < a.T && is_read(nsrc);
+    uint32_t k = 0;
+    int32_t tok[GRPO_TOPK_MAX / 32];
+    auto load_tokens = [&](int64_t src) {
+#pragma unroll
+      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j) {
+        tok[j] = -1;
+        if (32 * j + lane < a.K) tok[j] = a.top_idx[src * a.ld_top + 32 * j + lane];
+        if (tok[j] < 0 || (int64_t)tok[j] >= V) tok[j] = -1;
+      }
+    };
+    if (nread) load_tokens(nsrc);
     for (int64_t r = first; r < a.T && ok; r += stride) {
       const bool read = nread;
       if (r + stride < a.T) {  // the next row's index and mask while this row's tiles are issued
         nsrc = src_of(r + stride);
         nread = is_read(nsrc);
+      } else {
+        nread = false;
       }
-      if (!read) continue;
+      if (!read) {
+        if (nread) load_tokens(nsrc);
+        continue;
+      }
       const T* row = base + r * a.ld;
       const int off = ALIGNED ? 0 : row_off(row);
       const uint32_t bytes = kTileBytes + (off ? 16u : 0u);
-      auto at = [&](int i, int& slot, uint32_t& round) {
+      auto place = [&](int i, int& slot, uint32_t& round) {
         slot = slot0 + i;
         round = round0;
         if (slot >= S) {
@@ -390,7 +402,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         if (i < mine && !edge(i)) {
           int slot;
           uint32_t round;
-          at(i, slot, round);
+          place(i, slot, round);
           if (round == 0 || mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort)) {
             mbar_arrive_expect_tx(&sh.full[slot], bytes);
             bulk_g2s(ring + (size_t)slot * kSlotBytes,
@@ -406,10 +418,27 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         }
         int slot;
         uint32_t round;
-        at(i, slot, round);
+        place(i, slot, round);
         ok = round == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort));
         if (ok) fetch_tile<T>(ring + (size_t)slot * kSlotBytes, row, off, t0 + i, a.n_tiles, V, lane, &sh.full[slot]);
       }
+      const int buf = (int)(k & 1u);
+      if (k >= 2) {
+        mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
+        if (a.dlogits) mbar_wait_bounded(&sh.grads[buf], ((k >> 1) - 1u) & 1u, s_abort);
+      }
+#pragma unroll
+      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j)
+        if (32 * j < a.K) sh_tok[(int)(k & 3u) * padded + 32 * j + lane] = tok[j];
+      __syncwarp();
+      if (lane == 0) {
+        if (TAIL) mbar_arrive(&sh.listed[buf]);
+        // the row's stats and its list's dlogits will be counted (and the tokens are published)
+        mbar_arrive_expect_tx(&sh.ready[buf], 8u);
+        if (a.dlogits) mbar_arrive_expect_tx(&sh.grads[buf], 4u * (uint32_t)padded);
+      }
+      ++k;
+      if (nread) load_tokens(nsrc);
       ok = !__any_sync(0xffffffffu, *s_abort);
       slot0 += mine;
       if (slot0 >= S) {
@@ -426,39 +455,11 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         while (filled > 0 && !mbar_try_wait(&sh.full[s], (filled - 1) & 1u) && global_timer_ns() - begin < 1000000000ull) {}
       }
     }
-  } else if (warp == 1) {
-    // ---- tokens ----
-    uint32_t k = 0;
-    for (int64_t r = first; r < a.T; r += stride) {
-      const int64_t src = src_of(r);
-      if (!is_read(src)) continue;
-      int32_t tok[GRPO_TOPK_MAX / 32];
-#pragma unroll
-      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j) {
-        tok[j] = -1;
-        if (32 * j + lane < a.K) tok[j] = a.top_idx[src * a.ld_top + 32 * j + lane];
-        if (tok[j] < 0 || (int64_t)tok[j] >= V) tok[j] = -1;
-      }
-      const int buf = (int)(k & 1u);
-      if (k >= 2) {
-        mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
-        if (list_slots) mbar_wait_bounded(&sh.grads[buf], ((k >> 1) - 1u) & 1u, s_abort);
-      }
-#pragma unroll
-      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j)
-        if (32 * j < a.K) sh.tok[k & 3u][32 * j + lane] = tok[j];
-      __syncwarp();
-      if (lane == 0) {
-        if (TAIL) mbar_arrive(&sh.listed[buf]);
-        // the row's stats and its list's dlogits will be counted (and the tokens are published)
-        mbar_arrive_expect_tx(&sh.ready[buf], 8u);
-        if (list_slots) mbar_arrive_expect_tx(&sh.grads[buf], 128u * (uint32_t)list_slots);
-      }
-      ++k;
-    }
   } else if (warp < kFirstTileWarp) {
     // ---- the lists of the rows this CTA owns ----
     const int me = warp - kFirstListWarp;
+    const Entries entries(smem_raw + at.entries + (uint32_t)me * 4u * Entries::kWords * padded, padded);
+    const float2* part = sh_part + me * a.n_tiles;
     unsigned long long c_val = 0, c_bad = 0;
     uint32_t k = 0, own = 0;  // read rows, owned rows so far
     for (int64_t r = first; r < a.T; r += stride) {
@@ -471,11 +472,11 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       const uint32_t use = j_own / kListWarps;
       // the partials of all tiles will be counted: 8 bytes each
       if (lane == 0) mbar_arrive_expect_tx_relaxed(&sh.parts[me], 8u * (uint32_t)a.n_tiles);
-      List<T, KIND> list(sh.entries[me], a.K, V, lane);
+      List<T, KIND> list(entries, a.K, V, lane);
       list.load(a.top_idx + src * a.ld_top, a.top_logp + src * a.ld_top, base + r * a.ld);
       const float g = grad_scale_of(a, src);
       mbar_wait_bounded(&sh.parts[me], use & 1u, s_abort);
-      const Part p = join_blocks(a.n_tiles, lane, [&](int i) { return sh.part[me][i]; });
+      const Part p = join_blocks(a.n_tiles, lane, [&](int i) { return part[i]; });
       Stats st;
       bool finite;
       list.stats(p, a.c, g, st.shift, st.mult);
@@ -484,10 +485,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         st_async_v2f32(mapa_u32(smem_u32(&sh.stats[buf]), (uint32_t)lane), st.shift, st.mult,
                        mapa_u32(smem_u32(&sh.ready[buf]), (uint32_t)lane));
       const float loss = list.token_loss(g, finite);
-      if (list_slots)
+      if (a.dlogits)
         for (int k = lane; k < list.padded; k += 32) {
           const float d = list.entry_grad(k, g);
-          const uint32_t dst = smem_u32(&sh.corr[buf][k]), bar = smem_u32(&sh.grads[buf]);
+          const uint32_t dst = smem_u32(sh_corr + buf * padded + k), bar = smem_u32(&sh.grads[buf]);
           for (int c = 0; c < C; ++c) st_async_f32(mapa_u32(dst, (uint32_t)c), d, mapa_u32(bar, (uint32_t)c));
         }
       __syncwarp();  // the entries are rewritten by the next list
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
     // a read row on its way: where its tiles are (slot of the first, rounds of the ring there), its number
     struct Row {
       T* dz;
-      int off, align, slot0;
+      int off, off_out, slot0;  // bytes past a 16-byte boundary of the logits and the dlogits
       uint32_t round0, k;
     };
     auto pass1 = [&](const Row& q) {
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       if (TAIL) mbar_wait_bounded(&sh.listed[q.k & 1u], (q.k >> 1) & 1u, s_abort);
       // the row's owner and the list warp there that takes its partials
       const uint32_t owner = q.k % (uint32_t)C, box = (q.k / (uint32_t)C) % kListWarps;
-      const uint32_t part = mapa_u32(smem_u32(&sh.part[box][t0]), owner), bar = mapa_u32(smem_u32(&sh.parts[box]), owner);
+      const uint32_t part = mapa_u32(smem_u32(sh_part + box * a.n_tiles + t0), owner), bar = mapa_u32(smem_u32(&sh.parts[box]), owner);
       for (int i = w; i < mine; i += kTileWarps) {
         int slot = q.slot0 + i;
         uint32_t round = q.round0;
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         uint4 x[kTileVecs];
         read_tile<T, ALIGNED>(ring32 + (uint32_t)slot * kSlotBytes, q.off, lo4, x);
         const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
-        if (TAIL) drop_listed<T>(x, sh.tok[q.k & 3u], a.K, t0 + i, lane);
+        if (TAIL) drop_listed<T>(x, sh_tok + (int)(q.k & 3u) * padded, a.K, t0 + i, lane);
         const Part p = tile_part<T, false>(x, m, a.c);
         if (lane == 0) st_async_v2f32(part + 8u * (uint32_t)i, p.m, p.s, bar);
       }
@@ -539,25 +540,30 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         if (slot >= S) slot -= S;
         if (q.dz) {
           const int tile = t0 + i;
-          const bool inside = (int64_t)(tile + 1) * tile_elems<T>() <= V;
-          const uint32_t at = ring32 + (uint32_t)slot * kSlotBytes + (uint32_t)lane * 16u;
-          const int64_t j0 = (int64_t)tile * (32 * kTileVecs);
-          auto vec = [&](int u) -> uint4 {
-            uint4 v = lds128(at + (uint32_t)u * 512u);
-            if (!ALIGNED && q.off != 0) v = shift_vec<T>(v, lds128(at + (uint32_t)u * 512u + 16u), q.off);
+          const uint32_t src = ring32 + (uint32_t)slot * kSlotBytes + (uint32_t)lane * 16u;
+          const int64_t j0 = (int64_t)tile * (32 * kTileVecs) + lane;
+          auto vec = [&](int u, bool shifted) -> uint4 {
+            uint4 v = lds128(src + (uint32_t)u * 512u);
+            if (shifted) v = shift_vec<T>(v, lds128(src + (uint32_t)u * 512u + 16u), q.off);
             v = grad_vec<T>(v, a.c, st);
             return st.mult != 0.f ? v : make_uint4(0, 0, 0, 0);
           };
-          if (inside && (ALIGNED || q.align == 16)) {
+          if (ALIGNED || q.off == q.off_out) {
+            // the slot's vectors are aligned vectors of the row of dlogits, too
+            uint8_t* out = reinterpret_cast<uint8_t*>(q.dz) - q.off;
+            if ((tile > 0 || q.off == 0) && (int64_t)(tile + 1) * kTileBytes - q.off <= V * (int64_t)sizeof(T)) {
 #pragma unroll
-            for (int u = 0; u < kTileVecs; ++u) reinterpret_cast<uint4*>(q.dz)[j0 + u * 32 + lane] = vec(u);
-          } else if (!ALIGNED && sizeof(T) == 2 && inside && q.align == 2) {
-#pragma unroll
-            for (int u = 0; u < kTileVecs; ++u)
-              store_odd(reinterpret_cast<__nv_bfloat16*>(q.dz), j0 + u * 32, lane, vec(u));
+              for (int u = 0; u < kTileVecs; ++u) reinterpret_cast<uint4*>(out)[j0 + u * 32] = vec(u, false);
+            } else {
+#pragma unroll 1
+              for (int u = 0; u < kTileVecs; ++u) store_cover(q.dz, j0 + u * 32, q.off, V, vec(u, false));
+            }
+            // and the vector that the last tile reaches into
+            if (!ALIGNED && tile == a.n_tiles - 1 && q.off && lane == 0)
+              store_cover(q.dz, j0 + kTileVecs * 32, q.off, V, vec(kTileVecs, false));
           } else {
 #pragma unroll 1
-            for (int u = 0; u < kTileVecs; ++u) store_vec(q.dz, (j0 + u * 32 + lane) * E, V, q.align, vec(u));
+            for (int u = 0; u < kTileVecs; ++u) store_vec(q.dz, (j0 + u * 32) * E, V, vec(u, q.off != 0));
           }
         }
         __syncwarp();
@@ -566,14 +572,15 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       if (!q.dz) return;
       // the listed tokens' over what other lanes have stored (the barriers of the warp above order them)
       mbar_wait_bounded(&sh.grads[buf], (q.k >> 1) & 1u, s_abort);
-      for (int i = w; i < mine; i += kTileWarps)
-        for_listed<T>(sh.tok[q.k & 3u], a.K, t0 + i, lane, [&](int d, int e) {
-          if (lane == 0) put_elem(q.dz + (int64_t)(t0 + i) * tile_elems<T>() + d, sh.corr[buf][e]);
+      const int lead = ALIGNED || q.off == q.off_out ? q.off / (int)sizeof(T) : 0;
+      for (int i = w; i < mine; i += kTileWarps) {
+        // the elements that this warp has stored
+        const int64_t e0 = (int64_t)(t0 + i) * tile_elems<T>() - lead;
+        for_listed<T>(sh_tok + (int)(q.k & 3u) * padded, a.K, e0, t0 + i == a.n_tiles - 1 ? V : tile_elems<T>(), [&](int d, int e) {
+          if (lane == 0) put_elem(q.dz + e0 + d, sh_corr[buf * padded + e]);
         });
+      }
     };
-    const bool ahead = 2 * most <= S;  // (the same in every CTA)
-    Row prev{};
-    bool pending = false;
     int slot0 = 0;        // slot of the next row's first tile
     uint32_t round0 = 0;  // times the ring had gone round there
     unsigned long long c_tok = 0;
@@ -589,31 +596,27 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       }
       ++c_tok;
       T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + r * a.ld_out : nullptr;
-      const int align = dz ? row_align(dz) : 16;
+      const int off_out = !ALIGNED && dz ? row_off(dz) : 0;
       if (!read) {
         if (rank == 0 && w == 0 && lane == 0 && src >= 0) a.loss_tok[src] = 0.f;
         if (dz)
-          for (int i = w; i < mine; i += kTileWarps)
-            for (int u = 0; u < kTileVecs; ++u)
-              store_vec(dz, ((int64_t)(t0 + i) * (32 * kTileVecs) + u * 32 + lane) * E, V, align, make_uint4(0, 0, 0, 0));
+          for (int i = w; i < mine; i += kTileWarps) {
+            const int64_t j0 = (int64_t)(t0 + i) * (32 * kTileVecs) + lane;
+            for (int u = 0; u < kTileVecs; ++u) store_cover(dz, j0 + u * 32, off_out, V, make_uint4(0, 0, 0, 0));
+            if (!ALIGNED && t0 + i == a.n_tiles - 1 && lane == 0)
+              store_cover(dz, j0 + kTileVecs * 32, off_out, V, make_uint4(0, 0, 0, 0));
+          }
         continue;
       }
-      const Row cur{dz, ALIGNED ? 0 : row_off(base + r * a.ld), align, slot0, round0, k++};
+      const Row cur{dz, ALIGNED ? 0 : row_off(base + r * a.ld), off_out, slot0, round0, k++};
       slot0 += mine;
       if (slot0 >= S) {
         slot0 -= S;
         ++round0;
       }
       pass1(cur);
-      if (!ahead) {
-        pass2(cur);
-      } else {
-        if (pending) pass2(prev);
-        prev = cur;
-        pending = true;
-      }
+      pass2(cur);
     }
-    if (pending) pass2(prev);
     if (rank == 0 && w == 0 && lane == 0) count(a.acc, c_tok, 0, 0);
   }
   __syncthreads();
@@ -629,15 +632,15 @@ int cluster_size(int64_t T, int n_tiles, int slots, int sms) {
   return C;
 }
 
-int cluster_slots() {
-  const size_t optin = max_smem_optin();
-  return optin > cluster_head_bytes() ? (int)std::min<size_t>(kMaxSlots, (optin - cluster_head_bytes()) / kSlotBytes) : 0;
+int cluster_slots(int K, int n_tiles) {
+  const size_t optin = max_smem_optin(), head = ClusterLayout(K, n_tiles).ring;
+  return optin > head ? (int)std::min<size_t>(kMaxSlots, (optin - head) / kSlotBytes) : 0;
 }
 
 template <typename T, int KIND, bool ALIGNED>
 int launch_cluster(Args a, int C, cudaStream_t st) {
   auto kern = cluster_kernel<T, KIND, ALIGNED>;
-  const size_t smem = cluster_head_bytes() + (size_t)a.slots * kSlotBytes;
+  const size_t smem = ClusterLayout(a.K, a.n_tiles).ring + (size_t)a.slots * kSlotBytes;
   int dev = 0, n_clusters = 0;
   GRPO_CUDA_TRY(cudaGetDevice(&dev));
   cudaLaunchConfig_t cfg = {};
@@ -659,12 +662,12 @@ int launch_cluster(Args a, int C, cudaStream_t st) {
     std::lock_guard<std::mutex> lock(mu);
     const bool known = dev >= 0 && dev < 64;
     if (!known || !ready[dev]) {
-      GRPO_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      GRPO_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)max_smem_optin()));
       if (known) ready[dev] = true;
     }
     if (known) n_clusters = fit[dev][lc];
     if (n_clusters == 0) {
-      cfg.gridDim = dim3((unsigned)(C * 1024), 1, 1);
+      cfg.gridDim = dim3((unsigned)(C * 1024), 1, 1);  // (any smem above half an SM's: one CTA each)
       GRPO_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n_clusters, kern, &cfg));
       if (n_clusters < 1) return GRPO_ERR_UNSUPPORTED;
       if (known) fit[dev][lc] = n_clusters;
@@ -677,14 +680,14 @@ int launch_cluster(Args a, int C, cudaStream_t st) {
 
 template <typename T, int KIND, bool ALIGNED>
 int launch(Args a, cudaStream_t st) {
-  a.slots = cluster_slots();
+  a.slots = cluster_slots(a.K, a.n_tiles);
   if (a.n_tiles >= kMinTiles && a.n_tiles <= kMaxTiles && 8 * a.slots >= a.n_tiles)
     return launch_cluster<T, KIND, ALIGNED>(a, cluster_size(a.T, a.n_tiles, a.slots, sm_count()), st);
   a.fold = (a.n_tiles + kMaxBlocks - 1) / kMaxBlocks;
   a.n_blocks = (a.n_tiles + a.fold - 1) / a.fold;
   // short rows: small blocks, several rows in flight on an SM
   if (a.n_tiles < kMinTiles) return launch_row_nt<T, KIND, ALIGNED, 128>(a, 8, st);
-  return launch_row_nt<T, KIND, ALIGNED, 512>(a, 2, st);
+  return launch_row_nt<T, KIND, ALIGNED, 512>(a, 1, st);
 }
 
 template <typename T>

@@ -53,19 +53,25 @@ __device__ __forceinline__ Part join_blocks(int n, int lane, G get) {
   return {m, warp_sum(s), 0.f};
 }
 
-// A list's entries in shared memory, unused ones with token -1.
-struct alignas(16) Entries {
-  int32_t tok[GRPO_TOPK_MAX];
-  float tlp[GRPO_TOPK_MAX];  // log q
-  float z[GRPO_TOPK_MAX];    // the student's logit; from stats on z c - shift, log2 of its share
-  float q[GRPO_TOPK_MAX];    // the teacher's probability (FORWARD_TOPK: of the renormalised list)
+// K rounded up to whole warps: the entries that a list takes in shared memory.
+__host__ __device__ __forceinline__ int padded_list(int K) { return (K + 31) & ~31; }
+
+// A list's entries in shared memory (16-byte aligned), unused ones with token -1.
+struct Entries {
+  int32_t* tok;
+  float *tlp,  // log q
+      *z,      // the student's logit; from stats on z c - shift, log2 of its share
+      *q;      // the teacher's probability (FORWARD_TOPK: of the renormalised list)
+  static constexpr int kWords = 4;
+  __device__ Entries(void* mem, int padded)
+      : tok(static_cast<int32_t*>(mem)), tlp(static_cast<float*>(mem) + padded), z(tlp + padded), q(z + padded) {}
 };
 
 // One token's list, held by one warp from the loads to the gradients. The entries stay in shared memory,
 // lane l working on entries l, l + 32, ... (in registers, 8 a lane spilled and 2 a lane were no faster).
 template <typename T, int KIND>
 struct List {
-  Entries& en;
+  const Entries en;
   const int K, padded, lane;  // padded: K rounded up to whole warps
   const int64_t V;
   float log_norm;  // FORWARD_TOPK: log of the list's mass, its log-probs taken from their largest
@@ -78,7 +84,7 @@ struct List {
 
   static constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
 
-  __device__ List(Entries& entries, int k, int64_t v, int l) : en(entries), K(k), padded((k + 31) & ~31), lane(l), V(v) {}
+  __device__ List(const Entries& entries, int k, int64_t v, int l) : en(entries), K(k), padded(padded_list(k)), lane(l), V(v) {}
 
   // Loads the list and the listed logits. A bad list is left without tokens.
   __device__ __forceinline__ void load(const int32_t* top_idx, const float* top_logp, const T* row) {

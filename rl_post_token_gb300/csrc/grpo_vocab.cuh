@@ -166,12 +166,27 @@ __device__ __forceinline__ void read_tile(uint32_t slot, int off, const LaneOffs
 }
 
 // Vector j of a row straight from global memory, -inf past its end. ALIGNED: the row starts on a
-// 16-byte boundary.
+// 16-byte boundary. Of other rows the two aligned vectors that hold it, where both are inside the row.
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ uint4 load_vec(const T* row, int64_t j, int64_t V) {
   constexpr int E = 16 / (int)sizeof(T);
-  if (ALIGNED && (j + 1) * E <= V) return __ldg(reinterpret_cast<const uint4*>(row) + j);
+  if (ALIGNED) {
+    if ((j + 1) * E <= V) return __ldg(reinterpret_cast<const uint4*>(row) + j);
+  } else if (j > 0 && (j + 2) * E <= V) {
+    const int off = row_off(row);
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(row) - off) + j;
+    return off ? shift_vec<T>(__ldg(p), __ldg(p + 1), off) : __ldg(p);
+  }
   return edge_vec(row, j * E, V);
+}
+
+// Aligned vector j of those that hold a row (vector 0 holds its first element), -inf outside the row.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ uint4 load_cover(const T* row, int64_t j, int off, int64_t V) {
+  const int64_t b = j * 16 - (ALIGNED ? 0 : off);
+  if (b >= 0 && b + 16 <= V * (int64_t)sizeof(T))
+    return __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(row) + b));
+  return edge_vec(row, b / (int64_t)sizeof(T), V);
 }
 
 // Element i of a vector (a run-time index).
