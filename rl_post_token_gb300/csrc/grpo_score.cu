@@ -34,7 +34,6 @@ constexpr int kMaxGroups = 5120;            // group maxima kept per row
 constexpr int kMaxBlocks = kMaxGroups / 32;  // blocks (of `fold` tiles) per row
 constexpr int kBuckets = 256;
 constexpr int kListCap = 1024;  // listed groups; more (rows of ties) are walked without a list
-constexpr int kRankMax = 256;   // candidates ranked by counting; more are sorted
 
 struct Args {
   const void* logits;
@@ -72,7 +71,10 @@ struct Finish {
   static_assert(GRPO_TOPK_MAX + NT * 4 <= kCap && (kCap & (kCap - 1)) == 0, "a round fits; the sort takes a power of two");
   unsigned long long cand[kCap];
   int hist[kBuckets];
-  uint16_t list[kListCap];
+  union {
+    uint16_t list[kListCap];  // the groups that reach the bound
+    uint16_t place[kCap];     // candidates by bucket
+  };
   float lse_m, lse_l;
   uint32_t zmin;  // the listed groups' smallest maximum, as an ordered integer
   int bucket, n_list, n_cand;
@@ -156,9 +158,9 @@ __device__ __forceinline__ void finish_row(const Args& a, const T* row, int64_t 
   // ---- a histogram of the group maxima; every warp finds its range from the blocks' extremes. The
   // maxima of the groups that matter lie within a few tens of the largest; whatever lies below the
   // range (masks) falls into bucket 0 ----
-  float blo = 0.f, bsc = 0.f;
+  float blo = 0.f, bsc = 0.f, h = -INFINITY;
   if (K > 0) {
-    float h = -INFINITY, l = INFINITY;
+    float l = INFINITY;
     for (int i = lane; i < a.n_blocks; i += 32) {
       h = fmaxf(h, st.part[i].w);
       l = fminf(l, st.lo[i]);
@@ -283,28 +285,41 @@ __device__ __forceinline__ void finish_row(const Args& a, const T* row, int64_t 
     }
   };
   // first all at once, kBatch vectors a thread in flight; the buffer holds their candidates but for
-  // rows full of ties or masks
+  // rows full of ties or masks. Thread i takes vector i % 8 of its groups' tiles.
   constexpr int kBatch = 4;
-  for (uint32_t i0 = tid; i0 < n_vec; i0 += NT * kBatch) {
+  static_assert(kTileVecs == 8 && NT % kTileVecs == 0, "vectors by threads");
+  const uint32_t n_unit = a.by_vec ? n_list : n_list * (uint32_t)a.fold;
+  const uint32_t step = a.by_vec ? NT : NT / kTileVecs, k_at = ((tid >> 2) & 1u) * 128u + (tid & 3u);
+  for (uint32_t u0 = a.by_vec ? tid : tid / kTileVecs; u0 < n_unit; u0 += step * kBatch) {
     uint4 x[kBatch];
-    int64_t j[kBatch];
+    uint32_t j[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      j[i] = i0 + i * NT < n_vec ? vec_at(i0 + i * NT) : INT32_MAX;  // a vector past every row
-      x[i] = load_vec<T, ALIGNED>(row, j[i], V);
+      const uint32_t u = u0 + i * step, li = a.fold == 1 ? u : u / (uint32_t)a.fold;
+      const uint32_t ninf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+      x[i] = make_uint4(ninf, ninf, ninf, ninf);
+      j[i] = INT32_MAX;  // a vector past every row
+      if (u < n_unit) {
+        const uint32_t g = listed ? sh.list[li] : li;
+        j[i] = g;
+        if (!a.by_vec) j[i] = ((g >> 5) * (uint32_t)a.fold + (u - li * (uint32_t)a.fold)) * (32u * kTileVecs) + (g & 31u) * 4u + k_at;
+        x[i] = load_vec<T, ALIGNED>(row, j[i], V);
+      }
     }
+    uint32_t hit = 0;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (!(vec_max<T>(x[i]) >= zthr)) continue;
       float z[E];
       vec_floats<T>(x[i], z);
-      uint32_t hit = 0;
+      if (vec_max<T>(x[i]) >= zthr) {
 #pragma unroll
-      for (int k = 0; k < E; ++k) hit |= (z[k] >= zthr ? 1u : 0u) << k;
-      for (; hit; hit &= hit - 1) {
-        const int k = __ffs(hit) - 1;
-        if (j[i] * E + k < V) offer(j[i] * E + k, vec_elem<T>(x[i], k));
+        for (int k = 0; k < E; ++k) hit |= (z[k] >= zthr ? 1u : 0u) << (i * E + k);
       }
+    }
+    for (; hit; hit &= hit - 1) {
+      const uint32_t b = (uint32_t)__ffs(hit) - 1u, i = b / E;
+      const int64_t e = (int64_t)(i & 2u ? (i & 1u ? j[3] : j[2]) : (i & 1u ? j[1] : j[0])) * E + b % E;
+      if (e < V) offer(e, elem_f32(row + e));
     }
     if (*static_cast<volatile int*>(&sh.n_cand) > kCap) break;  // it only grows: the rounds below start over
   }
@@ -342,17 +357,53 @@ __device__ __forceinline__ void finish_row(const Args& a, const T* row, int64_t 
     a.top_idx[out * a.ld_top + r] = (int32_t)key_idx(key);
     if (a.top_logp) a.top_logp[out * a.ld_top + r] = (fmaf(key_logit(key), a.c, -m) - l2) * kLn2;
   };
-  if (n <= kRankMax) {
-    for (int i = tid; i < n; i += NT) {
-      const unsigned long long key = sh.cand[i];
+  if (n <= NT) {  // each against all
+    if (tid < n) {
+      const unsigned long long key = sh.cand[tid];
       int r = 0;
 #pragma unroll 8
       for (int j = 0; j < n; ++j) r += sh.cand[j] > key;
       if (r < K) write(r, key);
     }
-  } else {
-    sort_candidates<NT>(sh.cand, n, tid, bar);
-    for (int i = tid; i < K; i += NT) write(i, sh.cand[i]);
+    return;
+  }
+  // into buckets by their logits (bucket 255 first), then each against those of its bucket. (Sorting a
+  // row's 300 candidates for K = 256 took twice the time of reading the row, 17,000 cycles.)
+  const float clo = fmaxf(zthr, h - 128.f), csc = h > clo ? (kBuckets - 0.5f) / (h - clo) : 0.f;
+  auto bucket = [&](unsigned long long key) { return bucket_of(key_logit(key), clo, csc); };
+  for (int i = tid; i < kBuckets; i += NT) sh.hist[i] = 0;
+  named_bar_sync(bar, NT);
+  for (int i = tid; i < n; i += NT) atomicAdd(&sh.hist[bucket(sh.cand[i])], 1);
+  named_bar_sync(bar, NT);
+  if (warp == 0) {  // each bucket's first place
+    constexpr int PB = kBuckets / 32;
+    int c[PB], own = 0;
+#pragma unroll
+    for (int i = 0; i < PB; ++i) own += c[i] = sh.hist[PB * (31 - lane) + i];
+    int pre = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    pre -= own;
+#pragma unroll
+    for (int i = PB - 1; i >= 0; --i) {
+      sh.hist[PB * (31 - lane) + i] = pre;
+      pre += c[i];
+    }
+  }
+  named_bar_sync(bar, NT);
+  static_assert(kCap <= 65536, "16-bit places");
+  for (int i = tid; i < n; i += NT) sh.place[atomicAdd(&sh.hist[bucket(sh.cand[i])], 1)] = (uint16_t)i;
+  named_bar_sync(bar, NT);
+  for (int i = tid; i < n; i += NT) {
+    const unsigned long long key = sh.cand[i];
+    const int b = bucket(key), first = b == kBuckets - 1 ? 0 : sh.hist[b + 1], end = sh.hist[b];
+    if (first >= K) continue;
+    int r = first;
+    for (int j = first; j < end; ++j) r += sh.cand[sh.place[j]] > key;
+    if (r < K) write(r, key);
   }
 }
 
@@ -447,8 +498,6 @@ __global__ void __launch_bounds__(kThreads, 2) row_kernel(Args a) {
     const int tile = b * a.fold + f;
     const bool last = f + 1 == a.fold || tile + 1 == a.n_tiles;  // of its block
     const float lm = tile_lane_max<T>(x);
-    const Part tp = tile_part<T, true>(x, warp_max_nan(lm) * a.c, a.c);
-    p = f == 0 ? tp : part_join(p, tp);
     gm = f == 0 ? lm : max_nan(gm, lm);
     if (a.by_vec && a.K > 0) {
 #pragma unroll
@@ -461,6 +510,8 @@ __global__ void __launch_bounds__(kThreads, 2) row_kernel(Args a) {
         }
       }
     }
+    const Part tp = tile_part<T, true>(x, warp_max_nan(lm) * a.c, a.c);
+    p = f == 0 ? tp : part_join(p, tp);
     if (last) {
       if (!a.by_vec) {
         put(&sh.gmax[b * 32 + lane], gm);

@@ -271,6 +271,32 @@ __device__ __forceinline__ Part warp_part(Part v) {
   return {M, s, q};
 }
 
+// A tile's vectors by value.
+struct Tile {
+  uint4 x[kTileVecs];
+};
+
+// A lane's q where elements without mass made it 0 * -inf: their t is taken as the lowest finite value.
+// (Out of line: the streaming loops are short of instruction cache.)
+template <typename T>
+__device__ __noinline__ float masked_q(Tile tile, float shift, float c) {
+  constexpr int E = 16 / (int)sizeof(T);
+  float2 q[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+  for (int u = 0; u < kTileVecs; ++u) {
+    float f[E];
+    vec_floats<T>(tile.x[u], f);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      float2 t = __ffma2_rn(make_float2(f[i], f[i + 1]), make_float2(c, c), make_float2(-shift, -shift));
+      const float2 e = make_float2(ex2(t.x), ex2(t.y));
+      t = make_float2(fmaxf(t.x, -3.4028235e38f), fmaxf(t.y, -3.4028235e38f));
+      q[(i / 2) & 1] = __ffma2_rn(e, t, q[(i / 2) & 1]);
+    }
+  }
+  return (q[0].x + q[1].x) + (q[0].y + q[1].y);
+}
+
 // A tile's partial from its vectors, m its maximum in log2 units, c = log2(e)/tau. The sums run in
 // packed pairs over the lane's vectors, then by a fixed tree over the lanes; every lane gets them. A
 // NaN or +inf in the tile makes s NaN or inf. Logits that c z takes below the float32 range (the type's
@@ -297,22 +323,11 @@ __device__ __forceinline__ Part tile_part(const uint4 (&x)[kTileVecs], float m, 
   float ss = (s[0].x + s[1].x) + (s[0].y + s[1].y), qq = 0.f;
   if (Q) {
     qq = (q[0].x + q[1].x) + (q[0].y + q[1].y);
-    if (qq != qq) {  // 0 * -inf of an element without mass (or a NaN row): once more without them
-      qq = 0.f;
-#pragma unroll 1
-      for (int i = 0; i < kTileVecs; ++i) {
-        uint4 v = x[0];
+    if (qq != qq) {  // (or a NaN row)
+      Tile tile;
 #pragma unroll
-        for (int u = 1; u < kTileVecs; ++u)
-          if (u == i) v = x[u];
-        float f[E];
-        vec_floats<T>(v, f);
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const float t = fmaf(f[k], c, -shift), e = ex2(t);
-          if (e != 0.f) qq = fmaf(e, t, qq);
-        }
-      }
+      for (int u = 0; u < kTileVecs; ++u) tile.x[u] = x[u];
+      qq = masked_q<T>(tile, shift, c);
     }
   }
 #pragma unroll
