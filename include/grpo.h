@@ -600,7 +600,8 @@ GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W, int64_t T
                                          void* stream);
 
 /* Bytes of device workspace grpo_lmhead_distill_topk_fwd_bwd needs: grpo_lmhead_workspace_size's,
- * and per token an int32 and K floats (each part rounded up to 256 bytes). 0 on bad sizes. */
+ * per token an int32 and K floats, and with few tokens up to 76 partial tiles of d_h (20 MB; each
+ * part rounded up to 256 bytes). 0 on bad sizes. */
 GRPO_API size_t grpo_lmhead_distill_workspace_size(int64_t T, int64_t V, int64_t H, int64_t K);
 
 /* grpo_distill_topk_fwd_bwd's FORWARD_TOPK loss (temperature 1) from hidden states: z = h W^T is
@@ -608,6 +609,7 @@ GRPO_API size_t grpo_lmhead_distill_workspace_size(int64_t T, int64_t V, int64_t
  * loss_tok, acc and workspace rules hold (workspace: grpo_lmhead_distill_workspace_size(T, V, H, K)
  * bytes); H at most 16384. top_idx, top_logp, ld_top, K, w_tok as in grpo_distill_topk_fwd_bwd.
  * The logits of the listed tokens are formed once more as float32 dot products of h and W's rows.
+ * The order of d_h's sums depends on T, V and H.
  * The tail kinds have no LM-head form: the student's mass outside the list would have to be formed
  * as a difference. A token whose |LSE| is above 4096 counts as non-finite.
  * Errors: those of grpo_lmhead_loss_fwd_bwd, and GRPO_ERR_INVALID for a bad K, ld_top, H or

@@ -537,6 +537,26 @@ int forward(int cg, const void* h, const void* W, int64_t T, int64_t V, int64_t 
   return GRPO_OK;
 }
 
+// d_h of the live tokens from the runs' partials, summed in order.
+__global__ void __launch_bounds__(256) split_sum_kernel(const int32_t* live_n, const int32_t* row_idx, int64_t T, int64_t H,
+                                                        const float* part, int split, float* d_h) {
+  const int64_t n = (int64_t)*live_n * (H / 4), stride = T * (H / 4);
+  const float4* p = reinterpret_cast<const float4*>(part);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float4 v = p[i];
+#pragma unroll 4
+    for (int s = 1; s < split; ++s) {
+      const float4 o = p[s * stride + i];
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    }
+    const int64_t r = i / (H / 4);
+    reinterpret_cast<float4*>(d_h)[(int64_t)row_idx[r] * (H / 4) + (i - r * (H / 4))] = v;
+  }
+}
+
 // The backward's second stream and its events, one set per device, created by the first call
 // that needs them (with the device current) and kept for the process lifetime. A call holds
 // `lock` while it enqueues its backward, so calls from several host threads never interleave
@@ -585,10 +605,12 @@ Overlap* overlap_state(std::unique_lock<std::mutex>& lock) {
 // chunk's recompute runs beside them. d_h's launches stay in chunk order on one stream (its
 // accumulation order), and a buffer is rewritten only after the launches reading it two chunks before.
 // ent_grad: the dlogits take the entropy form p (ea + eb z).
+// split > 1: d_h's reduction in that many runs, run s of every chunk summed into part[s] [T, H] by
+// compact rows, their sums (in order) into d_h at the end.
 template <typename AfterDz>
 int backward(int cg, const void* h, const void* W, int64_t T, int64_t V, int64_t H, const int32_t* target,
              bool ent_grad, float* d_h, float* dW, uint32_t flags, grpo_step_acc* acc, const WsLayout& ws,
-             const Scratch& sc, cudaStream_t st, AfterDz after_dz) {
+             const Scratch& sc, cudaStream_t st, AfterDz after_dz, int split = 1, float* part = nullptr) {
   int rc = GRPO_OK;
   const int n_chunks = (ws.n_col_tiles + ws.chunk_tiles - 1) / ws.chunk_tiles;
   std::unique_lock<std::mutex> ov_lock;
@@ -657,6 +679,13 @@ int backward(int cg, const void* h, const void* W, int64_t T, int64_t V, int64_t
       b.ldc = H;
       b.accumulate = c > 0;
       b.acc = acc;
+      if (split > 1) {  // (the last chunk may have fewer K blocks than the others)
+        b.split = (int)std::min<int64_t>(split, (vc + BK - 1) / BK);
+        b.n_n *= b.split;
+        b.split_stride = T * H;
+        b.C = part;
+        b.row_idx = nullptr;
+      }
       rc = launch<EPI_STORE_F32, false, true>(cg, ma, mb, ma, b, bst);
       if (rc != GRPO_OK) return rc;
     }
@@ -683,6 +712,11 @@ int backward(int cg, const void* h, const void* W, int64_t T, int64_t V, int64_t
   return GRPO_OK;
   };
   rc = chunks();
+  if (rc == GRPO_OK && d_h && split > 1) {
+    const int64_t blocks = std::min<int64_t>((T * H / 4 + 255) / 256, (int64_t)sm_count() * 8);
+    split_sum_kernel<<<(unsigned)blocks, 256, 0, bst>>>(sc.live_n, sc.idx, T, H, part, split, d_h);
+    if (cudaGetLastError() != cudaSuccess) rc = GRPO_ERR_CUDA;
+  }
   if (ov) {  // the caller's stream continues after every launch of the call (also after an error)
     const bool joined = cudaEventRecord(ov->joined, bst) == cudaSuccess &&
                         cudaStreamWaitEvent(st, ov->joined, 0) == cudaSuccess;
@@ -745,11 +779,21 @@ extern "C" GRPO_API int grpo_lmhead_loss_fwd_bwd(const void* h, const void* W, i
 
 namespace {
 
-// The loss's workspace layout, then a target array without targets and the list entries' dlogits.
+// The loss's workspace layout, then a target array without targets, the list entries' dlogits and
+// the partials of a d_h cut into runs.
 struct DistillLayout {
   WsLayout base;
-  size_t target, corr, total;
+  size_t target, corr, part, total;
+  int split;
 };
+
+// Runs that d_h's reduction over a chunk is cut into: as many as fill 76 CTA pairs, each of 16 K
+// blocks or more. At 300 tokens and H = 1024 a chunk's d_h is 8 units of 264 K blocks, 85 us in one
+// run each.
+int d_h_split(int64_t T, int64_t H, int chunk_tiles) {
+  const int64_t units = ((T + 2 * BM - 1) / (2 * BM)) * ((H + BN - 1) / BN);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(76 / units, (int64_t)chunk_tiles * (BN / BK) / 16));
+}
 
 DistillLayout distill_layout(int64_t T, int64_t V, int64_t H, int64_t K) {
   DistillLayout d{};
@@ -757,7 +801,9 @@ DistillLayout distill_layout(int64_t T, int64_t V, int64_t H, int64_t K) {
   d.base = ws_layout(T, V, H);
   d.target = up(d.base.total);
   d.corr = d.target + up((size_t)T * 4);
-  d.total = d.corr + up((size_t)T * K * 4);
+  d.part = d.corr + up((size_t)T * K * 4);
+  d.split = d_h_split(T, H, d.base.chunk_tiles);
+  d.total = d.part + (d.split > 1 ? up((size_t)d.split * T * H * 4) : 0);
   return d;
 }
 
@@ -830,7 +876,8 @@ extern "C" GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const vo
                                                            v0, vc);
                     GRPO_CUDA_TRY(cudaGetLastError());
                     return GRPO_OK;
-                  });
+                  },
+                  dl.split, reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dl.part));
 }
 
 // ---- allocation-free forward entry point -----------------------------------------------------

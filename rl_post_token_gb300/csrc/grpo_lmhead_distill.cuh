@@ -15,10 +15,10 @@
 namespace grpo {
 namespace lmhead {
 
-constexpr int kLseWarps = 8;
+constexpr int kLseWarps = 16;
 
 // A block takes 32 tokens (lane = token: a partial's load is one 128-byte line), its warps every
-// 8th tile in order; warp 0 joins the warps' in order. idx / live_n: the compact order of a pass A
+// 16th tile in order; warp 0 joins the warps' in order. idx / live_n: the compact order of a pass A
 // that skipped the masked tokens (row i holds token idx[i]), or NULL.
 __global__ void __launch_bounds__(kLseWarps * 32) lse_kernel(int64_t T, int n_col_tiles, const float* part_m,
                                                              const float* part_s, const int32_t* idx,

@@ -54,7 +54,7 @@ struct Shape {
   static constexpr int B_BYTES = B_ROWS * BK * 2;        // 16 KB (CG = 2) or 32 KB
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // bytes this CTA receives per stage
   static constexpr int STAGES = CG == 2 ? 6 : 4;
-  static constexpr int EPI_BYTES = EPI == EPI_DLOGITS ? EPI_WARPS * 2 * EPI_BUF_BYTES : 0;
+  static constexpr int EPI_BYTES = EPI == EPI_DLOGITS || EPI == EPI_STORE_F32 ? EPI_WARPS * 2 * EPI_BUF_BYTES : 0;
   static constexpr size_t SMEM = 1024 /*alignment slack*/ + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + 256;
 };
 
@@ -241,6 +241,10 @@ struct GemmArgs {
   float* C;
   int64_t ldc;
   int accumulate;
+  // split > 1: the reduction is cut into `split` runs of K blocks, run s a unit of its own that goes
+  // to C + s split_stride (n_n counts the runs: N tiles x split; no more runs than K blocks)
+  int split;
+  int64_t split_stride;
   grpo_step_acc* acc;
   // A compact order of the tokens that the partition kernel wrote earlier in stream order:
   // *live_n of them, row i of the compact order being token row_idx[i]. The backward runs
@@ -435,30 +439,61 @@ __device__ __forceinline__ void epi_dlogits(const GemmArgs& g, const CUtensorMap
 }
 
 // float32 output tile: C[row][n0 .. n0 + 256) = (accumulate ? C : 0) + D, columns past N skipped
-// (N is a multiple of 64, so a 32-column group is wholly inside or outside).
-__device__ __forceinline__ void epi_store_f32(const GemmArgs& g, uint32_t taddr, int64_t row, bool rok, int64_t n0) {
-  // d_h over the live tokens: compact row -> the token's row of C
-  const int64_t crow_i = (rok && g.row_idx) ? (int64_t)g.row_idx[row] : row;
-  float* crow = g.C + crow_i * g.ldc;
+// (N is a multiple of 64, so a 32-column group is wholly inside or outside). Each 32-column group of
+// the warp's 32 rows goes through shared memory (128-byte rows, chunk q of row r at q ^ (r & 7):
+// conflict-free both ways), so that a warp's access to C covers 4 rows of 128 bytes. Straight from the
+// accumulator's lanes it covered 16 bytes of 32 rows: dW of 270 tokens, 16896 x 1024, took 34 us.
+__device__ __forceinline__ void epi_store_f32(const GemmArgs& g, float* C, uint32_t taddr, int64_t row, bool rok,
+                                              int64_t n0, uint32_t buf, int lane) {
+  // d_h over the live tokens: compact row -> the token's row of C; -1 past the rows
+  const int crow_i = !rok ? -1 : g.row_idx ? g.row_idx[row] : (int)row;
+  const uint32_t put = buf + (uint32_t)lane * 128u, sw = (uint32_t)(lane & 7);
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
     float v[32];
     tmem_ld32(taddr + c * 32, v);
     const int64_t col = n0 + c * 32;
-    if (!rok || col >= g.N) continue;
-    float4* p = reinterpret_cast<float4*>(crow + col);
-    if (g.accumulate) {
+    if (col >= g.N) continue;  // warp-uniform
+    __syncwarp();              // the group before has been read
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float4 o = p[q];
-        v[4 * q] += o.x;
-        v[4 * q + 1] += o.y;
-        v[4 * q + 2] += o.z;
-        v[4 * q + 3] += o.w;
+    for (int q = 0; q < 8; ++q)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(put + (((uint32_t)q ^ sw) << 4)), "f"(v[4 * q]),
+                   "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
+                   : "memory");
+    __syncwarp();
+    // lane: chunk lane % 8 of rows lane / 8 + 4 i
+    float* at = C + col + (lane & 7) * 4;
+    if (g.accumulate) {
+      float4 o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int cr = __shfl_sync(0xffffffffu, crow_i, i * 4 + (lane >> 3));
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (cr >= 0) o[i] = *reinterpret_cast<const float4*>(at + cr * g.ldc);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3), cr = __shfl_sync(0xffffffffu, crow_i, r);
+        float4 d;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+                     : "r"(buf + (uint32_t)r * 128u + (((uint32_t)(lane & 7) ^ (uint32_t)(r & 7)) << 4))
+                     : "memory");
+        if (cr >= 0)
+          *reinterpret_cast<float4*>(at + cr * g.ldc) = make_float4(d.x + o[i].x, d.y + o[i].y, d.z + o[i].z, d.w + o[i].w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3), cr = __shfl_sync(0xffffffffu, crow_i, r);
+        float4 d;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+                     : "r"(buf + (uint32_t)r * 128u + (((uint32_t)(lane & 7) ^ (uint32_t)(r & 7)) << 4))
+                     : "memory");
+        if (cr >= 0) *reinterpret_cast<float4*>(at + cr * g.ldc) = d;
       }
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
   }
 }
 
@@ -521,6 +556,18 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   const int first = CG == 2 ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int stride = CG == 2 ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   const int KB = (int)((K + BK - 1) / BK);
+  // a unit's N tile and its K blocks [k0, k1)
+  const int split = EPI == EPI_STORE_F32 && g.split > 1 ? g.split : 1;
+  auto unit_k = [&](int& nu, int& k0, int& k1) -> int {
+    k0 = 0;
+    k1 = KB;
+    if (EPI != EPI_STORE_F32 || split == 1) return 0;
+    const int n_nt = g.n_n / split, run = nu / n_nt;
+    nu -= run * n_nt;
+    k0 = (int)((int64_t)run * KB / split);
+    k1 = (int)((int64_t)(run + 1) * KB / split);
+    return run;
+  };
 
   if (warp == 0) {
     // ---- TMA producer: this CTA's A rows and B rows of every stage ----
@@ -530,9 +577,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       for (int t = first; t < n_units; t += stride) {
         int mu, nu;
         unit_coords(g, n_m, t, mu, nu);
+        int k0, k1;
+        unit_k(nu, k0, k1);
         const int a_row = mu * BM * CG + (int)rank * BM;
         const int b_row = (g.col_tile0 + nu) * BN + (int)rank * S::B_ROWS;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = k0; kb < k1; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, s_abort)) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * S::STAGE_BYTES);
           const uint32_t sa = sbase + stage * S::STAGE_BYTES;
@@ -571,7 +620,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         if (!free_acc) break;
         fence_after();
         const uint32_t d = tmem + ab * BN;
-        for (int kb = 0; kb < KB; ++kb) {
+        int k0 = 0, k1 = KB;
+        if (EPI == EPI_STORE_F32) {
+          int mu, nu;
+          unit_coords(g, n_m, t, mu, nu);
+          unit_k(nu, k0, k1);
+        }
+        for (int kb = k0; kb < k1; ++kb) {
           // Not tested for a break: after a wait gives up, the unit's remaining MMAs issue
           // without waiting (they read whatever the stages hold; the step is flagged) and the
           // abort check below stops the issuer before the accumulator is committed. A break
@@ -582,7 +637,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
           const uint64_t da = sdesc<A_MN>(sa), db = sdesc<B_MN>(sa + S::A_BYTES);
 #pragma unroll
           for (int j = 0; j < BK / 16; ++j)
-            mma_bf16<CG>(d, da + kstep<A_MN>() * j, db + kstep<B_MN>() * j, ID, kb > 0 || j > 0);
+            mma_bf16<CG>(d, da + kstep<A_MN>() * j, db + kstep<B_MN>() * j, ID, kb > k0 || j > 0);
           const uint32_t eb = smem_u32(&empty[stage]);
           mma_commit<CG>(eb);
           if (CG == 2) mma_commit<CG>(mapa_u32(eb, 1));
@@ -621,8 +676,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       else if constexpr (EPI == EPI_DLOGITS)
         epi_dlogits(g, &map_c, taddr, row, rok, g.col_tile0 + nu, row - lane, rows_store,
                     epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
-      else
-        epi_store_f32(g, taddr, row, rok, (int64_t)nu * BN);
+      else {
+        int k0, k1;
+        const int run = unit_k(nu, k0, k1);
+        epi_store_f32(g, g.C + run * g.split_stride, taddr, row, rok, (int64_t)nu * BN,
+                      epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
+      }
       fence_before();
       __syncwarp();
       if (lane == 0) {
