@@ -94,6 +94,24 @@ __device__ __forceinline__ void drop_listed(uint4 (&x)[kTileVecs], const int32_t
   });
 }
 
+// The same for a tile in shared memory, before it is read: `tile0` is its first element's address.
+template <typename T>
+__device__ __forceinline__ void drop_listed_smem(uint32_t tile0, const int32_t* sh_tok, int K, int tile, int lane) {
+  const int64_t e0 = (int64_t)tile * tile_elems<T>();
+#pragma unroll 1
+  for (int k0 = 0; k0 < K; k0 += 32) {
+    const int64_t tok = sh_tok[k0 + lane], d = tok - e0;
+    if (tok >= 0 && d >= 0 && d < tile_elems<T>()) {
+      const uint32_t at = tile0 + (uint32_t)d * (uint32_t)sizeof(T);
+      if constexpr (sizeof(T) == 2)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)0xFF80u) : "memory");
+      else
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0xFF800000u) : "memory");
+    }
+  }
+  __syncwarp();
+}
+
 template <typename T>
 __device__ __forceinline__ void put_elem(T* p, float v) {
   if constexpr (sizeof(T) == 2)
@@ -198,8 +216,8 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 8 : 1) row_kernel(Args a) {
 #pragma unroll
         for (int u = 0; u < kTileVecs; ++u)
           x[u] = load_vec<T, ALIGNED>(row, (int64_t)tile * (32 * kTileVecs) + tile_vec(lane, u), V);
-        const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
         if (TAIL) drop_listed<T>(x, entries.tok, a.K, tile, lane);
+        const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
         const Part tp = tile_part<T, false>(x, m, a.c);
         p = f == 0 ? tp : part_join(p, tp);
       }
@@ -385,6 +403,24 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         if (nread) load_tokens(nsrc);
         continue;
       }
+      // the tokens first: the tail kinds' pass 1 waits for them
+      const int buf = (int)(k & 1u);
+      if (k >= 2) {
+        mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
+        if (a.dlogits) mbar_wait_bounded(&sh.grads[buf], ((k >> 1) - 1u) & 1u, s_abort);
+      }
+#pragma unroll
+      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j)
+        if (32 * j < a.K) sh_tok[(int)(k & 3u) * padded + 32 * j + lane] = tok[j];
+      __syncwarp();
+      if (lane == 0) {
+        if (TAIL) mbar_arrive(&sh.listed[buf]);
+        // the row's stats and its list's dlogits will be counted (and the tokens are published)
+        mbar_arrive_expect_tx(&sh.ready[buf], 8u);
+        if (a.dlogits) mbar_arrive_expect_tx(&sh.grads[buf], 4u * (uint32_t)padded);
+      }
+      ++k;
+      if (nread) load_tokens(nsrc);
       const T* row = base + r * a.ld;
       const int off = ALIGNED ? 0 : row_off(row);
       const uint32_t bytes = kTileBytes + (off ? 16u : 0u);
@@ -404,6 +440,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
           uint32_t round;
           place(i, slot, round);
           if (round == 0 || mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort)) {
+            // (the tail kinds' warps have written to the slot)
+            if (TAIL) fence_proxy_async_smem();
             mbar_arrive_expect_tx(&sh.full[slot], bytes);
             bulk_g2s(ring + (size_t)slot * kSlotBytes,
                      reinterpret_cast<const uint8_t*>(row) + (int64_t)(t0 + i) * kTileBytes - off, bytes, &sh.full[slot]);
@@ -420,25 +458,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         uint32_t round;
         place(i, slot, round);
         ok = round == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort));
+        if (TAIL) fence_proxy_async_smem();
         if (ok) fetch_tile<T>(ring + (size_t)slot * kSlotBytes, row, off, t0 + i, a.n_tiles, V, lane, &sh.full[slot]);
       }
-      const int buf = (int)(k & 1u);
-      if (k >= 2) {
-        mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
-        if (a.dlogits) mbar_wait_bounded(&sh.grads[buf], ((k >> 1) - 1u) & 1u, s_abort);
-      }
-#pragma unroll
-      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j)
-        if (32 * j < a.K) sh_tok[(int)(k & 3u) * padded + 32 * j + lane] = tok[j];
-      __syncwarp();
-      if (lane == 0) {
-        if (TAIL) mbar_arrive(&sh.listed[buf]);
-        // the row's stats and its list's dlogits will be counted (and the tokens are published)
-        mbar_arrive_expect_tx(&sh.ready[buf], 8u);
-        if (a.dlogits) mbar_arrive_expect_tx(&sh.grads[buf], 4u * (uint32_t)padded);
-      }
-      ++k;
-      if (nread) load_tokens(nsrc);
       ok = !__any_sync(0xffffffffu, *s_abort);
       slot0 += mine;
       if (slot0 >= S) {
@@ -522,10 +544,11 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
           ++round;
         }
         mbar_wait_bounded(&sh.full[slot], round & 1u, s_abort);
+        const uint32_t tile0 = ring32 + (uint32_t)slot * kSlotBytes;
+        if (TAIL) drop_listed_smem<T>(tile0 + (uint32_t)q.off, sh_tok + (int)(q.k & 3u) * padded, a.K, t0 + i, lane);
         uint4 x[kTileVecs];
-        read_tile<T, ALIGNED>(ring32 + (uint32_t)slot * kSlotBytes, q.off, lo4, x);
+        read_tile<T, ALIGNED>(tile0, q.off, lo4, x);
         const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
-        if (TAIL) drop_listed<T>(x, sh_tok + (int)(q.k & 3u) * padded, a.K, t0 + i, lane);
         const Part p = tile_part<T, false>(x, m, a.c);
         if (lane == 0) st_async_v2f32(part + 8u * (uint32_t)i, p.m, p.s, bar);
       }

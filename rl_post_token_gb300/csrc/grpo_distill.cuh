@@ -164,6 +164,14 @@ struct List {
   // distribution or with a bad list has NaN throughout.
   __device__ __forceinline__ void stats(Part p, float c, float g, float& shift, float& mult) {
     float se = 0.f;
+    if constexpr (TAIL) {  // to the largest of all logits
+      float top = p.m;
+      for (int k = lane; k < padded; k += 32)
+        if (en.tok[k] != -1) top = max_nan(top, en.z[k] * c);
+      top = warp_max_nan(top);
+      if (p.m != -INFINITY) p.s *= ex2(p.m - top);
+      p.m = top;
+    }
     for (int k = lane; k < padded; k += 32) {
       const float t = fmaf(en.z[k], c, -p.m);
       en.z[k] = t;

@@ -90,7 +90,8 @@ __device__ __noinline__ int2 fetch_edges(uint8_t* slot, const T* row, int off, i
   if (lane == 0 && cut < all) reinterpret_cast<uint4*>(slot)[cut] = edge_vec(row, e0 + (int64_t)cut * E, V);
   const uint32_t ninf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
   for (int v = cut + 1 + lane; v < all; v += 32) reinterpret_cast<uint4*>(slot)[v] = make_uint4(ninf, ninf, ninf, ninf);
-  __syncwarp();  // before lane 0's arrive on the slot's barrier
+  fence_proxy_async_smem();  // before the copy that refills the slot
+  __syncwarp();              // before lane 0's arrive on the slot's barrier
   return make_int2(v0, v1);
 }
 

@@ -3,7 +3,8 @@
 Tolerances, from the arithmetic (t = (z - max) log2(e)/tau, E over the student's distribution):
   dS = 2^-22 + 50 2^-24 + 2^-23 ln2 E|t|    relative error of a sum of exponentials (ex2 within
        2^-22; at most 16 additions in a lane, 2 + 5 over the tile, 12 joins and 5 additions over the
-       tiles, 8 + 5 over the list, one to add its part, and the joins' rescaling)
+       tiles, 8 + 5 over the list, one to add its part, and two rescalings: by the join, and to the
+       largest of all logits, 2^-22 each and a product)
   dlp = dS + 2^-24 |log S| + 2^-23 (|z - max|/tau + |log p|)     of a log-prob (natural units)
   dp  = dS + 2^-22 + 2^-23 |t| ln2 + 4 2^-24                     relative, of a probability
        = what 2^t carries, the reciprocal of S and three products
