@@ -599,9 +599,9 @@ GRPO_API int grpo_lmhead_loss_fwd_bwd_ex(const void* h, const void* W, int64_t T
                                          grpo_step_acc* acc, void* workspace, size_t workspace_bytes,
                                          void* stream);
 
-/* Bytes of device workspace grpo_lmhead_distill_topk_fwd_bwd needs: grpo_lmhead_workspace_size's,
- * per token an int32 and K floats, and with few tokens up to 76 partial tiles of d_h (20 MB; each
- * part rounded up to 256 bytes). 0 on bad sizes. */
+/* Bytes of device workspace grpo_lmhead_distill_topk_fwd_bwd needs: grpo_lmhead_workspace_size's with
+ * vocabulary chunks of up to 32 MB of dlogits, per token an int32 and K floats, and with few tokens
+ * the partial sums of d_h's runs. 0 on bad sizes. */
 GRPO_API size_t grpo_lmhead_distill_workspace_size(int64_t T, int64_t V, int64_t H, int64_t K);
 
 /* grpo_distill_topk_fwd_bwd's FORWARD_TOPK loss (temperature 1) from hidden states: z = h W^T is

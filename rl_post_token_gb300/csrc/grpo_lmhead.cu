@@ -381,11 +381,11 @@ struct WsLayout {
   int64_t vchunk;  // columns of the dlogits chunk buffer
 };
 
-WsLayout ws_layout(int64_t T, int64_t V, int64_t H) {
+WsLayout ws_layout(int64_t T, int64_t V, int64_t H, int max_chunk_tiles = kMaxChunkTiles) {
   WsLayout w{};
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   w.n_col_tiles = (int)((V + BN - 1) / BN);
-  const int n_chunks = (w.n_col_tiles + kMaxChunkTiles - 1) / kMaxChunkTiles;
+  const int n_chunks = (w.n_col_tiles + max_chunk_tiles - 1) / max_chunk_tiles;
   w.chunk_tiles = (w.n_col_tiles + n_chunks - 1) / n_chunks;
   w.vchunk = (int64_t)w.chunk_tiles * BN;
   size_t off = 0;
@@ -787,18 +787,34 @@ struct DistillLayout {
   int split;
 };
 
-// Runs that d_h's reduction over a chunk is cut into: as many as fill 76 CTA pairs, each of 16 K
-// blocks or more. At 300 tokens and H = 1024 a chunk's d_h is 8 units of 264 K blocks, 85 us in one
-// run each.
+// Vocabulary tiles per chunk: with few tokens more than the loss's, as long as a chunk's dlogits take at
+// most 32 MB (they are read back from L2). 300 tokens, V = 50257, H = 1024: one chunk 206 us, three 294.
+int distill_chunk_tiles(int64_t T) {
+  return (int)std::max<int64_t>(kMaxChunkTiles, std::min<int64_t>(((int64_t)32 << 20) / (T * BN * 2), INT32_MAX / BN));
+}
+
+// CTAs per tile: 1 where tiles of 128 tokens come to fewer rounds over the SMs in pass A than the pairs'
+// of 256 (a round takes the same time). 300 tokens at V = 50257: 4 rounds, not 6, 206 us against 239 of the
+// whole call; 1000 at V = 32000: 7 and 7, 461 against 524 the other way. GRPO_LMHEAD_CTA_GROUP
+// decides where it is set.
+int distill_cta_group(int64_t T, int n_col_tiles) {
+  if (getenv("GRPO_LMHEAD_CTA_GROUP")) return cta_group();
+  auto rounds = [&](int64_t rows, int64_t slots) { return ((T + rows - 1) / rows * n_col_tiles + slots - 1) / slots; };
+  return rounds(BM, 152) < rounds(2 * BM, 76) ? 1 : 2;
+}
+
+// Runs that d_h's reduction over a chunk is cut into: as many as fill 152 SMs, each of 16 K blocks or
+// more, and of kMaxChunkTiles vocabulary tiles at most. At 300 tokens, V = 50257, H = 1024 d_h took 255 us
+// of 491 in one run per chunk of 66 tiles.
 int d_h_split(int64_t T, int64_t H, int chunk_tiles) {
-  const int64_t units = ((T + 2 * BM - 1) / (2 * BM)) * ((H + BN - 1) / BN);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(76 / units, (int64_t)chunk_tiles * (BN / BK) / 16));
+  const int64_t units = ((T + BM - 1) / BM) * ((H + BN - 1) / BN), blocks = (int64_t)chunk_tiles * (BN / BK);
+  return (int)std::max<int64_t>((chunk_tiles + kMaxChunkTiles - 1) / kMaxChunkTiles, std::min<int64_t>(152 / units, blocks / 16));
 }
 
 DistillLayout distill_layout(int64_t T, int64_t V, int64_t H, int64_t K) {
   DistillLayout d{};
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  d.base = ws_layout(T, V, H);
+  d.base = ws_layout(T, V, H, distill_chunk_tiles(T));
   d.target = up(d.base.total);
   d.corr = d.target + up((size_t)T * 4);
   d.part = d.corr + up((size_t)T * K * 4);
@@ -835,7 +851,7 @@ extern "C" GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const vo
   const Scratch sc = carve(workspace, ws, true);
   int32_t* target = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + dl.target);
   float* corr = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dl.corr);
-  const int cg = cta_group();
+  const int cg = distill_cta_group(T, ws.n_col_tiles);
   const bool skip = (flags & GRPO_LMHEAD_SKIP_MASKED) != 0;
   // no target: pass A picks up no target logit, the recompute's dlogits are the dense coef p_v
   GRPO_CUDA_TRY(cudaMemsetAsync(target, 0xFF, (size_t)T * 4, st));

@@ -258,12 +258,11 @@ def test_lmhead_distill_argument_checks(kw, code):
 
 
 def test_lmhead_distill_workspace():
-    up = lambda x: (x + 255) // 256 * 256
-    # the last: runs of d_h's reduction whose partials it holds (1: none)
-    for T, V, H, K, runs in [(1, 5, 64, 5, 1), (300, 40000, 512, 33, 13), (64, 150000, 256, 8, 16), (4096, 40000, 2048, 9, 1)]:
+    for T, V, H, K in [(1, 5, 64, 5), (300, 40000, 512, 33), (64, 150000, 256, 8), (4096, 40000, 2048, 9)]:
         n = _lib.grpo_lmhead_distill_workspace_size(T, V, H, K)
-        part = up(4 * runs * T * H) if runs > 1 else 0
-        assert n == up(_lib.grpo_lmhead_workspace_size(T, V, H)) + up(4 * T) + up(4 * T * K) + part
+        # the loss's own scratch and the lists' dlogits fit; few tokens take little more
+        base = _lib.grpo_lmhead_workspace_size(T, V, H) + 4 * T * (K + 1)
+        assert base <= n <= base + 2 * (32 << 20) + 4 * H * (T + 255) * 40 + 4096
         assert _lm_distill(T=T, V=V, H=H, K=K, ld_top=K, ws_bytes=n - 1) == _lib.ERR_CAPACITY
     for bad in [(0, 8, 64, 1), (8, 0, 64, 1), (8, 8, 0, 1), (8, 8, 64, 0)]:
         assert _lib.grpo_lmhead_distill_workspace_size(*bad) == 0
