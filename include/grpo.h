@@ -39,7 +39,8 @@
  *       GRPO_ROWPASS_FWD=0        forward-only calls take the general cluster kernel instead of
  *                                 the streaming forward kernel;
  *       GRPO_LMHEAD_CTA_GROUP=1   fused LM-head: one-CTA 128 x 256 tiles instead of paired
- *                                 2-CTA 256 x 256 tiles;
+ *                                 2-CTA 256 x 256 tiles (unset, the distillation's form chooses
+ *                                 by its number of tokens);
  *       GRPO_LMHEAD_OVERLAP=0     fused LM-head: the backward's launches all on the caller's
  *                                 stream instead of two streams.
  */
