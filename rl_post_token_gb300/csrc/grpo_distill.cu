@@ -282,7 +282,8 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 //   1, 2    lists of the rows this CTA owns, in turn: loads a list and the listed logits ahead of time,
 //           joins the row's partials once all have arrived, and sends what pass 2 needs (stats, the
 //           listed tokens' dlogits) to every CTA
-//   3..18   the tiles, tile i of the CTA by warp 3 + i % 16. Pass 1: the tile's partial, sent to the
+//   3..18   the tiles, dealt to the 16 warps in turn, from row to row on where a row has one for every
+//           warp (38 tiles a row started afresh: DEAL_OLD us at 8192 x 151936 bf16; so: DEAL_NEW). Pass 1: the tile's partial, sent to the
 //           row's owner. Pass 2: dlogits from the same slot, the listed tokens' over them; then the
 //           slot is free.
 // Everything sent goes by asynchronous stores that an mbarrier of the receiver counts, so nobody waits
@@ -298,7 +299,8 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 // row k, hence through pass 2 of row k - 1. So what is sent to ready[k & 1] and grads[k & 1] then finds row
 // k - 2 done with in every CTA, and no phase of ready, grads, listed or parts is overtaken by a round. The
 // tokens of row k are written when the stats of row k - 2 have come, with which row k - 3 is done with:
-// they have four buffers. Warps without a tile in the CTA wait for nothing.
+// they have four buffers. Warps without a tile in the CTA's rows wait for nothing; where rows have fewer
+// tiles than warps, the same warps work on all of them, so that "every tile warp" holds.
 // ------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 16;
 constexpr int kListWarps = 2;  // (3: 4% slower at 152K and 10% at 50K, issue slots)
@@ -529,6 +531,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       T* dz;
       int off, off_out, slot0;  // bytes past a 16-byte boundary of the logits and the dlogits
       uint32_t round0, k;
+      int i0;  // this warp's first tile
     };
     auto pass1 = [&](const Row& q) {
       if (w >= mine) return;
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       // the row's owner and the list warp there that takes its partials
       const uint32_t owner = q.k % (uint32_t)C, box = (q.k / (uint32_t)C) % kListWarps;
       const uint32_t part = mapa_u32(smem_u32(sh_part + box * a.n_tiles + t0), owner), bar = mapa_u32(smem_u32(&sh.parts[box]), owner);
-      for (int i = w; i < mine; i += kTileWarps) {
+      for (int i = q.i0; i < mine; i += kTileWarps) {
         int slot = q.slot0 + i;
         uint32_t round = q.round0;
         if (slot >= S) {
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       const int buf = (int)(q.k & 1u);
       mbar_wait_bounded(&sh.ready[buf], (q.k >> 1) & 1u, s_abort);
       const Stats st = sh.stats[buf];
-      for (int i = w; i < mine; i += kTileWarps) {
+      for (int i = q.i0; i < mine; i += kTileWarps) {
         int slot = q.slot0 + i;
         if (slot >= S) slot -= S;
         if (q.dz) {
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       // the listed tokens' over what other lanes have stored (the barriers of the warp above order them)
       mbar_wait_bounded(&sh.grads[buf], (q.k >> 1) & 1u, s_abort);
       const int lead = ALIGNED || q.off == q.off_out ? q.off / (int)sizeof(T) : 0;
-      for (int i = w; i < mine; i += kTileWarps) {
+      for (int i = q.i0; i < mine; i += kTileWarps) {
         // the elements that this warp has stored
         const int64_t e0 = (int64_t)(t0 + i) * tile_elems<T>() - lead;
         for_listed<T>(sh_tok + (int)(q.k & 3u) * padded, a.K, e0, t0 + i == a.n_tiles - 1 ? V : tile_elems<T>(), [&](int d, int e) {
@@ -608,6 +611,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
     uint32_t round0 = 0;  // times the ring had gone round there
     unsigned long long c_tok = 0;
     uint32_t k = 0;  // read rows so far
+    int i0 = w;
     int64_t nsrc = first < a.T ? src_of(first) : -1;
     bool nread = first < a.T && is_read(nsrc);
     for (int64_t r = first; r < a.T; r += stride) {
@@ -631,7 +635,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
           }
         continue;
       }
-      const Row cur{dz, ALIGNED ? 0 : row_off(base + r * a.ld), off_out, slot0, round0, k++};
+      const Row cur{dz, ALIGNED ? 0 : row_off(base + r * a.ld), off_out, slot0, round0, k++, i0};
+      if (mine >= kTileWarps) i0 = (i0 + kTileWarps - mine % kTileWarps) % kTileWarps;
       slot0 += mine;
       if (slot0 >= S) {
         slot0 -= S;

@@ -60,7 +60,7 @@ __host__ __device__ __forceinline__ int padded_list(int K) { return (K + 31) & ~
 struct Entries {
   int32_t* tok;
   float *tlp,  // log q
-      *z,      // the student's logit; from stats on z c - shift, log2 of its share
+      *z,      // the student's logit; from token_loss (tail kinds: stats) on z c - shift, log2 of its share
       *q;      // the teacher's probability (FORWARD_TOPK: of the renormalised list)
   static constexpr int kWords = 4;
   __device__ Entries(void* mem, int padded)
@@ -79,7 +79,8 @@ struct List {
   float q_all;     // FORWARD_TOPK: 1, or 0 without a list; FORWARD_TAIL: Q + q_R
   int n;           // tokens listed
   bool bad;        // a token twice or outside the vocabulary, a NaN or +inf log-prob
-  float l2s, inv, pr, alpha, loss;  // from stats on
+  float pm, cz, sum, inv, pr, alpha;  // from stats on
+  float l2s, loss;                    // from token_loss on (REVERSE_TAIL: from stats)
   bool ok;
 
   static constexpr bool TAIL = KIND != GRPO_DISTILL_FORWARD_TOPK;
@@ -163,30 +164,33 @@ struct List {
   // dlogits are mult 2^(z c - shift) outside the list. g: the gradient scale. A row without a
   // distribution or with a bad list has NaN throughout.
   __device__ __forceinline__ void stats(Part p, float c, float g, float& shift, float& mult) {
-    float se = 0.f;
-    if constexpr (TAIL) {  // to the largest of all logits
-      float top = p.m;
-      for (int k = lane; k < padded; k += 32)
-        if (en.tok[k] != -1) top = max_nan(top, en.z[k] * c);
-      top = warp_max_nan(top);
-      if (p.m != -INFINITY) p.s *= ex2(p.m - top);
-      p.m = top;
+    pm = p.m;
+    cz = c;
+    float S = p.s;
+    if constexpr (TAIL) {
+      for (int k = lane; k < padded; k += 32)  // to the largest of all logits
+        if (en.tok[k] != -1) pm = max_nan(pm, en.z[k] * c);
+      pm = warp_max_nan(pm);
+      if (p.m != -INFINITY) p.s *= ex2(p.m - pm);
+      p.m = pm;
+      float se = 0.f;
+      for (int k = lane; k < padded; k += 32) {
+        const float t = fmaf(en.z[k], c, -pm);
+        en.z[k] = t;
+        if (en.tok[k] != -1) se += ex2(t);
+      }
+      S = p.s + warp_sum(se);
     }
-    for (int k = lane; k < padded; k += 32) {
-      const float t = fmaf(en.z[k], c, -p.m);
-      en.z[k] = t;
-      if (TAIL && en.tok[k] != -1) se += ex2(t);
-    }
-    const float S = TAIL ? p.s + warp_sum(se) : p.s;
     ok = !bad && fabsf(p.m) < INFINITY && S > 0.f && S < INFINITY;
     inv = 1.f / S;
     pr = TAIL ? p.s * inv : 0.f;
-    l2s = log2f(S);
+    sum = S;
     if constexpr (KIND == GRPO_DISTILL_FORWARD_TOPK) {
       alpha = q_all;
     } else if constexpr (KIND == GRPO_DISTILL_FORWARD_TAIL) {
       alpha = q_all - (q_rest > 0.f ? q_rest / pr : 0.f);
     } else {
+      l2s = log2f(S);
       sum_loss();
       const bool tail = pr > 0.f && n < V;
       const float fr = tail ? logf(pr / q_rest) : 0.f;
@@ -203,23 +207,26 @@ struct List {
 
   // The list's terms of the loss.
   __device__ __forceinline__ void sum_loss() {
-    float sum = 0.f;
+    float part = 0.f;
     for (int k = lane; k < padded; k += 32) {
       const float lp = (en.z[k] - l2s) * kLn2;
       if (KIND == GRPO_DISTILL_REVERSE_TAIL) {
         const float pk = share(k);
-        sum += pk > 0.f ? pk * (lp - en.tlp[k]) : 0.f;
+        part += pk > 0.f ? pk * (lp - en.tlp[k]) : 0.f;
       } else {
         const float q = en.q[k];
-        sum += q > 0.f ? q * ((en.tlp[k] - log_norm) - lp) : 0.f;  // (q = 0 without a token)
+        part += q > 0.f ? q * ((en.tlp[k] - log_norm) - lp) : 0.f;  // (q = 0 without a token)
       }
     }
-    loss = warp_sum(sum);
+    loss = warp_sum(part);
   }
 
-  // The token's loss (after stats).
+  // The token's loss (after stats, which does what the other warps wait for).
   __device__ __forceinline__ float token_loss(float g, bool& finite) {
     if constexpr (KIND != GRPO_DISTILL_REVERSE_TAIL) {
+      l2s = log2f(sum);
+      if (!TAIL)
+        for (int k = lane; k < padded; k += 32) en.z[k] = fmaf(en.z[k], cz, -pm);
       sum_loss();
       if (KIND == GRPO_DISTILL_FORWARD_TAIL && q_rest > 0.f) loss += q_rest * logf(q_rest / pr);
     }
@@ -228,7 +235,7 @@ struct List {
     return loss;
   }
 
-  // dlogits of entry k (after stats).
+  // dlogits of entry k (after token_loss).
   __device__ __forceinline__ float entry_grad(int k, float g) const {
     const float pk = share(k);
     float corr;
