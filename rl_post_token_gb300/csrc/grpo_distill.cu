@@ -277,13 +277,13 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 // The cluster kernel: persistent clusters of C CTAs, one CTA per SM; the tiles of a row are split
 // evenly over the CTAs. Read row k (masked and padding rows are not read) is owned by CTA k % C, which
 // does its list's arithmetic. Warps of a CTA:
-//   0       producer: fetches the CTA's tiles, row after row, into a ring of slots, as far ahead as
-//           there are free ones, and puts every row's listed tokens into shared memory
-//   1, 2    lists of the rows this CTA owns, in turn: loads a list and the listed logits ahead of time,
+//   0, 1    producers: fetch the CTA's tiles, row after row, into a ring of slots, as far ahead as there
+//           are free ones; warp 0 puts every row's listed tokens into shared memory
+//   2, 3    lists of the rows this CTA owns, in turn: loads a list and the listed logits ahead of time,
 //           joins the row's partials once all have arrived, and sends what pass 2 needs (stats, the
 //           listed tokens' dlogits) to every CTA
-//   3..18   the tiles, dealt to the 16 warps in turn, from row to row on where a row has one for every
-//           warp (38 tiles a row started afresh: DEAL_OLD us at 8192 x 151936 bf16; so: DEAL_NEW). Pass 1: the tile's partial, sent to the
+//   4..19   the tiles, dealt to the 16 warps in turn, from row to row on where a row has one for every
+//           warp (38 tiles a row started afresh: 818 us at 8192 x 151936 bf16; so: 811). Pass 1: the tile's partial, sent to the
 //           row's owner. Pass 2: dlogits from the same slot, the listed tokens' over them; then the
 //           slot is free.
 // Everything sent goes by asynchronous stores that an mbarrier of the receiver counts, so nobody waits
@@ -304,7 +304,9 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 // ------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 16;
 constexpr int kListWarps = 2;  // (3: 4% slower at 152K and 10% at 50K, issue slots)
-constexpr int kFirstListWarp = 1;
+constexpr int kIssueWarps = 2;  // producers, each taking every second tile
+constexpr int kIssueLanes = 4;  // tiles that one of them issues together
+constexpr int kFirstListWarp = kIssueWarps;
 constexpr int kFirstTileWarp = kFirstListWarp + kListWarps;
 constexpr int kClusterThreads = (kFirstTileWarp + kTileWarps) * 32;
 constexpr int kMaxTiles = 384;
@@ -372,11 +374,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
   auto src_of = [&](int64_t r) -> int64_t { return a.tok_src ? a.tok_src[r] : r; };
   auto is_read = [&](int64_t src) { return src >= 0 && a.mask[src] != 0; };
 
-  if (warp == 0) {
-    // ---- producer ----
-    // A lane per tile: the lanes' waits and copies overlap (one lane issuing tile after tile took 500
-    // cycles each, longer than a row's share of the bandwidth). Tiles at a row's ends, which the whole
-    // warp fills up, come after the others.
+  if (warp < kIssueWarps) {
+    // ---- producers ----
+    // A wait on a slot and a copy's issue take 150 to 250 cycles each, together longer than a row's share of
+    // the bandwidth for one warp: two take turns, a few lanes issue together, and a batch waits for its own
+    // slots alone, so that what is free is filled while the tiles' warps wait for the list (8192 x 151936
+    // bf16: one warp, 32 lanes 812 us; two, 16 lanes 806; two, 4 lanes 757). Tiles at a row's ends, which the
+    // whole warp fills up, come after the others.
     int slot0 = 0;         // slot of the row's first tile
     uint32_t round0 = 0;   // times the ring had gone round there
     bool ok = true;
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         if (tok[j] < 0 || (int64_t)tok[j] >= V) tok[j] = -1;
       }
     };
-    if (nread) load_tokens(nsrc);
+    if (warp == 0 && nread) load_tokens(nsrc);
     for (int64_t r = first; r < a.T && ok; r += stride) {
       const bool read = nread;
       if (r + stride < a.T) {  // the next row's index and mask while this row's tiles are issued
@@ -402,27 +406,28 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         nread = false;
       }
       if (!read) {
-        if (nread) load_tokens(nsrc);
+        if (warp == 0 && nread) load_tokens(nsrc);
         continue;
       }
-      // the tokens first: the tail kinds' pass 1 waits for them
-      const int buf = (int)(k & 1u);
-      if (k >= 2) {
-        mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
-        if (a.dlogits) mbar_wait_bounded(&sh.grads[buf], ((k >> 1) - 1u) & 1u, s_abort);
-      }
+      if (warp == 0) {  // the tokens first: the tail kinds' pass 1 waits for them
+        const int buf = (int)(k & 1u);
+        if (k >= 2) {
+          mbar_wait_bounded(&sh.ready[buf], ((k >> 1) - 1u) & 1u, s_abort);
+          if (a.dlogits) mbar_wait_bounded(&sh.grads[buf], ((k >> 1) - 1u) & 1u, s_abort);
+        }
 #pragma unroll
-      for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j)
-        if (32 * j < a.K) sh_tok[(int)(k & 3u) * padded + 32 * j + lane] = tok[j];
-      __syncwarp();
-      if (lane == 0) {
-        if (TAIL) mbar_arrive(&sh.listed[buf]);
-        // the row's stats and its list's dlogits will be counted (and the tokens are published)
-        mbar_arrive_expect_tx(&sh.ready[buf], 8u);
-        if (a.dlogits) mbar_arrive_expect_tx(&sh.grads[buf], 4u * (uint32_t)padded);
+        for (int j = 0; j < GRPO_TOPK_MAX / 32; ++j)
+          if (32 * j < a.K) sh_tok[(int)(k & 3u) * padded + 32 * j + lane] = tok[j];
+        __syncwarp();
+        if (lane == 0) {
+          if (TAIL) mbar_arrive(&sh.listed[buf]);
+          // the row's stats and its list's dlogits will be counted (and the tokens are published)
+          mbar_arrive_expect_tx(&sh.ready[buf], 8u);
+          if (a.dlogits) mbar_arrive_expect_tx(&sh.grads[buf], 4u * (uint32_t)padded);
+        }
+        ++k;
+        if (nread) load_tokens(nsrc);
       }
-      ++k;
-      if (nread) load_tokens(nsrc);
       const T* row = base + r * a.ld;
       const int off = ALIGNED ? 0 : row_off(row);
       const uint32_t bytes = kTileBytes + (off ? 16u : 0u);
@@ -435,25 +440,30 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         }
       };
       auto edge = [&](int i) { return (t0 + i == 0 && off) || t0 + i >= a.n_tiles - 2; };
-      for (int i0 = 0; i0 < mine; i0 += 32) {
-        const int i = i0 + lane;
-        if (i < mine && !edge(i)) {
+      for (int i0 = warp; i0 < mine && ok; i0 += kIssueWarps * kIssueLanes) {
+        for (int i = i0; i < min(mine, i0 + kIssueWarps * kIssueLanes) && ok; i += kIssueWarps) {
           int slot;
           uint32_t round;
           place(i, slot, round);
-          if (round == 0 || mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort)) {
-            // (the tail kinds' warps have written to the slot)
-            if (TAIL) fence_proxy_async_smem();
-            mbar_arrive_expect_tx(&sh.full[slot], bytes);
-            bulk_g2s(ring + (size_t)slot * kSlotBytes,
-                     reinterpret_cast<const uint8_t*>(row) + (int64_t)(t0 + i) * kTileBytes - off, bytes, &sh.full[slot]);
-          }
+          if (round > 0) ok = mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        const int i = i0 + lane * kIssueWarps;
+        if (ok && lane < kIssueLanes && i < mine && !edge(i)) {
+          int slot;
+          uint32_t round;
+          place(i, slot, round);
+          // (the tail kinds' warps have written to the slot)
+          if (TAIL) fence_proxy_async_smem();
+          mbar_arrive_expect_tx(&sh.full[slot], bytes);
+          bulk_g2s(ring + (size_t)slot * kSlotBytes,
+                   reinterpret_cast<const uint8_t*>(row) + (int64_t)(t0 + i) * kTileBytes - off, bytes, &sh.full[slot]);
         }
         __syncwarp();
       }
       for (int i = 0; i < mine && ok; ++i) {
-        if (!edge(i)) {
-          if (t0 + i < a.n_tiles - 3) i = max(i, min(mine, a.n_tiles - 2 - t0) - 1);  // on to the last tiles
+        if (!edge(i) || i % kIssueWarps != warp) {
+          if (!edge(i) && t0 + i < a.n_tiles - 3) i = max(i, min(mine, a.n_tiles - 2 - t0) - 1);  // on to the last tiles
           continue;
         }
         int slot;
