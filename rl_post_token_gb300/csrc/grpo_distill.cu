@@ -283,14 +283,18 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 //           joins the row's partials once all have arrived, and sends what pass 2 needs (stats, the
 //           listed tokens' dlogits) to every CTA
 //   4..19   the tiles, dealt to the 16 warps in turn, from row to row on where a row has one for every
-//           warp (38 tiles a row started afresh: 818 us at 8192 x 151936 bf16; so: 811). Pass 1: the tile's partial, sent to the
-//           row's owner. Pass 2: dlogits from the same slot, the listed tokens' over them; then the
-//           slot is free.
+//           warp (each row from warp 4 on: 818 us at 8192 x 151936 bf16, so 811). Pass 1: the tile's
+//           partial, sent to the row's owner. Pass 2: dlogits from the same slot, the listed tokens'
+//           over them; then the slot is free.
 // Everything sent goes by asynchronous stores that an mbarrier of the receiver counts, so nobody waits
-// for a cluster barrier. The list's arithmetic by every CTA of the cluster (no owner) took 1.9x at C = 4,
-// as one list is about 14,000 cycles of latency and a row 6,300 of bandwidth. Pass 1 of a row before
-// pass 2 of the row before it hid the exchange but left no free slots: 8192 x 50257 bf16 499 against
-// 398 us.
+// for a cluster barrier. The list's arithmetic by every CTA of the cluster (no owner) took 1.9x at C = 4:
+// a list is thousands of cycles of latency. Pass 1 of a row before pass 2 of the row before it hides the
+// exchange, but leaves no free slots (8192 x 50257 bf16: 499 against 398 us) or takes more CTAs a row,
+// each with its own waits (8192 x 151936 on 4: 892 against 785).
+//
+// 8192 x 151936 bf16, K = 64: 757 us, 6.6 TB/s, bound by HBM (reads and writes mixed; 735 us at the copy
+// rate). On rows of 25 tiles (50257) the exchange and the two rounds of tiles are longer than the row's
+// share of the bandwidth: 400 us against 243.
 //
 // Barriers: full/empty of the slots; listed[k & 1] (the tokens are in shared memory; the tail kinds,
 // which need them in pass 1); parts (owner, per list warp: the row's partials are in); ready[k & 1] (the
