@@ -3,10 +3,11 @@
 // tail kinds leave the listed tokens out of them and add them singly), the list's arithmetic by one
 // warp, and dlogits over the tiles again.
 //
-// Two kernels with the same bits, chosen by the row length:
-//  * cluster_kernel  rows of 16 to 384 tiles: the row stays in the shared memory of a cluster of 1 to 8
-//                    CTAs between its two readings, so HBM sees one read and one write of it
-//  * row_kernel      shorter and longer rows: one CTA per row, the second reading from L2
+// Two kernels with the same bits, chosen at the end of the file:
+//  * cluster_kernel  the row stays in the shared memory of a cluster of 1 to 8 CTAs between its two
+//                    readings, so HBM sees one read and one write of it
+//  * row_kernel      one CTA per row, the second reading from L2 (or HBM, where the rows at work are
+//                    larger): short and very long rows, and the loss alone of many rows
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -175,9 +176,9 @@ __device__ __forceinline__ void store_cover(T* row, int64_t j, int off, int64_t 
 }
 
 // ------------------------------------------------------------------------------------------
-// Rows outside the cluster kernel's range: one CTA per row.
+// One CTA per row.
 // ------------------------------------------------------------------------------------------
-constexpr int kMaxBlocks = 160;  // softmax partials kept per row
+constexpr int kMaxBlocks = 384;  // softmax partials kept per row: the tiles of the cluster kernel's longest
 
 template <typename T, int KIND, bool ALIGNED, int NT>
 __global__ void __launch_bounds__(NT, NT == 128 ? 8 : 1) row_kernel(Args a) {
@@ -313,7 +314,7 @@ constexpr int kIssueLanes = 4;  // tiles that one of them issues together
 constexpr int kFirstListWarp = kIssueWarps;
 constexpr int kFirstTileWarp = kFirstListWarp + kListWarps;
 constexpr int kClusterThreads = (kFirstTileWarp + kTileWarps) * 32;
-constexpr int kMaxTiles = 384;
+constexpr int kMaxTiles = kMaxBlocks;
 constexpr int kMaxSlots = 56;
 constexpr int kMinTiles = 16;
 
@@ -722,13 +723,19 @@ int launch_cluster(Args a, int C, cudaStream_t st) {
 
 template <typename T, int KIND, bool ALIGNED>
 int launch(Args a, cudaStream_t st) {
+  // The cluster kernel where a row has 16 tiles or more and fits, and dlogits are wanted or the rows are
+  // fewer than the SMs. 8192 rows of bf16, FORWARD_TOPK: 13 tiles, cluster 220 us, row_kernel 224; 17 tiles
+  // 271 and 306; 25 tiles 297 and 480. Their loss alone needs no second reading: 17 tiles 200 and 114, 25 tiles
+  // 235 and 147; but 64 rows of 17 tiles 11 and 16.
+  const int sms = sm_count();
   a.slots = cluster_slots(a.K, a.n_tiles);
-  if (a.n_tiles >= kMinTiles && a.n_tiles <= kMaxTiles && 8 * a.slots >= a.n_tiles)
-    return launch_cluster<T, KIND, ALIGNED>(a, cluster_size(a.T, a.n_tiles, a.slots, sm_count()), st);
+  if (a.n_tiles >= kMinTiles && a.n_tiles <= kMaxTiles && 8 * a.slots >= a.n_tiles && (a.dlogits || 2 * a.T <= sms))
+    return launch_cluster<T, KIND, ALIGNED>(a, cluster_size(a.T, a.n_tiles, a.slots, sms), st);
   a.fold = (a.n_tiles + kMaxBlocks - 1) / kMaxBlocks;
   a.n_blocks = (a.n_tiles + a.fold - 1) / a.fold;
-  // short rows: small blocks, several rows in flight on an SM
-  if (a.n_tiles < kMinTiles) return launch_row_nt<T, KIND, ALIGNED, 128>(a, 8, st);
+  // many rows: small blocks, eight rows in flight on an SM (2048 x 400008 fp32: 1912 us, one large block each
+  // 2589); few: large ones
+  if (a.T > 2 * sms) return launch_row_nt<T, KIND, ALIGNED, 128>(a, 8, st);
   return launch_row_nt<T, KIND, ALIGNED, 512>(a, 1, st);
 }
 

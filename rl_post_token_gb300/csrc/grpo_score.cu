@@ -15,7 +15,8 @@
 //
 // Two kernels, chosen by the number and length of the rows (launch rule at the end of the file):
 //  * stream_kernel  many long rows: one persistent CTA per SM whose 12 streaming warps never stop,
-//                   while 8 others finish (LSE, bound, ranking) the rows before
+//                   while 8 others finish (LSE, bound, ranking) the rows before. 8192 x 151936 bf16,
+//                   K = 64: 386 us, 6.46 TB/s, bound by HBM; K = 256: 586 us, bound by the finishing warps
 //  * row_kernel     few or short rows: one CTA per row, or a cluster that shares its reading
 #include <algorithm>
 #include <atomic>
@@ -868,11 +869,14 @@ int launch_stream(const Args& a, cudaStream_t st) {
 
 template <typename T>
 int dispatch(Args& a, bool aligned, cudaStream_t st) {
-  // Few rows (at most one per SM and a half): row_kernel, a cluster sharing each row's reading, as
-  // many CTAs as the SMs hold at once and as have a block per warp. Short rows (under 16 tiles) and
-  // rows past the streaming kernel's states: row_kernel. All others: stream_kernel.
+  // Up to three rows per SM: row_kernel, with few of them a cluster sharing each row's reading, as many
+  // CTAs as the SMs hold at once and as have a block per warp. Short rows (under 16 tiles) and rows past
+  // the streaming kernel's states: row_kernel. All others: stream_kernel. K = 20, row_kernel and
+  // stream_kernel: 229 x 50264 bf16 13.0 and 15.5 us, 300 x 151936 21.8 and 23.5, 460 x 50264 21.9 and 21.1,
+  // 2048 x 151936 125 and 103, 8192 x 32776 222 and 154. 64 x 151936 fp32 by four CTAs a row 15.6 us, by one
+  // 21.9.
   const int64_t sms = sm_count();
-  if (2 * a.T > 3 * sms && a.fold == 1 && !a.by_vec) {
+  if (a.T > 3 * sms && a.fold == 1 && !a.by_vec) {
     a.slots = kMaxSlots;
     while (a.slots > kMinSlots && stream_smem(a) > max_smem_optin()) --a.slots;
     if (stream_smem(a) <= max_smem_optin())

@@ -34,7 +34,7 @@ def _same(a, b):
 @pytest.mark.parametrize("V, dtype, K, pad, out_pad", [(50257, "bf16", 37, 0, 0), (50257, "bf16", 256, 0, 6),
                                                        (40000, "bf16", 64, 8, 0), (151936, "bf16", 200, 0, 0),
                                                        (60001, "f32", 70, 0, 0), (60001, "f32", 70, 0, 2),
-                                                       (4104, "bf16", 33, 3, 3)])
+                                                       (4104, "bf16", 33, 3, 3), (200003, "f32", 12, 0, 0)])
 def test_distillation_of_many_rows_is_that_of_each(V, dtype, K, pad, out_pad, kind):
     # persistent clusters walk over hundreds of rows, masked and padding rows among them
     T = 420
@@ -66,6 +66,8 @@ def test_distillation_of_many_rows_is_that_of_each(V, dtype, K, pad, out_pad, ki
             assert _same(dz[i], want[i % 30]) and _same(loss[put[i]], wl[i % 30]), i
         else:
             assert not dz[i].any() and (put[i] < 0 or loss[put[i]] == 0), i
+    only, _, _ = D._call(z, ti2, tl2, kind, 1.0, mask=mask, dz=None, tok_src=at, rows=T)
+    assert _same(only, loss)
     live = int((mask[put[keep]] != 0).sum())
     res = _lib.grpo_finish_step(acc, loss, expected_N=live)
     assert res["n_tokens"] == T and res["n_valid"] == live and res["status"] == 0
@@ -74,7 +76,7 @@ def test_distillation_of_many_rows_is_that_of_each(V, dtype, K, pad, out_pad, ki
         assert torch.all(whole[:, V:] == 7)
 
 
-@pytest.mark.parametrize("T", [2, 300])
+@pytest.mark.parametrize("T", [2, 470])
 @pytest.mark.parametrize("V, dtype", [(50257, "bf16"), (36001, "f32"), (9000, "bf16")])
 def test_scores_of_rows_full_of_ties(V, dtype, T):
     # a few hundred equal logits around the K-th place: more candidates than K, ranked by index
@@ -86,7 +88,7 @@ def test_scores_of_rows_full_of_ties(V, dtype, T):
         S._check(z, K, rows=(0, 1, T - 1) if T > 2 else (0, 1))
 
 
-@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("T", [3, 470])
 @pytest.mark.parametrize("V, dtype", [(50257, "bf16"), (36000, "f32")])
 def test_scores_of_masked_vocabularies(V, dtype, T):
     z = S._logits(T, V, dtype, 3.0, 7)
@@ -102,18 +104,18 @@ def test_scores_of_masked_vocabularies(V, dtype, T):
 
 def _work(seed):
     """Inputs of the three calls, and a function that runs them into new outputs."""
-    z = S._logits(310, 50257, "bf16", 3.0, seed)
+    z = S._logits(470, 50257, "bf16", 3.0, seed)
     lg, idx, lq = D._inputs(200, 50257, 40, "bf16", seed + 1)
     ti, tl = torch.from_numpy(idx).to(DEV), torch.from_numpy(lq).to(DEV)
     mask = torch.ones(200, dtype=torch.uint8, device=DEV)
     h, Wt, li, ll, lm = L._inputs(40, 20000, 256, 12, seed + 2)
     li, ll, lm = L._t(li), L._t(ll), L._t(lm)
-    y = torch.arange(310, dtype=torch.int32, device=DEV)
+    y = torch.arange(470, dtype=torch.int32, device=DEV)
     torch.cuda.synchronize()
 
     def outputs():
-        return dict(logp=torch.zeros(310, device=DEV), ent=torch.zeros(310, device=DEV),
-                    top=torch.zeros((310, 30), dtype=torch.int32, device=DEV), lp=torch.zeros((310, 30), device=DEV),
+        return dict(logp=torch.zeros(470, device=DEV), ent=torch.zeros(470, device=DEV),
+                    top=torch.zeros((470, 30), dtype=torch.int32, device=DEV), lp=torch.zeros((470, 30), device=DEV),
                     dz=torch.zeros_like(lg), loss=torch.zeros(200, device=DEV), acc=_lib.new_step_acc(DEV),
                     d_h=torch.zeros((40, 256), device=DEV), dW=torch.zeros((20000, 256), device=DEV),
                     lloss=torch.zeros(40, device=DEV), lacc=_lib.new_step_acc(DEV),
