@@ -291,11 +291,11 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 // for a cluster barrier. The list's arithmetic by every CTA of the cluster (no owner) took 1.9x at C = 4:
 // a list is thousands of cycles of latency. Pass 1 of a row before pass 2 of the row before it hides the
 // exchange, but leaves no free slots (8192 x 50257 bf16: 499 against 398 us) or takes more CTAs a row,
-// each with its own waits (8192 x 151936 on 4: 892 against 785).
+// each with its own waits (8192 x 151936 on 4: 892 against 785, one producer).
 //
-// 8192 x 151936 bf16, K = 64: 757 us, 6.6 TB/s, bound by HBM (reads and writes mixed; 735 us at the copy
+// 8192 x 151936 bf16, K = 64: 748 us, 6.67 TB/s, bound by HBM (reads and writes mixed; 735 us at the copy
 // rate). On rows of 25 tiles (50257) the exchange and the two rounds of tiles are longer than the row's
-// share of the bandwidth: 400 us against 243.
+// share of the bandwidth: 380 us against 243.
 //
 // Barriers: full/empty of the slots; listed[k & 1] (the tokens are in shared memory; the tail kinds,
 // which need them in pass 1); parts (owner, per list warp: the row's partials are in); ready[k & 1] (the
@@ -309,7 +309,7 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 // ------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 16;
 constexpr int kListWarps = 2;  // (3: 4% slower at 152K and 10% at 50K, issue slots)
-constexpr int kIssueWarps = 2;  // producers, each taking every second tile
+constexpr int kIssueWarps = 2;  // producers: the even slots and the odd ones
 constexpr int kIssueLanes = 4;  // tiles that one of them issues together
 constexpr int kFirstListWarp = kIssueWarps;
 constexpr int kFirstTileWarp = kFirstListWarp + kListWarps;
@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
     // the bandwidth for one warp: two take turns, a few lanes issue together, and a batch waits for its own
     // slots alone, so that what is free is filled while the tiles' warps wait for the list (8192 x 151936
     // bf16: one warp, 32 lanes 812 us; two, 16 lanes 806; two, 4 lanes 757). Tiles at a row's ends, which the
-    // whole warp fills up, come after the others.
+    // whole warp fills up, come after the others. A slot belongs to one producer: were it another's turn, a
+    // wait for the slot's last use could take the use before it for it (their parity is the same).
     int slot0 = 0;         // slot of the row's first tile
     uint32_t round0 = 0;   // times the ring had gone round there
     bool ok = true;
@@ -436,47 +437,41 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       const T* row = base + r * a.ld;
       const int off = ALIGNED ? 0 : row_off(row);
       const uint32_t bytes = kTileBytes + (off ? 16u : 0u);
-      auto place = [&](int i, int& slot, uint32_t& round) {
-        slot = slot0 + i;
-        round = round0;
-        if (slot >= S) {
-          slot -= S;
-          ++round;
-        }
-      };
       auto edge = [&](int i) { return (t0 + i == 0 && off) || t0 + i >= a.n_tiles - 2; };
-      for (int i0 = warp; i0 < mine && ok; i0 += kIssueWarps * kIssueLanes) {
-        for (int i = i0; i < min(mine, i0 + kIssueWarps * kIssueLanes) && ok; i += kIssueWarps) {
-          int slot;
-          uint32_t round;
-          place(i, slot, round);
-          if (round > 0) ok = mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort);
+      // the row's tiles up to the ring's end, then those from its start on
+      const int n1 = min(mine, S - slot0);
+#pragma unroll 1
+      for (int part = 0; part < 2 && ok; ++part) {
+        const int lo = part ? n1 : 0, hi = part ? mine : n1;  // tile i is in slot base_slot + i
+        const int base_slot = part ? -n1 : slot0;
+        const uint32_t round = round0 + (part ? 1u : 0u);
+        for (int i0 = lo + ((base_slot + lo + warp) & 1); i0 < hi && ok; i0 += kIssueWarps * kIssueLanes) {
+          if (round > 0)
+            for (int i = i0; i < min(hi, i0 + kIssueWarps * kIssueLanes) && ok; i += kIssueWarps)
+              ok = mbar_wait_bounded(&sh.empty[base_slot + i], (round - 1) & 1u, s_abort);
+          ok = __all_sync(0xffffffffu, ok);
+          const int i = i0 + lane * kIssueWarps;
+          if (ok && lane < kIssueLanes && i < hi && !edge(i)) {
+            const int slot = base_slot + i;
+            // (the tail kinds' warps have written to the slot)
+            if (TAIL) fence_proxy_async_smem();
+            mbar_arrive_expect_tx(&sh.full[slot], bytes);
+            bulk_g2s(ring + (size_t)slot * kSlotBytes,
+                     reinterpret_cast<const uint8_t*>(row) + (int64_t)(t0 + i) * kTileBytes - off, bytes, &sh.full[slot]);
+          }
+          __syncwarp();
         }
-        ok = __all_sync(0xffffffffu, ok);
-        const int i = i0 + lane * kIssueWarps;
-        if (ok && lane < kIssueLanes && i < mine && !edge(i)) {
-          int slot;
-          uint32_t round;
-          place(i, slot, round);
-          // (the tail kinds' warps have written to the slot)
-          if (TAIL) fence_proxy_async_smem();
-          mbar_arrive_expect_tx(&sh.full[slot], bytes);
-          bulk_g2s(ring + (size_t)slot * kSlotBytes,
-                   reinterpret_cast<const uint8_t*>(row) + (int64_t)(t0 + i) * kTileBytes - off, bytes, &sh.full[slot]);
-        }
-        __syncwarp();
       }
+      // (their slots are free: the waits above took in every tile)
       for (int i = 0; i < mine && ok; ++i) {
-        if (!edge(i) || i % kIssueWarps != warp) {
-          if (!edge(i) && t0 + i < a.n_tiles - 3) i = max(i, min(mine, a.n_tiles - 2 - t0) - 1);  // on to the last tiles
+        if (!edge(i)) {
+          if (t0 + i < a.n_tiles - 3) i = max(i, min(mine, a.n_tiles - 2 - t0) - 1);  // on to the last tiles
           continue;
         }
-        int slot;
-        uint32_t round;
-        place(i, slot, round);
-        ok = round == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&sh.empty[slot], (round - 1) & 1u, s_abort));
+        const int slot = i < n1 ? slot0 + i : i - n1;
+        if (slot % kIssueWarps != warp) continue;
         if (TAIL) fence_proxy_async_smem();
-        if (ok) fetch_tile<T>(ring + (size_t)slot * kSlotBytes, row, off, t0 + i, a.n_tiles, V, lane, &sh.full[slot]);
+        fetch_tile<T>(ring + (size_t)slot * kSlotBytes, row, off, t0 + i, a.n_tiles, V, lane, &sh.full[slot]);
       }
       ok = !__any_sync(0xffffffffu, *s_abort);
       slot0 += mine;

@@ -34,7 +34,10 @@ def _same(a, b):
 @pytest.mark.parametrize("V, dtype, K, pad, out_pad", [(50257, "bf16", 37, 0, 0), (50257, "bf16", 256, 0, 6),
                                                        (40000, "bf16", 64, 8, 0), (151936, "bf16", 200, 0, 0),
                                                        (60001, "f32", 70, 0, 0), (60001, "f32", 70, 0, 2),
-                                                       (4104, "bf16", 33, 3, 3), (200003, "f32", 12, 0, 0)])
+                                                       (4104, "bf16", 33, 3, 3), (200003, "f32", 12, 0, 0),
+                                                       # a row takes the whole ring of slots, or all but one or two
+                                                       (106400, "bf16", 32, 0, 0), (108500, "bf16", 32, 0, 0),
+                                                       (110501, "bf16", 32, 0, 0)])
 def test_distillation_of_many_rows_is_that_of_each(V, dtype, K, pad, out_pad, kind):
     # persistent clusters walk over hundreds of rows, masked and padding rows among them
     T = 420
