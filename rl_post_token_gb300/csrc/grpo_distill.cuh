@@ -81,6 +81,7 @@ struct List {
   float q_all;     // FORWARD_TOPK: 1, or 0 without a list; FORWARD_TAIL: Q + q_R
   int n;           // tokens listed
   bool bad;        // a token twice or outside the vocabulary, a NaN or +inf log-prob
+  float z_max;                        // the largest listed logit (NaN if one is)
   float pm, cz, sum, inv, pr, alpha;  // from stats on
   float l2s, loss;                    // from token_loss on (REVERSE_TAIL: from stats)
   bool ok;
@@ -94,6 +95,7 @@ struct List {
     bool b = false;
     n = 0;
     float mx = -INFINITY;
+    z_max = -INFINITY;
     // a token listed twice is found by hashing (all pairs of 256 tokens took longer than their row:
     // 8192 x 151936 bf16, K = 256: 1120 us, so 954)
     const uint32_t places = 2u * (uint32_t)padded;
@@ -125,11 +127,13 @@ struct List {
       b |= tok != -1 && (!in || tlp != tlp || tlp == INFINITY);
       n += __popc(__ballot_sync(0xffffffffu, tok != -1));
       mx = fmaxf(mx, tlp);
+      z_max = max_nan(z_max, z);
       en.tok[k] = tok;
       en.tlp[k] = tlp;
       en.z[k] = z;
     }
     bad = __any_sync(0xffffffffu, b);
+    if (TAIL) z_max = bad ? -INFINITY : warp_max_nan(z_max);  // (a bad list has no tokens)
     __syncwarp();
     log_norm = q_rest = 0.f;
     if constexpr (!TAIL) {  // takes the list up to a constant
@@ -175,12 +179,11 @@ struct List {
     cz = c;
     float S = p.s;
     if constexpr (TAIL) {
-      for (int k = lane; k < padded; k += 32)  // to the largest of all logits
-        if (en.tok[k] != -1) pm = max_nan(pm, en.z[k] * c);
-      pm = warp_max_nan(pm);
+      pm = max_nan(pm, z_max * c);  // to the largest of all logits
       if (p.m != -INFINITY) p.s *= ex2(p.m - pm);
       p.m = pm;
       float se = 0.f;
+#pragma unroll 4
       for (int k = lane; k < padded; k += 32) {
         const float t = fmaf(en.z[k], c, -pm);
         en.z[k] = t;
@@ -215,6 +218,7 @@ struct List {
   // The list's terms of the loss.
   __device__ __forceinline__ void sum_loss() {
     float part = 0.f;
+#pragma unroll 4
     for (int k = lane; k < padded; k += 32) {
       const float lp = (en.z[k] - l2s) * kLn2;
       if (KIND == GRPO_DISTILL_REVERSE_TAIL) {
