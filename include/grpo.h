@@ -400,9 +400,10 @@ GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t
  * loss_tok and acc go to grpo_finish_step as those of the policy loss (no token counts as clipped).
  * A token whose list holds a token twice or outside [0, V), or a NaN or +inf log-prob, or whose row
  * has a NaN or +inf logit or no mass, has loss and gradient NaN; it and a token with an infinite
- * loss (a listed token the student cannot produce; for REVERSE_TAIL one the teacher cannot) count as
- * non-finite. Logits below the float32 range after the scaling have no mass, as in
- * grpo_token_topk_logprobs.
+ * loss (a listed token, or for FORWARD_TAIL a remainder, that has mass with the teacher and none with the
+ * student; for REVERSE_TAIL a listed token the other way round) count as non-finite. Logits below the
+ * float32 range after the scaling have no mass, as in grpo_token_topk_logprobs. Above it the forward kinds
+ * count a token however small its share of the row; REVERSE_TAIL takes shares below 2^-126 as none.
  * Errors: GRPO_ERR_INVALID (sizes, kind, temperature, a non-finite grad_scale, NULL required
  * pointer, alignment, overlap), GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CUDA. */
 #define GRPO_DISTILL_FORWARD_TOPK 0

@@ -41,7 +41,10 @@ def row_loss(z, idx, tlogp, kind, tau=1.0):
     p, lp = e / tot, d - np.log(tot)
     out = np.ones(V, bool)
     out[S] = False
-    pr = float(np.sum(e[out]) / tot)
+    # the mass outside the list, by its logarithm: as a share of the row it may underflow
+    mo = np.max(d[out]) if out.any() else -np.inf
+    lr = mo + np.log(np.sum(np.exp(d[out] - mo))) - np.log(tot) if mo > -np.inf else -np.inf
+    pr = float(np.exp(lr))
     q = np.exp(lq)
     dx = np.zeros(V)
     parts = dict(p=p, lp=lp, pr=pr, m=m, tot=tot, out=out)
@@ -61,16 +64,16 @@ def row_loss(z, idx, tlogp, kind, tau=1.0):
         if kind == FORWARD_TAIL:
             qr = 0.0 if qr < TAIL_MIN or not out.any() else qr
             loss = float(np.sum(np.where(q > 0, q * (lq - lp[S]), 0.0)))
-            loss += qr * np.log(qr / np.float64(pr)) if qr > 0 else 0.0
+            loss += qr * (np.log(qr) - lr) if qr > 0 else 0.0
             mass = q.sum() + qr  # d/dx of -sum q_i log p_i is (sum q) p - q
             alpha = mass - (qr / np.float64(pr) if qr > 0 else 0.0)
-            dx[out] = alpha * p[out]
+            dx[out] = mass * p[out] - (qr * np.exp(lp[out] - lr) if qr > 0 else 0.0)
             dx[S] = mass * p[S] - q
             return loss, dx / tau, dict(parts, q=q, qr=qr, alpha=alpha)
         qr = max(qr, TAIL_MIN)
         tail = pr > 0
         f = np.where(p[S] > 0, lp[S] - lq, 0.0)
-        fr = np.log(pr / qr) if tail else 0.0
+        fr = lr - np.log(qr) if tail else 0.0
         loss = float(np.sum(p[S] * f) + pr * fr)
         dx[out] = p[out] * (fr - loss)
         dx[S] = p[S] * (f - loss)

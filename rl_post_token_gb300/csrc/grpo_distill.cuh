@@ -14,7 +14,12 @@
 //   REVERSE_TAIL  alpha = f_R - L                corr_k = p_k (f_k - L)
 //
 // p_R is summed over the tokens outside S, never formed as 1 - P: a confident student leaves a
-// remainder that 1 - P would round away.
+// remainder that 1 - P would round away. It may even lie below the float32 range as a share of the row
+// (every token outside 88 nats or more below the largest), where q_R log p_R and q_R p_v/p_R are ordinary
+// numbers. So FORWARD_TAIL keeps the sum outside against its own shift m_R = max z c over the tokens
+// outside, s_R = sum 2^(z c - m_R):
+//
+//   log2 p_R = (m_R - m) + log2 s_R - log2 S,   alpha p_v = (Q p_R + q_R p_R - q_R) 2^(z c - m_R) / s_R
 #include "grpo_vocab.cuh"
 
 namespace grpo {
@@ -82,7 +87,9 @@ struct List {
   int n;           // tokens listed
   bool bad;        // a token twice or outside the vocabulary, a NaN or +inf log-prob
   float z_max;                        // the largest listed logit (NaN if one is)
-  float pm, cz, sum, inv, pr, alpha;  // from stats on
+  float pm, cz, sum, inv, pr;         // from stats on
+  float alpha;                        // (FORWARD_TAIL: alpha p_R)
+  float rest_m, rest_s;               // FORWARD_TAIL: the sum outside the list and its shift
   float l2s, loss;                    // from token_loss on (REVERSE_TAIL: from stats)
   bool ok;
 
@@ -173,12 +180,15 @@ struct List {
 
   // The row's part of dlogits from its partial p (the tail kinds': without the listed tokens):
   // dlogits are mult 2^(z c - shift) outside the list. g: the gradient scale. A row without a
-  // distribution or with a bad list has NaN throughout.
+  // distribution or with a bad list has NaN throughout, one that needs a remainder and has none of it
+  // (FORWARD_TAIL, nothing outside with mass) an infinite loss.
   __device__ __forceinline__ void stats(Part p, float c, float g, float& shift, float& mult) {
     pm = p.m;
     cz = c;
     float S = p.s;
     if constexpr (TAIL) {
+      rest_m = p.m;
+      rest_s = p.s;
       pm = max_nan(pm, z_max * c);  // to the largest of all logits
       if (p.m != -INFINITY) p.s *= ex2(p.m - pm);
       p.m = pm;
@@ -198,7 +208,7 @@ struct List {
     if constexpr (KIND == GRPO_DISTILL_FORWARD_TOPK) {
       alpha = q_all;
     } else if constexpr (KIND == GRPO_DISTILL_FORWARD_TAIL) {
-      alpha = q_all - (q_rest > 0.f ? q_rest / pr : 0.f);
+      alpha = rest_m != -INFINITY ? fmaf(q_all, pr, -q_rest) : q_rest > 0.f ? -INFINITY : 0.f;
     } else {
       l2s = log2f(S);
       sum_loss();
@@ -210,6 +220,10 @@ struct List {
     if (!ok) alpha = __int_as_float(0x7fc00000);
     shift = ok ? p.m : 0.f;
     mult = ok ? alpha * g * inv : alpha;
+    if (KIND == GRPO_DISTILL_FORWARD_TAIL && ok && rest_m != -INFINITY) {
+      shift = rest_m;
+      mult = alpha * g / rest_s;
+    }
   }
 
   // The student's probability of entry k.
@@ -239,7 +253,10 @@ struct List {
       if (!TAIL)
         for (int k = lane; k < padded; k += 32) en.z[k] = fmaf(en.z[k], cz, -pm);
       sum_loss();
-      if (KIND == GRPO_DISTILL_FORWARD_TAIL && q_rest > 0.f) loss += q_rest * logf(q_rest / pr);
+      // the quotient where p_R is far from the end of the range: the logarithms of the sums cancel
+      if (KIND == GRPO_DISTILL_FORWARD_TAIL && q_rest > 0.f)
+        loss += q_rest * (pr > 0x1p-100f ? logf(q_rest / pr)
+                                         : logf(q_rest) - ((rest_m - pm) + (log2f(rest_s) - l2s)) * kLn2);
     }
     if (!ok) loss = __int_as_float(0x7fc00000);
     finite = isfinite(loss) && isfinite(alpha * g);
