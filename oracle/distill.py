@@ -60,6 +60,8 @@ def row_loss(z, idx, tlogp, kind, tau=1.0):
             dx = p.copy()
             dx[S] -= q
             return loss, dx / tau, dict(parts, q=q, alpha=1.0)
+        if not len(S):  # no list: nothing to learn (1 log(1/1), the gradient of a constant)
+            return 0.0, dx, dict(parts, q=q, qr=0.0, alpha=0.0, f=q, fr=0.0)
         qr = 1.0 - q.sum()
         if kind == FORWARD_TAIL:
             qr = 0.0 if qr < TAIL_MIN or not out.any() else qr

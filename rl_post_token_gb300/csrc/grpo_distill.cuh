@@ -82,7 +82,7 @@ struct List {
   const int K, padded, lane;  // padded: K rounded up to whole warps
   const int64_t V;
   float log_norm;  // FORWARD_TOPK: log of the list's mass, its log-probs taken from their largest
-  float q_rest;    // q_R (tail kinds), floored as above; 0 where nothing lies outside the list
+  float q_rest;    // q_R (tail kinds), floored as above; FORWARD_TAIL: 0 where the list is all or nothing
   float q_all;     // FORWARD_TOPK: 1, or 0 without a list; FORWARD_TAIL: Q + q_R
   int n;           // tokens listed
   bool bad;        // a token twice or outside the vocabulary, a NaN or +inf log-prob
@@ -171,7 +171,7 @@ struct List {
       }
       const double Q = warp_sum(sum), qr = 1.0 - Q;
       if (KIND == GRPO_DISTILL_FORWARD_TAIL)
-        q_rest = qr < kTailMin || n >= V ? 0.f : (float)qr;
+        q_rest = qr < kTailMin || n >= V || n == 0 ? 0.f : (float)qr;  // (no list: loss and gradient 0)
       else
         q_rest = (float)fmax(qr, kTailMin);
       q_all = (float)(Q + (double)q_rest);
@@ -212,7 +212,7 @@ struct List {
     } else {
       l2s = log2f(S);
       sum_loss();
-      const bool tail = pr > 0.f && n < V;
+      const bool tail = pr > 0.f && n < V && n > 0;
       const float fr = tail ? logf(pr / q_rest) : 0.f;
       if (tail) loss = fmaf(pr, fr, loss);
       alpha = tail ? fr - loss : 0.f;

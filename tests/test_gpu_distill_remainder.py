@@ -1,6 +1,7 @@
-"""FORWARD_TAIL where nearly all of the student's mass is on the listed tokens: the remainder p_R, far
-below the float32 range as a share of the row, still has a finite logarithm, and the tokens outside the
-list still share the gradient -q_R by their shares of p_R.
+"""The remainder of the tail kinds at its ends: rows without a list, and FORWARD_TAIL where nearly all of
+the student's mass is on the listed tokens: the remainder p_R, far below the float32 range as a share of
+the row, still has a finite logarithm, and the tokens outside the list still share the gradient -q_R by
+their shares of p_R.
 
 Tolerances (t, E and dS as in test_gpu_distill: U = 2^-24, dS = 2^-22 + 50 U + 2 U E|t| ln2 of a sum of
 exponentials). Outside the list the kernel forms dlogits = (mass p_R - q_R) g/s 2^t with t taken from the
@@ -118,3 +119,28 @@ def test_tokens_far_below_the_largest_outside_keep_their_gradient():
     assert np.all(np.abs(got + (1 - q) * share) <= 1e-5 * share)
     assert abs(dz.double().sum().item()) <= 924 * 2.0 ** -24
     assert np.isfinite(loss.item())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T, V", [(5, 300), (400, 1000), (300, 5003), (40, 40000), (3, 151936), (400, 36001)])
+def test_rows_without_a_list_have_loss_and_gradient_zero(T, V, dtype):
+    # the remainder is everything: 1 log(1/1) and a gradient of 0, not what s/s rounds to
+    lg, idx, lq = D._inputs(T, V, 7, dtype, V)
+    none = np.arange(T) % 5 != 3
+    idx[none] = -1
+    for kind in D.KINDS:
+        for tau in (1.0, 0.3):
+            loss, dz, acc = D._call(lg, idx, lq, kind, 1.0, temperature=tau)
+            at = torch.from_numpy(none).to(DEV)
+            assert not loss[at].any() and not dz[at].any()
+            assert torch.all(dz[~at].abs().amax(1) > 0)
+            res = _lib.grpo_finish_step(acc, loss, expected_N=T)
+            assert res["n_nonfinite"] == 0 and res["n_valid"] == T
+            only, _, _ = D._call(lg, idx, lq, kind, 1.0, temperature=tau, dz=None)
+            assert torch.equal(only, loss)
+    # such a row is still one that can be bad
+    lg[0, 1] = float("nan")
+    for kind in D.KINDS:
+        loss, dz, acc = D._call(lg, idx, lq, kind, 1.0)
+        assert torch.isnan(loss[0]) and torch.isnan(dz[0]).all()
+        assert _lib.grpo_finish_step(acc, loss)["n_nonfinite"] == 1
