@@ -144,3 +144,29 @@ def test_rows_without_a_list_have_loss_and_gradient_zero(T, V, dtype):
         loss, dz, acc = D._call(lg, idx, lq, kind, 1.0)
         assert torch.isnan(loss[0]) and torch.isnan(dz[0]).all()
         assert _lib.grpo_finish_step(acc, loss)["n_nonfinite"] == 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T, V, K, most", [(400, 4000, 20, 20), (60, 50264, 64, 64), (500, 36001, 256, 200)])
+def test_a_teacher_and_a_student_restricted_to_the_same_tokens(T, V, K, most, dtype):
+    # every allowed token is listed: the teacher's masses sum to 1 up to the rounding of their log-probs,
+    # and the student has nothing outside the list to put a remainder on
+    g = torch.Generator(device=DEV).manual_seed(V)
+    allow = torch.rand((T, V), device=DEV, generator=g).argsort(1) < torch.randint(2, most + 1, (T, 1), generator=g, device=DEV)
+    floor = torch.where(torch.rand((T, 1), generator=g, device=DEV) < 0.5, float("-inf"), torch.finfo(D.DT[dtype]).min)
+    rows = [torch.where(allow, 2 * torch.randn((T, V), generator=g, device=DEV), floor).to(D.DT[dtype]) for _ in range(2)]
+    ti, tl = torch.empty((T, K), dtype=torch.int32, device=DEV), torch.empty((T, K), device=DEV)
+    _lib.grpo_token_topk_logprobs(rows[0], K, top_idx=ti, top_logp=tl)
+    rest = 1.0 - tl.double().exp().sum(1)
+    assert int((rest >= 2.0 ** -24).sum()) > 0 and float(rest.abs().max()) < 2.0 ** -16
+    idx, lq = ti.cpu().numpy(), tl.cpu().numpy()
+    for kind in D.KINDS:
+        loss, dz, acc = D._check(rows[1], idx, lq, kind, scale=1.0 / T, dtype=dtype, rows=range(0, T, 7))
+        res = _lib.grpo_finish_step(acc, loss, expected_N=T, grad_bufs=[dz])
+        assert res["n_nonfinite"] == 0 and res["status"] == 0 and torch.isfinite(dz).all()
+        assert not dz[~allow].any()
+    # a remainder worth the name still has no place to go
+    lq[:, 0] -= 0.01
+    loss, _, acc = D._call(rows[1], idx, lq, _lib.DISTILL_FORWARD_TAIL, 1.0)
+    short = 1.0 - np.exp(lq.astype(np.float64)).sum(1) >= 2.0 ** -15
+    assert short.any() and torch.isinf(loss[torch.from_numpy(short).to(DEV)]).all()
