@@ -421,7 +421,10 @@ def grpo_logprob_loss_fwd_bwd_host(logits_host, target, old_logp, adv_tok, mask,
 def _device_args(logits, *tensors) -> None:
     """Raise unless `logits` and every given tensor, (name, tensor or None, dtype, least element
     count), is on the current CUDA device: a launch goes to the current device, and another
-    device's memory would fault there. 1-D tensors must be contiguous."""
+    device's memory would fault there. The kernels walk per-token tensors and flat outputs by
+    element: those must be contiguous in any number of dimensions (a slice of a [B, S] tensor is
+    not). A count of None leaves extents and strides to the caller (the 2-D tensors with a row
+    stride)."""
     import torch
 
     dev = logits.get_device() if logits.is_cuda else -1
@@ -432,7 +435,7 @@ def _device_args(logits, *tensors) -> None:
             continue
         if t.dtype is not dtype or t.get_device() != dev:
             raise ValueError(f"{name} must be {dtype} on {logits.device}, not {t.dtype} on {t.device}")
-        if t.numel() < n or (t.dim() == 1 and n > 1 and t.stride(0) != 1):
+        if n is not None and (t.numel() < n or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous with at least {n} elements")
 
 
@@ -478,8 +481,8 @@ def grpo_token_topk_logprobs(logits, K: int, target=None, logp_tok=None, entropy
     n = 0 if tok_src is not None else T
     f32, i32 = torch.float32, torch.int32
     _device_args(logits, ("target", target, i32, n), ("mask", mask, torch.uint8, n), ("tok_src", tok_src, torch.int64, T),
-                 ("logp_tok", logp_tok, f32, n), ("entropy_tok", entropy_tok, f32, n), ("top_idx", top_idx, i32, n * K),
-                 ("top_logp", top_logp, f32, n * K))
+                 ("logp_tok", logp_tok, f32, n), ("entropy_tok", entropy_tok, f32, n), ("top_idx", top_idx, i32, None),
+                 ("top_logp", top_logp, f32, None))
     ld_top = K
     if K > 0 and top_idx is not None:
         ld_top = _rows2d(top_idx, "top_idx", K, n)
@@ -515,8 +518,8 @@ def grpo_distill_topk_fwd_bwd(logits, top_idx, top_logp, mask, kind: int, grad_s
     dt = _logits_dtype(logits)
     n = 0 if tok_src is not None else T
     f32, u8 = torch.float32, torch.uint8
-    _device_args(logits, ("top_idx", top_idx, torch.int32, 0), ("top_logp", top_logp, f32, 0), ("mask", mask, u8, n),
-                 ("w_tok", w_tok, f32, n), ("tok_src", tok_src, torch.int64, T), ("dlogits", dlogits, logits.dtype, 0),
+    _device_args(logits, ("top_idx", top_idx, torch.int32, None), ("top_logp", top_logp, f32, None), ("mask", mask, u8, n),
+                 ("w_tok", w_tok, f32, n), ("tok_src", tok_src, torch.int64, T), ("dlogits", dlogits, logits.dtype, None),
                  ("loss_tok", loss_tok, f32, n), ("acc", acc, u8, ACC_BYTES))
     K, ld_top = _teacher_list(top_idx, top_logp, n)
     ld_out = 0 if dlogits is None else _rows2d(dlogits, "dlogits", V, T)
@@ -632,8 +635,8 @@ def grpo_lmhead_distill_topk_fwd_bwd(h, W, top_idx, top_logp, mask, grad_scale: 
     V = W.shape[0]
     f32, bf16 = torch.float32, torch.bfloat16
     u8 = torch.uint8
-    _device_args(h, ("h", h, bf16, 0), ("W", W, bf16, 0), ("top_idx", top_idx, torch.int32, 0),
-                 ("top_logp", top_logp, f32, 0), ("mask", mask, u8, T), ("w_tok", w_tok, f32, T),
+    _device_args(h, ("h", h, bf16, 0), ("W", W, bf16, 0), ("top_idx", top_idx, torch.int32, None),
+                 ("top_logp", top_logp, f32, None), ("mask", mask, u8, T), ("w_tok", w_tok, f32, T),
                  ("d_h", d_h, f32, T * H), ("dW", dW, f32, V * H), ("loss_tok", loss_tok, f32, T),
                  ("acc", acc, u8, ACC_BYTES))
     for name, t in (("d_h", d_h), ("dW", dW), ("workspace", workspace)):
