@@ -767,7 +767,7 @@ extern "C" GRPO_API int grpo_distill_topk_fwd_bwd(const void* logits, int32_t dt
   if (!logits || !top_idx || !top_logp || !mask || !loss_tok) return GRPO_ERR_INVALID;
   const size_t es = dtype == GRPO_DTYPE_F32 ? 4 : 2;
   const uintptr_t in = reinterpret_cast<uintptr_t>(logits), out = reinterpret_cast<uintptr_t>(dlogits);
-  if (in % es || out % es) return GRPO_ERR_INVALID;
+  if (in % es || out % es || reinterpret_cast<uintptr_t>(acc) % alignof(grpo_step_acc)) return GRPO_ERR_INVALID;
   // dlogits is written while other rows of the logits are still to be read
   if (dlogits && in < out + ((T - 1) * ld_out + V) * es && out < in + ((T - 1) * ld + V) * es) return GRPO_ERR_INVALID;
 

@@ -841,7 +841,7 @@ extern "C" GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const vo
   if (arc != GRPO_OK || T == 0) return arc;
   if (flags & ~(uint32_t)(GRPO_LMHEAD_DW_ACCUMULATE | GRPO_LMHEAD_SKIP_MASKED)) return GRPO_ERR_INVALID;
   if (!workspace || ((uintptr_t)workspace & 255u)) return GRPO_ERR_INVALID;
-  if (((uintptr_t)d_h | (uintptr_t)dW) & 15u) return GRPO_ERR_INVALID;
+  if (((uintptr_t)d_h | (uintptr_t)dW) & 15u || (uintptr_t)acc % alignof(grpo_step_acc)) return GRPO_ERR_INVALID;
   const size_t list_smem = (size_t)H * 2;  // a hidden state in shared memory
   if (list_smem > 32 * 1024) return GRPO_ERR_INVALID;
   const DistillLayout dl = distill_layout(T, V, H, K);
