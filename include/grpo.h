@@ -365,11 +365,11 @@ GRPO_API int grpo_logprob_loss_fwd_bwd_host(const void* logits_host, int32_t dty
  *  K         0 <= K <= min(V, GRPO_TOPK_MAX); 0: no alternatives, top_idx and top_logp unused
  *  logp_tok, entropy_tok  device float or NULL
  *  top_idx   device int32, row stride ld_top >= K; top_logp device float, the same stride, or NULL
- * -inf logits (and logits whose z log2(e)/tau lies below the float32 range) have probability 0;
+ * -inf logits (and logits whose z log2(e)/tau lies below the float32 range, -2^127 or so) have probability 0;
  * where fewer than K are left they fill up the list with log-prob -inf. A row with a NaN or +inf
  * logit, or none with mass, has no distribution: float outputs NaN, top_idx -1.
- * Errors: GRPO_ERR_INVALID (sizes, K, a temperature that is not positive and finite, NULL required
- * pointer, logits not aligned to their element), GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CUDA. */
+ * Errors: GRPO_ERR_INVALID (sizes, K, a temperature that is not positive and finite (log2(e)/tau
+ * below 2^126, too), NULL required pointer, logits not aligned to their element), GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CUDA. */
 GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V,
                                       int64_t ld, const int64_t* tok_src, const int32_t* target,
                                       const uint8_t* mask, float temperature, int32_t K,

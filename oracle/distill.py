@@ -17,6 +17,7 @@ from __future__ import annotations
 import numpy as np
 
 from .loss import as_f64
+from .score import range_limit
 
 FORWARD_TOPK, FORWARD_TAIL, REVERSE_TAIL = 0, 1, 2
 TAIL_MIN = 2.0 ** -24
@@ -33,7 +34,7 @@ def row_loss(z, idx, tlogp, kind, tau=1.0):
     bad = (np.any(S < 0) or np.any(S >= V) or len(set(S.tolist())) != len(S) or np.any(np.isnan(lq))
            or np.any(lq == np.inf))
     with np.errstate(invalid="ignore"):
-        z = np.where(z * np.log2(np.e) / float(tau) < -float(np.finfo(np.float32).max), -np.inf, z)
+        z = np.where(z < -range_limit(tau), -np.inf, z)
     m = np.max(z)
     if bad or not np.isfinite(m):
         return np.nan, np.full(V, np.nan), None
@@ -45,7 +46,8 @@ def row_loss(z, idx, tlogp, kind, tau=1.0):
     out[S] = False
     # the mass outside the list, by its logarithm: as a share of the row it may underflow
     mo = np.max(d[out]) if out.any() else -np.inf
-    lr = mo + np.log(np.sum(np.exp(d[out] - mo))) - np.log(tot) if mo > -np.inf else -np.inf
+    w = np.exp(d[out] - mo) if mo > -np.inf else np.zeros(int(out.sum()))
+    lr = mo + np.log(np.sum(w)) - np.log(tot) if mo > -np.inf else -np.inf
     pr = float(np.exp(lr))
     q = np.exp(lq)
     dx = np.zeros(V)
@@ -71,7 +73,7 @@ def row_loss(z, idx, tlogp, kind, tau=1.0):
             loss += qr * (np.log(qr) - lr) if qr > 0 else 0.0
             mass = q.sum() + qr  # d/dx of -sum q_i log p_i is (sum q) p - q
             alpha = mass - (qr / np.float64(pr) if qr > 0 else 0.0)
-            dx[out] = mass * p[out] - (qr * np.exp(lp[out] - lr) if qr > 0 else 0.0)
+            dx[out] = mass * p[out] - (qr * w / np.sum(w) if qr > 0 else 0.0)
             dx[S] = mass * p[S] - q
             return loss, dx / tau, dict(parts, q=q, qr=qr, alpha=alpha)
         qr = max(qr, TAIL_MIN)

@@ -43,7 +43,7 @@ struct Args {
 
 // What the list's warp leaves for the others.
 struct Stats {
-  float shift, mult;  // dlogits = mult 2^(z c - shift) outside the list
+  float shift, mult;  // dlogits = mult 2^(z c - shift) outside the list, c = scale_at(shift)
 };
 
 __device__ __forceinline__ float grad_scale_of(const Args& a, int64_t src) {
@@ -218,8 +218,7 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 8 : 1) row_kernel(Args a) {
         for (int u = 0; u < kTileVecs; ++u)
           x[u] = load_vec<T, ALIGNED>(row, (int64_t)tile * (32 * kTileVecs) + tile_vec(lane, u), V);
         if (TAIL) drop_listed<T>(x, entries.tok, a.K, tile, lane);
-        const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
-        const Part tp = tile_part<T, false>(x, m, a.c);
+        const Part tp = tile_part<T, false>(x, warp_max_nan(tile_lane_max<T>(x)), a.c);
         p = f == 0 ? tp : part_join(p, tp);
       }
       if (lane == 0) {
@@ -244,16 +243,17 @@ __global__ void __launch_bounds__(NT, NT == 128 ? 8 : 1) row_kernel(Args a) {
     __syncthreads();
     if (dz) {
       const Stats st = stats;
+      const float c = scale_at(st.shift, a.c);
       if (ALIGNED || off == row_off(row)) {
         for (int64_t j = tid; j <= nvec; j += NT) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (st.mult != 0.f) v = grad_vec<T>(load_cover<T, ALIGNED>(row, j, off, V), a.c, st);
+          if (st.mult != 0.f) v = grad_vec<T>(load_cover<T, ALIGNED>(row, j, off, V), c, st);
           store_cover(dz, j, off, V, v);
         }
       } else {
         for (int64_t j = tid; j < nvec; j += NT) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (st.mult != 0.f) v = grad_vec<T>(load_vec<T, ALIGNED>(row, j, V), a.c, st);
+          if (st.mult != 0.f) v = grad_vec<T>(load_vec<T, ALIGNED>(row, j, V), c, st);
           store_vec(dz, j * E, V, v);
         }
       }
@@ -561,8 +561,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
         if (TAIL) drop_listed_smem<T>(tile0 + (uint32_t)q.off, sh_tok + (int)(q.k & 3u) * padded, a.K, t0 + i, lane);
         uint4 x[kTileVecs];
         read_tile<T, ALIGNED>(tile0, q.off, lo4, x);
-        const float m = warp_max_nan(tile_lane_max<T>(x)) * a.c;
-        const Part p = tile_part<T, false>(x, m, a.c);
+        const Part p = tile_part<T, false>(x, warp_max_nan(tile_lane_max<T>(x)), a.c);
         if (lane == 0) st_async_v2f32(part + 8u * (uint32_t)i, p.m, p.s, bar);
       }
     };
@@ -571,6 +570,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
       const int buf = (int)(q.k & 1u);
       mbar_wait_bounded(&sh.ready[buf], (q.k >> 1) & 1u, s_abort);
       const Stats st = sh.stats[buf];
+      const float c = scale_at(st.shift, a.c);
       for (int i = q.i0; i < mine; i += kTileWarps) {
         int slot = q.slot0 + i;
         if (slot >= S) slot -= S;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) cluster_kernel(Args a, int
           auto vec = [&](int u, bool shifted) -> uint4 {
             uint4 v = lds128(src + (uint32_t)u * 512u);
             if (shifted) v = shift_vec<T>(v, lds128(src + (uint32_t)u * 512u + 16u), q.off);
-            v = grad_vec<T>(v, a.c, st);
+            v = grad_vec<T>(v, c, st);
             return st.mult != 0.f ? v : make_uint4(0, 0, 0, 0);
           };
           if (ALIGNED || q.off == q.off_out) {
@@ -762,7 +762,7 @@ extern "C" GRPO_API int grpo_distill_topk_fwd_bwd(const void* logits, int32_t dt
   if (dlogits && ld_out < V) return GRPO_ERR_INVALID;
   if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(grad_scale)) return GRPO_ERR_INVALID;
   const float c = (float)(1.4426950408889634 / (double)temperature);
-  if (!std::isfinite(c) || c < 1.1754944e-38f) return GRPO_ERR_INVALID;
+  if (!(c < 0x1p126f) || c < 1.1754944e-38f) return GRPO_ERR_INVALID;  // (its powers of two are float32 numbers)
   if (T == 0) return GRPO_OK;
   if (!logits || !top_idx || !top_logp || !mask || !loss_tok) return GRPO_ERR_INVALID;
   const size_t es = dtype == GRPO_DTYPE_F32 ? 4 : 2;

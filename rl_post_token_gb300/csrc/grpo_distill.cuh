@@ -92,9 +92,10 @@ struct List {
   int n;           // tokens listed
   bool bad;        // a token twice or outside the vocabulary, a NaN or +inf log-prob
   float z_max;                        // the largest listed logit (NaN if one is)
-  float pm, cz, sum, inv, pr;         // from stats on
+  float pm, cz, sum, inv, pr;         // from stats on; cz: the scale that goes with the shift pm
+  float unit;                         // from its t to log2 units
   float alpha;                        // (FORWARD_TAIL: alpha p_R)
-  float rest_m, rest_s;               // FORWARD_TAIL: the sum outside the list and its shift
+  float rest_m, rest_s, rest_gap;     // FORWARD_TAIL: the sum outside the list, its shift, and m_R - m
   float l2s, loss;                    // from token_loss on (REVERSE_TAIL: from stats)
   bool ok;
 
@@ -189,23 +190,25 @@ struct List {
   // (FORWARD_TAIL, nothing outside with mass) an infinite loss.
   __device__ __forceinline__ void stats(Part p, float c, float g, float& shift, float& mult) {
     pm = p.m;
-    cz = c;
     float S = p.s;
     if constexpr (TAIL) {
       rest_m = p.m;
       rest_s = p.s;
-      pm = max_nan(pm, z_max * c);  // to the largest of all logits
+      pm = max_nan(pm, shift_of(z_max, c));  // to the largest of all logits
       if (p.m != -INFINITY) p.s *= ex2(p.m - pm);
       p.m = pm;
+      cz = scale_at(pm, c);
       float se = 0.f;
 #pragma unroll 4
       for (int k = lane; k < padded; k += 32) {
-        const float t = fmaf(en.z[k], c, -pm);
+        const float t = fmaf(en.z[k], cz, -pm);
         en.z[k] = t;
         if (en.tok[k] != -1) se += ex2(t);
       }
       S = p.s + warp_sum(se);
     }
+    if (!TAIL) cz = scale_at(pm, c);
+    unit = unit_at(pm, c);
     ok = !bad && fabsf(p.m) < INFINITY && S > 0.f && S < INFINITY;
     inv = 1.f / S;
     pr = TAIL ? p.s * inv : 0.f;
@@ -229,6 +232,7 @@ struct List {
     if (!ok) alpha = __int_as_float(0x7fc00000);
     shift = ok ? p.m : 0.f;
     mult = ok ? alpha * g * inv : alpha;
+    if (KIND == GRPO_DISTILL_FORWARD_TAIL) rest_gap = is_far(pm) ? (rest_m - pm) * unit : rest_m * unit_at(rest_m, c) - pm;
     if (KIND == GRPO_DISTILL_FORWARD_TAIL && ok && rest_m != -INFINITY) {
       shift = rest_m;
       mult = alpha * g / rest_s;
@@ -243,7 +247,7 @@ struct List {
     float part = 0.f;
 #pragma unroll 4
     for (int k = lane; k < padded; k += 32) {
-      const float lp = (en.z[k] - l2s) * kLn2;
+      const float lp = fmaf(en.z[k], unit, -l2s) * kLn2;
       if (KIND == GRPO_DISTILL_REVERSE_TAIL) {
         const float pk = share(k);
         part += pk > 0.f ? pk * (lp - en.tlp[k]) : 0.f;
@@ -265,7 +269,7 @@ struct List {
       // the quotient where p_R is far from the end of the range: the logarithms of the sums cancel
       if (KIND == GRPO_DISTILL_FORWARD_TAIL && q_rest > 0.f)
         loss += q_rest * (pr > 0x1p-100f ? logf(q_rest / pr)
-                                         : logf(q_rest) - ((rest_m - pm) + (log2f(rest_s) - l2s)) * kLn2);
+                                         : logf(q_rest) - (rest_gap + (log2f(rest_s) - l2s)) * kLn2);
     }
     if (!ok) loss = __int_as_float(0x7fc00000);
     finite = isfinite(loss) && isfinite(alpha * g);
@@ -281,7 +285,7 @@ struct List {
     else if (KIND == GRPO_DISTILL_FORWARD_TAIL)
       corr = fmaf(q_all, pk, -en.q[k]);
     else
-      corr = pk > 0.f ? pk * (((en.z[k] - l2s) * kLn2 - en.tlp[k]) - loss) : 0.f;
+      corr = pk > 0.f ? pk * ((fmaf(en.z[k], unit, -l2s) * kLn2 - en.tlp[k]) - loss) : 0.f;
     return ok ? corr * g : __int_as_float(0x7fc00000);
   }
 };

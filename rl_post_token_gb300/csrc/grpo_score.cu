@@ -96,6 +96,11 @@ __device__ __forceinline__ unsigned long long make_key(float z, uint32_t idx) {
 __device__ __forceinline__ uint32_t key_idx(unsigned long long k) { return ~(uint32_t)k; }
 __device__ __forceinline__ float key_logit(unsigned long long k) { return of_order((uint32_t)(k >> 32)); }
 
+// The log-prob of a logit in a row with shift m and log2 l2 of its sum.
+__device__ __forceinline__ float logp_of(float z, float c, float m, float l2) {
+  return fmaf(fmaf(z, scale_at(m, c), -m), unit_at(m, c), -l2) * kLn2;
+}
+
 // Bucket of a logit in [0, kBuckets): monotone in z.
 __device__ __forceinline__ int bucket_of(float z, float lo, float scale) {
   return min(kBuckets - 1, max(0, __float2int_rd((z - lo) * scale)));
@@ -194,7 +199,7 @@ __device__ __forceinline__ void finish_row(const Args& a, const T* row, int64_t 
       const float l2 = ok ? log2f(r.s) : nan;
       sh.lse_m = r.m;
       sh.lse_l = l2;
-      if (a.logp) a.logp[out] = y_ok && ok ? (fmaf(zy, a.c, -r.m) - l2) * kLn2 : nan;
+      if (a.logp) a.logp[out] = y_ok && ok ? logp_of(zy, a.c, r.m, l2) : nan;
       if (a.entropy) a.entropy[out] = ok ? (l2 - r.q / r.s) * kLn2 : nan;
     }
   }
@@ -356,7 +361,7 @@ __device__ __forceinline__ void finish_row(const Args& a, const T* row, int64_t 
   // ---- rank the candidates and write the K best ----
   auto write = [&](int r, unsigned long long key) {
     a.top_idx[out * a.ld_top + r] = (int32_t)key_idx(key);
-    if (a.top_logp) a.top_logp[out * a.ld_top + r] = (fmaf(key_logit(key), a.c, -m) - l2) * kLn2;
+    if (a.top_logp) a.top_logp[out * a.ld_top + r] = logp_of(key_logit(key), a.c, m, l2);
   };
   if (n <= NT) {  // each against all
     if (tid < n) {
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2) row_kernel(Args a) {
         }
       }
     }
-    const Part tp = tile_part<T, true>(x, warp_max_nan(lm) * a.c, a.c);
+    const Part tp = tile_part<T, true>(x, warp_max_nan(lm), a.c);
     p = f == 0 ? tp : part_join(p, tp);
     if (last) {
       if (!a.by_vec) {
@@ -761,7 +766,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(Args a) {
       const Flight after = fetch(s);
       const float lm = tile_lane_max<T>(x);
       const float hi = warp_max_nan(lm);
-      const Part p = tile_part<T, true>(x, hi * a.c, a.c);
+      const Part p = tile_part<T, true>(x, hi, a.c);
       const float lo = -warp_max_f32(lm > -INFINITY ? -lm : -INFINITY);
       st.gmax[cur.t * 32 + lane] = lm;
       if (lane == 0) {
@@ -903,7 +908,7 @@ extern "C" GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dty
   if (!(temperature > 0.f) || !std::isfinite(temperature)) return GRPO_ERR_INVALID;
   const double cd = 1.4426950408889634 / (double)temperature;
   const float c = (float)cd;
-  if (!std::isfinite(c) || c < 1.1754944e-38f) return GRPO_ERR_INVALID;
+  if (!(c < 0x1p126f) || c < 1.1754944e-38f) return GRPO_ERR_INVALID;  // (its powers of two are float32 numbers)
   if (K > 0 && ld_top < K) return GRPO_ERR_INVALID;
   if (T == 0) return GRPO_OK;
   if (!logits || (logp_tok && !target) || (K > 0 && !top_idx)) return GRPO_ERR_INVALID;

@@ -3,7 +3,8 @@
 //
 // A row of V logits is cut into tiles of 4 KB (2048 bf16 or 1024 float32 logits), one warp's work: 8
 // vectors of 16 bytes a lane. A tile's softmax partial is taken against its own maximum,
-//     m = max z log2(e)/tau,   s = sum 2^t,   q = sum 2^t t,   t = z log2(e)/tau - m,
+//     m = max z log2(e)/tau,   s = sum 2^t,   q = sum 2^t t,   t = z log2(e)/tau - m
+//     (another scale where |m| is past 2^31: shift_of),
 // and the row's from its tiles'. Element -> lane -> tile depends on V alone, so a row's sums are the
 // same bits however many CTAs, and whichever of them, read its tiles and however the row is aligned
 // in memory.
@@ -241,6 +242,26 @@ __device__ __forceinline__ void vec_floats(const uint4& v, float (&f)[16 / sizeo
   }
 }
 
+// The shift of a tile (or row) whose largest logit is z, and the scale that goes with it. z c rounded is
+// off by half its last place, which fma(z, c, -m) leaves in the exponent. That costs nothing below |z c| =
+// 2^31: every t of the tile has the same term, of 64 at most. Above it 2^t would overflow or vanish for
+// z itself (tiles of nothing but a mask of -1e30 made their row NaN). There the scale is the power of two
+// above c, under which nothing is rounded and shifts keep the order of their logits; all other float32
+// logits are 2^7 or more below z under either scale, so that their 2^t are 0 alike.
+constexpr float kFarShift = 2147483648.f;
+
+__device__ __forceinline__ float far_scale(float c) {
+  return __uint_as_float((__float_as_uint(c) + 0x00800000u) & 0x7F800000u);
+}
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFarShift; }
+__device__ __forceinline__ float scale_at(float m, float c) { return is_far(m) ? far_scale(c) : c; }
+__device__ __forceinline__ float shift_of(float z, float c) {
+  const float m = z * c;
+  return is_far(m) ? z * far_scale(c) : m;
+}
+// From t or a difference of shifts under scale_at(m, c) to log2 units.
+__device__ __forceinline__ float unit_at(float m, float c) { return is_far(m) ? c / far_scale(c) : 1.f; }
+
 // A softmax partial: (m, s, q) as above. m = -inf where nothing has mass.
 struct Part {
   float m, s, q;
@@ -298,13 +319,14 @@ __device__ __noinline__ float masked_q(Tile tile, float shift, float c) {
   return (q[0].x + q[1].x) + (q[0].y + q[1].y);
 }
 
-// A tile's partial from its vectors, m its maximum in log2 units, c = log2(e)/tau. The sums run in
-// packed pairs over the lane's vectors, then by a fixed tree over the lanes; every lane gets them. A
-// NaN or +inf in the tile makes s NaN or inf. Logits that c z takes below the float32 range (the type's
-// lowest value as a mask) have no mass, like -inf.
+// A tile's partial from its vectors, z_max its largest logit, c = log2(e)/tau. The sums run in packed
+// pairs over the lane's vectors, then by a fixed tree over the lanes; every lane gets them. A NaN or +inf
+// in the tile makes s NaN or inf. Logits that the scale takes below the float32 range (the type's lowest
+// value as a mask) have no mass, like -inf.
 template <typename T, bool Q>
-__device__ __forceinline__ Part tile_part(const uint4 (&x)[kTileVecs], float m, float c) {
+__device__ __forceinline__ Part tile_part(const uint4 (&x)[kTileVecs], float z_max, float tau_c) {
   constexpr int E = 16 / (int)sizeof(T);
+  const float m = shift_of(z_max, tau_c), c = scale_at(m, tau_c);
   const float shift = m == -INFINITY ? 0.f : m;
   const float2 c2 = make_float2(c, c), m2 = make_float2(-shift, -shift);
   float2 s[2] = {{0.f, 0.f}, {0.f, 0.f}}, q[2] = {{0.f, 0.f}, {0.f, 0.f}};
