@@ -367,9 +367,11 @@ GRPO_API int grpo_logprob_loss_fwd_bwd_host(const void* logits_host, int32_t dty
  *  top_idx   device int32, row stride ld_top >= K; top_logp device float, the same stride, or NULL
  * -inf logits (and logits whose z log2(e)/tau lies below the float32 range, -2^127 or so) have probability 0;
  * where fewer than K are left they fill up the list with log-prob -inf. A row with a NaN or +inf
- * logit, or none with mass, has no distribution: float outputs NaN, top_idx -1.
- * Errors: GRPO_ERR_INVALID (sizes, K, a temperature that is not positive and finite (log2(e)/tau
- * below 2^126, too), NULL required pointer, logits not aligned to their element), GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CUDA. */
+ * logit (or one whose z log2(e)/tau lies above 2^127 or so: the type's largest value at tau = 1), or
+ * none with mass, has no distribution: float outputs NaN, top_idx -1.
+ * Errors: GRPO_ERR_INVALID (sizes, K, a temperature that is not positive and finite or whose log2(e)/tau
+ * is 2^126 or more, NULL required pointer, logits not aligned to their element), GRPO_ERR_UNSUPPORTED
+ * (dtype), GRPO_ERR_CUDA. */
 GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V,
                                       int64_t ld, const int64_t* tok_src, const int32_t* target,
                                       const uint8_t* mask, float temperature, int32_t K,
@@ -401,7 +403,8 @@ GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t
  *            rows are written as zeros, and masked tokens get loss 0
  * loss_tok and acc go to grpo_finish_step as those of the policy loss (no token counts as clipped).
  * A token whose list holds a token twice or outside [0, V), or a NaN or +inf log-prob, or whose row
- * has a NaN or +inf logit or no mass, has loss and gradient NaN; it and a token with an infinite
+ * has a NaN or +inf logit (or one past the float32 range after the scaling, as in
+ * grpo_token_topk_logprobs) or no mass, has loss and gradient NaN; it and a token with an infinite
  * loss (a listed token, or for FORWARD_TAIL a remainder, that has mass with the teacher and none with the
  * student; for REVERSE_TAIL a listed token the other way round) count as non-finite. Logits below the
  * float32 range after the scaling have no mass, as in grpo_token_topk_logprobs. Above it the forward kinds

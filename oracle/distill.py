@@ -36,7 +36,7 @@ def row_loss(z, idx, tlogp, kind, tau=1.0):
     with np.errstate(invalid="ignore"):
         z = np.where(z < -range_limit(tau), -np.inf, z)
     m = np.max(z)
-    if bad or not np.isfinite(m):
+    if bad or not np.isfinite(m) or m > range_limit(tau):
         return np.nan, np.full(V, np.nan), None
     d = (z - m) / float(tau)
     e = np.exp(d)

@@ -7,7 +7,7 @@ Test infrastructure only; see ``oracle/__init__.py``. For a row of logits z and 
 and the alternatives are the K largest logits in descending order, equal ones by ascending index.
 A row with a NaN or +inf logit, or none above -inf, has no distribution: NaN and index -1. A logit
 whose z log2(e)/tau lies below the float32 range (a mask by the type's lowest value; range_limit) has no
-mass, as -inf has none; the order still goes by its value.
+mass, as -inf has none; the order still goes by its value. One above the range counts as +inf.
 """
 from __future__ import annotations
 
@@ -31,7 +31,7 @@ def score_row(z, y, K, tau=1.0):
     with np.errstate(invalid="ignore"):
         z = np.where(z < -range_limit(tau), -np.inf, z)
     m = np.max(z)
-    if not np.isfinite(m):
+    if not np.isfinite(m) or m > range_limit(tau):
         return np.nan, np.nan, np.full(K, -1, np.int64), np.full(K, np.nan)
     d = (z - m) / float(tau)
     e = np.exp(d)
