@@ -93,9 +93,9 @@ struct List {
   bool bad;        // a token twice or outside the vocabulary, a NaN or +inf log-prob
   float z_max;                        // the largest listed logit (NaN if one is)
   float pm, cz, sum, inv, pr;         // from stats on; cz: the scale that goes with the shift pm
-  float unit;                         // from its t to log2 units
+  float unit, tau_c;                  // from its t to log2 units; log2(e)/tau
   float alpha;                        // (FORWARD_TAIL: alpha p_R)
-  float rest_m, rest_s, rest_gap;     // FORWARD_TAIL: the sum outside the list, its shift, and m_R - m
+  float rest_m, rest_s, rest_inv;     // FORWARD_TAIL: the shift of the sum outside the list, the sum and its inverse
   float l2s, loss;                    // from token_loss on (REVERSE_TAIL: from stats)
   bool ok;
 
@@ -190,10 +190,12 @@ struct List {
   // (FORWARD_TAIL, nothing outside with mass) an infinite loss.
   __device__ __forceinline__ void stats(Part p, float c, float g, float& shift, float& mult) {
     pm = p.m;
+    tau_c = c;
     float S = p.s;
     if constexpr (TAIL) {
       rest_m = p.m;
       rest_s = p.s;
+      rest_inv = 1.f / rest_s;
       pm = max_nan(pm, shift_of(z_max, c));  // to the largest of all logits
       if (p.m != -INFINITY) p.s *= ex2(p.m - pm);
       p.m = pm;
@@ -232,10 +234,9 @@ struct List {
     if (!ok) alpha = __int_as_float(0x7fc00000);
     shift = ok ? p.m : 0.f;
     mult = ok ? alpha * g * inv : alpha;
-    if (KIND == GRPO_DISTILL_FORWARD_TAIL) rest_gap = is_far(pm) ? (rest_m - pm) * unit : rest_m * unit_at(rest_m, c) - pm;
     if (KIND == GRPO_DISTILL_FORWARD_TAIL && ok && rest_m != -INFINITY) {
       shift = rest_m;
-      mult = alpha * g / rest_s;
+      mult = alpha * g * rest_inv;
     }
   }
 
@@ -267,9 +268,14 @@ struct List {
         for (int k = lane; k < padded; k += 32) en.z[k] = fmaf(en.z[k], cz, -pm);
       sum_loss();
       // the quotient where p_R is far from the end of the range: the logarithms of the sums cancel
-      if (KIND == GRPO_DISTILL_FORWARD_TAIL && q_rest > 0.f)
-        loss += q_rest * (pr > 0x1p-100f ? logf(q_rest / pr)
-                                         : logf(q_rest) - (rest_gap + (log2f(rest_s) - l2s)) * kLn2);
+      if (KIND == GRPO_DISTILL_FORWARD_TAIL && q_rest > 0.f) {
+        if (pr > 0x1p-100f) {
+          loss += q_rest * logf(q_rest / pr);
+        } else {
+          const float gap = is_far(pm) ? (rest_m - pm) * unit : rest_m * unit_at(rest_m, tau_c) - pm;  // m_R - m
+          loss += q_rest * (logf(q_rest) - (gap + (log2f(rest_s) - l2s)) * kLn2);
+        }
+      }
     }
     if (!ok) loss = __int_as_float(0x7fc00000);
     finite = isfinite(loss) && isfinite(alpha * g);

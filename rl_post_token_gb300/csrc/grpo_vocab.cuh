@@ -259,8 +259,11 @@ __device__ __forceinline__ float shift_of(float z, float c) {
   const float m = z * c;
   return is_far(m) ? z * far_scale(c) : m;
 }
-// From t or a difference of shifts under scale_at(m, c) to log2 units.
-__device__ __forceinline__ float unit_at(float m, float c) { return is_far(m) ? c / far_scale(c) : 1.f; }
+// From t or a difference of shifts under scale_at(m, c) to log2 units: 1, or c over its far scale (c's
+// mantissa in [1/2, 1)).
+__device__ __forceinline__ float unit_at(float m, float c) {
+  return is_far(m) ? __uint_as_float((__float_as_uint(c) & 0x007FFFFFu) | 0x3F000000u) : 1.f;
+}
 
 // A softmax partial: (m, s, q) as above. m = -inf where nothing has mass.
 struct Part {
@@ -326,8 +329,12 @@ __device__ __noinline__ float masked_q(Tile tile, float shift, float c) {
 template <typename T, bool Q>
 __device__ __forceinline__ Part tile_part(const uint4 (&x)[kTileVecs], float z_max, float tau_c) {
   constexpr int E = 16 / (int)sizeof(T);
-  const float m = shift_of(z_max, tau_c), c = scale_at(m, tau_c);
-  const float shift = m == -INFINITY ? 0.f : m;
+  float m = z_max * tau_c, c = tau_c, shift = m;
+  if (is_far(m)) {  // (or -inf)
+    c = far_scale(tau_c);
+    m = z_max * c;
+    shift = m == -INFINITY ? 0.f : m;
+  }
   const float2 c2 = make_float2(c, c), m2 = make_float2(-shift, -shift);
   float2 s[2] = {{0.f, 0.f}, {0.f, 0.f}}, q[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
