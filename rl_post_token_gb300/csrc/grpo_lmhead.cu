@@ -800,11 +800,13 @@ int distill_chunk_tiles(int64_t T) {
 int distill_cta_group(int64_t T, int n_col_tiles) {
   if (getenv("GRPO_LMHEAD_CTA_GROUP")) return cta_group();
   auto rounds = [&](int64_t rows, int64_t slots) { return ((T + rows - 1) / rows * n_col_tiles + slots - 1) / slots; };
-  return rounds(BM, 152) < rounds(2 * BM, 76) ? 1 : 2;
+  const int64_t sms = sm_count();
+  return rounds(BM, sms) < rounds(2 * BM, std::max<int64_t>(sms / 2, 1)) ? 1 : 2;
 }
 
-// Runs that d_h's reduction over a chunk is cut into: as many as fill 152 SMs, each of 16 K blocks or
-// more, and of kMaxChunkTiles vocabulary tiles at most. At 300 tokens, V = 50257, H = 1024 d_h took 255 us
+// Runs that d_h's reduction over a chunk is cut into: as many as fill 152 SMs (a constant: the workspace's
+// size and the order of the sums follow from it), each of 16 K blocks or more, and of kMaxChunkTiles
+// vocabulary tiles at most. At 300 tokens, V = 50257, H = 1024 d_h took 255 us
 // of 491 in one run per chunk of 66 tiles.
 int d_h_split(int64_t T, int64_t H, int chunk_tiles) {
   const int64_t units = ((T + BM - 1) / BM) * ((H + BN - 1) / BN), blocks = (int64_t)chunk_tiles * (BN / BK);
