@@ -357,8 +357,8 @@ GRPO_API int grpo_logprob_loss_fwd_bwd_host(const void* logits_host, int32_t dty
  * in one pass over the logits. A teacher's top_idx / top_logp are what the distillation calls
  * below take.
  *  logits    device [T, ld] GRPO_DTYPE_F32 or _BF16, row-major, V <= ld, any alignment of the rows
- *  tok_src   device int64 [T] or NULL: the index of row t in target, mask and the outputs (a
- *            negative one marks a padding row, which is skipped); NULL means t
+ *  tok_src   device int64 [T] or NULL: the index of row t in target, mask and the outputs, each at
+ *            most once (a negative one marks a padding row, which is skipped); NULL means t
  *  target    device int32, required with logp_tok; outside [0, V): log-prob NaN
  *  mask      device uint8 or NULL (every row counts). A masked row is not read: its log-prob and
  *            entropy are 0, its top_idx -1 and its top_logp -inf
@@ -400,8 +400,9 @@ GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t
  *            list is empty (FORWARD_TOPK: or has no mass) has loss and gradient 0
  *  w_tok     device float per token, indexed like mask, or NULL: a weight on grad_scale (see
  *            grpo_loss_terms); loss_tok stays unweighted
- *  dlogits   device [T, ld_out], same dtype, or NULL (loss only); it must not overlap logits. Masked
- *            rows are written as zeros, and masked tokens get loss 0
+ *  dlogits   device [T, ld_out], same dtype, or NULL (loss only); its memory, from the first row to the
+ *            last, must not overlap that of logits. Masked rows are written as zeros, and masked tokens
+ *            get loss 0
  * loss_tok and acc go to grpo_finish_step as those of the policy loss (no token counts as clipped).
  * A token whose list holds a token twice or outside [0, V), or a NaN or +inf log-prob, or whose row
  * has a NaN or +inf logit (or one past the float32 range after the scaling, as in
@@ -617,7 +618,9 @@ GRPO_API size_t grpo_lmhead_distill_workspace_size(int64_t T, int64_t V, int64_t
  * loss_tok, acc and workspace rules hold (workspace: grpo_lmhead_distill_workspace_size(T, V, H, K)
  * bytes); H at most 16384. top_idx, top_logp, ld_top, K, w_tok as in grpo_distill_topk_fwd_bwd.
  * The logits of the listed tokens are formed once more as float32 dot products of h and W's rows.
- * The order of d_h's sums depends on T, V and H.
+ * dlogits go into the products with W and h as bf16, as in the loss; d_h and dW are float32 sums, the
+ * order of d_h's depending on T, V and H. For a list scored at another temperature pass h / tau: dW is
+ * then the gradient, and d_h / tau.
  * The tail kinds have no LM-head form: the student's mass outside the list would have to be formed
  * as a difference. A token whose |LSE| is above 4096 counts as non-finite.
  * Errors: those of grpo_lmhead_loss_fwd_bwd, and GRPO_ERR_INVALID for a bad K, ld_top, H or

@@ -293,9 +293,10 @@ int launch_row_nt(const Args& a, int per_sm, cudaStream_t st) {
 // exchange, but leaves no free slots (8192 x 50257 bf16: 499 against 398 us) or takes more CTAs a row,
 // each with its own waits (8192 x 151936 on 4: 892 against 785, one producer).
 //
-// 8192 x 151936 bf16, K = 64: 748 us, 6.67 TB/s, bound by HBM (reads and writes mixed; 735 us at the copy
-// rate). On rows of 25 tiles (50257) the exchange and the two rounds of tiles are longer than the row's
-// share of the bandwidth: 380 us against 243.
+// 8192 x 151936 bf16, K = 64: 752 us, 6.63 TB/s, bound by HBM (reads and writes mixed; 735 us at the copy
+// rate); FORWARD_TAIL 824, REVERSE_TAIL 856. On rows of 25 tiles the exchange and the two rounds of tiles are
+// longer than the row's share of the bandwidth, 243 us: 50264 columns, K = 37, 290 us (330 and 342); 50257,
+// whose tiles are shifted as they are read and whose rows' ends are filled in, 391 (406 and 419).
 //
 // Barriers: full/empty of the slots; listed[k & 1] (the tokens are in shared memory; the tail kinds,
 // which need them in pass 1); parts (owner, per list warp: the row's partials are in); ready[k & 1] (the
@@ -719,9 +720,9 @@ int launch_cluster(Args a, int C, cudaStream_t st) {
 template <typename T, int KIND, bool ALIGNED>
 int launch(Args a, cudaStream_t st) {
   // The cluster kernel where a row has 16 tiles or more and fits, and dlogits are wanted or the rows are
-  // fewer than the SMs. 8192 rows of bf16, FORWARD_TOPK: 13 tiles, cluster 220 us, row_kernel 224; 17 tiles
-  // 271 and 306; 25 tiles 297 and 480. Their loss alone needs no second reading: 17 tiles 200 and 114, 25 tiles
-  // 235 and 147; but 64 rows of 17 tiles 11 and 16.
+  // fewer than the SMs. 8192 rows of bf16, FORWARD_TOPK, K = 64: 13 tiles, cluster 226 us, row_kernel 247
+  // (K = 37: 220 and 224); 17 tiles 278 and 327; 25 tiles 291 and 483. Their loss alone needs no second
+  // reading: 17 tiles 180 and 119, 25 tiles 210 and 154; 64 rows of 17 tiles 10 to 12 either way.
   const int sms = sm_count();
   a.slots = cluster_slots(a.K, a.n_tiles);
   if (a.n_tiles >= kMinTiles && a.n_tiles <= kMaxTiles && 8 * a.slots >= a.n_tiles && (a.dlogits || 2 * a.T <= sms))
@@ -768,7 +769,8 @@ extern "C" GRPO_API int grpo_distill_topk_fwd_bwd(const void* logits, int32_t dt
   const size_t es = dtype == GRPO_DTYPE_F32 ? 4 : 2;
   const uintptr_t in = reinterpret_cast<uintptr_t>(logits), out = reinterpret_cast<uintptr_t>(dlogits);
   if (in % es || out % es || reinterpret_cast<uintptr_t>(acc) % alignof(grpo_step_acc)) return GRPO_ERR_INVALID;
-  // dlogits is written while other rows of the logits are still to be read
+  // dlogits is written while other rows of the logits are still to be read; the logits' own buffer would not be
+  // (each row is read before it is written), but row_kernel reads by the non-coherent path what it writes
   if (dlogits && in < out + ((T - 1) * ld_out + V) * es && out < in + ((T - 1) * ld + V) * es) return GRPO_ERR_INVALID;
 
   distill::Args a{};

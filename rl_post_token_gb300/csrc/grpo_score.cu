@@ -16,7 +16,9 @@
 // Two kernels, chosen by the number and length of the rows (launch rule at the end of the file):
 //  * stream_kernel  many long rows: one persistent CTA per SM whose 12 streaming warps never stop,
 //                   while 8 others finish (LSE, bound, ranking) the rows before. 8192 x 151936 bf16,
-//                   K = 64: 386 us, 6.46 TB/s, bound by HBM; K = 256: 586 us, bound by the finishing warps
+//                   K = 64: 390 us, 6.39 TB/s, bound by HBM; K = 256: 600 us, and shorter rows (50264: 148 us
+//                   at K = 0, 187 at 20, 200 at 37), by the finishing warps: about 8 us a row and group,
+//                   against 2.4 us of reading at 50264
 //  * row_kernel     few or short rows: one CTA per row, or a cluster that shares its reading
 #include <algorithm>
 #include <atomic>
@@ -589,10 +591,10 @@ int launch_row(const Args& a, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------------
-// Many long rows: a persistent CTA per SM. Warps 0..11 stream: the blocks (two tiles) of the CTA's
-// rows, in row order, go round-robin over them; each warp fetches its next block with bulk copies
-// while it reduces this one (rows that are not 16-byte aligned: into registers, one tile ahead). A
-// row's results go to one of a.slots row states. Every streaming warp passes every row, also where
+// Many long rows: a persistent CTA per SM. Warps 0..11 stream: the tiles of the CTA's rows, in row
+// order, go round-robin over them (a block is one tile here). Each warp has two slots of shared memory:
+// bulk copies fetch its next two tiles while it reduces this one; the tiles of a row that is not 16-byte
+// aligned are shifted as they are read from their slot. A row's results go to one of a.slots row states. Every streaming warp passes every row, also where
 // none of the tiles is its own: before it enters a row it waits until the row's state was handed back
 // (mbarrier freed), and it arrives on the state's other mbarrier (done) when it leaves it. So rows
 // are done in order, and both barriers' phases follow the rows one by one: a phase bit is never a
@@ -608,7 +610,7 @@ constexpr int kMinSlots = 3, kMaxSlots = 8;
 static_assert(kFinishGroups <= kMinSlots, "the phases' order");
 struct StreamShared {
   Finish<kFinishThreads> fin[kFinishGroups];
-  uint64_t full[kStreamWarps][2];  // the copy of a tile of the block has landed
+  uint64_t full[kStreamWarps][2];  // the tile in the slot has landed
   uint64_t done[kMaxSlots];        // every streaming warp has left the row
   uint64_t freed[kMaxSlots];       // the row state may be rewritten
   int abort;
@@ -877,8 +879,8 @@ int dispatch(Args& a, bool aligned, cudaStream_t st) {
   // Up to three rows per SM: row_kernel, with few of them a cluster sharing each row's reading, as many
   // CTAs as the SMs hold at once and as have a block per warp. Short rows (under 16 tiles) and rows past
   // the streaming kernel's states: row_kernel. All others: stream_kernel. K = 20, row_kernel and
-  // stream_kernel: 229 x 50264 bf16 13.0 and 15.5 us, 300 x 151936 21.8 and 23.5, 460 x 50264 21.9 and 21.1,
-  // 2048 x 151936 125 and 103, 8192 x 32776 222 and 154. 64 x 151936 fp32 by four CTAs a row 15.6 us, by one
+  // stream_kernel: 229 x 50264 bf16 12.4 and 14.4 us, 300 x 151936 21.0 and 22.8, 460 x 50264 22.4 and 20.6,
+  // 2048 x 151936 128 and 106, 8192 x 32776 228 and 165. 64 x 151936 fp32 by four CTAs a row 15.6 us, by one
   // 21.9.
   const int64_t sms = sm_count();
   if (a.T > 3 * sms && a.fold == 1 && !a.by_vec) {
