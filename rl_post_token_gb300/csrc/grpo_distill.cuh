@@ -273,7 +273,9 @@ struct List {
         if (pr > 0x1p-100f) {
           loss += q_rest * logf(q_rest / pr);
         } else {
-          const float gap = is_far(pm) ? (rest_m - pm) * unit : rest_m * unit_at(rest_m, tau_c) - pm;  // m_R - m
+          // m_R - m, exact where both have the far scale
+          const float gap =
+              is_far(pm) && is_far(rest_m) ? (rest_m - pm) * unit : rest_m * unit_at(rest_m, tau_c) - pm * unit;
           loss += q_rest * (logf(q_rest) - (gap + (log2f(rest_s) - l2s)) * kLn2);
         }
       }

@@ -128,3 +128,19 @@ def test_temperatures_next_to_zero(T, V, tau, dtype):
         ties = (z[r] == z[r].max()).sum().item()
         assert abs(o["logp_tok"][r].item() + np.log(ties)) <= 1e-5 and abs(o["entropy_tok"][r].item() - H) <= 1e-5
         _far_top(o, r, zh[r], tau, 4)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T, V", [(8, 900), (8, 40001), (330, 36008)])
+@pytest.mark.parametrize("tau, top", [(1e-6, 29952.0), (1e-6, 600.0), (1e-3, 1e7), (1.0, 1e10), (1e-8, 40.0)])
+def test_a_listed_token_far_above_a_row_of_ordinary_ones(T, V, tau, top, dtype):
+    # the shifts of the row and of the tokens outside the list are under different scales
+    z, idx, lq = D._inputs(T, V, 7, dtype, V, unused=0.0)
+    for r in range(T):
+        z[r, int(idx[r, r % 7])] = top
+    lq -= 0.1
+    loss, dz, acc = D._call(z, idx, lq, _lib.DISTILL_FORWARD_TAIL, 0.5, temperature=tau)
+    assert int(acc[16:24].view(torch.int64)[0]) == 0
+    zh = W.logits_to_host(z[:8])
+    for r in range(8):
+        R._check_row(loss[r].item(), dz[r].double().cpu().numpy(), zh[r], idx[r], lq[r], tau, 0.5, dtype)
