@@ -389,10 +389,10 @@ GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t
  *   dlogits_t = grad_scale w_t m_t dL/dz (the 1/tau of dL/dz included, no tau^2 factor)
  * The tail kinds treat every other token as one; where the list holds the whole vocabulary there
  * is no such term. A q_R below 2^-24 (what float32 log-probs cannot resolve) counts as 0 in
- * FORWARD_TAIL and as 2^-24 in REVERSE_TAIL's logarithm. Where the student's p_R is below 2^-126 (unlisted
- * tokens masked), one below 2^-16 (what the errors of a whole list's log-probs add up to) counts as 0 in
- * FORWARD_TAIL, so that a teacher and a student restricted to the same tokens, all of them listed, have the
- * loss of these tokens, whatever the mask.
+ * FORWARD_TAIL and as 2^-24 in REVERSE_TAIL's logarithm. Where every unlisted token is more than 2^126 times
+ * less probable than the student's most probable (masked), a q_R below 2^-16 (what the errors of a whole
+ * list's log-probs add up to) counts as 0 in FORWARD_TAIL, so that a teacher and a student restricted to the
+ * same tokens, all of them listed, have the loss of these tokens, whatever the mask.
  *  logits    device [T, ld], dtype, tok_src, mask, loss_tok, acc: as grpo_logprob_loss_fwd_bwd (the
  *            rows may start at any multiple of their element)
  *  top_idx, top_logp  device int32 / float, row t's list at t (or tok_src[t]) * ld_top; entries with

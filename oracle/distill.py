@@ -9,8 +9,8 @@ tokens, Q = sum_S q, q_R = 1 - Q and p_R = sum of p outside S:
     REVERSE_TAIL  L = sum_S p log(p/q) + p_R log(p_R/q_R)
 
 with 0 log 0 = 0, no remainder term where S is the whole row or empty (loss and gradient 0), and a q_R
-below 2^-24 counted as 0 (FORWARD_TAIL; below 2^-16 where p_R < 2^-126) or as 2^-24 (REVERSE_TAIL). The gradient
-is dL/dz.
+below 2^-24 counted as 0 (FORWARD_TAIL; below 2^-16 where every token outside S is 2^126 times less probable than
+the row's most probable) or as 2^-24 (REVERSE_TAIL). The gradient is dL/dz.
 """
 from __future__ import annotations
 
@@ -22,7 +22,6 @@ from .score import range_limit
 FORWARD_TOPK, FORWARD_TAIL, REVERSE_TAIL = 0, 1, 2
 TAIL_MIN = 2.0 ** -24
 TAIL_NONE = 2.0 ** -16
-P_MIN = 2.0 ** -126
 
 
 def row_loss(z, idx, tlogp, kind, tau=1.0):
@@ -69,7 +68,7 @@ def row_loss(z, idx, tlogp, kind, tau=1.0):
             return 0.0, dx, dict(parts, q=q, qr=0.0, alpha=0.0, f=q, fr=0.0)
         qr = 1.0 - q.sum()
         if kind == FORWARD_TAIL:
-            qr = 0.0 if qr < (TAIL_MIN if lr >= np.log(P_MIN) else TAIL_NONE) or not out.any() else qr
+            qr = 0.0 if qr < (TAIL_MIN if mo >= -126 * np.log(2) else TAIL_NONE) or not out.any() else qr
             loss = float(np.sum(np.where(q > 0, q * (lq - lp[S]), 0.0)))
             loss += qr * (np.log(qr) - lr) if qr > 0 else 0.0
             mass = q.sum() + qr  # d/dx of -sum q_i log p_i is (sum q) p - q

@@ -31,8 +31,9 @@ constexpr double kTailMin = 5.9604644775390625e-08;
 // Where the student has no mass outside the list, a remainder makes the loss infinite, or as large as a finite
 // mask. A teacher that has none either (both rows restricted to the same few tokens) lists log-probs whose
 // masses sum to 1 only up to their errors: sum q |d log q| <= 2^-22 + 39 2^-24 of the scoring call's row sum,
-// 2 log2(V) 2^-24 ln2 and 2^-23 (|log q| + |z - max|/tau) on average, 6e-6 in all. So where p_R is below
-// 2^-126, FORWARD_TAIL counts a remainder below 2^-16 as none.
+// 2 log2(V) 2^-24 ln2 and 2^-23 (|log q| + |z - max|/tau) on average, 6e-6 in all. So where every token
+// outside is 2^126 times less probable than the row's most probable, FORWARD_TAIL counts a remainder below
+// 2^-16 as none.
 constexpr float kTailNone = 1.52587890625e-05f;
 
 template <typename F>
@@ -219,7 +220,7 @@ struct List {
     if constexpr (KIND == GRPO_DISTILL_FORWARD_TOPK) {
       alpha = q_all;
     } else if constexpr (KIND == GRPO_DISTILL_FORWARD_TAIL) {
-      if (pr < 0x1p-126f && q_rest < kTailNone) {
+      if (rest_m - pm < -126.f && q_rest < kTailNone) {
         q_all -= q_rest;
         q_rest = 0.f;
       }

@@ -174,3 +174,23 @@ def test_a_teacher_and_a_student_restricted_to_the_same_tokens(T, V, K, most, dt
     away = (floor[:, 0] < -3e38).cpu().numpy()
     assert torch.isinf(loss[torch.from_numpy(short & away).to(DEV)]).all() and (short & away).any()
     assert torch.isfinite(loss[torch.from_numpy(~away).to(DEV)]).all()
+
+
+@pytest.mark.parametrize("gap, none", [(80.0, False), (87.0, False), (88.0, True), (100.0, True)])
+def test_many_tokens_just_past_the_limit_of_the_float32_range(gap, none):
+    # 100,000 tokens hold e^11 times the share of one: what counts is how far each of them lies below the
+    # largest (126 ln 2 = 87.34), in the oracle and in the kernel
+    V, K = 100000, 8
+    z = torch.full((6, V), -gap, device=DEV)
+    idx = np.tile(np.arange(K, dtype=np.int32), (6, 1))
+    z[:, :K] = torch.linspace(0, -2, K, device=DEV)
+    q = np.full(K, 1 / K)
+    lq = np.log(np.stack([q * (1 - r) for r in (0.3, 1e-3, 2e-5, 1e-5, 2e-6, 0.0)])).astype(np.float32)
+    loss, dz, _ = D._call(z, idx, lq, _lib.DISTILL_FORWARD_TAIL, 1.0)
+    zh = W.logits_to_host(z)
+    for r in range(6):
+        _check_row(loss[r].item(), dz[r].double().cpu().numpy(), zh[r], idx[r], lq[r], 1.0, 1.0, "f32")
+        # the gradient outside sums to -q_R where it counts (p_R itself is below 2^-100)
+        counts = r < 3 or not none
+        qr = 1.0 - np.exp(lq[r].astype(np.float64)).sum()
+        assert r == 5 or abs(dz[r, K:].double().sum().item() + (qr if counts else 0.0)) <= 1e-5 * qr
