@@ -618,7 +618,8 @@ GRPO_API size_t grpo_lmhead_distill_workspace_size(int64_t T, int64_t V, int64_t
  * formed tile by tile and never stored, as in grpo_lmhead_loss_fwd_bwd, whose h, W, d_h, dW, flags,
  * loss_tok, acc and workspace rules hold (workspace: grpo_lmhead_distill_workspace_size(T, V, H, K)
  * bytes); H at most 16384. top_idx, top_logp, ld_top, K, w_tok as in grpo_distill_topk_fwd_bwd.
- * The logits of the listed tokens are formed once more as float32 dot products of h and W's rows.
+ * The logits of the listed tokens are formed once more as float32 dot products of h and W's rows (other
+ * sums than the GEMM's: a log-prob is right to 1e-6 of the row's largest |logit|, not better near 0).
  * dlogits go into the products with W and h as bf16, as in the loss; d_h and dW are float32 sums, the
  * order of d_h's depending on T, V and H. For a list scored at another temperature pass h / tau: dW is
  * then the gradient, and d_h / tau.
