@@ -243,9 +243,9 @@ __device__ __forceinline__ void vec_floats(const uint4& v, float (&f)[16 / sizeo
 }
 
 // The shift of a tile (or row) whose largest logit is z, and the scale that goes with it. z c rounded is
-// off by half its last place, which fma(z, c, -m) leaves in the exponent. That costs nothing below |z c| =
-// 2^31: every t of the tile has the same term, of 64 at most. Above it 2^t would overflow or vanish for
-// z itself (tiles of nothing but a mask of -1e30 made their row NaN). There the scale is the power of two
+// off by half its last place, which fma(z, c, -m) leaves in the exponent. That costs only range below
+// |z c| = 2^31: every t of the tile has the same term, of 64 at most. Above it 2^t would overflow or vanish
+// for z itself (tiles of nothing but a mask of -1e30 made their row NaN). There the scale is the power of two
 // above c, under which nothing is rounded and shifts keep the order of their logits; all other float32
 // logits are 2^7 or more below z under either scale, so that their 2^t are 0 alike.
 constexpr float kFarShift = 2147483648.f;
