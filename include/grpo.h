@@ -411,7 +411,7 @@ GRPO_API int grpo_token_topk_logprobs(const void* logits, int32_t dtype, int64_t
  * student; for REVERSE_TAIL a listed token the other way round) count as non-finite. Logits below the
  * float32 range after the scaling have no mass, as in grpo_token_topk_logprobs. Above it the forward kinds
  * count a token however small its share of the row; REVERSE_TAIL takes one more than 2^126 times less
- * probable than the row's most probable as having none.
+ * probable than the row's most probable (2^62, where |z log2(e)/tau| comes near 2^31) as having none.
  * Errors: GRPO_ERR_INVALID (sizes, kind, temperature, a non-finite grad_scale, NULL required
  * pointer, alignment, overlap), GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CUDA. */
 #define GRPO_DISTILL_FORWARD_TOPK 0
