@@ -464,6 +464,58 @@ GRPO_API int grpo_finish_step_ex(grpo_step_acc* acc, const float* loss_tok, int6
                                  const int64_t* grad_numels, const int32_t* grad_dtypes,
                                  int32_t n_bufs, grpo_step_result* result_host, void* stream);
 
+/* ---- gradient norm and clipping ------------------------------------------------------------- */
+
+/* Between a step's finish and the optimizer ("Sizing mini-batches and micro-batches", "The hard part:
+ * deferred normalization": scale, then clip, then step). The result stays on the device: an optimizer
+ * multiplies by `coef` itself, or grpo_grad_clip does. */
+typedef struct grpo_grad_norm_result {
+  double  sum_sq;    /* sum of the squares of every element, before the scale s (data-parallel ranks with
+                        a part of the gradients each add theirs) */
+  float   norm;      /* s sqrt(sum_sq), inf past float32's range (coef is formed in float64) */
+  float   coef;      /* s min(1, max_norm / norm); 0 when the step is skipped */
+  int32_t status;    /* GRPO_OK; GRPO_STEP_SKIPPED_NONFINITE: sum_sq is not finite; else acc's status */
+  int32_t reserved0;
+  int64_t reserved1;
+} grpo_grad_norm_result;
+
+/* Bytes of device workspace grpo_grad_norm needs for n tensors of total_numel elements together (256 and 8
+ * per chunk of 8192 elements or more: 0.4 MB at most for up to 32768 tensors). 0 on bad sizes. */
+GRPO_API size_t grpo_grad_norm_workspace_size(int64_t total_numel, int32_t n);
+
+/* The norm over all elements of n gradient tensors, each tensor's own norm, and the clip's factor.
+ *  grads      host array of n device pointers, aligned to their element; numels host int64 [n] (0 is
+ *             allowed); dtypes host int32 [n] GRPO_DTYPE_* (they may differ). A tensor listed twice counts
+ *             twice
+ *  max_norm   >= 0; INFINITY: no clip (coef = s)
+ *  acc        device grpo_step_acc of the finished step, or NULL. When its result's status is not GRPO_OK
+ *             the step is skipped: that status, coef 0
+ *  deferred   != 0 (acc required): the gradients are sums that the finish has not scaled: s =
+ *             1/max(acc->divisor, 1); else s = 1
+ *  tensor_norms  device float [n] or NULL: s times each tensor's norm
+ *  result     device grpo_grad_norm_result, written whole
+ *  workspace  device, 8-byte aligned
+ * Squares are summed in float32 within a thread's run of up to 16, in float64 beyond, and in float64
+ * throughout where float32's range does not hold them (any float32 gradient has a finite sum). The result
+ * depends on the values and sizes alone. Host arrays may be freed when the call returns; a captured call
+ * keeps the pointers. n = 0: norm 0, coef s.
+ * Errors: GRPO_ERR_INVALID (sizes, NULL, alignment, a negative or NaN max_norm, deferred without acc),
+ * GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CAPACITY (workspace too small), GRPO_ERR_CUDA. */
+GRPO_API int grpo_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n,
+                            float max_norm, const grpo_step_acc* acc, int32_t deferred, float* tensor_norms,
+                            grpo_grad_norm_result* result, void* workspace, size_t workspace_bytes, void* stream);
+
+/* dst_i = coef src_i for n tensors, rounded once to dst's type; zeros where the step is skipped (src is
+ * then not read). dst_i may be src_i with the same dtype (in place: a coef of 1 writes nothing); otherwise
+ * no tensor that is written may overlap any other of the call.
+ *  src, dst   host arrays of n device pointers; src_dtypes, dst_dtypes, numels host arrays, as above
+ *  result     device, from grpo_grad_norm earlier on this stream (or filled by the caller)
+ * Errors: GRPO_ERR_INVALID (sizes, NULL, alignment, overlap), GRPO_ERR_UNSUPPORTED (dtype),
+ * GRPO_ERR_CAPACITY (host memory), GRPO_ERR_CUDA. */
+GRPO_API int grpo_grad_clip(const void* const* src, const int32_t* src_dtypes, void* const* dst,
+                            const int32_t* dst_dtypes, const int64_t* numels, int32_t n,
+                            const grpo_grad_norm_result* result, void* stream);
+
 /* ---- accumulation window (host) ----------------------------------------------------------- */
 
 /* The trainer's view of one optimizer step fed chunk by chunk ("Sizing mini-batches and
@@ -634,6 +686,54 @@ GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const void* W, int6
                                               float* dW, uint32_t flags, float* loss_tok,
                                               grpo_step_acc* acc, void* workspace,
                                               size_t workspace_bytes, void* stream);
+
+/* Softmax cross entropy from hidden states, for the supervised steps beside the policy's (warm-up and
+ * rejection fine-tuning, a pre-training mix, evaluation): loss, d_h and dW in one call. Per token, with
+ * x = h W^T, z = x (soft_cap 0) or soft_cap tanh(x / soft_cap), lse = log sum_v e^z_v, y the target:
+ *   L = (1 - eps) (lse - z_y) + eps (lse - mean_v z_v) + lambda lse^2
+ *   dL/dz_v = (1 + 2 lambda lse) p_v - (1 - eps) [v = y] - eps / V,  dL/dx = dL/dz (1 - (z / soft_cap)^2)
+ *   d_h_t = grad_scale w_t m_t dL/dx W,  dW = sum_t grad_scale w_t m_t dL/dx_t h_t
+ * x is formed tile by tile over pieces of the vocabulary and never stored, as in
+ * grpo_lmhead_loss_fwd_bwd; the masked tokens cost no product (their hidden states are not read and may
+ * hold anything). */
+typedef struct grpo_ce_terms {
+  float label_smoothing;  /* eps in [0, 1]: the share of the uniform distribution in the target */
+  float z_loss;           /* lambda >= 0, finite */
+  float soft_cap;         /* in [1e-6, 1e6], or 0: none */
+  const float* w_tok;     /* device float [T] or NULL: a weight on grad_scale (see grpo_loss_terms);
+                             loss_tok stays unweighted */
+} grpo_ce_terms;
+
+/* Bytes of device workspace grpo_lmhead_ce_fwd_bwd needs. 0 on bad sizes. */
+GRPO_API size_t grpo_lmhead_ce_workspace_size(int64_t T, int64_t V, int64_t H);
+
+/*  h, W       device bf16 [T, H], [V, H] row-major, 16-byte aligned; H a multiple of 8
+ *  target     device int32 [T]; outside [0, V) on an unmasked token: its loss is NaN
+ *  mask       device uint8 [T] or NULL (every token counts); masked tokens get 0 in loss_tok, logp_tok and
+ *             lse_tok and a zero d_h row, and their target may be anything
+ *  terms      host, or NULL: none
+ *  grad_scale 1/max(N, 1) (or 1 with a deferred finish or clip)
+ *  d_h        device [T, H] of d_h_dtype, or NULL; dW device [V, H] of dW_dtype, or NULL (both NULL: loss
+ *             only); GRPO_DTYPE_*, 16-byte aligned. dlogits go into the products as bf16, the sums are
+ *             float32, a bf16 gradient is their one rounding
+ *  flags      0, or GRPO_LMHEAD_DW_ACCUMULATE: dW += (float32 only)
+ *  loss_tok   device float [T]; logp_tok (log p_y) and lse_tok device float [T] or NULL
+ *  acc        device grpo_step_acc; loss_tok and acc go to grpo_finish_step (no token counts as clipped)
+ *  workspace  device, 256-byte aligned, grpo_lmhead_ce_workspace_size(T, V, H) bytes; overlapping calls
+ *             need one each
+ * A token with a non-finite loss (a bad target, a NaN or infinite logit, |lse| above 4096) counts as
+ * non-finite, and its gradient is NaN. T = 0 writes dW as zeros (or leaves it, accumulating).
+ * Results of a token do not depend on the masked ones; dW sums the unmasked tokens in order; d_h's order of
+ * sums depends on T, V and H. Environment: as grpo_lmhead_loss_fwd_bwd.
+ * Errors: GRPO_ERR_INVALID (sizes, terms, a non-finite grad_scale, NULL required pointer, alignment,
+ * DW_ACCUMULATE on a bf16 dW, unknown flags), GRPO_ERR_CAPACITY (workspace too small),
+ * GRPO_ERR_UNSUPPORTED (dtype, tensor-map creation), GRPO_ERR_CUDA. */
+GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int64_t T, int64_t V, int64_t H,
+                                    const int32_t* target, const uint8_t* mask, const grpo_ce_terms* terms,
+                                    float grad_scale, void* d_h, int32_t d_h_dtype, void* dW,
+                                    int32_t dW_dtype, uint32_t flags, float* loss_tok, float* logp_tok,
+                                    float* lse_tok, grpo_step_acc* acc, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /* Allocation-free forward pass of the fused LM-head variant. The pages have no counterpart:
  * this entry point exists for callers that cannot allocate device memory when they need the

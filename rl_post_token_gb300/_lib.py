@@ -43,6 +43,7 @@ DISTILL_FORWARD_TAIL = 1
 DISTILL_REVERSE_TAIL = 2
 TOPK_MAX = 256  # largest K of the top-K calls
 ACC_BYTES = 128
+GRAD_NORM_BYTES = 32  # grpo_grad_norm_result
 
 _i32p = C.POINTER(C.c_int32)
 _i64p = C.POINTER(C.c_int64)
@@ -85,6 +86,16 @@ class grpo_window(C.Structure):
 class grpo_loss_terms(C.Structure):
     _fields_ = [("kl_kind", C.c_int32), ("kl_coef", C.c_float), ("ref_logp", C.c_void_p),
                 ("ent_coef", C.c_float), ("entropy_tok", C.c_void_p), ("w_tok", C.c_void_p)]
+
+
+class grpo_ce_terms(C.Structure):
+    _fields_ = [("label_smoothing", C.c_float), ("z_loss", C.c_float), ("soft_cap", C.c_float),
+                ("w_tok", C.c_void_p)]
+
+
+class grpo_grad_norm_result(C.Structure):
+    _fields_ = [("sum_sq", C.c_double), ("norm", C.c_float), ("coef", C.c_float), ("status", C.c_int32),
+                ("reserved0", C.c_int32), ("reserved1", C.c_int64)]
 
 
 class grpo_step_result(C.Structure):
@@ -137,6 +148,18 @@ def _lib() -> C.CDLL:
     lib.grpo_combine_step_results.argtypes = [C.POINTER(grpo_step_result), C.c_int32, C.c_int64,
                                               C.POINTER(grpo_step_result)]
     lib.grpo_combine_step_results.restype = C.c_int
+    lib.grpo_lmhead_ce_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64]
+    lib.grpo_lmhead_ce_workspace_size.restype = C.c_size_t
+    lib.grpo_lmhead_ce_fwd_bwd.argtypes = [vp, vp, C.c_int64, C.c_int64, C.c_int64, vp, vp, C.POINTER(grpo_ce_terms),
+                                           C.c_float, vp, C.c_int32, vp, C.c_int32, C.c_uint32, vp, vp, vp, vp, vp,
+                                           C.c_size_t, vp]
+    lib.grpo_lmhead_ce_fwd_bwd.restype = C.c_int
+    lib.grpo_grad_norm_workspace_size.argtypes = [C.c_int64, C.c_int32]
+    lib.grpo_grad_norm_workspace_size.restype = C.c_size_t
+    lib.grpo_grad_norm.argtypes = [vp, vp, vp, C.c_int32, C.c_float, vp, C.c_int32, vp, vp, vp, C.c_size_t, vp]
+    lib.grpo_grad_norm.restype = C.c_int
+    lib.grpo_grad_clip.argtypes = [vp, vp, vp, vp, vp, C.c_int32, vp, vp]
+    lib.grpo_grad_clip.restype = C.c_int
     lib.grpo_lmhead_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64]
     lib.grpo_lmhead_workspace_size.restype = C.c_size_t
     lib.grpo_lmhead_loss_fwd_bwd.argtypes = [vp, vp, C.c_int64, C.c_int64, C.c_int64, vp, vp, vp, vp, C.c_float,
@@ -576,6 +599,80 @@ def grpo_finish_step_ex(acc, loss_tok, w_tok=None, divisor: int = -1, n_tok: Opt
     return _finish_rc(rc, res, sync, "grpo_finish_step_ex")
 
 
+def _grad_list(grads, name: str):
+    """(pointers, numels, dtypes) of gradient tensors as host arrays; each contiguous (any shape) float32
+    or bf16 on the current CUDA device."""
+    import torch
+
+    dev = torch._C._cuda_getDevice()
+    f32, bf16 = torch.float32, torch.bfloat16
+    n = len(grads)
+    p, numels, dts = np.empty(n, np.uint64), np.empty(n, np.int64), np.empty(n, np.int32)
+    for i, g in enumerate(grads):
+        dt = g.dtype
+        if dt is not f32 and dt is not bf16:
+            raise ValueError(f"{name}[{i}] must be float32 or bfloat16, not {dt}")
+        if g.get_device() != dev or not g.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous on the current CUDA device, not on {g.device}")
+        p[i], numels[i], dts[i] = g.data_ptr(), g.numel(), dt is bf16
+    return p, numels, dts
+
+
+def _addr(a: np.ndarray) -> int:
+    return a.ctypes.data
+
+
+def grpo_grad_norm_workspace_size(grads) -> int:
+    """Workspace bytes of grpo_grad_norm for these tensors."""
+    return int(_lib().grpo_grad_norm_workspace_size(sum(g.numel() for g in grads), len(grads)))
+
+
+def grpo_grad_norm(grads, max_norm: float, result, workspace, tensor_norms=None, acc=None, deferred: bool = False,
+                   stream=None) -> None:
+    """The norm over the tensors of `grads`, each one's own into tensor_norms (float32 [len(grads)] or None)
+    and the clip's factor into `result` (new_grad_norm_result); see grpo.h."""
+    import torch
+
+    p, numels, dts = _grad_list(grads, "grads")
+    _device_args(result, ("result", result, torch.uint8, GRAD_NORM_BYTES),
+                 ("tensor_norms", tensor_norms, torch.float32, len(grads)), ("acc", acc, torch.uint8, ACC_BYTES),
+                 ("workspace", workspace, workspace.dtype, 0))
+    rc = _lib().grpo_grad_norm(_addr(p), _addr(numels), _addr(dts), len(grads), float(max_norm), _ptr(acc),
+                               int(bool(deferred)), _ptr(tensor_norms), _ptr(result), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != OK:
+        raise GrpoError(rc, "grpo_grad_norm")
+
+
+def grpo_grad_clip(grads, result, out=None, stream=None) -> None:
+    """out[i] = result's factor times grads[i] (out None: in place); see grpo.h."""
+    import torch
+
+    p, numels, dts = _grad_list(grads, "grads")
+    q, qdts = p, dts
+    if out is not None:
+        q, qn, qdts = _grad_list(out, "out")
+        if len(out) != len(grads) or not np.array_equal(qn, numels):
+            raise ValueError("out must have as many tensors as grads, of the same sizes")
+    _device_args(result, ("result", result, torch.uint8, GRAD_NORM_BYTES))
+    rc = _lib().grpo_grad_clip(_addr(p), _addr(dts), _addr(q), _addr(qdts), _addr(numels), len(grads), _ptr(result),
+                               _stream(stream))
+    if rc != OK:
+        raise GrpoError(rc, "grpo_grad_clip")
+
+
+def new_grad_norm_result(device="cuda"):
+    """A device-resident grpo_grad_norm_result (caller-owned, 32 bytes)."""
+    import torch
+    return torch.zeros(GRAD_NORM_BYTES, dtype=torch.uint8, device=device)
+
+
+def read_grad_norm_result(result) -> dict:
+    """Decode a grpo_grad_norm_result (copies 32 bytes to host): sum_sq, norm, coef, status."""
+    r = grpo_grad_norm_result.from_buffer_copy(result[:GRAD_NORM_BYTES].cpu().numpy().tobytes())
+    return {k: getattr(r, k) for k in ("sum_sq", "norm", "coef", "status")}
+
+
 def grpo_lmhead_workspace_size(T: int, V: int, H: int) -> int:
     return int(_lib().grpo_lmhead_workspace_size(T, V, H))
 
@@ -650,6 +747,50 @@ def grpo_lmhead_distill_topk_fwd_bwd(h, W, top_idx, top_logp, mask, grad_scale: 
                                                  workspace.numel() * workspace.element_size(), _stream(stream))
     if rc != OK:
         raise GrpoError(rc, "grpo_lmhead_distill_topk_fwd_bwd")
+
+
+def grpo_lmhead_ce_workspace_size(T: int, V: int, H: int) -> int:
+    return int(_lib().grpo_lmhead_ce_workspace_size(T, V, H))
+
+
+def _grad_dtype(t, name: str) -> int:
+    """GRPO_DTYPE_* of a gradient tensor (0 for None)."""
+    import torch
+
+    if t is None or t.dtype is torch.float32:
+        return DTYPE_F32
+    if t.dtype is torch.bfloat16:
+        return DTYPE_BF16
+    raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+
+
+def grpo_lmhead_ce_fwd_bwd(h, W, target, mask, grad_scale: float, d_h, dW, loss_tok, acc, workspace,
+                           label_smoothing: float = 0.0, z_loss: float = 0.0, soft_cap: float = 0.0, w_tok=None,
+                           logp_tok=None, lse_tok=None, dw_accumulate: bool = False, stream=None) -> None:
+    """Cross entropy of h [T, H] and W [V, H] (bf16, contiguous) against target (int32 [T]) over the
+    tokens with mask != 0 (uint8 [T], or None: all): loss_tok, and d_h [T, H] and dW [V, H] (float32 or
+    bf16, or None); see grpo.h."""
+    import torch
+
+    if h.dim() != 2 or W.dim() != 2 or h.shape[1] != W.shape[1] or not (h.is_contiguous() and W.is_contiguous()):
+        raise ValueError("h [T, H] and W [V, H] must be contiguous with one H")
+    T, H = h.shape
+    V = W.shape[0]
+    f32, bf16, u8 = torch.float32, torch.bfloat16, torch.uint8
+    dt_h, dt_w = _grad_dtype(d_h, "d_h"), _grad_dtype(dW, "dW")
+    _device_args(h, ("h", h, bf16, 0), ("W", W, bf16, 0), ("target", target, torch.int32, T), ("mask", mask, u8, T),
+                 ("w_tok", w_tok, f32, T), ("d_h", d_h, d_h.dtype if d_h is not None else None, T * H),
+                 ("dW", dW, dW.dtype if dW is not None else None, V * H), ("loss_tok", loss_tok, f32, T),
+                 ("logp_tok", logp_tok, f32, T), ("lse_tok", lse_tok, f32, T), ("acc", acc, u8, ACC_BYTES),
+                 ("workspace", workspace, workspace.dtype, 0))
+    tm = grpo_ce_terms(float(label_smoothing), float(z_loss), float(soft_cap), _ptr(w_tok))
+    rc = _lib().grpo_lmhead_ce_fwd_bwd(_ptr(h), _ptr(W), T, V, H, _ptr(target), _ptr(mask), C.byref(tm),
+                                       float(grad_scale), _ptr(d_h), dt_h, _ptr(dW), dt_w,
+                                       LMHEAD_DW_ACCUMULATE if dw_accumulate else 0, _ptr(loss_tok), _ptr(logp_tok),
+                                       _ptr(lse_tok), _ptr(acc), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != OK:
+        raise GrpoError(rc, "grpo_lmhead_ce_fwd_bwd")
 
 
 def grpo_lmhead_forward_noalloc(h, W, target, old_logp, adv_tok, mask, clip_eps: float,

@@ -1,0 +1,483 @@
+// Softmax cross entropy from hidden states: z = h W^T is formed tile by tile on the tensor cores and
+// consumed in the GEMM's epilogue (formulas in grpo_lmhead_ce.cuh); no [T, V] matrix is stored.
+//
+//  compact    the unmasked tokens first, in token order, and their hidden states gathered: every GEMM
+//             below runs over them only (a fine-tuning batch masks its prompts). mask NULL: none of it
+//  pass A     per (token, 256 vocabulary entries) the softmax's (shift, sum), the target logit and, with
+//             label smoothing, the sum of the logits
+//  reduce     per token the tiles joined in a fixed order: loss, log-prob, lse and the gradient's factors
+//  backward   per vocabulary piece the logits once more, their bf16 dlogits into one of two buffers of
+//             that piece; d_h (+)= dz W_c and dW_c = dz^T h on a second stream beside the next piece
+//
+// Bound by the tensor cores with many tokens: 2 T V H flops of pass A and 6 T V H of the backward, of which
+// the 2 T V H of the logits' second forming replace a store and two reads of the [T, V] logits. With few
+// tokens by the readings of W (three) and the writing of dW.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "grpo_lmhead_gemm.cuh"
+#include "grpo_lmhead_host.cuh"
+
+namespace grpo {
+namespace lmhead {
+
+// The unmasked tokens' indices first, in token order, then the masked ones', and the unmasked count. One
+// block: each thread counts a run of tokens, one scan over the threads, then each writes its run.
+constexpr int kCompactThreads = 1024;
+
+__global__ void __launch_bounds__(kCompactThreads) ce_compact_kernel(int64_t T, const uint8_t* mask, int32_t* idx,
+                                                                     int32_t* live_n) {
+  __shared__ int32_t warp_sum[kCompactThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int64_t per = (T + kCompactThreads - 1) / kCompactThreads;
+  const int64_t b = (int64_t)tid * per < T ? (int64_t)tid * per : T, e = b + per < T ? b + per : T;
+  int32_t c = 0;
+  for (int64_t t = b; t < e; ++t) c += mask[t] != 0;
+  int32_t x = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t v = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += v;
+  }
+  if (lane == 31) warp_sum[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    int32_t v = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    warp_sum[lane] = v;
+  }
+  __syncthreads();
+  const int32_t total = warp_sum[kCompactThreads / 32 - 1];
+  int32_t pos = (w > 0 ? warp_sum[w - 1] : 0) + x - c;  // unmasked tokens before this thread's run
+  for (int64_t t = b; t < e; ++t) {
+    if (mask[t] != 0)
+      idx[pos++] = (int32_t)t;
+    else
+      idx[total + (t - pos)] = (int32_t)t;  // t - pos = masked tokens before t
+  }
+  if (tid == 0) *live_n = total;
+}
+
+// Row i of the compact order, one warp per row: an unmasked token's hidden state is copied; the rows up to
+// the padded count are zeroed (dW reduces over them); a masked token's d_h row is zeroed (dh_vec 16-byte
+// vectors; no GEMM writes it).
+__global__ void __launch_bounds__(256) ce_gather_kernel(int64_t T, int H, const __nv_bfloat16* h, const int32_t* idx,
+                                                        const int32_t* live_n, __nv_bfloat16* h_live, void* d_h,
+                                                        int dh_vec) {
+  const int64_t nl = *live_n;
+  const int64_t pad = live_pad(nl, T) < T ? live_pad(nl, T) : T;
+  const int lane = threadIdx.x & 31, nvec = H >> 3;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < T; i += warps) {
+    const int64_t tok = idx[i];
+    uint4* dst = reinterpret_cast<uint4*>(h_live) + i * nvec;
+    if (i < nl) {
+      const uint4* src = reinterpret_cast<const uint4*>(h) + tok * nvec;
+#pragma unroll 4
+      for (int k = lane; k < nvec; k += 32) dst[k] = src[k];
+      continue;
+    }
+    if (i < pad)
+      for (int k = lane; k < nvec; k += 32) dst[k] = z4;
+    if (d_h) {
+      uint4* row = reinterpret_cast<uint4*>(d_h) + tok * dh_vec;
+      for (int k = lane; k < dh_vec; k += 32) row[k] = z4;
+    }
+  }
+}
+
+struct CeReduceArgs {
+  int64_t T, V;
+  int n_col_tiles;
+  const float *part_m, *part_s, *part_z, *zy;  // part_z: with label smoothing
+  const int32_t* target;
+  const float* w_tok;
+  float scale, smoothing, z_loss;
+  float *lse2, *coef, *ea;  // [T] out, by token: what the dlogits epilogue takes
+  float *loss_tok, *logp_tok, *lse_tok;
+  grpo_step_acc* acc;
+  const int32_t *idx, *live_n;  // the compact order, or NULL
+};
+
+// A block takes 32 tokens (lane = token: a partial's load is one 128-byte line), its warps every 16th
+// vocabulary tile in order; warp 0 joins the warps' in order.
+constexpr int kCeReduceWarps = 16;
+
+__global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduceArgs a) {
+  __shared__ float wm[kCeReduceWarps][32], ws[kCeReduceWarps][32], wz[kCeReduceWarps][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+  const bool in = i < a.T, live = in && (!a.idx || i < (int64_t)*a.live_n);
+  MS t{-INFINITY, 0.f};
+  float z = 0.f;
+  if (live) {
+#pragma unroll 4
+    for (int c = w; c < a.n_col_tiles; c += kCeReduceWarps) {
+      const int64_t k = (int64_t)c * a.T + i;
+      t = ms2_combine(t, MS{a.part_m[k], a.part_s[k]});
+      if (a.part_z) z += a.part_z[k];
+    }
+  }
+  wm[w][lane] = t.m;
+  ws[w][lane] = t.s;
+  wz[w][lane] = z;
+  __syncthreads();
+  if (w != 0) return;
+  bool bad = false;
+  if (in) {
+    const int64_t tok = a.idx ? (int64_t)a.idx[i] : i;
+    float loss = 0.f, logp = 0.f, lse = 0.f, l2 = 0.f, sw = 0.f, cp = 0.f;
+    if (live) {
+      MS tot{wm[0][lane], ws[0][lane]};
+      z = wz[0][lane];
+#pragma unroll
+      for (int k = 1; k < kCeReduceWarps; ++k) {
+        tot = ms2_combine(tot, MS{wm[k][lane], ws[k][lane]});
+        z += wz[k][lane];
+      }
+      const float nan = __int_as_float(0x7fc00000);
+      const int32_t y = a.target[tok];
+      const float zy = y >= 0 && (int64_t)y < a.V ? a.zy[tok] : nan;
+      const float l2s = log2f(tot.s);
+      l2 = tot.m + l2s;
+      // rows past the vouched range of logits count as non-finite, as in the policy loss
+      const bool ok = fabsf(l2) <= kLseMax * kLog2e;
+      lse = ok ? l2 * kLn2 : nan;
+      logp = ok ? (fmaf(zy, kLog2e, -tot.m) - l2s) * kLn2 : nan;  // without cancellation
+      loss = -(1.f - a.smoothing) * logp + a.z_loss * lse * lse;
+      // lse - mean z, from the shift too
+      if (a.part_z) loss += a.smoothing * ((tot.m - z / (float)a.V * kLog2e) + l2s) * kLn2;
+      sw = a.w_tok ? a.scale * a.w_tok[tok] : a.scale;
+      cp = sw * fmaf(2.f * a.z_loss, lse, 1.f);
+      if (!isfinite(loss)) cp = nan;
+      bad = !isfinite(cp);
+    }
+    a.loss_tok[tok] = loss;
+    if (a.logp_tok) a.logp_tok[tok] = logp;
+    if (a.lse_tok) a.lse_tok[tok] = lse;
+    a.lse2[tok] = l2;
+    a.coef[tok] = sw;
+    a.ea[tok] = cp;
+  }
+  const unsigned n_tok = __popc(__ballot_sync(0xffffffffu, in)), n_live = __popc(__ballot_sync(0xffffffffu, live)),
+                 n_bad = __popc(__ballot_sync(0xffffffffu, bad));
+  if (lane == 0) {
+    atomicAdd(reinterpret_cast<unsigned long long*>(&a.acc->n_tokens), (unsigned long long)n_tok);
+    if (n_live) atomicAdd(reinterpret_cast<unsigned long long*>(&a.acc->n_valid), (unsigned long long)n_live);
+    if (n_bad) atomicAdd(reinterpret_cast<unsigned long long*>(&a.acc->n_nonfinite), (unsigned long long)n_bad);
+  }
+}
+
+// d_h from the runs' partial sums, in order; compact row r to its token's row.
+__global__ void __launch_bounds__(256) ce_split_sum_kernel(const int32_t* live_n, const int32_t* row_idx, int64_t T,
+                                                           int64_t H, const float* part, int split, void* d_h,
+                                                           int out_bf16) {
+  const int64_t n = (live_n ? (int64_t)*live_n : T) * (H / 4), stride = T * (H / 4);
+  const float4* p = reinterpret_cast<const float4*>(part);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float4 v = p[i];
+#pragma unroll 4
+    for (int s = 1; s < split; ++s) {
+      const float4 o = p[s * stride + i];
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    const int64_t r = i / (H / 4), to = (row_idx ? (int64_t)row_idx[r] : r) * (H / 4) + (i - r * (H / 4));
+    if (out_bf16)
+      reinterpret_cast<uint2*>(d_h)[to] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    else
+      reinterpret_cast<float4*>(d_h)[to] = v;
+  }
+}
+
+}  // namespace lmhead
+}  // namespace grpo
+
+using namespace grpo;
+using namespace grpo::lmhead;
+
+namespace {
+
+struct CeLayout {
+  size_t part_m, part_s, part_z, zy, lse2, coef, ea, idx, live_n, h_live, dz[2], part, total;
+  int n_col_tiles, chunk_tiles, n_chunks, split;
+  int64_t vchunk;  // columns of a dlogits buffer
+};
+
+CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
+  CeLayout w{};
+  w.n_col_tiles = (int)((V + BN - 1) / BN);
+  const int most = distill_chunk_tiles(T);
+  w.n_chunks = (w.n_col_tiles + most - 1) / most;
+  w.chunk_tiles = (w.n_col_tiles + w.n_chunks - 1) / w.n_chunks;
+  w.n_chunks = (w.n_col_tiles + w.chunk_tiles - 1) / w.chunk_tiles;
+  w.vchunk = (int64_t)w.chunk_tiles * BN;
+  w.split = d_h_split(T, H, w.chunk_tiles);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t t4 = (size_t)T * 4, parts = (size_t)w.n_col_tiles * t4;
+  w.part_m = take(parts);
+  w.part_s = take(parts);
+  w.part_z = take(parts);
+  w.zy = take(t4);
+  w.lse2 = take(t4);
+  w.coef = take(t4);
+  w.ea = take(t4);
+  w.idx = take(t4);
+  w.live_n = take(4);
+  w.h_live = take((size_t)T * H * 2);
+  w.dz[0] = take((size_t)T * w.vchunk * 2);
+  w.dz[1] = w.n_chunks > 1 ? take((size_t)T * w.vchunk * 2) : w.dz[0];
+  // d_h's float sums: of each run, or over the pieces
+  w.part = take(w.split > 1 ? (size_t)w.split * T * H * 4 : w.n_chunks > 1 ? (size_t)T * H * 4 : 0);
+  w.total = off;
+  return w;
+}
+
+struct CeCall {
+  const void *h, *W;
+  int64_t T, V, H;
+  const int32_t* target;
+  float smoothing, cap;
+  void *d_h, *dW;
+  int dh_bf16, dw_bf16, dw_accumulate, cg;
+  grpo_step_acc* acc;
+  CeLayout ws;
+  uint8_t* base;
+  const void* h_src;      // h, or the compact hidden states
+  const int32_t *idx, *live_n;
+  cudaStream_t st;
+  float* f(size_t off) const { return reinterpret_cast<float*>(base + off); }
+};
+
+template <int PLAIN, int CAP>
+int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc) {
+  CUtensorMap ma, mb, mc = {};
+  if (!map_k(&ma, c.h_src, c.T, c.H, c.H, BM) || !map_k(&mb, c.W, c.V, c.H, c.H, BN / c.cg)) return GRPO_ERR_UNSUPPORTED;
+  if (epi_is_dlogits(PLAIN) && !map_dz_store(&mc, g.dz, c.T, vc, g.ldz)) return GRPO_ERR_UNSUPPORTED;
+  g.M = c.T;
+  g.K = c.H;
+  g.V = c.V;
+  g.m_fast = 1;  // consecutive units share the W tile
+  g.target = c.target;
+  g.row_idx = c.idx;
+  g.live_n = c.live_n;
+  g.acc = c.acc;
+  g.zy = c.f(c.ws.zy);
+  g.cap = c.cap;
+  g.inv_cap = 1.f / c.cap;
+  return c.cap > 0.f ? launch<CAP, false, false>(c.cg, ma, mb, mc, g, st) : launch<PLAIN, false, false>(c.cg, ma, mb, mc, g, st);
+}
+
+// d_h of one piece: dz [T, vc] W_c [vc, H], cut into runs where the layout says so.
+int ce_dh(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0, int64_t vc, cudaStream_t st) {
+  CUtensorMap ma, mb;
+  if (!map_k(&ma, dz, c.T, vc, c.ws.vchunk, BM) ||
+      !map_mn(&mb, static_cast<const __nv_bfloat16*>(c.W) + v0 * c.H, vc, c.H, c.H))
+    return GRPO_ERR_UNSUPPORTED;
+  GemmArgs g{};
+  g.live_n = c.live_n;
+  g.live_mode = c.live_n ? LIVE_ROWS : LIVE_NONE;
+  g.row_idx = c.idx;
+  g.M = c.T;
+  g.N = c.H;
+  g.K = vc;
+  g.n_n = (int)((c.H + BN - 1) / BN);
+  g.ldc = c.H;
+  g.acc = c.acc;
+  g.out = c.d_h;
+  g.out_bf16 = c.dh_bf16;
+  g.accumulate = chunk > 0;
+  if (c.ws.split > 1) {  // (the last piece may have fewer K blocks than the others)
+    g.split = (int)std::min<int64_t>(c.ws.split, (vc + BK - 1) / BK);
+    g.n_n *= g.split;
+    g.split_stride = c.T * c.H;
+    g.C = c.f(c.ws.part);
+  } else if (chunk + 1 < c.ws.n_chunks) {
+    g.C = c.f(c.ws.part);
+  } else if (chunk > 0) {
+    g.add = c.f(c.ws.part);
+  }
+  return launch<EPI_CE_STORE, false, true>(c.cg, ma, mb, ma, g, st);
+}
+
+// dW_c [vc, H] = dz^T h over the (unmasked) tokens.
+int ce_dw(const CeCall& c, const __nv_bfloat16* dz, int64_t v0, int64_t vc, cudaStream_t st) {
+  CUtensorMap ma, mb;
+  if (!map_mn(&ma, dz, c.T, vc, c.ws.vchunk) || !map_mn(&mb, c.h_src, c.T, c.H, c.H)) return GRPO_ERR_UNSUPPORTED;
+  GemmArgs g{};
+  g.live_n = c.live_n;
+  g.live_mode = c.live_n ? LIVE_K : LIVE_NONE;
+  g.M = vc;
+  g.N = c.H;
+  g.K = c.T;
+  g.n_n = (int)((c.H + BN - 1) / BN);
+  g.ldc = c.H;
+  g.acc = c.acc;
+  g.out = static_cast<uint8_t*>(c.dW) + v0 * c.H * (c.dw_bf16 ? 2 : 4);
+  g.out_bf16 = c.dw_bf16;
+  g.add = c.dw_accumulate ? static_cast<const float*>(g.out) : nullptr;
+  return launch<EPI_CE_STORE, true, true>(c.cg, ma, mb, ma, g, st);
+}
+
+int ce_backward(const CeCall& c) {
+  std::unique_lock<std::mutex> lock;
+  Overlap* ov = overlap_on() && c.ws.n_chunks > 1 ? overlap_state(lock, c.st) : nullptr;
+  const cudaStream_t bst = ov ? ov->aux : c.st;
+  auto pieces = [&]() -> int {
+    for (int i = 0; i < c.ws.n_chunks; ++i) {
+      const int ct0 = i * c.ws.chunk_tiles, nct = std::min(c.ws.chunk_tiles, c.ws.n_col_tiles - ct0);
+      const int64_t v0 = (int64_t)ct0 * BN, vc = std::min<int64_t>((int64_t)nct * BN, c.V - v0);
+      __nv_bfloat16* dz = reinterpret_cast<__nv_bfloat16*>(c.base + c.ws.dz[ov ? i & 1 : 0]);
+      if (ov && i >= 2) GRPO_CUDA_TRY(cudaStreamWaitEvent(c.st, ov->buf_free[i & 1], 0));
+      GemmArgs g{};
+      g.lse2 = c.f(c.ws.lse2);
+      g.coef = c.f(c.ws.coef);
+      g.ea = c.f(c.ws.ea);
+      g.ce_hot = 1.f - c.smoothing;
+      g.ce_smooth = c.smoothing / (float)c.V;
+      g.dz = dz;
+      g.ldz = c.ws.vchunk;
+      g.v0 = v0;
+      g.col_tile0 = ct0;
+      g.n_n = nct;
+      g.live_mode = c.live_n ? LIVE_ROWS_PADDED : LIVE_NONE;
+      int rc = ce_logits<EPI_CE_DLOGITS, EPI_CE_DLOGITS_CAP>(c, g, c.st, vc);
+      if (rc != GRPO_OK) return rc;
+      if (ov) {
+        GRPO_CUDA_TRY(cudaEventRecord(ov->dz_ready, c.st));
+        GRPO_CUDA_TRY(cudaStreamWaitEvent(bst, ov->dz_ready, 0));
+      }
+      if (c.d_h && (rc = ce_dh(c, dz, i, v0, vc, bst)) != GRPO_OK) return rc;
+      if (c.dW && (rc = ce_dw(c, dz, v0, vc, bst)) != GRPO_OK) return rc;
+      if (ov) GRPO_CUDA_TRY(cudaEventRecord(ov->buf_free[i & 1], bst));
+    }
+    if (c.d_h && c.ws.split > 1) {
+      const int64_t blocks = std::min<int64_t>((c.T * c.H / 4 + 255) / 256, (int64_t)sm_count() * 8);
+      ce_split_sum_kernel<<<(unsigned)blocks, 256, 0, bst>>>(c.live_n, c.idx, c.T, c.H, c.f(c.ws.part), c.ws.split, c.d_h,
+                                                             c.dh_bf16);
+      GRPO_CUDA_TRY(cudaGetLastError());
+    }
+    return GRPO_OK;
+  };
+  int rc = pieces();
+  // the caller's stream continues after every launch of the call (also after an error)
+  if (ov && (cudaEventRecord(ov->joined, bst) != cudaSuccess || cudaStreamWaitEvent(c.st, ov->joined, 0) != cudaSuccess)) {
+    (void)cudaGetLastError();
+    if (rc == GRPO_OK) rc = GRPO_ERR_CUDA;
+  }
+  return rc;
+}
+
+bool known_dtype(int32_t d) { return d == GRPO_DTYPE_F32 || d == GRPO_DTYPE_BF16; }
+
+}  // namespace
+
+extern "C" GRPO_API size_t grpo_lmhead_ce_workspace_size(int64_t T, int64_t V, int64_t H) {
+  if (T <= 0 || V <= 0 || H <= 0 || T > INT32_MAX / 2 || V > INT32_MAX / 2 || H > INT32_MAX / 2) return 0;
+  return ce_layout(T, V, H).total;
+}
+
+extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int64_t T, int64_t V, int64_t H,
+                                               const int32_t* target, const uint8_t* mask, const grpo_ce_terms* terms,
+                                               float grad_scale, void* d_h, int32_t d_h_dtype, void* dW,
+                                               int32_t dW_dtype, uint32_t flags, float* loss_tok, float* logp_tok,
+                                               float* lse_tok, grpo_step_acc* acc, void* workspace,
+                                               size_t workspace_bytes, void* stream) {
+  const grpo_ce_terms none = {0.f, 0.f, 0.f, nullptr};
+  const grpo_ce_terms& tm = terms ? *terms : none;
+  if (!(tm.label_smoothing >= 0.f && tm.label_smoothing <= 1.f) || !(tm.z_loss >= 0.f && std::isfinite(tm.z_loss)))
+    return GRPO_ERR_INVALID;
+  if (tm.soft_cap != 0.f && !(tm.soft_cap >= 1e-6f && tm.soft_cap <= 1e6f)) return GRPO_ERR_INVALID;
+  if (!std::isfinite(grad_scale)) return GRPO_ERR_INVALID;
+  if (T < 0 || V < 1 || H < 8 || H % 8 != 0 || !acc || (uintptr_t)acc % alignof(grpo_step_acc)) return GRPO_ERR_INVALID;
+  if (T > INT32_MAX / 2 || V > INT32_MAX / 2 || H > INT32_MAX / 2) return GRPO_ERR_INVALID;
+  if (flags & ~(uint32_t)GRPO_LMHEAD_DW_ACCUMULATE) return GRPO_ERR_INVALID;
+  if ((d_h && !known_dtype(d_h_dtype)) || (dW && !known_dtype(dW_dtype))) return GRPO_ERR_UNSUPPORTED;
+  // (a bf16 sum would be rounded at every call)
+  if (dW && (flags & GRPO_LMHEAD_DW_ACCUMULATE) && dW_dtype != GRPO_DTYPE_F32) return GRPO_ERR_INVALID;
+  if (T == 0) {
+    if (dW && !(flags & GRPO_LMHEAD_DW_ACCUMULATE))
+      GRPO_CUDA_TRY(cudaMemsetAsync(dW, 0, (size_t)V * H * (dW_dtype == GRPO_DTYPE_BF16 ? 2 : 4), as_stream(stream)));
+    return GRPO_OK;
+  }
+  if (!h || !W || !target || !loss_tok || !workspace) return GRPO_ERR_INVALID;
+  if (((uintptr_t)h | (uintptr_t)W | (uintptr_t)d_h | (uintptr_t)dW) & 15u || ((uintptr_t)workspace & 255u))
+    return GRPO_ERR_INVALID;
+  CeCall c{};
+  c.ws = ce_layout(T, V, H);
+  if (workspace_bytes < c.ws.total) return GRPO_ERR_CAPACITY;
+  c.h = c.h_src = h;
+  c.W = W;
+  c.T = T;
+  c.V = V;
+  c.H = H;
+  c.target = target;
+  c.smoothing = tm.label_smoothing;
+  c.cap = tm.soft_cap;
+  c.d_h = d_h;
+  c.dW = dW;
+  c.dh_bf16 = d_h_dtype == GRPO_DTYPE_BF16;
+  c.dw_bf16 = dW_dtype == GRPO_DTYPE_BF16;
+  c.dw_accumulate = (flags & GRPO_LMHEAD_DW_ACCUMULATE) != 0;
+  c.cg = distill_cta_group(T, c.ws.n_col_tiles);
+  c.acc = acc;
+  c.base = static_cast<uint8_t*>(workspace);
+  c.st = as_stream(stream);
+  if (mask) {
+    int32_t* idx = reinterpret_cast<int32_t*>(c.base + c.ws.idx);
+    int32_t* live_n = reinterpret_cast<int32_t*>(c.base + c.ws.live_n);
+    __nv_bfloat16* h_live = reinterpret_cast<__nv_bfloat16*>(c.base + c.ws.h_live);
+    ce_compact_kernel<<<1, kCompactThreads, 0, c.st>>>(T, mask, idx, live_n);
+    GRPO_CUDA_TRY(cudaGetLastError());
+    const int64_t blocks = std::min<int64_t>((T + 7) / 8, (int64_t)sm_count() * 16);
+    ce_gather_kernel<<<(unsigned)blocks, 256, 0, c.st>>>(T, (int)H, static_cast<const __nv_bfloat16*>(h), idx, live_n,
+                                                         h_live, d_h, (int)(H / (c.dh_bf16 ? 8 : 4)));
+    GRPO_CUDA_TRY(cudaGetLastError());
+    c.h_src = h_live;
+    c.idx = idx;
+    c.live_n = live_n;
+  }
+  GemmArgs g{};
+  g.part_m = c.f(c.ws.part_m);
+  g.part_s = c.f(c.ws.part_s);
+  g.part_s2 = c.smoothing > 0.f ? c.f(c.ws.part_z) : nullptr;
+  g.n_n = c.ws.n_col_tiles;
+  g.live_mode = c.live_n ? LIVE_ROWS : LIVE_NONE;
+  const int rc = ce_logits<EPI_CE_PARTIALS, EPI_CE_PARTIALS_CAP>(c, g, c.st, 0);
+  if (rc != GRPO_OK) return rc;
+  CeReduceArgs r{};
+  r.T = T;
+  r.V = V;
+  r.n_col_tiles = c.ws.n_col_tiles;
+  r.part_m = g.part_m;
+  r.part_s = g.part_s;
+  r.part_z = g.part_s2;
+  r.zy = c.f(c.ws.zy);
+  r.target = target;
+  r.w_tok = tm.w_tok;
+  r.scale = grad_scale;
+  r.smoothing = c.smoothing;
+  r.z_loss = tm.z_loss;
+  r.lse2 = c.f(c.ws.lse2);
+  r.coef = c.f(c.ws.coef);
+  r.ea = c.f(c.ws.ea);
+  r.loss_tok = loss_tok;
+  r.logp_tok = logp_tok;
+  r.lse_tok = lse_tok;
+  r.acc = acc;
+  r.idx = c.idx;
+  r.live_n = c.live_n;
+  ce_reduce_kernel<<<(unsigned)((T + 31) / 32), kCeReduceWarps * 32, 0, c.st>>>(r);
+  GRPO_CUDA_TRY(cudaGetLastError());
+  return d_h || dW ? ce_backward(c) : GRPO_OK;
+}

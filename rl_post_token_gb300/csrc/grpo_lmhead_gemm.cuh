@@ -37,7 +37,22 @@ constexpr int NTHREADS = 192;
 constexpr int TMEM_COLS = 2 * BN;
 
 // EPI_PARTIALS_ENT: the partials plus sum e z per tile (the entropy's third accumulator)
-enum Epi : int { EPI_PARTIALS = 0, EPI_DLOGITS = 1, EPI_STORE_F32 = 2, EPI_PARTIALS_ENT = 3 };
+// EPI_CE_*: the cross entropy's partials, dlogits and products (grpo_lmhead_ce.cuh); _CAP: the logits
+// through the soft cap
+enum Epi : int {
+  EPI_PARTIALS = 0,
+  EPI_DLOGITS = 1,
+  EPI_STORE_F32 = 2,
+  EPI_PARTIALS_ENT = 3,
+  EPI_CE_PARTIALS = 4,
+  EPI_CE_PARTIALS_CAP = 5,
+  EPI_CE_DLOGITS = 6,
+  EPI_CE_DLOGITS_CAP = 7,
+  EPI_CE_STORE = 8
+};
+
+constexpr bool epi_is_dlogits(int e) { return e == EPI_DLOGITS || e == EPI_CE_DLOGITS || e == EPI_CE_DLOGITS_CAP; }
+constexpr bool epi_is_store(int e) { return e == EPI_STORE_F32 || e == EPI_CE_STORE; }
 
 // Dlogits epilogue staging: each epilogue warp writes its 32 rows x 32 columns of bf16 (2 KB,
 // 64-byte rows in the 64-byte swizzle a TMA store expects) into one of two buffers, and one lane
@@ -54,7 +69,7 @@ struct Shape {
   static constexpr int B_BYTES = B_ROWS * BK * 2;        // 16 KB (CG = 2) or 32 KB
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // bytes this CTA receives per stage
   static constexpr int STAGES = CG == 2 ? 6 : 4;
-  static constexpr int EPI_BYTES = EPI == EPI_DLOGITS || EPI == EPI_STORE_F32 ? EPI_WARPS * 2 * EPI_BUF_BYTES : 0;
+  static constexpr int EPI_BYTES = epi_is_dlogits(EPI) || epi_is_store(EPI) ? EPI_WARPS * 2 * EPI_BUF_BYTES : 0;
   static constexpr size_t SMEM = 1024 /*alignment slack*/ + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + 256;
 };
 
@@ -256,6 +271,15 @@ struct GemmArgs {
   const int32_t* live_n;
   const int32_t* row_idx;
   int live_mode;
+  // the cross entropy's epilogues (part_s2: [n_col_tiles_total][T] sum of the tile's logits, or NULL;
+  // ea: [T] s w (1 + 2 lambda lse); coef: [T] s w)
+  float cap, inv_cap;      // the soft cap c and 1 / c (_CAP)
+  float ce_hot, ce_smooth; // 1 - eps, eps / V
+  // EPI_CE_STORE: out[row][ldc] = add[compact row][ldc] + A B (add NULL: the product alone); out_bf16:
+  // out is bf16, else float. C, when not NULL, takes the float sums instead of out.
+  void* out;
+  const float* add;
+  int out_bf16;
 };
 
 enum { LIVE_NONE = 0, LIVE_ROWS_PADDED = 1, LIVE_ROWS = 2, LIVE_K = 3 };
@@ -493,6 +517,14 @@ __device__ __forceinline__ void epi_store_f32(const GemmArgs& g, float* C, uint3
   }
 }
 
+}  // namespace lmhead
+}  // namespace grpo
+
+#include "grpo_lmhead_ce.cuh"  // the cross entropy's epilogues
+
+namespace grpo {
+namespace lmhead {
+
 // ---- the kernel ---------------------------------------------------------------------------------
 
 template <int CG, int EPI, bool A_MN, bool B_MN>
@@ -553,11 +585,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   const int stride = CG == 2 ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   const int KB = (int)((K + BK - 1) / BK);
   // a unit's N tile and its K blocks [k0, k1)
-  const int split = EPI == EPI_STORE_F32 && g.split > 1 ? g.split : 1;
+  const int split = epi_is_store(EPI) && g.split > 1 ? g.split : 1;
   auto unit_k = [&](int& nu, int& k0, int& k1) -> int {
     k0 = 0;
     k1 = KB;
-    if (EPI != EPI_STORE_F32 || split == 1) return 0;
+    if (!epi_is_store(EPI) || split == 1) return 0;
     const int n_nt = g.n_n / split, run = nu / n_nt;
     nu -= run * n_nt;
     k0 = (int)((int64_t)run * KB / split);
@@ -617,7 +649,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         fence_after();
         const uint32_t d = tmem + ab * BN;
         int k0 = 0, k1 = KB;
-        if (EPI == EPI_STORE_F32) {
+        if (epi_is_store(EPI)) {
           int mu, nu;
           unit_coords(g, n_m, t, mu, nu);
           unit_k(nu, k0, k1);
@@ -672,7 +704,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       else if constexpr (EPI == EPI_DLOGITS)
         epi_dlogits(g, &map_c, taddr, row, rok, g.col_tile0 + nu, row - lane, rows_store,
                     epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
-      else {
+      else if constexpr (EPI == EPI_CE_PARTIALS || EPI == EPI_CE_PARTIALS_CAP)
+        epi_ce_partials<EPI == EPI_CE_PARTIALS_CAP>(g, taddr, row, rok, g.col_tile0 + nu);
+      else if constexpr (EPI == EPI_CE_DLOGITS || EPI == EPI_CE_DLOGITS_CAP)
+        epi_ce_dlogits<EPI == EPI_CE_DLOGITS_CAP>(g, &map_c, taddr, row, rok, g.col_tile0 + nu, row - lane, rows_store,
+                                                  epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
+      else if constexpr (EPI == EPI_CE_STORE) {
+        int k0, k1;
+        const int run = unit_k(nu, k0, k1);
+        epi_ce_store(g, run, taddr, row, rok, (int64_t)nu * BN, epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
+      } else {
         int k0, k1;
         const int run = unit_k(nu, k0, k1);
         epi_store_f32(g, g.C + run * g.split_stride, taddr, row, rok, (int64_t)nu * BN,
@@ -691,7 +732,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         aphase ^= 1u;
       }
     }
-    if (EPI == EPI_DLOGITS && lane == 0) bulk_wait_all();  // this warp's stores are complete
+    if (epi_is_dlogits(EPI) && lane == 0) bulk_wait_all();  // this warp's stores are complete
   }
 
   fence_before();
