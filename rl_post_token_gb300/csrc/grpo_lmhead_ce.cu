@@ -98,7 +98,7 @@ struct CeReduceArgs {
   const float *part_m, *part_s, *part_z, *zy;  // part_z: with label smoothing
   const int32_t* target;
   const float* w_tok;
-  float scale, smoothing, z_loss;
+  float smoothing, z_loss;
   float *lse2, *coef, *ea;  // [T] out, by token: what the dlogits epilogue takes
   float *loss_tok, *logp_tok, *lse_tok;
   grpo_step_acc* acc;
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduce
   MS t{-INFINITY, 0.f};
   float z = 0.f;
   if (live) {
-#pragma unroll 4
+#pragma unroll 8
     for (int c = w; c < a.n_col_tiles; c += kCeReduceWarps) {
       const int64_t k = (int64_t)c * a.T + i;
       t = ms2_combine(t, MS{a.part_m[k], a.part_s[k]});
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduce
       loss = -(1.f - a.smoothing) * logp + a.z_loss * lse * lse;
       // lse - mean z, from the shift too
       if (a.part_z) loss += a.smoothing * ((tot.m - z / (float)a.V * kLog2e) + l2s) * kLn2;
-      sw = a.w_tok ? a.scale * a.w_tok[tok] : a.scale;
+      sw = a.w_tok ? a.w_tok[tok] : 1.f;
       cp = sw * fmaf(2.f * a.z_loss, lse, 1.f);
       if (!isfinite(loss)) cp = nan;
       bad = !isfinite(cp);
@@ -174,20 +174,40 @@ __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduce
   }
 }
 
-// d_h from the runs' partial sums, in order; compact row r to its token's row.
-__global__ void __launch_bounds__(256) ce_split_sum_kernel(const int32_t* live_n, const int32_t* row_idx, int64_t T,
-                                                           int64_t H, const float* part, int split, void* d_h,
-                                                           int out_bf16) {
-  const int64_t n = (live_n ? (int64_t)*live_n : T) * (H / 4), stride = T * (H / 4);
+// d_h = scale (the runs' float sums, joined in an order that goes by `split`), rounded once; compact row r to
+// its token's row. A block takes 256 / G vectors of 4, G groups of its threads every G-th run.
+template <int G>
+__global__ void __launch_bounds__(256) ce_dh_kernel(const int32_t* live_n, const int32_t* row_idx, int64_t T, int H4,
+                                                    const float* part, int split, float scale, void* d_h, int out_bf16) {
+  constexpr int W = 256 / G;
+  __shared__ float4 sh[G > 1 ? G : 1][W];
+  const int64_t n = (live_n ? (int64_t)*live_n : T) * H4, stride = T * H4;
   const float4* p = reinterpret_cast<const float4*>(part);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    float4 v = p[i];
-#pragma unroll 4
-    for (int s = 1; s < split; ++s) {
-      const float4 o = p[s * stride + i];
-      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+  const int x = threadIdx.x % W, y = threadIdx.x / W;
+  for (int64_t i0 = (int64_t)blockIdx.x * W; i0 < n; i0 += (int64_t)gridDim.x * W) {
+    const int64_t i = i0 + x;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) {
+#pragma unroll 2
+      for (int s = y; s < split; s += G) {
+        const float4 o = p[s * stride + i];
+        v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+      }
     }
-    const int64_t r = i / (H / 4), to = (row_idx ? (int64_t)row_idx[r] : r) * (H / 4) + (i - r * (H / 4));
+    if constexpr (G > 1) {
+      __syncthreads();
+      sh[y][x] = v;
+      __syncthreads();
+      if (y == 0)
+#pragma unroll
+        for (int k = 1; k < G; ++k) {
+          const float4 o = sh[k][x];
+          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
+    }
+    if (y != 0 || i >= n) continue;
+    v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+    const int64_t r = i / H4, to = (row_idx ? (int64_t)row_idx[r] : r) * H4 + (i - r * H4);
     if (out_bf16)
       reinterpret_cast<uint2*>(d_h)[to] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     else
@@ -209,6 +229,14 @@ struct CeLayout {
   int64_t vchunk;  // columns of a dlogits buffer
 };
 
+// Runs that d_h's reduction over a piece is cut into: as many as fill 152 SMs (a constant: the workspace's
+// size and the order of the sums follow from it), each of 8 K blocks or more (16 tokens, V = 32000, H = 768:
+// 50 runs of 10 blocks, not 31 of 16, fill 150 SMs for 93), and of kMaxChunkTiles vocabulary tiles at most.
+int ce_split(int64_t T, int64_t H, int chunk_tiles) {
+  const int64_t units = ((T + BM - 1) / BM) * ((H + BN - 1) / BN), blocks = (int64_t)chunk_tiles * (BN / BK);
+  return (int)std::max<int64_t>((chunk_tiles + kMaxChunkTiles - 1) / kMaxChunkTiles, std::min<int64_t>(152 / units, blocks / 8));
+}
+
 CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
   CeLayout w{};
   w.n_col_tiles = (int)((V + BN - 1) / BN);
@@ -217,7 +245,7 @@ CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
   w.chunk_tiles = (w.n_col_tiles + w.n_chunks - 1) / w.n_chunks;
   w.n_chunks = (w.n_col_tiles + w.chunk_tiles - 1) / w.chunk_tiles;
   w.vchunk = (int64_t)w.chunk_tiles * BN;
-  w.split = d_h_split(T, H, w.chunk_tiles);
+  w.split = ce_split(T, H, w.chunk_tiles);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -237,8 +265,7 @@ CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
   w.h_live = take((size_t)T * H * 2);
   w.dz[0] = take((size_t)T * w.vchunk * 2);
   w.dz[1] = w.n_chunks > 1 ? take((size_t)T * w.vchunk * 2) : w.dz[0];
-  // d_h's float sums: of each run, or over the pieces
-  w.part = take(w.split > 1 ? (size_t)w.split * T * H * 4 : w.n_chunks > 1 ? (size_t)T * H * 4 : 0);
+  w.part = take((size_t)w.split * T * H * 4);  // d_h's float sums, of each run
   w.total = off;
   return w;
 }
@@ -247,7 +274,7 @@ struct CeCall {
   const void *h, *W;
   int64_t T, V, H;
   const int32_t* target;
-  float smoothing, cap;
+  float smoothing, cap, scale;
   void *d_h, *dW;
   int dh_bf16, dw_bf16, dw_accumulate, cg;
   grpo_step_acc* acc;
@@ -278,42 +305,46 @@ int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc) {
   return c.cap > 0.f ? launch<CAP, false, false>(c.cg, ma, mb, mc, g, st) : launch<PLAIN, false, false>(c.cg, ma, mb, mc, g, st);
 }
 
-// d_h of one piece: dz [T, vc] W_c [vc, H], cut into runs where the layout says so.
+// The target of EPI_CE_STORE: [runs][rows][cols], boxes of 32 rows x 64 bytes in the 64-byte swizzle.
+bool map_out(CUtensorMap* m, void* base, int64_t cols, int64_t rows, int64_t runs, bool bf16) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t size = bf16 ? 2 : 4;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)runs};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * rows * size};
+  cuuint32_t box[3] = {(cuuint32_t)(64 / size), 32, 1}, estr[3] = {1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// d_h's float sums of one piece: dz [T, vc] W_c [vc, H] in runs, added to those of the pieces before.
 int ce_dh(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0, int64_t vc, cudaStream_t st) {
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mc;
   if (!map_k(&ma, dz, c.T, vc, c.ws.vchunk, BM) ||
-      !map_mn(&mb, static_cast<const __nv_bfloat16*>(c.W) + v0 * c.H, vc, c.H, c.H))
+      !map_mn(&mb, static_cast<const __nv_bfloat16*>(c.W) + v0 * c.H, vc, c.H, c.H) ||
+      !map_out(&mc, c.f(c.ws.part), c.H, c.T, c.ws.split, false))
     return GRPO_ERR_UNSUPPORTED;
   GemmArgs g{};
   g.live_n = c.live_n;
   g.live_mode = c.live_n ? LIVE_ROWS : LIVE_NONE;
-  g.row_idx = c.idx;
   g.M = c.T;
   g.N = c.H;
   g.K = vc;
-  g.n_n = (int)((c.H + BN - 1) / BN);
-  g.ldc = c.H;
+  g.split = (int)std::min<int64_t>(c.ws.split, (vc + BK - 1) / BK);  // (the last piece may have few K blocks)
+  g.n_n = (int)((c.H + BN - 1) / BN) * g.split;
   g.acc = c.acc;
-  g.out = c.d_h;
-  g.out_bf16 = c.dh_bf16;
+  g.out_scale = 1.f;
   g.accumulate = chunk > 0;
-  if (c.ws.split > 1) {  // (the last piece may have fewer K blocks than the others)
-    g.split = (int)std::min<int64_t>(c.ws.split, (vc + BK - 1) / BK);
-    g.n_n *= g.split;
-    g.split_stride = c.T * c.H;
-    g.C = c.f(c.ws.part);
-  } else if (chunk + 1 < c.ws.n_chunks) {
-    g.C = c.f(c.ws.part);
-  } else if (chunk > 0) {
-    g.add = c.f(c.ws.part);
-  }
-  return launch<EPI_CE_STORE, false, true>(c.cg, ma, mb, ma, g, st);
+  return launch<EPI_CE_STORE, false, true>(c.cg, ma, mb, mc, g, st);
 }
 
-// dW_c [vc, H] = dz^T h over the (unmasked) tokens.
+// dW_c [vc, H] = scale dz^T h over the (unmasked) tokens.
 int ce_dw(const CeCall& c, const __nv_bfloat16* dz, int64_t v0, int64_t vc, cudaStream_t st) {
-  CUtensorMap ma, mb;
-  if (!map_mn(&ma, dz, c.T, vc, c.ws.vchunk) || !map_mn(&mb, c.h_src, c.T, c.H, c.H)) return GRPO_ERR_UNSUPPORTED;
+  CUtensorMap ma, mb, mc;
+  if (!map_mn(&ma, dz, c.T, vc, c.ws.vchunk) || !map_mn(&mb, c.h_src, c.T, c.H, c.H) ||
+      !map_out(&mc, static_cast<uint8_t*>(c.dW) + v0 * c.H * (c.dw_bf16 ? 2 : 4), c.H, vc, 1, c.dw_bf16))
+    return GRPO_ERR_UNSUPPORTED;
   GemmArgs g{};
   g.live_n = c.live_n;
   g.live_mode = c.live_n ? LIVE_K : LIVE_NONE;
@@ -321,12 +352,11 @@ int ce_dw(const CeCall& c, const __nv_bfloat16* dz, int64_t v0, int64_t vc, cuda
   g.N = c.H;
   g.K = c.T;
   g.n_n = (int)((c.H + BN - 1) / BN);
-  g.ldc = c.H;
   g.acc = c.acc;
-  g.out = static_cast<uint8_t*>(c.dW) + v0 * c.H * (c.dw_bf16 ? 2 : 4);
+  g.out_scale = c.scale;
   g.out_bf16 = c.dw_bf16;
-  g.add = c.dw_accumulate ? static_cast<const float*>(g.out) : nullptr;
-  return launch<EPI_CE_STORE, true, true>(c.cg, ma, mb, ma, g, st);
+  g.accumulate = c.dw_accumulate;
+  return launch<EPI_CE_STORE, true, true>(c.cg, ma, mb, mc, g, st);
 }
 
 int ce_backward(const CeCall& c) {
@@ -361,10 +391,11 @@ int ce_backward(const CeCall& c) {
       if (c.dW && (rc = ce_dw(c, dz, v0, vc, bst)) != GRPO_OK) return rc;
       if (ov) GRPO_CUDA_TRY(cudaEventRecord(ov->buf_free[i & 1], bst));
     }
-    if (c.d_h && c.ws.split > 1) {
-      const int64_t blocks = std::min<int64_t>((c.T * c.H / 4 + 255) / 256, (int64_t)sm_count() * 8);
-      ce_split_sum_kernel<<<(unsigned)blocks, 256, 0, bst>>>(c.live_n, c.idx, c.T, c.H, c.f(c.ws.part), c.ws.split, c.d_h,
-                                                             c.dh_bf16);
+    if (c.d_h) {
+      const int H4 = (int)(c.H / 4);
+      auto kern = c.ws.split > 4 ? ce_dh_kernel<8> : ce_dh_kernel<1>;
+      const int64_t per = c.ws.split > 4 ? 32 : 256, blocks = std::min<int64_t>((c.T * H4 + per - 1) / per, (int64_t)sm_count() * 16);
+      kern<<<(unsigned)blocks, 256, 0, bst>>>(c.live_n, c.idx, c.T, H4, c.f(c.ws.part), c.ws.split, c.scale, c.d_h, c.dh_bf16);
       GRPO_CUDA_TRY(cudaGetLastError());
     }
     return GRPO_OK;
@@ -424,6 +455,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   c.target = target;
   c.smoothing = tm.label_smoothing;
   c.cap = tm.soft_cap;
+  c.scale = grad_scale;
   c.d_h = d_h;
   c.dW = dW;
   c.dh_bf16 = d_h_dtype == GRPO_DTYPE_BF16;
@@ -465,7 +497,6 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   r.zy = c.f(c.ws.zy);
   r.target = target;
   r.w_tok = tm.w_tok;
-  r.scale = grad_scale;
   r.smoothing = c.smoothing;
   r.z_loss = tm.z_loss;
   r.lse2 = c.f(c.ws.lse2);

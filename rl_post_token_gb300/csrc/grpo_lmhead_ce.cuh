@@ -5,8 +5,9 @@
 //   L         = (1 - eps) (lse - z_y) + eps (lse - mean_v z_v) + lambda lse^2
 //   dL/dx_v   = ((1 + 2 lambda lse) p_v - (1 - eps) [v = y] - eps / V) (1 - (z_v / c)^2)
 //
-// A tile's epilogue must end before the next tile's products (256 x 256 x H: 4 H clocks of the tensor
-// pipe); per element it takes one exponential and, with the cap, one or two more and a reciprocal.
+// A tile's epilogue must end before the next tile's products (256 x 256 x H on a pair of SMs: about 9 H
+// clocks); per element it takes one exponential and, with the cap, another and a reciprocal. Eight warps
+// share it, two to each quarter of the accumulator's lanes: `half` is the columns' half that is a warp's.
 
 namespace grpo {
 namespace lmhead {
@@ -35,17 +36,22 @@ __device__ __forceinline__ void tanh_pair(float u, float& t, float& d) {
 }
 
 // Softmax partials of one 256-column tile, the sum of its logits (with label smoothing) and the target
-// logit. The columns past the vocabulary count as -inf, and add nothing to the sum.
+// logit. The columns past the vocabulary count as -inf, and add nothing to the sum. The second half's warp
+// hands its row's three numbers to the first's through `join` (trow: the row there); named barrier `bar`
+// belongs to the two warps and the accumulator's buffer, so that its next use comes two tiles later, after
+// both have released that buffer.
 template <bool CAP>
-__device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t taddr, int64_t row, bool rok, int ct) {
+__device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t taddr, int64_t row, bool rok, int ct,
+                                                int half, float* join, int trow, int bar) {
   const int64_t c0 = (int64_t)ct * BN;
   const int64_t tok = (rok && g.row_idx) ? (int64_t)g.row_idx[row] : row;
   const int32_t y = rok ? g.target[tok] : -1;
   const bool own = y >= c0 && y < c0 + BN;
   MS acc{-INFINITY, 0.f};
   float zy = 0.f, zsum = 0.f;
+  bool got = false;
 #pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
+  for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
     float v[32];
     tmem_ld32(taddr + c * 32, v);
     const int64_t cb = c0 + c * 32;
@@ -59,6 +65,7 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t tadd
       }
     }
     if (own && y >= cb && y < cb + 32) {
+      got = true;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         if (cb + i == y) zy = v[i];
@@ -77,31 +84,43 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t tadd
     }
     lazy_online2<32>(acc, v);
   }
+  if (got) g.zy[tok] = zy;
+  float* j = join + trow * 3;
+  if (half) {
+    j[0] = acc.m;
+    j[1] = acc.s;
+    j[2] = zsum;
+    asm volatile("bar.arrive %0, 64;" ::"r"(bar) : "memory");
+    return;
+  }
+  asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+  acc = ms2_combine(acc, MS{j[0], j[1]});
   if (rok) {
     g.part_m[(int64_t)ct * g.M + row] = acc.m;
     g.part_s[(int64_t)ct * g.M + row] = acc.s;
-    if (g.part_s2) g.part_s2[(int64_t)ct * g.M + row] = zsum;
-    if (own) g.zy[tok] = zy;
+    if (g.part_s2) g.part_s2[(int64_t)ct * g.M + row] = zsum + j[2];
   }
 }
 
-// bf16 dlogits of one tile (with respect to x), staged in shared memory and written by TMA stores as
-// those of the policy loss (epi_dlogits). The products with W and h take them as bf16: the operands'
-// type of the tensor cores at their full rate, half a step (2^-9 of the largest of a binade) per entry.
+// bf16 dlogits of one tile (with respect to x, without the uniform grad_scale), staged in shared memory and
+// written by TMA stores as those of the policy loss (epi_dlogits). The products with W and h take them as
+// bf16, the operands' type at the tensor cores' full rate: half a step (2^-8) per entry. grad_scale is
+// applied to the float sums: an unlikely target's entry is then next to -1 and loses nothing, where scaled
+// by 1/N every such entry would be rounded the same way (0.3% of the gradients' length at N = 4117).
 template <bool CAP>
 __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensorMap* map_c, uint32_t taddr,
-                                               int64_t row, bool rok, int ct, int64_t warp_row0, int64_t rows_store,
-                                               uint32_t stage_buf, int lane) {
+                                               int64_t row, bool rok, int ct, int half, int64_t warp_row0,
+                                               int64_t rows_store, uint32_t stage_buf, uint32_t& box, int lane) {
   const int64_t c0 = (int64_t)ct * BN;
   const int64_t tok = (rok && g.row_idx) ? (int64_t)g.row_idx[row] : row;
   const int32_t y = rok ? g.target[tok] : -1;
-  const float sw = rok ? g.coef[tok] : 0.f;  // s w
+  const float sw = rok ? g.coef[tok] : 0.f;  // w
   const float l2 = rok ? g.lse2[tok] : 0.f, cp = rok ? g.ea[tok] : 0.f;
   const float ce = sw * g.ce_smooth, cy = sw * g.ce_hot;
   const bool live = sw != 0.f;
   const uint32_t swz = (uint32_t)((lane >> 1) & 3);
 #pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
+  for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
     float v[32];
     tmem_ld32(taddr + c * 32, v);
     const int64_t cb = c0 + c * 32;
@@ -137,8 +156,8 @@ __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensor
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[i] = 0u;
     }
-    const uint32_t buf = stage_buf + (uint32_t)(c & 1) * EPI_BUF_BYTES;
-    if (lane == 0) bulk_wait_read<1>();  // the store issued from this buffer two groups ago has read it
+    const uint32_t buf = stage_buf + (box++ & 1u) * EPI_BUF_BYTES;
+    if (lane == 0) bulk_wait_read<1>();  // the store before the last, from this buffer, has read it
     __syncwarp();
     const uint32_t rb = buf + (uint32_t)lane * 64u;
 #pragma unroll
@@ -155,58 +174,64 @@ __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensor
   }
 }
 
-// One output tile of d_h or dW: out[row][n0 .. n0 + 256) = (add ? add : 0) + D as float or, rounded once,
-// bf16; with g.C set, the float sums of run `run` to it instead (g.accumulate: added to it). Columns past N are skipped (N is a
-// multiple of 8). The shared-memory transposition of epi_store_f32: a warp's access covers 4 rows.
-__device__ __forceinline__ void epi_ce_store(const GemmArgs& g, int run, uint32_t taddr, int64_t row, bool rok,
-                                             int64_t n0, uint32_t buf, int lane) {
-  float* part = g.C ? g.C + run * g.split_stride : nullptr;
-  const float* add = part ? (g.accumulate ? part : nullptr) : g.add;
-  // the row of out (d_h over the compact tokens: the token's), -1 past the rows
-  const int crow = !rok ? -1 : g.row_idx && !part ? g.row_idx[row] : (int)row;
-  const int64_t row0 = row - lane;
-  const uint32_t put = buf + (uint32_t)lane * 128u, sw = (uint32_t)(lane & 7);
+// 3-D TMA tile store, plain or as a float addition (every element gets one addition per launch: the order
+// of the sums is that of the launches).
+__device__ __forceinline__ void tma_store3d(const CUtensorMap* map, uint32_t src, int x, int y, int z, bool add) {
+  if (add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// One staged box: lane's 64 bytes (32 bf16 or 16 floats of its row) in the 64-byte swizzle, then the store.
+// `box` counts a warp's boxes over all its tiles: the two buffers are used in turn whatever a tile leaves out.
+__device__ __forceinline__ void put_box(const CUtensorMap* map, uint32_t stage_buf, uint32_t& box, int lane, const uint32_t (&w)[16], int x,
+                                        int y, int z, bool add) {
+  const uint32_t buf = stage_buf + (box++ & 1u) * EPI_BUF_BYTES;
+  if (lane == 0) bulk_wait_read<1>();  // the store before the last, from this buffer, has read it
+  __syncwarp();
+  const uint32_t rb = (buf + (uint32_t)lane * 64u) | ((uint32_t)((lane >> 1) & 3) << 4);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rb ^ ((uint32_t)q << 4)), "r"(w[4 * q]),
+                 "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                 : "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store3d(map, buf, x, y, z, add);
+    bulk_commit();
+  }
+}
+
+// One output tile of d_h (its float sums: rows are compact, run `run` the map's third extent) or dW: the
+// product times out_scale, as float or, rounded once, bf16. The map's extents clip the rows and columns.
+__device__ __forceinline__ void epi_ce_store(const GemmArgs& g, const CUtensorMap* map_c, int run, uint32_t taddr,
+                                             int64_t warp_row0, int64_t M, int64_t n0, int half, uint32_t buf, uint32_t& box,
+                                             int lane) {
 #pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
+  for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
     float v[32];
     tmem_ld32(taddr + c * 32, v);
     const int64_t col = n0 + c * 32;
-    if (col >= g.N) continue;  // warp-uniform
-    __syncwarp();              // the group before has been read
+    if (col >= g.N || warp_row0 >= M) continue;  // warp-uniform
+    uint32_t w[16];
+    if (g.out_bf16) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(put + (((uint32_t)q ^ sw) << 4)), "f"(v[4 * q]),
-                   "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
-                   : "memory");
-    __syncwarp();
-    const int64_t at = col + (lane & 7) * 4;  // lane: columns at .. at + 3 of rows lane / 8 + 4 i
-    const bool in = at < g.N;
-    float4 o[8];
+      for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * g.out_scale, v[2 * i + 1] * g.out_scale);
+      put_box(map_c, buf, box, lane, w, (int)col, (int)warp_row0, run, false);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int64_t r = i * 4 + (lane >> 3);
-      const bool on = __shfl_sync(0xffffffffu, crow, (int)r) >= 0 && in;
-      if (add && on) o[i] = *reinterpret_cast<const float4*>(add + (row0 + r) * g.ldc + at);
-    }
+      for (int b = 0; b < 2; ++b) {
+        if (col + b * 16 >= g.N) break;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3), cr = __shfl_sync(0xffffffffu, crow, r);
-      float4 d;
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
-                   : "r"(buf + (uint32_t)r * 128u + (((uint32_t)(lane & 7) ^ (uint32_t)(r & 7)) << 4))
-                   : "memory");
-      if (cr < 0 || !in) continue;
-      const int64_t to = cr * g.ldc + at;
-      d = make_float4(o[i].x + d.x, o[i].y + d.y, o[i].z + d.z, o[i].w + d.w);
-      if (part)
-        *reinterpret_cast<float4*>(part + to) = d;
-      else if (g.out_bf16)
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.out) + to) =
-            make_uint2(pack_bf16x2(d.x, d.y), pack_bf16x2(d.z, d.w));
-      else
-        *reinterpret_cast<float4*>(static_cast<float*>(g.out) + to) = d;
+        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[b * 16 + i] * g.out_scale);
+        put_box(map_c, buf, box, lane, w, (int)col + b * 16, (int)warp_row0, run, g.accumulate);
+      }
     }
   }
 }

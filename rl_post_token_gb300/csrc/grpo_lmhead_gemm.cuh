@@ -33,7 +33,6 @@ namespace lmhead {
 constexpr int BM = 128;  // accumulator rows per CTA (TMEM lanes)
 constexpr int BN = 256;  // accumulator columns per tile
 constexpr int BK = 64;   // K per stage: one 128-byte swizzle row of bf16
-constexpr int NTHREADS = 192;
 constexpr int TMEM_COLS = 2 * BN;
 
 // EPI_PARTIALS_ENT: the partials plus sum e z per tile (the entropy's third accumulator)
@@ -53,6 +52,7 @@ enum Epi : int {
 
 constexpr bool epi_is_dlogits(int e) { return e == EPI_DLOGITS || e == EPI_CE_DLOGITS || e == EPI_CE_DLOGITS_CAP; }
 constexpr bool epi_is_store(int e) { return e == EPI_STORE_F32 || e == EPI_CE_STORE; }
+constexpr bool epi_is_ce(int e) { return e >= EPI_CE_PARTIALS; }
 
 // Dlogits epilogue staging: each epilogue warp writes its 32 rows x 32 columns of bf16 (2 KB,
 // 64-byte rows in the 64-byte swizzle a TMA store expects) into one of two buffers, and one lane
@@ -69,8 +69,13 @@ struct Shape {
   static constexpr int B_BYTES = B_ROWS * BK * 2;        // 16 KB (CG = 2) or 32 KB
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // bytes this CTA receives per stage
   static constexpr int STAGES = CG == 2 ? 6 : 4;
-  static constexpr int EPI_BYTES = epi_is_dlogits(EPI) || epi_is_store(EPI) ? EPI_WARPS * 2 * EPI_BUF_BYTES : 0;
-  static constexpr size_t SMEM = 1024 /*alignment slack*/ + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + 256;
+  // epilogue warps: with 4 (a warp per scheduler) a tile's epilogue takes longer than its products below
+  // H = 1536 or so; the cross entropy's instances have 8, two to a lane quarter, each half of the columns
+  static constexpr int WARPS = epi_is_ce(EPI) ? 2 * EPI_WARPS : EPI_WARPS;
+  static constexpr int THREADS = 64 + 32 * WARPS;
+  static constexpr int EPI_BYTES = epi_is_dlogits(EPI) || epi_is_store(EPI) ? WARPS * 2 * EPI_BUF_BYTES : 0;
+  static constexpr int JOIN_BYTES = epi_is_ce(EPI) && !epi_is_dlogits(EPI) && !epi_is_store(EPI) ? 2 * BM * 12 : 0;
+  static constexpr size_t SMEM = 1024 /*alignment slack*/ + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + JOIN_BYTES + 256;
 };
 
 // Instruction descriptor of tcgen05.mma kind::f16: D f32, A and B bf16, the major-ness of each
@@ -275,10 +280,9 @@ struct GemmArgs {
   // ea: [T] s w (1 + 2 lambda lse); coef: [T] s w)
   float cap, inv_cap;      // the soft cap c and 1 / c (_CAP)
   float ce_hot, ce_smooth; // 1 - eps, eps / V
-  // EPI_CE_STORE: out[row][ldc] = add[compact row][ldc] + A B (add NULL: the product alone); out_bf16:
-  // out is bf16, else float. C, when not NULL, takes the float sums instead of out.
-  void* out;
-  const float* add;
+  // EPI_CE_STORE: the product times out_scale to map_c (rows x columns x runs): float, or bf16 (out_bf16),
+  // or added to the float there (accumulate)
+  float out_scale;
   int out_bf16;
 };
 
@@ -441,7 +445,14 @@ __device__ __forceinline__ void epi_dlogits(const GemmArgs& g, const CUtensorMap
       for (int i = 0; i < 16; ++i) w[i] = 0u;
     }
     const uint32_t buf = stage_buf + (uint32_t)(c & 1) * EPI_BUF_BYTES;
-    if (lane == 0) bulk_wait_read<1>();  // the store issued from this buffer two groups ago has read it
+    // the store issued from this buffer two groups ago has read it; a tile's first group waits for them
+    // all (the tile before may have ended on this buffer: a vocabulary's tail may leave out groups)
+    if (lane == 0) {
+      if (c == 0)
+        bulk_wait_read<0>();
+      else
+        bulk_wait_read<1>();
+    }
     __syncwarp();
     const uint32_t rb = buf + (uint32_t)lane * 64u;
 #pragma unroll
@@ -528,7 +539,7 @@ namespace lmhead {
 // ---- the kernel ---------------------------------------------------------------------------------
 
 template <int CG, int EPI, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(Shape<CG, EPI>::THREADS, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_c, GemmArgs g) {
   using S = Shape<CG, EPI>;
@@ -537,7 +548,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
   const uint32_t epi_base = sbase + S::STAGES * S::STAGE_BYTES;  // dlogits staging (1024-aligned)
-  uint64_t* full = reinterpret_cast<uint64_t*>(sgen + S::STAGES * S::STAGE_BYTES + S::EPI_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sgen + S::STAGES * S::STAGE_BYTES + S::EPI_BYTES + S::JOIN_BYTES);
   uint64_t* empty = full + S::STAGES;
   uint64_t* tfull = empty + S::STAGES;  // [2]
   uint64_t* tempty = tfull + 2;         // [2]
@@ -553,7 +564,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4 * CG);  // every epilogue warp of the cluster releases the buffer
+      mbar_init(&tempty[b], S::WARPS * CG);  // every epilogue warp of the cluster releases the buffer
     }
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -685,10 +696,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       }
     }
   } else {
-    // ---- epilogue: warps 2..5, thread = TMEM lane = accumulator row ----
+    // ---- epilogue: warps 2 and on, thread = TMEM lane = accumulator row ----
     const int quarter = warp & 3;  // the TMEM lane quarter this warp may access
     const int trow = quarter * 32 + lane;
-    uint32_t ab = 0, aphase = 0;
+    const int half = (warp - 2) >> 2;  // the columns' half, of 8 warps
+    const uint32_t ce_buf = epi_base + (uint32_t)(half * 4 + quarter) * 2u * EPI_BUF_BYTES;
+    uint32_t ab = 0, aphase = 0, box = 0;
     for (int t = first; t < n_units; t += stride) {
       int mu, nu;
       unit_coords(g, n_m, t, mu, nu);
@@ -705,14 +718,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         epi_dlogits(g, &map_c, taddr, row, rok, g.col_tile0 + nu, row - lane, rows_store,
                     epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
       else if constexpr (EPI == EPI_CE_PARTIALS || EPI == EPI_CE_PARTIALS_CAP)
-        epi_ce_partials<EPI == EPI_CE_PARTIALS_CAP>(g, taddr, row, rok, g.col_tile0 + nu);
+        epi_ce_partials<EPI == EPI_CE_PARTIALS_CAP>(g, taddr, row, rok, g.col_tile0 + nu, half,
+                                                    reinterpret_cast<float*>(sgen + S::STAGES * S::STAGE_BYTES) + ab * BM * 3,
+                                                    trow, 1 + (int)ab * 4 + quarter);
       else if constexpr (EPI == EPI_CE_DLOGITS || EPI == EPI_CE_DLOGITS_CAP)
-        epi_ce_dlogits<EPI == EPI_CE_DLOGITS_CAP>(g, &map_c, taddr, row, rok, g.col_tile0 + nu, row - lane, rows_store,
-                                                  epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
+        epi_ce_dlogits<EPI == EPI_CE_DLOGITS_CAP>(g, &map_c, taddr, row, rok, g.col_tile0 + nu, half, row - lane,
+                                                  rows_store, ce_buf, box, lane);
       else if constexpr (EPI == EPI_CE_STORE) {
         int k0, k1;
         const int run = unit_k(nu, k0, k1);
-        epi_ce_store(g, run, taddr, row, rok, (int64_t)nu * BN, epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
+        epi_ce_store(g, &map_c, run, taddr, row - lane, M, (int64_t)nu * BN, half, ce_buf, box, lane);
       } else {
         int k0, k1;
         const int run = unit_k(nu, k0, k1);
@@ -732,7 +747,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         aphase ^= 1u;
       }
     }
-    if (epi_is_dlogits(EPI) && lane == 0) bulk_wait_all();  // this warp's stores are complete
+    if ((epi_is_dlogits(EPI) || EPI == EPI_CE_STORE) && lane == 0) bulk_wait_all();  // this warp's stores are complete
   }
 
   fence_before();

@@ -83,7 +83,7 @@ int launch_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc
   attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(NTHREADS, 1, 1);
+  cfg.blockDim = dim3(S::THREADS, 1, 1);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
