@@ -6,8 +6,9 @@
 //  pass A     per (token, 256 vocabulary entries) the softmax's (shift, sum), the target logit and, with
 //             label smoothing, the sum of the logits
 //  reduce     per token the tiles joined in a fixed order: loss, log-prob, lse and the gradient's factors
-//  backward   per vocabulary piece the logits once more, their bf16 dlogits into one of two buffers of
-//             that piece; d_h (+)= dz W_c and dW_c = dz^T h on a second stream beside the next piece
+//  backward   per vocabulary piece the logits once more, their bf16 dlogits into one of two buffers; then
+//             d_h (+)= dz W_c and dW_c = dz^T h in one launch (grpo_lmhead_ce_bwd.cuh), on a second stream
+//             beside the next piece's
 //
 // Bound by the tensor cores with many tokens: 2 T V H flops of pass A and 6 T V H of the backward, of which
 // the 2 T V H of the logits' second forming replace a store and two reads of the [T, V] logits. With few
@@ -16,7 +17,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "grpo_lmhead_gemm.cuh"
+#include "grpo_lmhead_ce_bwd.cuh"
 #include "grpo_lmhead_host.cuh"
 
 namespace grpo {
@@ -105,9 +106,9 @@ struct CeReduceArgs {
   const int32_t *idx, *live_n;  // the compact order, or NULL
 };
 
-// A block takes 32 tokens (lane = token: a partial's load is one 128-byte line), its warps every 16th
-// vocabulary tile in order; warp 0 joins the warps' in order.
-constexpr int kCeReduceWarps = 16;
+// A block takes 32 tokens (lane = token: a partial's load is one 128-byte line), its warps every 32nd
+// vocabulary tile in order; four warps join eight warps' each, warp 0 the four, in order.
+constexpr int kCeReduceWarps = 32;
 
 __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduceArgs a) {
   __shared__ float wm[kCeReduceWarps][32], ws[kCeReduceWarps][32], wz[kCeReduceWarps][32];
@@ -128,19 +129,32 @@ __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduce
   ws[w][lane] = t.s;
   wz[w][lane] = z;
   __syncthreads();
+  auto join = [&](int first, int step, int n) {
+    MS r{wm[first][lane], ws[first][lane]};
+    float s = wz[first][lane];
+#pragma unroll
+    for (int k = 1; k < n; ++k) {
+      r = ms2_combine(r, MS{wm[first + k * step][lane], ws[first + k * step][lane]});
+      s += wz[first + k * step][lane];
+    }
+    t = r;
+    z = s;
+  };
+  if (w < 4) {
+    join(w * 8, 1, 8);
+    wm[w * 8][lane] = t.m;
+    ws[w * 8][lane] = t.s;
+    wz[w * 8][lane] = z;
+  }
+  __syncthreads();
   if (w != 0) return;
   bool bad = false;
   if (in) {
     const int64_t tok = a.idx ? (int64_t)a.idx[i] : i;
     float loss = 0.f, logp = 0.f, lse = 0.f, l2 = 0.f, sw = 0.f, cp = 0.f;
     if (live) {
-      MS tot{wm[0][lane], ws[0][lane]};
-      z = wz[0][lane];
-#pragma unroll
-      for (int k = 1; k < kCeReduceWarps; ++k) {
-        tot = ms2_combine(tot, MS{wm[k][lane], ws[k][lane]});
-        z += wz[k][lane];
-      }
+      join(0, 8, 4);
+      const MS tot = t;
       const float nan = __int_as_float(0x7fc00000);
       const int32_t y = a.target[tok];
       const float zy = y >= 0 && (int64_t)y < a.V ? a.zy[tok] : nan;
@@ -229,18 +243,26 @@ struct CeLayout {
   int64_t vchunk;  // columns of a dlogits buffer
 };
 
-// Runs that d_h's reduction over a piece is cut into: as many as fill 152 SMs (a constant: the workspace's
-// size and the order of the sums follow from it), each of 8 K blocks or more (16 tokens, V = 32000, H = 768:
-// 50 runs of 10 blocks, not 31 of 16, fill 150 SMs for 93), and of kMaxChunkTiles vocabulary tiles at most.
+// Vocabulary tiles per piece: pieces of up to 256 MB of dlogits, 66 tiles at least (16896 columns: 277 MB
+// at 8192 tokens). Larger pieces mean fewer launches and fuller last rounds; the dlogits' way through memory
+// hides behind the products.
+int ce_chunk_tiles(int64_t T) {
+  return (int)std::max<int64_t>(kMaxChunkTiles, std::min<int64_t>(((int64_t)256 << 20) / (T * BN * 2), INT32_MAX / BN));
+}
+
+// Runs that d_h's reduction over a piece is cut into: so many that a unit of d_h is at most a third of what
+// one of 76 pairs of SMs has to do for d_h and dW together (the rest then evens out), each of 8 K blocks or
+// more. The sizes alone decide: the workspace's size and the order of the sums follow from it.
 int ce_split(int64_t T, int64_t H, int chunk_tiles) {
-  const int64_t units = ((T + BM - 1) / BM) * ((H + BN - 1) / BN), blocks = (int64_t)chunk_tiles * (BN / BK);
-  return (int)std::max<int64_t>((chunk_tiles + kMaxChunkTiles - 1) / kMaxChunkTiles, std::min<int64_t>(152 / units, blocks / 8));
+  const int64_t n_nt = (H + BN - 1) / BN, kb1 = (int64_t)chunk_tiles * (BN / BK), kb2 = (T + BK - 1) / BK;
+  const int64_t load = ((T + 2 * BM - 1) / (2 * BM) * n_nt * kb1 + (int64_t)chunk_tiles * n_nt * kb2) / 76;
+  return (int)std::max<int64_t>(1, std::min<int64_t>((3 * kb1 + load - 1) / std::max<int64_t>(load, 1), kb1 / 8));
 }
 
 CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
   CeLayout w{};
   w.n_col_tiles = (int)((V + BN - 1) / BN);
-  const int most = distill_chunk_tiles(T);
+  const int most = ce_chunk_tiles(T);
   w.n_chunks = (w.n_col_tiles + most - 1) / most;
   w.chunk_tiles = (w.n_col_tiles + w.n_chunks - 1) / w.n_chunks;
   w.n_chunks = (w.n_col_tiles + w.chunk_tiles - 1) / w.chunk_tiles;
@@ -318,45 +340,33 @@ bool map_out(CUtensorMap* m, void* base, int64_t cols, int64_t rows, int64_t run
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// d_h's float sums of one piece: dz [T, vc] W_c [vc, H] in runs, added to those of the pieces before.
-int ce_dh(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0, int64_t vc, cudaStream_t st) {
-  CUtensorMap ma, mb, mc;
-  if (!map_k(&ma, dz, c.T, vc, c.ws.vchunk, BM) ||
-      !map_mn(&mb, static_cast<const __nv_bfloat16*>(c.W) + v0 * c.H, vc, c.H, c.H) ||
-      !map_out(&mc, c.f(c.ws.part), c.H, c.T, c.ws.split, false))
+// Both products of piece `chunk`, the vocabulary columns [v0, v0 + vc).
+template <int CG>
+int ce_products(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0, int64_t vc, cudaStream_t st) {
+  CUtensorMap dz_k = {}, w = {}, part = {}, dz_mn = {}, h = {}, dw = {};
+  if (c.d_h && (!map_k(&dz_k, dz, c.T, vc, c.ws.vchunk, BM) ||
+                !map_mn(&w, static_cast<const __nv_bfloat16*>(c.W) + v0 * c.H, vc, c.H, c.H) ||
+                !map_out(&part, c.f(c.ws.part), c.H, c.T, c.ws.split, false)))
     return GRPO_ERR_UNSUPPORTED;
-  GemmArgs g{};
-  g.live_n = c.live_n;
-  g.live_mode = c.live_n ? LIVE_ROWS : LIVE_NONE;
-  g.M = c.T;
-  g.N = c.H;
-  g.K = vc;
+  if (c.dW && (!map_mn(&dz_mn, dz, c.T, vc, c.ws.vchunk) || !map_mn(&h, c.h_src, c.T, c.H, c.H) ||
+               !map_out(&dw, static_cast<uint8_t*>(c.dW) + v0 * c.H * (c.dw_bf16 ? 2 : 4), c.H, vc, 1, c.dw_bf16)))
+    return GRPO_ERR_UNSUPPORTED;
+  BwdArgs g{};
+  g.T = c.T;
+  g.H = c.H;
+  g.vc = vc;
+  g.with_dh = c.d_h != nullptr;
+  g.with_dw = c.dW != nullptr;
   g.split = (int)std::min<int64_t>(c.ws.split, (vc + BK - 1) / BK);  // (the last piece may have few K blocks)
-  g.n_n = (int)((c.H + BN - 1) / BN) * g.split;
-  g.acc = c.acc;
-  g.out_scale = 1.f;
-  g.accumulate = chunk > 0;
-  return launch<EPI_CE_STORE, false, true>(c.cg, ma, mb, mc, g, st);
-}
-
-// dW_c [vc, H] = scale dz^T h over the (unmasked) tokens.
-int ce_dw(const CeCall& c, const __nv_bfloat16* dz, int64_t v0, int64_t vc, cudaStream_t st) {
-  CUtensorMap ma, mb, mc;
-  if (!map_mn(&ma, dz, c.T, vc, c.ws.vchunk) || !map_mn(&mb, c.h_src, c.T, c.H, c.H) ||
-      !map_out(&mc, static_cast<uint8_t*>(c.dW) + v0 * c.H * (c.dw_bf16 ? 2 : 4), c.H, vc, 1, c.dw_bf16))
-    return GRPO_ERR_UNSUPPORTED;
-  GemmArgs g{};
+  g.dh_accumulate = chunk > 0;
+  g.dw_accumulate = c.dw_accumulate;
+  g.dw_bf16 = c.dw_bf16;
+  g.dw_scale = c.scale;
   g.live_n = c.live_n;
-  g.live_mode = c.live_n ? LIVE_K : LIVE_NONE;
-  g.M = vc;
-  g.N = c.H;
-  g.K = c.T;
-  g.n_n = (int)((c.H + BN - 1) / BN);
   g.acc = c.acc;
-  g.out_scale = c.scale;
-  g.out_bf16 = c.dw_bf16;
-  g.accumulate = c.dw_accumulate;
-  return launch<EPI_CE_STORE, true, true>(c.cg, ma, mb, mc, g, st);
+  const int64_t n_nt = (c.H + BN - 1) / BN, rows = BM * CG;
+  const int64_t units = n_nt * ((c.d_h ? (c.T + rows - 1) / rows * g.split : 0) + (c.dW ? (vc + rows - 1) / rows : 0));
+  return launch_units<CG, Shape<CG, EPI_CE_STORE>, &bwd_kernel<CG>>(units, st, dz_k, w, part, dz_mn, h, dw, g);
 }
 
 int ce_backward(const CeCall& c) {
@@ -387,8 +397,8 @@ int ce_backward(const CeCall& c) {
         GRPO_CUDA_TRY(cudaEventRecord(ov->dz_ready, c.st));
         GRPO_CUDA_TRY(cudaStreamWaitEvent(bst, ov->dz_ready, 0));
       }
-      if (c.d_h && (rc = ce_dh(c, dz, i, v0, vc, bst)) != GRPO_OK) return rc;
-      if (c.dW && (rc = ce_dw(c, dz, v0, vc, bst)) != GRPO_OK) return rc;
+      rc = c.cg == 2 ? ce_products<2>(c, dz, i, v0, vc, bst) : ce_products<1>(c, dz, i, v0, vc, bst);
+      if (rc != GRPO_OK) return rc;
       if (ov) GRPO_CUDA_TRY(cudaEventRecord(ov->buf_free[i & 1], bst));
     }
     if (c.d_h) {

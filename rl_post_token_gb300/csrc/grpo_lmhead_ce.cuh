@@ -35,18 +35,36 @@ __device__ __forceinline__ void tanh_pair(float u, float& t, float& d) {
   d = small ? fmaf(-ts, ts, 1.f) : 4.f * (e * r) * r;
 }
 
+// Gives a tile's accumulator back to the MMA issuer, once a warp has loaded its last columns: before it
+// computes on them and stores. (The loads have completed; nothing else is published, so that the arrive at
+// the other CTA need not wait for the tile's global stores.)
+struct AccRelease {
+  uint32_t remote;  // the even CTA's barrier as a cluster address, or 0: `local`
+  uint64_t* local;
+  int lane;
+  __device__ __forceinline__ void operator()() const {
+    fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (remote)
+        mbar_arrive_remote_relaxed(remote);
+      else
+        mbar_arrive(local);
+    }
+  }
+};
+
 // Softmax partials of one 256-column tile, the sum of its logits (with label smoothing) and the target
 // logit. The columns past the vocabulary count as -inf, and add nothing to the sum. The second half's warp
-// hands its row's three numbers to the first's through `join` (trow: the row there); named barrier `bar`
-// belongs to the two warps and the accumulator's buffer, so that its next use comes two tiles later, after
-// both have released that buffer.
+// hands its row's three numbers to the first's through `join` (its row's place there, one of two in turn);
+// the two warps meet at named barrier `bar` once a tile, so that the place is written again only after the
+// other has read it and met once more.
 template <bool CAP>
 __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t taddr, int64_t row, bool rok, int ct,
-                                                int half, float* join, int trow, int bar) {
-  const int64_t c0 = (int64_t)ct * BN;
+                                                int half, float* join, int bar, const AccRelease& release) {
+  const int V = (int)g.V, c0 = ct * BN;
   const int64_t tok = (rok && g.row_idx) ? (int64_t)g.row_idx[row] : row;
-  const int32_t y = rok ? g.target[tok] : -1;
-  const bool own = y >= c0 && y < c0 + BN;
+  const int y = rok ? g.target[tok] : -1;
   MS acc{-INFINITY, 0.f};
   float zy = 0.f, zsum = 0.f;
   bool got = false;
@@ -54,8 +72,9 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t tadd
   for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
     float v[32];
     tmem_ld32(taddr + c * 32, v);
-    const int64_t cb = c0 + c * 32;
-    if (cb >= g.V) continue;  // warp-uniform
+    if (c == (half + 1) * (BN / 64) - 1) release();
+    const int cb = c0 + c * 32;
+    if (cb >= V) continue;  // warp-uniform
     if constexpr (CAP) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -64,41 +83,44 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t tadd
         v[i] = g.cap * t;
       }
     }
-    if (own && y >= cb && y < cb + 32) {
+    const int k = y - cb;
+    if (y >= cb && k < 32) {
       got = true;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (cb + i == y) zy = v[i];
+        if (i == k) zy = v[i];
     }
-    const bool tail = cb + 32 > g.V;
-    if (g.part_s2) {
-      float s[32];
+    if (cb + 32 > V) {  // warp-uniform
+      if (g.part_s2) {
+        float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = !tail || cb + i < g.V ? v[i] : 0.f;
-      zsum += tree_sum<32>(s);
-    }
-    if (tail) {
+        for (int i = 0; i < 32; ++i) s += i < V - cb ? v[i] : 0.f;
+        zsum += s;
+      }
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (cb + i >= g.V) v[i] = -INFINITY;
+        if (i >= V - cb) v[i] = -INFINITY;
+    } else if (g.part_s2) {
+      float s[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = v[i];
+      zsum += tree_sum<32>(s);
     }
     lazy_online2<32>(acc, v);
   }
   if (got) g.zy[tok] = zy;
-  float* j = join + trow * 3;
   if (half) {
-    j[0] = acc.m;
-    j[1] = acc.s;
-    j[2] = zsum;
-    asm volatile("bar.arrive %0, 64;" ::"r"(bar) : "memory");
-    return;
+    join[0] = acc.m;
+    join[1] = acc.s;
+    join[2] = zsum;
   }
   asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
-  acc = ms2_combine(acc, MS{j[0], j[1]});
+  if (half) return;
+  acc = ms2_combine(acc, MS{join[0], join[1]});
   if (rok) {
     g.part_m[(int64_t)ct * g.M + row] = acc.m;
     g.part_s[(int64_t)ct * g.M + row] = acc.s;
-    if (g.part_s2) g.part_s2[(int64_t)ct * g.M + row] = zsum + j[2];
+    if (g.part_s2) g.part_s2[(int64_t)ct * g.M + row] = zsum + join[2];
   }
 }
 
@@ -110,10 +132,11 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t tadd
 template <bool CAP>
 __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensorMap* map_c, uint32_t taddr,
                                                int64_t row, bool rok, int ct, int half, int64_t warp_row0,
-                                               int64_t rows_store, uint32_t stage_buf, uint32_t& box, int lane) {
-  const int64_t c0 = (int64_t)ct * BN;
+                                               int64_t rows_store, uint32_t stage_buf, uint32_t& box, int lane,
+                                               const AccRelease& release) {
+  const int V = (int)g.V, c0 = ct * BN;
   const int64_t tok = (rok && g.row_idx) ? (int64_t)g.row_idx[row] : row;
-  const int32_t y = rok ? g.target[tok] : -1;
+  const int y = rok ? g.target[tok] : -1;
   const float sw = rok ? g.coef[tok] : 0.f;  // w
   const float l2 = rok ? g.lse2[tok] : 0.f, cp = rok ? g.ea[tok] : 0.f;
   const float ce = sw * g.ce_smooth, cy = sw * g.ce_hot;
@@ -123,19 +146,21 @@ __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensor
   for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
     float v[32];
     tmem_ld32(taddr + c * 32, v);
-    const int64_t cb = c0 + c * 32;
+    if (c == (half + 1) * (BN / 64) - 1) release();
+    const int cb = c0 + c * 32;
     // warp-uniform: past the vocabulary, or all 32 rows past the rows to be written
-    if (cb >= g.V || warp_row0 >= rows_store) continue;
+    if (cb >= V || warp_row0 >= rows_store) continue;
     uint32_t w[16];
     if (live) {
-      const bool hit = y >= cb && y < cb + 32;
+      const int k = y - cb;
+      const bool hit = y >= cb && k < 32;
       if constexpr (CAP) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float t, d;
           tanh_pair(v[i] * g.inv_cap, t, d);
           const float p = ex2(fmaf(g.cap * t, kLog2e, -l2));
-          v[i] = (fmaf(cp, p, -ce) - (cb + i == y ? cy : 0.f)) * d;
+          v[i] = (fmaf(cp, p, -ce) - (hit && i == k ? cy : 0.f)) * d;
         }
       } else {
 #pragma unroll
@@ -147,7 +172,7 @@ __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensor
         if (hit) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (cb + i == y) v[i] -= cy;
+            if (i == k) v[i] -= cy;
         }
       }
 #pragma unroll
@@ -209,28 +234,29 @@ __device__ __forceinline__ void put_box(const CUtensorMap* map, uint32_t stage_b
 }
 
 // One output tile of d_h (its float sums: rows are compact, run `run` the map's third extent) or dW: the
-// product times out_scale, as float or, rounded once, bf16. The map's extents clip the rows and columns.
-__device__ __forceinline__ void epi_ce_store(const GemmArgs& g, const CUtensorMap* map_c, int run, uint32_t taddr,
-                                             int64_t warp_row0, int64_t M, int64_t n0, int half, uint32_t buf, uint32_t& box,
-                                             int lane) {
+// product times `scale`, as float or, rounded once, bf16. The map's extents clip the rows and columns.
+__device__ __forceinline__ void epi_ce_store(const CUtensorMap* map, uint32_t taddr, int64_t warp_row0, int64_t M, int64_t N,
+                                             int n0, int run, int half, float scale, bool bf16, bool add, uint32_t buf,
+                                             uint32_t& box, int lane, const AccRelease& release) {
 #pragma unroll 1
   for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
     float v[32];
     tmem_ld32(taddr + c * 32, v);
-    const int64_t col = n0 + c * 32;
-    if (col >= g.N || warp_row0 >= M) continue;  // warp-uniform
+    if (c == (half + 1) * (BN / 64) - 1) release();
+    const int col = n0 + c * 32;
+    if (col >= N || warp_row0 >= M) continue;  // warp-uniform
     uint32_t w[16];
-    if (g.out_bf16) {
+    if (bf16) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * g.out_scale, v[2 * i + 1] * g.out_scale);
-      put_box(map_c, buf, box, lane, w, (int)col, (int)warp_row0, run, false);
+      for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * scale, v[2 * i + 1] * scale);
+      put_box(map, buf, box, lane, w, col, (int)warp_row0, run, false);
     } else {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        if (col + b * 16 >= g.N) break;
+        if (col + b * 16 >= N) break;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[b * 16 + i] * g.out_scale);
-        put_box(map_c, buf, box, lane, w, (int)col + b * 16, (int)warp_row0, run, g.accumulate);
+        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[b * 16 + i] * scale);
+        put_box(map, buf, box, lane, w, col + b * 16, (int)warp_row0, run, add);
       }
     }
   }

@@ -47,7 +47,7 @@ enum Epi : int {
   EPI_CE_PARTIALS_CAP = 5,
   EPI_CE_DLOGITS = 6,
   EPI_CE_DLOGITS_CAP = 7,
-  EPI_CE_STORE = 8
+  EPI_CE_STORE = 8  // (the shape of bwd_kernel, grpo_lmhead_ce_bwd.cuh)
 };
 
 constexpr bool epi_is_dlogits(int e) { return e == EPI_DLOGITS || e == EPI_CE_DLOGITS || e == EPI_CE_DLOGITS_CAP; }
@@ -280,10 +280,6 @@ struct GemmArgs {
   // ea: [T] s w (1 + 2 lambda lse); coef: [T] s w)
   float cap, inv_cap;      // the soft cap c and 1 / c (_CAP)
   float ce_hot, ce_smooth; // 1 - eps, eps / V
-  // EPI_CE_STORE: the product times out_scale to map_c (rows x columns x runs): float, or bf16 (out_bf16),
-  // or added to the float there (accumulate)
-  float out_scale;
-  int out_bf16;
 };
 
 enum { LIVE_NONE = 0, LIVE_ROWS_PADDED = 1, LIVE_ROWS = 2, LIVE_K = 3 };
@@ -596,11 +592,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   const int stride = CG == 2 ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   const int KB = (int)((K + BK - 1) / BK);
   // a unit's N tile and its K blocks [k0, k1)
-  const int split = epi_is_store(EPI) && g.split > 1 ? g.split : 1;
+  const int split = EPI == EPI_STORE_F32 && g.split > 1 ? g.split : 1;
   auto unit_k = [&](int& nu, int& k0, int& k1) -> int {
     k0 = 0;
     k1 = KB;
-    if (!epi_is_store(EPI) || split == 1) return 0;
+    if (EPI != EPI_STORE_F32 || split == 1) return 0;
     const int n_nt = g.n_n / split, run = nu / n_nt;
     nu -= run * n_nt;
     k0 = (int)((int64_t)run * KB / split);
@@ -660,7 +656,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         fence_after();
         const uint32_t d = tmem + ab * BN;
         int k0 = 0, k1 = KB;
-        if (epi_is_store(EPI)) {
+        if (EPI == EPI_STORE_F32) {
           int mu, nu;
           unit_coords(g, n_m, t, mu, nu);
           unit_k(nu, k0, k1);
@@ -710,6 +706,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
       const int64_t row = (int64_t)mu * BM * CG + (int64_t)rank * BM + trow;
       const bool rok = row < M;
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * BN;
+      // (the cross entropy's epilogues give the accumulator back by themselves)
+      const AccRelease release{CG == 2 && rank != 0 ? mapa_u32(smem_u32(&tempty[ab]), 0) : 0u, &tempty[ab], lane};
       if constexpr (EPI == EPI_PARTIALS)
         epi_partials(g, taddr, row, rok, g.col_tile0 + nu);
       else if constexpr (EPI == EPI_PARTIALS_ENT)
@@ -718,36 +716,34 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         epi_dlogits(g, &map_c, taddr, row, rok, g.col_tile0 + nu, row - lane, rows_store,
                     epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
       else if constexpr (EPI == EPI_CE_PARTIALS || EPI == EPI_CE_PARTIALS_CAP)
-        epi_ce_partials<EPI == EPI_CE_PARTIALS_CAP>(g, taddr, row, rok, g.col_tile0 + nu, half,
-                                                    reinterpret_cast<float*>(sgen + S::STAGES * S::STAGE_BYTES) + ab * BM * 3,
-                                                    trow, 1 + (int)ab * 4 + quarter);
+        epi_ce_partials<EPI == EPI_CE_PARTIALS_CAP>(
+            g, taddr, row, rok, g.col_tile0 + nu, half,
+            reinterpret_cast<float*>(sgen + S::STAGES * S::STAGE_BYTES) + (ab * BM + trow) * 3, 1 + quarter, release);
       else if constexpr (EPI == EPI_CE_DLOGITS || EPI == EPI_CE_DLOGITS_CAP)
         epi_ce_dlogits<EPI == EPI_CE_DLOGITS_CAP>(g, &map_c, taddr, row, rok, g.col_tile0 + nu, half, row - lane,
-                                                  rows_store, ce_buf, box, lane);
-      else if constexpr (EPI == EPI_CE_STORE) {
-        int k0, k1;
-        const int run = unit_k(nu, k0, k1);
-        epi_ce_store(g, &map_c, run, taddr, row - lane, M, (int64_t)nu * BN, half, ce_buf, box, lane);
-      } else {
+                                                  rows_store, ce_buf, box, lane, release);
+      else {
         int k0, k1;
         const int run = unit_k(nu, k0, k1);
         epi_store_f32(g, g.C + run * g.split_stride, taddr, row, rok, (int64_t)nu * BN,
                       epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 2 && rank != 0)
-          mbar_arrive_remote(mapa_u32(smem_u32(&tempty[ab]), 0));
-        else
-          mbar_arrive(&tempty[ab]);
+      if constexpr (!epi_is_ce(EPI)) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2 && rank != 0)
+            mbar_arrive_remote(mapa_u32(smem_u32(&tempty[ab]), 0));
+          else
+            mbar_arrive(&tempty[ab]);
+        }
       }
       if (++ab == 2) {
         ab = 0;
         aphase ^= 1u;
       }
     }
-    if ((epi_is_dlogits(EPI) || EPI == EPI_CE_STORE) && lane == 0) bulk_wait_all();  // this warp's stores are complete
+    if (epi_is_dlogits(EPI) && lane == 0) bulk_wait_all();  // this warp's stores are complete
   }
 
   fence_before();

@@ -68,13 +68,10 @@ inline int cta_group() {
   return (e && e[0] == '1') ? 1 : 2;
 }
 
-// One persistent launch over g's units. The first launch of an instance on a device sets its
-// shared-memory limit and caches how many CTAs (or CTA pairs) fit at once.
-template <int CG, int EPI, bool AMN, bool BMN>
-int launch_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, GemmArgs g, cudaStream_t st) {
-  using S = Shape<CG, EPI>;
-  auto kern = gemm_kernel<CG, EPI, AMN, BMN>;
-  g.n_m = (int)((g.M + BM * CG - 1) / (BM * CG));
+// One persistent launch of `units` work units on clusters of CG CTAs. The first launch of an instance on a
+// device sets its shared-memory limit and caches how many CTAs (or CTA pairs) fit at once.
+template <int CG, typename S, auto* kern, typename... Args>
+int launch_units(int64_t units, cudaStream_t st, const Args&... args) {
   int dev = 0;
   GRPO_CUDA_TRY(cudaGetDevice(&dev));
   cudaLaunchConfig_t cfg = {};
@@ -106,11 +103,18 @@ int launch_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc
       if (dev >= 0 && dev < 64) cached[dev] = max_units;
     }
   }
-  const int64_t units = std::min<int64_t>((int64_t)g.n_m * g.n_n, max_units);
+  units = std::min<int64_t>(units, max_units);
   if (units <= 0) return GRPO_OK;
   cfg.gridDim = dim3((unsigned)(CG * units), 1, 1);
-  GRPO_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, ma, mb, mc, g));
+  GRPO_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
   return GRPO_OK;
+}
+
+// One persistent launch over g's units.
+template <int CG, int EPI, bool AMN, bool BMN>
+int launch_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, GemmArgs g, cudaStream_t st) {
+  g.n_m = (int)((g.M + BM * CG - 1) / (BM * CG));
+  return launch_units<CG, Shape<CG, EPI>, &gemm_kernel<CG, EPI, AMN, BMN>>((int64_t)g.n_m * g.n_n, st, ma, mb, mc, g);
 }
 
 // mc: the TMA store target of the dlogits epilogue (unused by the other epilogues)
