@@ -29,6 +29,8 @@ constexpr int kCompactThreads = 1024;
 
 __global__ void __launch_bounds__(kCompactThreads) ce_compact_kernel(int64_t T, const uint8_t* mask, int32_t* idx,
                                                                      int32_t* live_n) {
+  pdl_launch();
+  pdl_wait();
   __shared__ int32_t warp_sum[kCompactThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int64_t per = (T + kCompactThreads - 1) / kCompactThreads;
@@ -70,6 +72,8 @@ __global__ void __launch_bounds__(kCompactThreads) ce_compact_kernel(int64_t T, 
 __global__ void __launch_bounds__(256) ce_gather_kernel(int64_t T, int H, const __nv_bfloat16* h, const int32_t* idx,
                                                         const int32_t* live_n, __nv_bfloat16* h_live, void* d_h,
                                                         int dh_vec) {
+  pdl_launch();
+  pdl_wait();
   const int64_t nl = *live_n;
   const int64_t pad = live_pad(nl, T) < T ? live_pad(nl, T) : T;
   const int lane = threadIdx.x & 31, nvec = H >> 3;
@@ -111,6 +115,8 @@ struct CeReduceArgs {
 constexpr int kCeReduceWarps = 32;
 
 __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduceArgs a) {
+  pdl_launch();
+  pdl_wait();
   __shared__ float wm[kCeReduceWarps][32], ws[kCeReduceWarps][32], wz[kCeReduceWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t i = (int64_t)blockIdx.x * 32 + lane;
@@ -188,11 +194,57 @@ __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduce
   }
 }
 
+struct CeDzArgs {
+  int64_t T, V, ld;  // ld: columns of x and dz
+  const float* x;    // [T][ld] the kept products, by compact row
+  __nv_bfloat16* dz;
+  const int32_t *target, *idx, *live_n;
+  const float *lse2, *coef, *ea;
+  float cap, inv_cap, ce_hot, ce_smooth;
+};
+
+// The dlogits of the kept logits (the formula of epi_ce_dlogits, 8 columns a thread): a block takes 2048
+// columns of every gridDim.y-th row. The rows up to the padded count are zeros (dW reduces over them).
+template <bool CAP>
+__global__ void __launch_bounds__(256) ce_dz_kernel(CeDzArgs a) {
+  pdl_launch();
+  pdl_wait();
+  const int64_t nl = a.live_n ? (int64_t)*a.live_n : a.T, pad = a.live_n ? live_pad(nl, a.T) : a.T;
+  const int64_t rows = pad < a.T ? pad : a.T, col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (col >= a.V) return;
+#pragma unroll 2
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    const int64_t tok = r < nl ? (a.idx ? (int64_t)a.idx[r] : r) : -1;
+    const float sw = tok >= 0 ? a.coef[tok] : 0.f;
+    if (sw != 0.f) {
+      const float4* src = reinterpret_cast<const float4*>(a.x + r * a.ld + col);
+      const float4 x0 = src[0], x1 = src[1];
+      const float l2 = a.lse2[tok], cp = a.ea[tok], ce = sw * a.ce_smooth, cy = sw * a.ce_hot;
+      const int64_t k = a.target[tok] - col;
+      float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float t = 0.f, d = 1.f;
+        if constexpr (CAP) {
+          tanh_pair(__fmul_rn(v[i], a.inv_cap), t, d);
+          v[i] = a.cap * t;
+        }
+        v[i] = (fmaf(cp, ex2(fmaf(v[i], kLog2e, -l2)), -ce) - (i == k ? cy : 0.f)) * d;
+      }
+      w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+    *reinterpret_cast<uint4*>(a.dz + r * a.ld + col) = w;
+  }
+}
+
 // d_h = scale (the runs' float sums, joined in an order that goes by `split`), rounded once; compact row r to
 // its token's row. A block takes 256 / G vectors of 4, G groups of its threads every G-th run.
 template <int G>
 __global__ void __launch_bounds__(256) ce_dh_kernel(const int32_t* live_n, const int32_t* row_idx, int64_t T, int H4,
                                                     const float* part, int split, float scale, void* d_h, int out_bf16) {
+  pdl_launch();
+  pdl_wait();
   constexpr int W = 256 / G;
   __shared__ float4 sh[G > 1 ? G : 1][W];
   const int64_t n = (live_n ? (int64_t)*live_n : T) * H4, stride = T * H4;
@@ -238,8 +290,8 @@ using namespace grpo::lmhead;
 namespace {
 
 struct CeLayout {
-  size_t part_m, part_s, part_z, zy, lse2, coef, ea, idx, live_n, h_live, dz[2], part, total;
-  int n_col_tiles, chunk_tiles, n_chunks, split;
+  size_t part_m, part_s, part_z, zy, lse2, coef, ea, idx, live_n, h_live, dz[2], part, x, total;
+  int n_col_tiles, chunk_tiles, n_chunks, split, keep;
   int64_t vchunk;  // columns of a dlogits buffer
 };
 
@@ -258,6 +310,10 @@ int ce_split(int64_t T, int64_t H, int chunk_tiles) {
   const int64_t load = ((T + 2 * BM - 1) / (2 * BM) * n_nt * kb1 + (int64_t)chunk_tiles * n_nt * kb2) / 76;
   return (int)std::max<int64_t>(1, std::min<int64_t>((3 * kb1 + load - 1) / std::max<int64_t>(load, 1), kb1 / 8));
 }
+
+// Whether pass A keeps its logits, as float, for the dlogits: where the vocabulary is one piece and they take
+// 256 MB at most (the bound of a piece). Otherwise they are formed again.
+bool ce_keep(int64_t T, int64_t vchunk, int n_chunks) { return n_chunks == 1 && T * vchunk <= ((int64_t)64 << 20); }
 
 CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
   CeLayout w{};
@@ -288,6 +344,8 @@ CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
   w.dz[0] = take((size_t)T * w.vchunk * 2);
   w.dz[1] = w.n_chunks > 1 ? take((size_t)T * w.vchunk * 2) : w.dz[0];
   w.part = take((size_t)w.split * T * H * 4);  // d_h's float sums, of each run
+  w.keep = ce_keep(T, w.vchunk, w.n_chunks);
+  w.x = w.keep ? take((size_t)T * w.vchunk * 4) : 0;
   w.total = off;
   return w;
 }
@@ -308,11 +366,41 @@ struct CeCall {
   float* f(size_t off) const { return reinterpret_cast<float*>(base + off); }
 };
 
+// A launch that may begin while the kernel before it on the stream still runs (see pdl_wait).
+template <typename... P, typename... A>
+int launch_dep(void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  GRPO_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, P(args)...));
+  return GRPO_OK;
+}
+
+// The target of EPI_CE_STORE: [runs][rows][cols], boxes of 32 rows x 64 bytes in the 64-byte swizzle.
+bool map_out(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t runs, int64_t ld, bool bf16) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t size = bf16 ? 2 : 4;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)runs};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * size, (cuuint64_t)ld * rows * size};
+  cuuint32_t box[3] = {(cuuint32_t)(64 / size), 32, 1}, estr[3] = {1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int PLAIN, int CAP>
-int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc) {
+int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc, bool pdl) {
   CUtensorMap ma, mb, mc = {};
   if (!map_k(&ma, c.h_src, c.T, c.H, c.H, BM) || !map_k(&mb, c.W, c.V, c.H, c.H, BN / c.cg)) return GRPO_ERR_UNSUPPORTED;
   if (epi_is_dlogits(PLAIN) && !map_dz_store(&mc, g.dz, c.T, vc, g.ldz)) return GRPO_ERR_UNSUPPORTED;
+  if (g.keep && !map_out(&mc, c.f(c.ws.x), c.V, c.T, 1, c.ws.vchunk, false)) return GRPO_ERR_UNSUPPORTED;
   g.M = c.T;
   g.K = c.H;
   g.V = c.V;
@@ -324,32 +412,20 @@ int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc) {
   g.zy = c.f(c.ws.zy);
   g.cap = c.cap;
   g.inv_cap = 1.f / c.cap;
-  return c.cap > 0.f ? launch<CAP, false, false>(c.cg, ma, mb, mc, g, st) : launch<PLAIN, false, false>(c.cg, ma, mb, mc, g, st);
-}
-
-// The target of EPI_CE_STORE: [runs][rows][cols], boxes of 32 rows x 64 bytes in the 64-byte swizzle.
-bool map_out(CUtensorMap* m, void* base, int64_t cols, int64_t rows, int64_t runs, bool bf16) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t size = bf16 ? 2 : 4;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)runs};
-  cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * rows * size};
-  cuuint32_t box[3] = {(cuuint32_t)(64 / size), 32, 1}, estr[3] = {1, 1, 1};
-  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return c.cap > 0.f ? launch<CAP, false, false>(c.cg, ma, mb, mc, g, st, pdl)
+                     : launch<PLAIN, false, false>(c.cg, ma, mb, mc, g, st, pdl);
 }
 
 // Both products of piece `chunk`, the vocabulary columns [v0, v0 + vc).
 template <int CG>
-int ce_products(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0, int64_t vc, cudaStream_t st) {
+int ce_products(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0, int64_t vc, cudaStream_t st, bool pdl) {
   CUtensorMap dz_k = {}, w = {}, part = {}, dz_mn = {}, h = {}, dw = {};
   if (c.d_h && (!map_k(&dz_k, dz, c.T, vc, c.ws.vchunk, BM) ||
                 !map_mn(&w, static_cast<const __nv_bfloat16*>(c.W) + v0 * c.H, vc, c.H, c.H) ||
-                !map_out(&part, c.f(c.ws.part), c.H, c.T, c.ws.split, false)))
+                !map_out(&part, c.f(c.ws.part), c.H, c.T, c.ws.split, c.H, false)))
     return GRPO_ERR_UNSUPPORTED;
   if (c.dW && (!map_mn(&dz_mn, dz, c.T, vc, c.ws.vchunk) || !map_mn(&h, c.h_src, c.T, c.H, c.H) ||
-               !map_out(&dw, static_cast<uint8_t*>(c.dW) + v0 * c.H * (c.dw_bf16 ? 2 : 4), c.H, vc, 1, c.dw_bf16)))
+               !map_out(&dw, static_cast<uint8_t*>(c.dW) + v0 * c.H * (c.dw_bf16 ? 2 : 4), c.H, vc, 1, c.H, c.dw_bf16)))
     return GRPO_ERR_UNSUPPORTED;
   BwdArgs g{};
   g.T = c.T;
@@ -366,7 +442,7 @@ int ce_products(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0,
   g.acc = c.acc;
   const int64_t n_nt = (c.H + BN - 1) / BN, rows = BM * CG;
   const int64_t units = n_nt * ((c.d_h ? (c.T + rows - 1) / rows * g.split : 0) + (c.dW ? (vc + rows - 1) / rows : 0));
-  return launch_units<CG, Shape<CG, EPI_CE_STORE>, &bwd_kernel<CG>>(units, st, dz_k, w, part, dz_mn, h, dw, g);
+  return launch_units<CG, Shape<CG, EPI_CE_STORE>, &bwd_kernel<CG>>(units, st, pdl, dz_k, w, part, dz_mn, h, dw, g);
 }
 
 int ce_backward(const CeCall& c) {
@@ -379,25 +455,33 @@ int ce_backward(const CeCall& c) {
       const int64_t v0 = (int64_t)ct0 * BN, vc = std::min<int64_t>((int64_t)nct * BN, c.V - v0);
       __nv_bfloat16* dz = reinterpret_cast<__nv_bfloat16*>(c.base + c.ws.dz[ov ? i & 1 : 0]);
       if (ov && i >= 2) GRPO_CUDA_TRY(cudaStreamWaitEvent(c.st, ov->buf_free[i & 1], 0));
-      GemmArgs g{};
-      g.lse2 = c.f(c.ws.lse2);
-      g.coef = c.f(c.ws.coef);
-      g.ea = c.f(c.ws.ea);
-      g.ce_hot = 1.f - c.smoothing;
-      g.ce_smooth = c.smoothing / (float)c.V;
-      g.dz = dz;
-      g.ldz = c.ws.vchunk;
-      g.v0 = v0;
-      g.col_tile0 = ct0;
-      g.n_n = nct;
-      g.live_mode = c.live_n ? LIVE_ROWS_PADDED : LIVE_NONE;
-      int rc = ce_logits<EPI_CE_DLOGITS, EPI_CE_DLOGITS_CAP>(c, g, c.st, vc);
+      int rc;
+      if (c.ws.keep) {
+        CeDzArgs a{c.T, c.V, c.ws.vchunk, c.f(c.ws.x), dz, c.target, c.idx, c.live_n, c.f(c.ws.lse2), c.f(c.ws.coef),
+                   c.f(c.ws.ea), c.cap, 1.f / c.cap, 1.f - c.smoothing, c.smoothing / (float)c.V};
+        const int64_t gx = (c.V + 2047) / 2048, gy = std::min<int64_t>(c.T, std::max<int64_t>(1, (int64_t)sm_count() * 16 / gx));
+        rc = launch_dep(c.cap > 0.f ? ce_dz_kernel<true> : ce_dz_kernel<false>, dim3((unsigned)gx, (unsigned)gy), 256, c.st, a);
+      } else {
+        GemmArgs g{};
+        g.lse2 = c.f(c.ws.lse2);
+        g.coef = c.f(c.ws.coef);
+        g.ea = c.f(c.ws.ea);
+        g.ce_hot = 1.f - c.smoothing;
+        g.ce_smooth = c.smoothing / (float)c.V;
+        g.dz = dz;
+        g.ldz = c.ws.vchunk;
+        g.v0 = v0;
+        g.col_tile0 = ct0;
+        g.n_n = nct;
+        g.live_mode = c.live_n ? LIVE_ROWS_PADDED : LIVE_NONE;
+        rc = ce_logits<EPI_CE_DLOGITS, EPI_CE_DLOGITS_CAP>(c, g, c.st, vc, !(ov && i >= 2));
+      }
       if (rc != GRPO_OK) return rc;
       if (ov) {
         GRPO_CUDA_TRY(cudaEventRecord(ov->dz_ready, c.st));
         GRPO_CUDA_TRY(cudaStreamWaitEvent(bst, ov->dz_ready, 0));
       }
-      rc = c.cg == 2 ? ce_products<2>(c, dz, i, v0, vc, bst) : ce_products<1>(c, dz, i, v0, vc, bst);
+      rc = c.cg == 2 ? ce_products<2>(c, dz, i, v0, vc, bst, !ov) : ce_products<1>(c, dz, i, v0, vc, bst, !ov);
       if (rc != GRPO_OK) return rc;
       if (ov) GRPO_CUDA_TRY(cudaEventRecord(ov->buf_free[i & 1], bst));
     }
@@ -405,8 +489,9 @@ int ce_backward(const CeCall& c) {
       const int H4 = (int)(c.H / 4);
       auto kern = c.ws.split > 4 ? ce_dh_kernel<8> : ce_dh_kernel<1>;
       const int64_t per = c.ws.split > 4 ? 32 : 256, blocks = std::min<int64_t>((c.T * H4 + per - 1) / per, (int64_t)sm_count() * 16);
-      kern<<<(unsigned)blocks, 256, 0, bst>>>(c.live_n, c.idx, c.T, H4, c.f(c.ws.part), c.ws.split, c.scale, c.d_h, c.dh_bf16);
-      GRPO_CUDA_TRY(cudaGetLastError());
+      const int rc = launch_dep(kern, dim3((unsigned)blocks), 256, bst, c.live_n, c.idx, c.T, H4, c.f(c.ws.part), c.ws.split,
+                                c.scale, c.d_h, c.dh_bf16);
+      if (rc != GRPO_OK) return rc;
     }
     return GRPO_OK;
   };
@@ -479,12 +564,12 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
     int32_t* idx = reinterpret_cast<int32_t*>(c.base + c.ws.idx);
     int32_t* live_n = reinterpret_cast<int32_t*>(c.base + c.ws.live_n);
     __nv_bfloat16* h_live = reinterpret_cast<__nv_bfloat16*>(c.base + c.ws.h_live);
-    ce_compact_kernel<<<1, kCompactThreads, 0, c.st>>>(T, mask, idx, live_n);
+    ce_compact_kernel<<<1, kCompactThreads, 0, c.st>>>(T, mask, idx, live_n);  // (not before the caller's own work ends)
     GRPO_CUDA_TRY(cudaGetLastError());
     const int64_t blocks = std::min<int64_t>((T + 7) / 8, (int64_t)sm_count() * 16);
-    ce_gather_kernel<<<(unsigned)blocks, 256, 0, c.st>>>(T, (int)H, static_cast<const __nv_bfloat16*>(h), idx, live_n,
-                                                         h_live, d_h, (int)(H / (c.dh_bf16 ? 8 : 4)));
-    GRPO_CUDA_TRY(cudaGetLastError());
+    const int rc = launch_dep(ce_gather_kernel, dim3((unsigned)blocks), 256, c.st, T, (int)H,
+                              static_cast<const __nv_bfloat16*>(h), idx, live_n, h_live, d_h, (int)(H / (c.dh_bf16 ? 8 : 4)));
+    if (rc != GRPO_OK) return rc;
     c.h_src = h_live;
     c.idx = idx;
     c.live_n = live_n;
@@ -495,7 +580,8 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   g.part_s2 = c.smoothing > 0.f ? c.f(c.ws.part_z) : nullptr;
   g.n_n = c.ws.n_col_tiles;
   g.live_mode = c.live_n ? LIVE_ROWS : LIVE_NONE;
-  const int rc = ce_logits<EPI_CE_PARTIALS, EPI_CE_PARTIALS_CAP>(c, g, c.st, 0);
+  g.keep = c.ws.keep && (d_h || dW);
+  int rc = ce_logits<EPI_CE_PARTIALS, EPI_CE_PARTIALS_CAP>(c, g, c.st, 0, mask != nullptr);
   if (rc != GRPO_OK) return rc;
   CeReduceArgs r{};
   r.T = T;
@@ -518,7 +604,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   r.acc = acc;
   r.idx = c.idx;
   r.live_n = c.live_n;
-  ce_reduce_kernel<<<(unsigned)((T + 31) / 32), kCeReduceWarps * 32, 0, c.st>>>(r);
-  GRPO_CUDA_TRY(cudaGetLastError());
+  rc = launch_dep(ce_reduce_kernel, dim3((unsigned)((T + 31) / 32)), kCeReduceWarps * 32, c.st, r);
+  if (rc != GRPO_OK) return rc;
   return d_h || dW ? ce_backward(c) : GRPO_OK;
 }

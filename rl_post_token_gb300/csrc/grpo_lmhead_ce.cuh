@@ -24,15 +24,50 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // e = exp(2 |u|), t = 1 - 2 / (1 + e), d = 4 e / (1 + e)^2. The exponent stops at 127: the reciprocal is
 // flushed to 0 there, so that t is 1 and d is 0 (they are within 2^-124 of it).
 __device__ __forceinline__ void tanh_pair(float u, float& t, float& d) {
-  const float a = fabsf(u), q = u * u;
+  // (explicit roundings: the bits of soft_cap32's packed form, whatever the compiler would contract)
+  const float a = fabsf(u), q = __fmul_rn(u, u);
   const bool small = a <= 1.f;
   const float w = a * (2.f * kLog2e);
   const float e = ex2(w > 127.f ? 127.f : w);  // a NaN stays one
   const float r = rcp_approx(small ? fmaf(q, fmaf(q, 15.f, 420.f), 945.f) : 1.f + e);
-  const float ts = u * fmaf(q, q + 105.f, 945.f) * r;
+  const float ts = __fmul_rn(__fmul_rn(u, fmaf(q, __fadd_rn(q, 105.f), 945.f)), r);
   const float tl = copysignf(fmaf(-2.f, r, 1.f), u);
   t = small ? ts : tl;
   d = small ? fmaf(-ts, ts, 1.f) : 4.f * (e * r) * r;
+}
+
+// tanh_pair of 32 logits x / c: z = c t in v, d in dz. Where no |x / c| of the warp's rows is above 1 -- the
+// cap's ordinary range -- by the convergent alone, two at a time.
+template <bool DERIV>
+__device__ __forceinline__ void soft_cap32(float (&v)[32], float (&dz)[DERIV ? 32 : 1], float cap, float inv_cap) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(v[i]));
+  if (__all_sync(0xffffffffu, top * inv_cap <= 1.f)) {  // (a NaN logit stays one either way)
+    const float2 k = make_float2(inv_cap, inv_cap), c0 = make_float2(945.f, 945.f);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 u = __fmul2_rn(make_float2(v[i], v[i + 1]), k), q = __fmul2_rn(u, u);
+      const float2 den = __ffma2_rn(q, __ffma2_rn(q, make_float2(15.f, 15.f), make_float2(420.f, 420.f)), c0);
+      const float2 num = __fmul2_rn(u, __ffma2_rn(q, __fadd2_rn(q, make_float2(105.f, 105.f)), c0));
+      const float2 t = __fmul2_rn(num, make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+      if constexpr (DERIV) {
+        const float2 d = __ffma2_rn(make_float2(-t.x, -t.y), t, make_float2(1.f, 1.f));
+        dz[i] = d.x;
+        dz[i + 1] = d.y;
+      }
+      v[i] = cap * t.x;
+      v[i + 1] = cap * t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float t, d;
+      tanh_pair(__fmul_rn(v[i], inv_cap), t, d);
+      if constexpr (DERIV) dz[i] = d;
+      v[i] = cap * t;
+    }
+  }
 }
 
 // Gives a tile's accumulator back to the MMA issuer, once a warp has loaded its last columns: before it
@@ -54,14 +89,52 @@ struct AccRelease {
   }
 };
 
+// 3-D TMA tile store, plain or as a float addition (every element gets one addition per launch: the order
+// of the sums is that of the launches).
+__device__ __forceinline__ void tma_store3d(const CUtensorMap* map, uint32_t src, int x, int y, int z, bool add) {
+  if (add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+// One staged box: lane's 64 bytes (32 bf16 or 16 floats of its row) in the 64-byte swizzle, then the store.
+// `box` counts a warp's boxes over all its tiles: its BUFS (1 or 2) buffers are used in turn whatever a tile
+// leaves out.
+template <int BUFS>
+__device__ __forceinline__ void put_box(const CUtensorMap* map, uint32_t stage_buf, uint32_t& box, int lane, const uint32_t (&w)[16], int x,
+                                        int y, int z, bool add) {
+  const uint32_t buf = stage_buf + (box++ & (BUFS - 1u)) * EPI_BUF_BYTES;
+  if (lane == 0) bulk_wait_read<BUFS - 1>();  // the last store from this buffer has read it
+  __syncwarp();
+  const uint32_t rb = (buf + (uint32_t)lane * 64u) | ((uint32_t)((lane >> 1) & 3) << 4);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rb ^ ((uint32_t)q << 4)), "r"(w[4 * q]),
+                 "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                 : "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store3d(map, buf, x, y, z, add);
+    bulk_commit();
+  }
+}
+
 // Softmax partials of one 256-column tile, the sum of its logits (with label smoothing) and the target
 // logit. The columns past the vocabulary count as -inf, and add nothing to the sum. The second half's warp
 // hands its row's three numbers to the first's through `join` (its row's place there, one of two in turn);
 // the two warps meet at named barrier `bar` once a tile, so that the place is written again only after the
-// other has read it and met once more.
+// other has read it and met once more. With g.keep the products are stored too (map_c).
 template <bool CAP>
-__device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t taddr, int64_t row, bool rok, int ct,
-                                                int half, float* join, int bar, const AccRelease& release) {
+__device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, const CUtensorMap* map_c, uint32_t taddr, int64_t row,
+                                                bool rok, int ct, int half, float* join, int bar, int64_t warp_row0,
+                                                int64_t rows, uint32_t stage_buf, uint32_t& box, int lane,
+                                                const AccRelease& release) {
   const int V = (int)g.V, c0 = ct * BN;
   const int64_t tok = (rok && g.row_idx) ? (int64_t)g.row_idx[row] : row;
   const int y = rok ? g.target[tok] : -1;
@@ -75,13 +148,19 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, uint32_t tadd
     if (c == (half + 1) * (BN / 64) - 1) release();
     const int cb = c0 + c * 32;
     if (cb >= V) continue;  // warp-uniform
-    if constexpr (CAP) {
+    if (g.keep && warp_row0 < rows) {  // the product itself, for the dlogits
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float t, d;
-        tanh_pair(v[i] * g.inv_cap, t, d);
-        v[i] = g.cap * t;
+      for (int b = 0; b < 2; ++b) {
+        if (cb + b * 16 >= V) break;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[b * 16 + i]);
+        put_box<1>(map_c, stage_buf, box, lane, w, cb + b * 16, (int)warp_row0, 0, false);
       }
+    }
+    if constexpr (CAP) {
+      float none[1];
+      soft_cap32<false>(v, none, g.cap, g.inv_cap);
     }
     const int k = y - cb;
     if (y >= cb && k < 32) {
@@ -151,32 +230,28 @@ __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensor
     // warp-uniform: past the vocabulary, or all 32 rows past the rows to be written
     if (cb >= V || warp_row0 >= rows_store) continue;
     uint32_t w[16];
-    if (live) {
+    if (__any_sync(0xffffffffu, live)) {
       const int k = y - cb;
       const bool hit = y >= cb && k < 32;
+      float d[CAP ? 32 : 1];
+      if constexpr (CAP) soft_cap32<true>(v, d, g.cap, g.inv_cap);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 p = __ffma2_rn(make_float2(cp, cp), ex2_pair(v[i], v[i + 1], l2), make_float2(-ce, -ce));
+        v[i] = p.x;
+        v[i + 1] = p.y;
+      }
+      if (hit) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i == k) v[i] -= cy;
+      }
       if constexpr (CAP) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float t, d;
-          tanh_pair(v[i] * g.inv_cap, t, d);
-          const float p = ex2(fmaf(g.cap * t, kLog2e, -l2));
-          v[i] = (fmaf(cp, p, -ce) - (hit && i == k ? cy : 0.f)) * d;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 p = ex2_pair(v[i], v[i + 1], l2);
-          v[i] = fmaf(cp, p.x, -ce);
-          v[i + 1] = fmaf(cp, p.y, -ce);
-        }
-        if (hit) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i == k) v[i] -= cy;
-        }
+        for (int i = 0; i < 32; ++i) v[i] *= d[i];
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 16; ++i) w[i] = live ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : 0u;
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[i] = 0u;
@@ -199,40 +274,6 @@ __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensor
   }
 }
 
-// 3-D TMA tile store, plain or as a float addition (every element gets one addition per launch: the order
-// of the sums is that of the launches).
-__device__ __forceinline__ void tma_store3d(const CUtensorMap* map, uint32_t src, int x, int y, int z, bool add) {
-  if (add)
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-  else
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
-
-// One staged box: lane's 64 bytes (32 bf16 or 16 floats of its row) in the 64-byte swizzle, then the store.
-// `box` counts a warp's boxes over all its tiles: the two buffers are used in turn whatever a tile leaves out.
-__device__ __forceinline__ void put_box(const CUtensorMap* map, uint32_t stage_buf, uint32_t& box, int lane, const uint32_t (&w)[16], int x,
-                                        int y, int z, bool add) {
-  const uint32_t buf = stage_buf + (box++ & 1u) * EPI_BUF_BYTES;
-  if (lane == 0) bulk_wait_read<1>();  // the store before the last, from this buffer, has read it
-  __syncwarp();
-  const uint32_t rb = (buf + (uint32_t)lane * 64u) | ((uint32_t)((lane >> 1) & 3) << 4);
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rb ^ ((uint32_t)q << 4)), "r"(w[4 * q]),
-                 "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
-                 : "memory");
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store3d(map, buf, x, y, z, add);
-    bulk_commit();
-  }
-}
-
 // One output tile of d_h (its float sums: rows are compact, run `run` the map's third extent) or dW: the
 // product times `scale`, as float or, rounded once, bf16. The map's extents clip the rows and columns.
 __device__ __forceinline__ void epi_ce_store(const CUtensorMap* map, uint32_t taddr, int64_t warp_row0, int64_t M, int64_t N,
@@ -249,14 +290,14 @@ __device__ __forceinline__ void epi_ce_store(const CUtensorMap* map, uint32_t ta
     if (bf16) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * scale, v[2 * i + 1] * scale);
-      put_box(map, buf, box, lane, w, col, (int)warp_row0, run, false);
+      put_box<2>(map, buf, box, lane, w, col, (int)warp_row0, run, false);
     } else {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         if (col + b * 16 >= N) break;
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[b * 16 + i] * scale);
-        put_box(map, buf, box, lane, w, col + b * 16, (int)warp_row0, run, add);
+        put_box<2>(map, buf, box, lane, w, col + b * 16, (int)warp_row0, run, add);
       }
     }
   }

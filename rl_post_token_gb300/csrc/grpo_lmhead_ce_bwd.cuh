@@ -111,6 +111,8 @@ bwd_kernel(const __grid_constant__ CUtensorMap dz_k, const __grid_constant__ CUt
   __syncthreads();
   if (CG == 2) cluster_sync_all();
   fence_after();
+  pdl_launch();
+  pdl_wait();
   const uint32_t tmem = *tmem_slot;
   const BwdPlan plan(g, CG, (int)gridDim.x / CG, (int)blockIdx.x / CG);
 

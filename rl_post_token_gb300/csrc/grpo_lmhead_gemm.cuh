@@ -73,9 +73,12 @@ struct Shape {
   // H = 1536 or so; the cross entropy's instances have 8, two to a lane quarter, each half of the columns
   static constexpr int WARPS = epi_is_ce(EPI) ? 2 * EPI_WARPS : EPI_WARPS;
   static constexpr int THREADS = 64 + 32 * WARPS;
-  static constexpr int EPI_BYTES = epi_is_dlogits(EPI) || epi_is_store(EPI) ? WARPS * 2 * EPI_BUF_BYTES : 0;
-  static constexpr int JOIN_BYTES = epi_is_ce(EPI) && !epi_is_dlogits(EPI) && !epi_is_store(EPI) ? 2 * BM * 12 : 0;
+  static constexpr bool JOIN = epi_is_ce(EPI) && !epi_is_dlogits(EPI) && !epi_is_store(EPI);  // (the partials)
+  static constexpr int BUFS = epi_is_dlogits(EPI) || epi_is_store(EPI) ? 2 : JOIN ? 1 : 0;      // staging, per warp
+  static constexpr int EPI_BYTES = WARPS * BUFS * EPI_BUF_BYTES;
+  static constexpr int JOIN_BYTES = JOIN ? 2 * BM * 12 : 0;
   static constexpr size_t SMEM = 1024 /*alignment slack*/ + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + JOIN_BYTES + 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
 };
 
 // Instruction descriptor of tcgen05.mma kind::f16: D f32, A and B bf16, the major-ness of each
@@ -214,6 +217,11 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// Programmatic dependent launch: the kernel after this one may begin its set-up; and this one waits until the
+// kernel before it is complete and its results are visible (at once where it was launched without).
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
@@ -280,6 +288,7 @@ struct GemmArgs {
   // ea: [T] s w (1 + 2 lambda lse); coef: [T] s w)
   float cap, inv_cap;      // the soft cap c and 1 / c (_CAP)
   float ce_hot, ce_smooth; // 1 - eps, eps / V
+  int keep;                // EPI_CE_PARTIALS: also store the products (float [T][ldz], map_c)
 };
 
 enum { LIVE_NONE = 0, LIVE_ROWS_PADDED = 1, LIVE_ROWS = 2, LIVE_K = 3 };
@@ -570,6 +579,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
   __syncthreads();
   if (CG == 2) cluster_sync_all();  // the peer's barriers exist before anything targets them
   fence_after();
+  if constexpr (epi_is_ce(EPI)) {
+    pdl_launch();
+    pdl_wait();
+  }
   const uint32_t tmem = *tmem_slot;
 
   // extents: the launch's, or, in the live-token backward, from the device count (written by
@@ -696,7 +709,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     const int quarter = warp & 3;  // the TMEM lane quarter this warp may access
     const int trow = quarter * 32 + lane;
     const int half = (warp - 2) >> 2;  // the columns' half, of 8 warps
-    const uint32_t ce_buf = epi_base + (uint32_t)(half * 4 + quarter) * 2u * EPI_BUF_BYTES;
+    const uint32_t ce_buf = epi_base + (uint32_t)((half * 4 + quarter) * S::BUFS * EPI_BUF_BYTES);
     uint32_t ab = 0, aphase = 0, box = 0;
     for (int t = first; t < n_units; t += stride) {
       int mu, nu;
@@ -717,8 +730,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     epi_base + (uint32_t)quarter * 2u * EPI_BUF_BYTES, lane);
       else if constexpr (EPI == EPI_CE_PARTIALS || EPI == EPI_CE_PARTIALS_CAP)
         epi_ce_partials<EPI == EPI_CE_PARTIALS_CAP>(
-            g, taddr, row, rok, g.col_tile0 + nu, half,
-            reinterpret_cast<float*>(sgen + S::STAGES * S::STAGE_BYTES) + (ab * BM + trow) * 3, 1 + quarter, release);
+            g, &map_c, taddr, row, rok, g.col_tile0 + nu, half,
+            reinterpret_cast<float*>(sgen + S::STAGES * S::STAGE_BYTES + S::EPI_BYTES) + (ab * BM + trow) * 3, 1 + quarter,
+            row - lane, M, ce_buf, box, lane, release);
       else if constexpr (EPI == EPI_CE_DLOGITS || EPI == EPI_CE_DLOGITS_CAP)
         epi_ce_dlogits<EPI == EPI_CE_DLOGITS_CAP>(g, &map_c, taddr, row, rok, g.col_tile0 + nu, half, row - lane,
                                                   rows_store, ce_buf, box, lane, release);
@@ -743,7 +757,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         aphase ^= 1u;
       }
     }
-    if (epi_is_dlogits(EPI) && lane == 0) bulk_wait_all();  // this warp's stores are complete
+    if ((epi_is_dlogits(EPI) || epi_is_ce(EPI)) && lane == 0) bulk_wait_all();  // this warp's stores are complete
   }
 
   fence_before();

@@ -70,21 +70,25 @@ inline int cta_group() {
 
 // One persistent launch of `units` work units on clusters of CG CTAs. The first launch of an instance on a
 // device sets its shared-memory limit and caches how many CTAs (or CTA pairs) fit at once.
+// pdl: launched while the kernel before it on the stream still runs; the kernel itself waits (pdl_wait).
 template <int CG, typename S, auto* kern, typename... Args>
-int launch_units(int64_t units, cudaStream_t st, const Args&... args) {
+int launch_units(int64_t units, cudaStream_t st, bool pdl, const Args&... args) {
   int dev = 0;
   GRPO_CUDA_TRY(cudaGetDevice(&dev));
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  int n_attr = 0;
+  if (CG == 2) {
+    attr[n_attr].id = cudaLaunchAttributeClusterDimension;
+    attr[n_attr].val.clusterDim.x = CG;
+    attr[n_attr].val.clusterDim.y = 1;
+    attr[n_attr++].val.clusterDim.z = 1;
+  }
   cfg.blockDim = dim3(S::THREADS, 1, 1);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
+  cfg.numAttrs = n_attr;
   int max_units = 0;
   {
     static std::mutex mu;
@@ -106,22 +110,28 @@ int launch_units(int64_t units, cudaStream_t st, const Args&... args) {
   units = std::min<int64_t>(units, max_units);
   if (units <= 0) return GRPO_OK;
   cfg.gridDim = dim3((unsigned)(CG * units), 1, 1);
+  if (pdl) {
+    attr[n_attr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n_attr++].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = n_attr;
+  }
   GRPO_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
   return GRPO_OK;
 }
 
 // One persistent launch over g's units.
 template <int CG, int EPI, bool AMN, bool BMN>
-int launch_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, GemmArgs g, cudaStream_t st) {
+int launch_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, GemmArgs g, cudaStream_t st,
+             bool pdl) {
   g.n_m = (int)((g.M + BM * CG - 1) / (BM * CG));
-  return launch_units<CG, Shape<CG, EPI>, &gemm_kernel<CG, EPI, AMN, BMN>>((int64_t)g.n_m * g.n_n, st, ma, mb, mc, g);
+  return launch_units<CG, Shape<CG, EPI>, &gemm_kernel<CG, EPI, AMN, BMN>>((int64_t)g.n_m * g.n_n, st, pdl, ma, mb, mc, g);
 }
 
 // mc: the TMA store target of the dlogits epilogue (unused by the other epilogues)
 template <int EPI, bool AMN, bool BMN>
 int launch(int cg, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const GemmArgs& g,
-           cudaStream_t st) {
-  return cg == 2 ? launch_t<2, EPI, AMN, BMN>(ma, mb, mc, g, st) : launch_t<1, EPI, AMN, BMN>(ma, mb, mc, g, st);
+           cudaStream_t st, bool pdl = false) {
+  return cg == 2 ? launch_t<2, EPI, AMN, BMN>(ma, mb, mc, g, st, pdl) : launch_t<1, EPI, AMN, BMN>(ma, mb, mc, g, st, pdl);
 }
 
 // Vocabulary tiles per backward chunk: at most 66 (16896 columns), the chunks of equal width
