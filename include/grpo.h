@@ -479,8 +479,8 @@ typedef struct grpo_grad_norm_result {
   int64_t reserved1;
 } grpo_grad_norm_result;
 
-/* Bytes of device workspace grpo_grad_norm needs for n tensors of total_numel elements together (256 and 8
- * per chunk of 8192 elements or more: 0.4 MB at most for up to 32768 tensors). 0 on bad sizes. */
+/* Bytes of device workspace grpo_grad_norm needs for n tensors of total_numel elements together (82 KB at
+ * most). 0 on bad sizes (more than 2^24 tensors or 2^38 elements). */
 GRPO_API size_t grpo_grad_norm_workspace_size(int64_t total_numel, int32_t n);
 
 /* The norm over all elements of n gradient tensors, each tensor's own norm, and the clip's factor.
@@ -495,9 +495,9 @@ GRPO_API size_t grpo_grad_norm_workspace_size(int64_t total_numel, int32_t n);
  *  tensor_norms  device float [n] or NULL: s times each tensor's norm
  *  result     device grpo_grad_norm_result, written whole
  *  workspace  device, 8-byte aligned
- * Squares are summed in float32 within a thread's run of up to 16, in float64 beyond, and in float64
- * throughout where float32's range does not hold them (any float32 gradient has a finite sum). The result
- * depends on the values and sizes alone. Host arrays may be freed when the call returns; a captured call
+ * Squares are summed in float32 chains of 16 (a part's sum is right to 2^-19 of itself), the parts in
+ * float64, and all of it in float64 where float32's range does not hold them (any finite gradients have a
+ * finite sum). The result depends on the values and sizes alone. Host arrays may be freed when the call returns; a captured call
  * keeps the pointers. n = 0: norm 0, coef s.
  * Errors: GRPO_ERR_INVALID (sizes, NULL, alignment, a negative or NaN max_norm, deferred without acc),
  * GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CAPACITY (workspace too small), GRPO_ERR_CUDA. */

@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from array import array
+from operator import attrgetter
 from typing import Optional, Sequence
 
 import numpy as np
@@ -599,27 +601,28 @@ def grpo_finish_step_ex(acc, loss_tok, w_tok=None, divisor: int = -1, n_tok: Opt
     return _finish_rc(rc, res, sync, "grpo_finish_step_ex")
 
 
+_dtype_of = attrgetter("dtype")
+
+
 def _grad_list(grads, name: str):
     """(pointers, numels, dtypes) of gradient tensors as host arrays; each contiguous (any shape) float32
     or bf16 on the current CUDA device."""
     import torch
 
+    T = torch.Tensor
+    dts = list(map({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}.get, map(_dtype_of, grads)))
+    if None in dts:
+        i = dts.index(None)
+        raise ValueError(f"{name}[{i}] must be float32 or bfloat16, not {grads[i].dtype}")
     dev = torch._C._cuda_getDevice()
-    f32, bf16 = torch.float32, torch.bfloat16
-    n = len(grads)
-    p, numels, dts = np.empty(n, np.uint64), np.empty(n, np.int64), np.empty(n, np.int32)
-    for i, g in enumerate(grads):
-        dt = g.dtype
-        if dt is not f32 and dt is not bf16:
-            raise ValueError(f"{name}[{i}] must be float32 or bfloat16, not {dt}")
-        if g.get_device() != dev or not g.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous on the current CUDA device, not on {g.device}")
-        p[i], numels[i], dts[i] = g.data_ptr(), g.numel(), dt is bf16
-    return p, numels, dts
+    if not all(map(T.is_contiguous, grads)) or any(map(dev.__ne__, map(T.get_device, grads))):
+        i = next(i for i, g in enumerate(grads) if not g.is_contiguous() or g.get_device() != dev)
+        raise ValueError(f"{name}[{i}] must be contiguous on the current CUDA device, not on {grads[i].device}")
+    return array("Q", map(T.data_ptr, grads)), array("q", map(T.numel, grads)), array("i", dts)
 
 
-def _addr(a: np.ndarray) -> int:
-    return a.ctypes.data
+def _addr(a: array) -> int:
+    return a.buffer_info()[0]
 
 
 def grpo_grad_norm_workspace_size(grads) -> int:
@@ -652,7 +655,7 @@ def grpo_grad_clip(grads, result, out=None, stream=None) -> None:
     q, qdts = p, dts
     if out is not None:
         q, qn, qdts = _grad_list(out, "out")
-        if len(out) != len(grads) or not np.array_equal(qn, numels):
+        if qn != numels:
             raise ValueError("out must have as many tensors as grads, of the same sizes")
     _device_args(result, ("result", result, torch.uint8, GRAD_NORM_BYTES))
     rc = _lib().grpo_grad_clip(_addr(p), _addr(dts), _addr(q), _addr(qdts), _addr(numels), len(grads), _ptr(result),
@@ -778,7 +781,7 @@ def grpo_lmhead_ce_fwd_bwd(h, W, target, mask, grad_scale: float, d_h, dW, loss_
     V = W.shape[0]
     f32, bf16, u8 = torch.float32, torch.bfloat16, torch.uint8
     dt_h, dt_w = _grad_dtype(d_h, "d_h"), _grad_dtype(dW, "dW")
-    _device_args(h, ("h", h, bf16, 0), ("W", W, bf16, 0), ("target", target, torch.int32, T), ("mask", mask, u8, T),
+    _device_args(h, ("h", h, bf16, None), ("W", W, bf16, None), ("target", target, torch.int32, T), ("mask", mask, u8, T),
                  ("w_tok", w_tok, f32, T), ("d_h", d_h, d_h.dtype if d_h is not None else None, T * H),
                  ("dW", dW, dW.dtype if dW is not None else None, V * H), ("loss_tok", loss_tok, f32, T),
                  ("logp_tok", logp_tok, f32, T), ("lse_tok", lse_tok, f32, T), ("acc", acc, u8, ACC_BYTES),

@@ -6,12 +6,14 @@
 //   out_ij = factor g_ij
 //
 // Bound by memory: every element is read once for the norm, and read and written once by the clip, which
-// cannot begin before the norm is known. A tensor is cut into chunks, a block each; the tensors' addresses
-// and sizes travel in the kernel's parameters (no table in device memory, nothing to keep alive, and a
-// captured call replays by itself).
+// cannot begin before the norm is known. The elements of all tensors are cut into equal shares, one to a
+// block; a block leaves a partial sum for each tensor of its share. The
+// tensors' addresses and sizes travel in the kernel's parameters: no table in device memory, nothing to keep
+// alive, and a captured call replays by itself.
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
+#include <type_traits>
 
 #include "grpo_common.cuh"
 
@@ -19,34 +21,39 @@ namespace grpo {
 namespace clip {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 8;               // elements a thread takes at a time
-constexpr int64_t kMinChunk = 8192;   // elements of a chunk, at least: 32 a thread
-constexpr int64_t kMaxChunks = 16384; // chunks of a call, about, at most: one block sums their partials
-constexpr int kFold = 16;             // vectors a thread sums in float before it folds them into a double
+constexpr int kVec = 8;        // elements a thread takes at a time
+constexpr int kSlot = 256;     // shares and tensors begin at multiples of so many elements (a tensor is padded)
+constexpr int kWave = 912;     // 152 SMs x 6 blocks: a constant, the order of the sums follows from it
+constexpr int kMaxShares = 6 * kWave;
+constexpr int kShare = 131072; // elements of a share where there are several waves (of larger ones: one)
+constexpr int kFold = 8;       // vectors a thread sums before it folds them into its compensated sum
 constexpr int kFinalThreads = 1024;
-constexpr int kSeg = 256;  // partials that a warp of the last kernel sums at a time
-constexpr int kFew = 8;    // a tensor of at most so many chunks is summed by one thread
+constexpr int kSeg = 16;  // partials of a tensor that a thread of the last kernel sums
+constexpr int kFew = 16;  // a tensor of at most so many such sums is finished by one thread, others by a warp
 
-// The tensors of one launch. chunk0[i]: the first chunk of tensor i among the launch's, chunk0[n] their count.
+// The tensors of one launch. slot0[i]: the first slot of tensor i among the launch's, slot0[n] their count. Share w
+// is the slots [w share, (w + 1) share); its partial sum of tensor i is number w + i.
 template <int N>
 struct Table {
+  static constexpr int kSize = N;
   int32_t n;
-  int32_t chunk0[N + 1];
+  int32_t slot0[N + 1];
   int64_t numel[N];
   const void* src[N];
-  void* dst[N];       // (clip)
-  uint8_t kind[N];    // bit 0: src is bf16, bit 1: dst is bf16
+  void* dst[N];     // (clip)
+  uint8_t kind[N];  // bit 0: src is bf16, bit 1: dst is bf16
 };
 
 constexpr int32_t kMaxTensors = 1 << 24;
+constexpr int64_t kMaxNumel = (int64_t)1 << 38;  // (slots are counted in 32 bits)
 constexpr int kSmall = 32, kLarge = 512;  // tensors per launch: 1 KB and 17 KB of parameters
 
 template <int N>
-__device__ __forceinline__ int tensor_of(const Table<N>& t, int chunk) {
-  int lo = 0, hi = t.n - 1;  // the last i with chunk0[i] <= chunk (tensors without elements have no chunk)
+__device__ __forceinline__ int tensor_of(const Table<N>& t, int slot) {
+  int lo = 0, hi = t.n - 1;  // the last i with slot0[i] <= slot (a tensor without elements has no slot)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (t.chunk0[mid] <= chunk)
+    if (t.slot0[mid] <= slot)
       lo = mid;
     else
       hi = mid - 1;
@@ -54,81 +61,91 @@ __device__ __forceinline__ int tensor_of(const Table<N>& t, int chunk) {
   return lo;
 }
 
-// (plain loads: the clip may run in place)
-__device__ __forceinline__ void load8(const float* p, bool aligned, float (&v)[kVec]) {
-  if (aligned) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = p[i];
-  }
+// The slots [from, to) of the launch that lie in tensor i, as elements of it.
+template <int N>
+__device__ __forceinline__ void piece(const Table<N>& t, int i, int from, int to, int64_t& at, int64_t& n) {
+  const int s0 = t.slot0[i], s1 = t.slot0[i + 1];
+  at = (int64_t)((from > s0 ? from : s0) - s0) * kSlot;
+  const int64_t end = (int64_t)((to < s1 ? to : s1) - s0) * kSlot;
+  n = (end < t.numel[i] ? end : t.numel[i]) - at;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, bool aligned, float (&v)[kVec]) {
-  if (aligned) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = __bfloat162float(p[i]);
-  }
-}
-
-__device__ __forceinline__ double block_sum(double s, double* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  __syncthreads();
-  if (lane == 0) red[warp] = s;
-  __syncthreads();
-  s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += red[w];
-  return s;
-}
-
-// The sum of the squares of n elements at p, the same in every thread. Thread t takes vectors t, t + 256, ..
-// of 8 elements, in float up to 16 of them, then in double (a chain of 16 and a tree: 20 roundings of
-// 2^-24 at most); the order goes by the index alone, whatever the address. A sum that may have left float's
-// range -- above 2^120, not a number, or below 2^-80 with an element that is not 0 -- is formed once more
-// in double, where no square over- or underflows.
+// A thread's 8 elements as they lie in memory: 16 bytes of bf16, 32 of float. (Plain loads: the clip may
+// run in place.)
 template <typename T>
-__device__ __forceinline__ double chunk_sum(const T* p, int64_t n, double* red) {
-  const bool aligned = (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-  const int64_t nv = n / kVec;
-  double s = 0.0;
-  uint32_t any = 0;
-  for (int64_t v0 = threadIdx.x; v0 < nv; v0 += (int64_t)kFold * kThreads) {
-    float a[kVec] = {};
-#pragma unroll 4
-    for (int k = 0; k < kFold; ++k) {
-      const int64_t v = v0 + (int64_t)k * kThreads;
-      if (v >= nv) break;
-      float x[kVec];
-      load8(p + v * kVec, aligned, x);
+struct Raw {
+  uint4 q[sizeof(T) / 2];
+};
+
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ Raw<T> load8(const T* p) {
+  Raw<T> r;
+  if constexpr (ALIGNED) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        a[i] = fmaf(x[i], x[i], a[i]);
-        any |= __float_as_uint(x[i]);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = reinterpret_cast<const uint4*>(p)[i];
+  } else if constexpr (sizeof(T) == 4) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+    r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    r.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    const uint16_t* w = reinterpret_cast<const uint16_t*>(p);
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (uint32_t)w[2 * i] | (uint32_t)w[2 * i + 1] << 16;
+    r.q[0] = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T>& r, float (&v)[kVec]) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+    const uint32_t w[4] = {r.q[i].x, r.q[i].y, r.q[i].z, r.q[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        v[4 * i + k] = __uint_as_float(w[k]);
+      } else {
+        v[2 * k] = bf16_lo(w[k]);
+        v[2 * k + 1] = bf16_hi(w[k]);
       }
     }
-    s += (double)tree_sum<kVec, false>(a);
   }
-  if (threadIdx.x < n - nv * kVec) {
-    const float x = (float)p[nv * kVec + threadIdx.x];
-    s += (double)(x * x);
-    any |= __float_as_uint(x);
+}
+
+// The bits that tell whether an element is not 0: all but the signs.
+template <typename T>
+__device__ __forceinline__ uint32_t magnitudes(const Raw<T>& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) m |= r.q[i].x | r.q[i].y | r.q[i].z | r.q[i].w;
+  return m & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
+}
+
+// The threads' values summed: in the warps as T (float: 5 roundings), over the warps in double. An SM adds two
+// doubles a clock: a tree of them over 256 threads takes longer than reading 16 KB.
+template <typename T>
+__device__ __forceinline__ double block_sum(T v, double* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane == 0) red[warp] = (double)v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = red[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) s += red[w];
+    red[0] = s;
   }
-  s = block_sum(s, red);
-  if (s >= 8.271806125530277e-25 && s <= 1.329227995784916e36) return s;  // 2^-80 .. 2^120
-  if (!__syncthreads_or((any & 0x7fffffffu) != 0)) return 0.0;
-  s = 0.0;
+  __syncthreads();
+  return red[0];
+}
+
+template <typename T>
+__device__ __noinline__ double wide_sum(const T* p, int64_t n, double* red) {
+  double s = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += kThreads) {
     const double x = (double)(float)p[i];
     s = fma(x, x, s);
@@ -136,19 +153,85 @@ __device__ __forceinline__ double chunk_sum(const T* p, int64_t n, double* red) 
   return block_sum(s, red);
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, int64_t chunk, double* part) {
-  __shared__ double red[kThreads / 32];
-  const int i = tensor_of(t, (int)blockIdx.x);
-  const int64_t at = (int64_t)((int)blockIdx.x - t.chunk0[i]) * chunk;
-  const int64_t n = t.numel[i] - at < chunk ? t.numel[i] - at : chunk;
-  const double s = (t.kind[i] & 1) ? chunk_sum(static_cast<const __nv_bfloat16*>(t.src[i]) + at, n, red)
-                                   : chunk_sum(static_cast<const float*>(t.src[i]) + at, n, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
+// The sum of the squares of the n elements at p, the same in every thread. Thread t takes vectors t, t + 256, ..
+// of 8 elements: 8 of them in four float chains, those folded into a float sum with its rounding errors
+// beside it, the threads' sums joined by block_sum (a chain of 16, a tree of 4, the joining: 26 roundings of
+// 2^-24 at most). The order goes by the index alone, whatever the address. A sum that may have left float's
+// range -- above 2^120, not a number, or below 2^-80 with an element that is not 0 -- is formed once more
+// in double, where no square over- or underflows.
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ double chunk_sum(const T* p, int64_t n, double* red) {
+  constexpr int kLoads = ALIGNED ? 8 / (int)sizeof(T) : 1;  // vectors in flight: 64 bytes a thread, 96 KB an SM
+  const int nv = (int)(n / kVec);  // (a share has 2^28 elements at most)
+  float s = 0.f, err = 0.f;
+  uint32_t any = 0;
+  float a[4] = {};
+  auto add = [&](const Raw<T>& r) {
+    float x[kVec];
+    unpack(r, x);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) a[i & 3] = fmaf(x[i], x[i], a[i & 3]);
+    any |= magnitudes(r);
+  };
+  auto fold = [&]() {  // s + err += the chains, s rounded, err what that leaves out (Knuth's two-sum)
+    const float x = __fadd_rn(__fadd_rn(a[0], a[2]), __fadd_rn(a[1], a[3])), t = __fadd_rn(s, x), b = __fsub_rn(t, s);
+    err = __fadd_rn(err, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
+    s = t;
+    a[0] = a[1] = a[2] = a[3] = 0.f;
+  };
+  int v = threadIdx.x;
+  for (; v + (kFold - 1) * kThreads < nv; v += kFold * kThreads) {
+#pragma unroll 1
+    for (int k = 0; k < kFold; k += kLoads) {
+      Raw<T> r[kLoads];
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) r[l] = load8<ALIGNED>(p + (int64_t)(v + (k + l) * kThreads) * kVec);
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) add(r[l]);
+    }
+    fold();
+  }
+#pragma unroll 1
+  for (; v < nv; v += kThreads) add(load8<ALIGNED>(p + (int64_t)v * kVec));
+  if (threadIdx.x < n - (int64_t)nv * kVec) {
+    const float x = (float)p[(int64_t)nv * kVec + threadIdx.x];
+    a[0] = fmaf(x, x, a[0]);
+    any |= __float_as_uint(x) & 0x7fffffffu;
+  }
+  fold();
+  const double sum = block_sum(s + err, red);
+  if (sum >= 8.271806125530277e-25 && sum <= 1.329227995784916e36) return sum;  // 2^-80 .. 2^120
+  return __syncthreads_or(any != 0) ? wide_sum(p, n, red) : 0.0;
 }
 
+template <int N>
+__global__ void __launch_bounds__(kThreads, 6) norm_kernel(const __grid_constant__ Table<N> t, int share, double* part) {
+  __shared__ double red[kThreads / 32];
+  pdl_launch();
+  const int from = (int)blockIdx.x * share, to = min(from + share, t.slot0[t.n]);
+  for (int i = tensor_of(t, from); i < t.n && t.slot0[i] < to; ++i) {
+    int64_t at, n;
+    piece(t, i, from, to, at, n);
+    if (n <= 0) continue;  // a tensor without elements
+    auto sum = [&](auto* p) {
+      return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 ? chunk_sum<true>(p, n, red) : chunk_sum<false>(p, n, red);
+    };
+    const double s = (t.kind[i] & 1) ? sum(static_cast<const __nv_bfloat16*>(t.src[i]) + at)
+                                     : sum(static_cast<const float*>(t.src[i]) + at);
+    if (threadIdx.x == 0) part[(int)blockIdx.x + i] = s;
+  }
+}
+
+// What the last kernel has to know of a launch's tensors: part0[i], the first of tensor i's partial sums,
+// count[i], and seg0[i], the first of its segments of kSeg partials.
+template <int N>
+struct Partials {
+  int32_t n, total;  // (total: the partials' places)
+  int32_t part0[N], count[N], seg0[N + 1];
+};
+
 struct FinalArgs {
-  const double* part;      // the launch's chunks
+  const double* part;      // the launch's partials
   const double* before;    // sum of the launches before, or NULL
   double* sum;             // out: with this launch's
   float* tensor_norms;     // this launch's tensors, or NULL
@@ -158,38 +241,40 @@ struct FinalArgs {
   grpo_grad_norm_result* result;
 };
 
-// The launch's partials summed per tensor, the tensors' sums, and with the last launch the result. Tensors
-// of a few chunks take a thread each; of the others a warp takes 256 chunks at a time (8 loads a lane in
-// flight), whose sums one thread adds in order.
+// sqrt(u) s, rounded to float: in float where u's range allows.
+__device__ __forceinline__ float scaled_root(double u, double s) {
+  const float f = (float)u;
+  return f > 1e-30f && f < 1e30f ? sqrtf(f) * (float)s : (float)(sqrt(u) * s);
+}
+
+// The launch's partials summed per tensor, the tensors' sums, and with the last launch the result: a thread
+// for each segment of a tensor, a thread or a warp for each tensor, a warp for all. The partials and the table are
+// brought into shared memory first, and few warps add doubles (see block_sum).
 template <int N>
-__global__ void __launch_bounds__(kFinalThreads) final_kernel(const __grid_constant__ Table<N> t, FinalArgs a) {
-  constexpr int kSegs = (int)(kMaxChunks / kSeg) + 2 * N;  // (a call has at most kMaxChunks + n chunks)
-  __shared__ double seg[kSegs], of[N], red[kFinalThreads / 32];
-  __shared__ int seg0[N + 1];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__global__ void __launch_bounds__(kFinalThreads) final_kernel(const __grid_constant__ Partials<N> t, FinalArgs a) {
+  extern __shared__ double part[];  // [t.total]
+  __shared__ double seg[kMaxShares / kSeg + N], of[N];
+  __shared__ int part0[N], count[N], seg0[N + 1];  // (a parameter indexed by the thread would be read lane by lane)
+  const int tid = threadIdx.x, lane = tid & 31;
+  {
+    const int32_t *p = t.part0, *c = t.count, *g = t.seg0;
+    asm("" : "+l"(p), "+l"(c), "+l"(g));  // by address
+    for (int i = tid; i <= t.n; i += kFinalThreads) {
+      if (i < t.n) {
+        part0[i] = p[i];
+        count[i] = c[i];
+      }
+      seg0[i] = g[i];
+    }
+  }
+  pdl_launch();
+  pdl_wait();
   double s = 1.0;
   if (a.deferred) s = 1.0 / (double)(a.acc->divisor > 1 ? a.acc->divisor : 1);
-  if (tid == 0) {
-    int k = 0;
-    for (int i = 0; i < t.n; ++i) {
-      seg0[i] = k;
-      const int c = t.chunk0[i + 1] - t.chunk0[i];
-      k += c <= kFew ? 0 : (c + kSeg - 1) / kSeg;
-    }
-    seg0[t.n] = k;
-  }
+#pragma unroll 4
+  for (int i = tid; i < t.total; i += kFinalThreads) part[i] = a.part[i];  // (places without a sum are not read below)
   __syncthreads();
-  for (int i = tid; i < t.n; i += kFinalThreads) {
-    const int c0 = t.chunk0[i], c = t.chunk0[i + 1] - c0;
-    if (c > kFew) continue;
-    double x[kFew], v = 0.0;
-#pragma unroll
-    for (int k = 0; k < kFew; ++k) x[k] = k < c ? a.part[c0 + k] : 0.0;
-#pragma unroll
-    for (int k = 0; k < kFew; ++k) v += x[k];
-    of[i] = v;
-  }
-  for (int g = warp; g < seg0[t.n]; g += kFinalThreads / 32) {
+  for (int g = tid; g < seg0[t.n]; g += kFinalThreads) {
     int lo = 0, hi = t.n - 1;  // the last tensor with seg0 <= g
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -198,35 +283,38 @@ __global__ void __launch_bounds__(kFinalThreads) final_kernel(const __grid_const
       else
         hi = mid - 1;
     }
-    const int c0 = t.chunk0[lo] + (g - seg0[lo]) * kSeg, c1 = min(c0 + kSeg, t.chunk0[lo + 1]);
-    double x[kSeg / 32], v = 0.0;
-#pragma unroll
-    for (int k = 0; k < kSeg / 32; ++k) x[k] = c0 + k * 32 + lane < c1 ? a.part[c0 + k * 32 + lane] : 0.0;
-#pragma unroll
-    for (int k = 0; k < kSeg / 32; ++k) v += x[k];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) seg[g] = v;
+    const int k0 = (g - seg0[lo]) * kSeg, k1 = min(k0 + kSeg, count[lo]);
+    double u = 0.0;
+    for (int k = k0; k < k1; ++k) u += part[part0[lo] + k];
+    seg[g] = u;
   }
   __syncthreads();
-  double v = 0.0;
   for (int i = tid; i < t.n; i += kFinalThreads) {
-    if (t.chunk0[i + 1] - t.chunk0[i] > kFew) {
-      double u = 0.0;
-      for (int g = seg0[i]; g < seg0[i + 1]; ++g) u += seg[g];
-      of[i] = u;
-    }
-    v += of[i];
-    if (a.tensor_norms) a.tensor_norms[i] = (float)(s * sqrt(of[i]));
+    if (seg0[i + 1] - seg0[i] > kFew) continue;
+    double u = 0.0;
+    for (int g = seg0[i]; g < seg0[i + 1]; ++g) u += seg[g];
+    of[i] = u;
+    if (a.tensor_norms) a.tensor_norms[i] = scaled_root(u, s);
   }
+  for (int i = tid >> 5; i < t.n; i += kFinalThreads / 32) {
+    if (seg0[i + 1] - seg0[i] <= kFew) continue;  // warp-uniform
+    double u = 0.0;
+    for (int g = seg0[i] + lane; g < seg0[i + 1]; g += 32) u += seg[g];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    if (lane == 0) {
+      of[i] = u;
+      if (a.tensor_norms) a.tensor_norms[i] = scaled_root(u, s);
+    }
+  }
+  __syncthreads();
+  if (tid >= 32) return;
+  double v = 0.0;
+  for (int i = lane; i < t.n; i += 32) v += of[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
   if (tid != 0) return;
-  double total = a.before ? *a.before : 0.0;
-#pragma unroll
-  for (int w = 0; w < kFinalThreads / 32; ++w) total += red[w];
+  const double total = a.before ? *a.before + v : v;
   *a.sum = total;
   if (!a.last) return;
   grpo_grad_norm_result r;
@@ -252,57 +340,88 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kVec])
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// out = f g, rounded once to out's type; zeros, with nothing read, where the step is skipped.
+// out = f g, rounded once to out's type; zeros, with nothing read, where the step is skipped. From the end, as
+// the shares are taken: what the norm has read last is still in L2.
 template <typename S, typename D>
-__device__ __forceinline__ void clip_chunk(const S* src, D* dst, int64_t n, float f, bool skip) {
+__device__ __forceinline__ void clip_piece(const S* src, D* dst, int64_t n, float f, bool skip) {
   const bool aligned = ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15u) == 0;
-  int64_t done = 0;
-  if (aligned) {
-    const int64_t nv = n / kVec;
-    done = nv * kVec;
-#pragma unroll 4
-    for (int64_t v = threadIdx.x; v < nv; v += kThreads) {
-      float x[kVec] = {};
-      if (!skip) load8(src + v * kVec, true, x);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = skip ? 0.f : x[i] * f;
-      store8(dst + v * kVec, x);
-    }
+  if (skip) {
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) put(dst + i, 0.f);
+    return;
   }
-#pragma unroll 4
-  for (int64_t i = done + threadIdx.x; i < n; i += kThreads) put(dst + i, skip ? 0.f : (float)src[i] * f);
+  const int64_t nv = aligned ? n / kVec : 0;
+  // past the last whole vector, or all of it: by element
+  int64_t i = n - 1 - threadIdx.x;
+  for (; i - 3 * kThreads >= nv * kVec; i -= 4 * kThreads) {
+    S x[4];
+#pragma unroll
+    for (int l = 0; l < 4; ++l) x[l] = src[i - l * kThreads];
+#pragma unroll
+    for (int l = 0; l < 4; ++l) put(dst + i - l * kThreads, (float)x[l] * f);
+  }
+  for (; i >= nv * kVec; i -= kThreads) put(dst + i, (float)src[i] * f);
+  constexpr int kLoads = 8 / (int)sizeof(S);
+  auto put8 = [&](int64_t at, const Raw<S>& r) {
+    float x[kVec];
+    unpack(r, x);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) x[k] *= f;
+    store8(dst + at * kVec, x);
+  };
+  int64_t v = nv - 1 - threadIdx.x;
+  for (; v - (kLoads - 1) * kThreads >= 0; v -= kLoads * kThreads) {  // (all loads of a group before its stores)
+    Raw<S> r[kLoads];
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) r[l] = load8<true>(src + (v - l * kThreads) * kVec);
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) put8(v - l * kThreads, r[l]);
+  }
+  for (; v >= 0; v -= kThreads) put8(v, load8<true>(src + v * kVec));
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, int64_t chunk,
-                                                        const grpo_grad_norm_result* result) {
-  const int b = (int)(gridDim.x - 1 - blockIdx.x);  // from the end: what the norm has read last is still in L2
+__global__ void __launch_bounds__(kThreads, 6) clip_kernel(const __grid_constant__ Table<N> t, int share,
+                                                           const grpo_grad_norm_result* result) {
+  const int from = (int)(gridDim.x - 1 - blockIdx.x) * share, to = min(from + share, t.slot0[t.n]);
+  int i = tensor_of(t, to - 1);
+  pdl_launch();
+  pdl_wait();
   const float f = result->coef;
   const bool skip = result->status != GRPO_OK;
-  const int i = tensor_of(t, b);
-  const int64_t at = (int64_t)(b - t.chunk0[i]) * chunk;
-  const int64_t n = t.numel[i] - at < chunk ? t.numel[i] - at : chunk;
-  if (t.src[i] == t.dst[i] && !skip && f == 1.f) return;  // in place, and the factor changes nothing
-  const float* sf = static_cast<const float*>(t.src[i]) + at;
-  const __nv_bfloat16* sb = static_cast<const __nv_bfloat16*>(t.src[i]) + at;
-  float* df = static_cast<float*>(t.dst[i]) + at;
-  __nv_bfloat16* db = static_cast<__nv_bfloat16*>(t.dst[i]) + at;
-  switch (t.kind[i]) {
-    case 0: clip_chunk(sf, df, n, f, skip); break;
-    case 1: clip_chunk(sb, df, n, f, skip); break;
-    case 2: clip_chunk(sf, db, n, f, skip); break;
-    default: clip_chunk(sb, db, n, f, skip); break;
+  for (; i >= 0 && t.slot0[i + 1] > from; --i) {
+    int64_t at, n;
+    piece(t, i, from, to, at, n);
+    if (n <= 0 || (t.src[i] == t.dst[i] && !skip && f == 1.f)) continue;  // (in place, a factor of 1 changes nothing)
+    const float* sf = static_cast<const float*>(t.src[i]) + at;
+    const __nv_bfloat16* sb = static_cast<const __nv_bfloat16*>(t.src[i]) + at;
+    float* df = static_cast<float*>(t.dst[i]) + at;
+    __nv_bfloat16* db = static_cast<__nv_bfloat16*>(t.dst[i]) + at;
+    switch (t.kind[i]) {
+      case 0: clip_piece(sf, df, n, f, skip); break;
+      case 1: clip_piece(sb, df, n, f, skip); break;
+      case 2: clip_piece(sf, db, n, f, skip); break;
+      default: clip_piece(sb, db, n, f, skip); break;
+    }
   }
 }
 
 // ---- host -------------------------------------------------------------------------------------
 
-// Elements of a chunk, by the call's sizes alone (the order of the sums follows from it): a power of two
-// that cuts the call into about 16384 chunks at most.
-int64_t chunk_of(int64_t total) {
-  int64_t c = kMinChunk;
-  while (c * kMaxChunks < total) c *= 2;
-  return c;
+// A launch that may begin while the kernel before it on the stream still runs (each waits for it itself).
+template <typename... P, typename... A>
+int launch_dep(void (*kern)(P...), int64_t blocks, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  GRPO_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
+  return GRPO_OK;
 }
 
 int check_list(const void* const* p, const int64_t* numels, const int32_t* dtypes, int32_t n, int64_t* total) {
@@ -311,10 +430,10 @@ int check_list(const void* const* p, const int64_t* numels, const int32_t* dtype
   for (int32_t i = 0; i < n; ++i) {
     if (dtypes[i] != GRPO_DTYPE_F32 && dtypes[i] != GRPO_DTYPE_BF16) return GRPO_ERR_UNSUPPORTED;
     const uintptr_t size = dtypes[i] == GRPO_DTYPE_BF16 ? 2 : 4;
-    if (numels[i] < 0 || numels[i] > ((int64_t)1 << 48) || (numels[i] > 0 && (!p[i] || (uintptr_t)p[i] % size)))
+    if (numels[i] < 0 || numels[i] > kMaxNumel || (numels[i] > 0 && (!p[i] || (uintptr_t)p[i] % size)))
       return GRPO_ERR_INVALID;
     *total += numels[i];
-    if (*total > ((int64_t)1 << 48)) return GRPO_ERR_INVALID;
+    if (*total > kMaxNumel) return GRPO_ERR_INVALID;
   }
   return GRPO_OK;
 }
@@ -344,37 +463,50 @@ bool overlaps(const void* const* src, const int32_t* sd, void* const* dst, const
   return false;
 }
 
-// The tables of a list, one launch each: go(table, first tensor, last launch).
+// Slots of a share of the norm. One wave of blocks up to 131072 elements each (8 slots at least: a vector a
+// thread); above, as many waves of such shares as fill the last, up to 6: blocks that end early then make
+// room for others (2^31 elements of bf16: one wave 627 us, six 588), and the last kernel's partials stay few.
+int norm_share(int32_t slots) {
+  const int waves = std::min(std::max(1, (int)((int64_t)slots * kSlot / ((int64_t)kWave * kShare))), kMaxShares / kWave);
+  return std::max(8, (slots + waves * kWave - 1) / (waves * kWave));
+}
+
+// The clip leaves nothing to sum: a wave of shares, or of 32768 elements each as many as there are (311M
+// float to bf16: 270 us with the norm's shares, 257 with these).
+int clip_share(int32_t slots) { return std::max(8, std::min((slots + kWave - 1) / kWave, 32768 / kSlot)); }
+
+// The tables of a list, one launch each: go(table, slots of a share, shares, first tensor, last launch).
 template <int N, typename Go>
 int each_table(const void* const* src, const int32_t* sd, void* const* dst, const int32_t* dd, const int64_t* numels,
-               int32_t n, int64_t chunk, Go go) {
+               int32_t n, int (*share_of)(int32_t), Go go) {
   for (int32_t i0 = 0; i0 == 0 || i0 < n; i0 += N) {
     Table<N> t;
     t.n = std::min(n - i0, N);
-    int64_t c = 0;
+    int32_t slots = 0;
     for (int32_t k = 0; k < t.n; ++k) {
       const int32_t i = i0 + k;
-      t.chunk0[k] = (int32_t)c;
-      c += (numels[i] + chunk - 1) / chunk;
+      t.slot0[k] = slots;
+      slots += (int32_t)((numels[i] + kSlot - 1) / kSlot);
       t.numel[k] = numels[i];
       t.src[k] = src[i];
       t.dst[k] = dst ? dst[i] : nullptr;
       t.kind[k] = (uint8_t)((sd[i] == GRPO_DTYPE_BF16) | (dd && dd[i] == GRPO_DTYPE_BF16) << 1);
     }
-    t.chunk0[t.n] = (int32_t)c;
-    const int rc = go(t, i0, i0 + N >= n);
+    t.slot0[t.n] = slots;
+    const int share = share_of(slots);
+    const int rc = go(t, share, (slots + share - 1) / share, i0, i0 + N >= n);
     if (rc != GRPO_OK) return rc;
   }
   return GRPO_OK;
 }
 
 template <int N>
-int norm_launches(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n, int64_t chunk,
-                  FinalArgs f, double* part, double* sum, cudaStream_t st) {
+int norm_launches(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n, FinalArgs f,
+                  double* part, double* sum, cudaStream_t st) {
   float* norms = f.tensor_norms;
-  return each_table<N>(grads, dtypes, nullptr, nullptr, numels, n, chunk, [&](const Table<N>& t, int32_t i0, bool last) -> int {
-    if (t.chunk0[t.n] > 0) {
-      norm_kernel<N><<<(unsigned)t.chunk0[t.n], kThreads, 0, st>>>(t, chunk, part);
+  return each_table<N>(grads, dtypes, nullptr, nullptr, numels, n, norm_share, [&](const Table<N>& t, int share, int shares, int32_t i0, bool last) -> int {
+    if (shares > 0) {
+      norm_kernel<N><<<(unsigned)shares, kThreads, 0, st>>>(t, share, part);
       GRPO_CUDA_TRY(cudaGetLastError());
     }
     f.part = part;
@@ -382,9 +514,23 @@ int norm_launches(const void* const* grads, const int64_t* numels, const int32_t
     f.sum = sum;
     f.tensor_norms = norms ? norms + i0 : nullptr;
     f.last = last;
-    final_kernel<N><<<1, kFinalThreads, 0, st>>>(t, f);
-    GRPO_CUDA_TRY(cudaGetLastError());
-    return GRPO_OK;
+    Partials<N> p;
+    p.n = t.n;
+    p.total = shares > 0 ? shares + t.n - 1 : 0;
+    int32_t segs = 0;
+    for (int32_t i = 0; i < t.n; ++i) {
+      const int32_t s0 = t.slot0[i], s1 = t.slot0[i + 1];
+      p.part0[i] = s0 / share + i;
+      p.count[i] = s1 > s0 ? (s1 - 1) / share - s0 / share + 1 : 0;
+      p.seg0[i] = segs;
+      segs += (p.count[i] + kSeg - 1) / kSeg;
+    }
+    p.seg0[t.n] = segs;
+    const size_t smem = sizeof(double) * (size_t)p.total;
+    if (smem > 16384)  // (with the static part past 48 KB)
+      GRPO_CUDA_TRY(cudaFuncSetAttribute(final_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(sizeof(double) * (kMaxShares + N))));
+    return launch_dep(final_kernel<N>, 1, kFinalThreads, smem, st, p, f);
   });
 }
 
@@ -395,9 +541,9 @@ using namespace grpo;
 using namespace grpo::clip;
 
 extern "C" GRPO_API size_t grpo_grad_norm_workspace_size(int64_t total_numel, int32_t n) {
-  if (total_numel < 0 || n < 0 || n > kMaxTensors || total_numel > ((int64_t)1 << 48)) return 0;
-  // the running sum, then the partials of a launch's chunks
-  return 256 + 8 * (size_t)(total_numel / chunk_of(total_numel) + n);
+  if (total_numel < 0 || n < 0 || n > kMaxTensors || total_numel > kMaxNumel) return 0;
+  // the running sum, then the partials of a launch
+  return 256 + 8 * (size_t)(std::min<int64_t>(kMaxShares, total_numel / kSlot + n) + std::min(n, kLarge));
 }
 
 extern "C" GRPO_API int grpo_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n,
@@ -419,8 +565,8 @@ extern "C" GRPO_API int grpo_grad_norm(const void* const* grads, const int64_t* 
   f.result = result;
   double* sum = static_cast<double*>(workspace);
   double* part = sum + 32;
-  return n <= kSmall ? norm_launches<kSmall>(grads, numels, dtypes, n, chunk_of(total), f, part, sum, as_stream(stream))
-                     : norm_launches<kLarge>(grads, numels, dtypes, n, chunk_of(total), f, part, sum, as_stream(stream));
+  return n <= kSmall ? norm_launches<kSmall>(grads, numels, dtypes, n, f, part, sum, as_stream(stream))
+                     : norm_launches<kLarge>(grads, numels, dtypes, n, f, part, sum, as_stream(stream));
 }
 
 extern "C" GRPO_API int grpo_grad_clip(const void* const* src, const int32_t* src_dtypes, void* const* dst,
@@ -441,15 +587,12 @@ extern "C" GRPO_API int grpo_grad_clip(const void* const* src, const int32_t* sr
   if (spans != few) std::free(spans);
   if (clash) return GRPO_ERR_INVALID;
   const cudaStream_t st = as_stream(stream);
-  const int64_t chunk = chunk_of(total);
-  auto go = [&](const auto& t, int32_t, bool) -> int {
-    if (t.chunk0[t.n] == 0) return GRPO_OK;
-    clip_kernel<<<(unsigned)t.chunk0[t.n], kThreads, 0, st>>>(t, chunk, result);
-    GRPO_CUDA_TRY(cudaGetLastError());
-    return GRPO_OK;
+  auto go = [&](const auto& t, int share, int shares, int32_t, bool) -> int {
+    if (shares == 0) return GRPO_OK;
+    return launch_dep(clip_kernel<std::decay_t<decltype(t)>::kSize>, shares, kThreads, 0, st, t, share, result);
   };
-  return n <= kSmall ? each_table<kSmall>(src, src_dtypes, dst, dst_dtypes, numels, n, chunk, go)
-                     : each_table<kLarge>(src, src_dtypes, dst, dst_dtypes, numels, n, chunk, go);
+  return n <= kSmall ? each_table<kSmall>(src, src_dtypes, dst, dst_dtypes, numels, n, clip_share, go)
+                     : each_table<kLarge>(src, src_dtypes, dst, dst_dtypes, numels, n, clip_share, go);
 }
 
 static_assert(sizeof(grpo_grad_norm_result) == 32, "grpo_grad_norm_result is 32 bytes");
