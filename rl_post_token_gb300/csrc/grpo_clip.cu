@@ -25,7 +25,7 @@ constexpr int kVec = 8;        // elements a thread takes at a time
 constexpr int kSlot = 256;     // shares and tensors begin at multiples of so many elements (a tensor is padded)
 constexpr int kWave = 912;     // 152 SMs x 6 blocks: a constant, the order of the sums follows from it
 constexpr int kMaxShares = 6 * kWave;
-constexpr int kShare = 131072; // elements of a share where there are several waves (of larger ones: one)
+constexpr int kShare = 32768;  // elements of a share where there are several waves (of larger ones: one)
 constexpr int kFold = 8;       // vectors a thread sums before it folds them into its compensated sum
 constexpr int kFinalThreads = 1024;
 constexpr int kSeg = 16;  // partials of a tensor that a thread of the last kernel sums

@@ -110,6 +110,39 @@ struct CeReduceArgs {
   const int32_t *idx, *live_n;  // the compact order, or NULL
 };
 
+// What a token's joined partials (t: shift and sum, z: sum of the logits) give; all 0 for a masked one.
+struct CeToken {
+  float loss, logp, lse, l2, sw, cp;
+  bool bad;
+};
+
+__device__ __forceinline__ CeToken ce_token(const CeReduceArgs& a, int64_t tok, MS t, float z) {
+  CeToken o;
+  const float nan = __int_as_float(0x7fc00000);
+  const int32_t y = a.target[tok];
+  const float zy = y >= 0 && (int64_t)y < a.V ? a.zy[tok] : nan;
+  const float l2s = log2f(t.s);
+  o.l2 = t.m + l2s;
+  // rows past the vouched range of logits count as non-finite, as in the policy loss
+  const bool ok = fabsf(o.l2) <= kLseMax * kLog2e;
+  o.lse = ok ? o.l2 * kLn2 : nan;
+  o.logp = ok ? (fmaf(zy, kLog2e, -t.m) - l2s) * kLn2 : nan;  // without cancellation
+  o.loss = -(1.f - a.smoothing) * o.logp + a.z_loss * o.lse * o.lse;
+  // lse - mean z, from the shift too
+  if (a.part_z) o.loss += a.smoothing * ((t.m - z / (float)a.V * kLog2e) + l2s) * kLn2;
+  o.sw = a.w_tok ? a.w_tok[tok] : 1.f;
+  o.cp = o.sw * fmaf(2.f * a.z_loss, o.lse, 1.f);
+  if (!isfinite(o.loss)) o.cp = nan;
+  o.bad = !isfinite(o.cp);
+  return o;
+}
+
+__device__ __forceinline__ void ce_store_token(const CeReduceArgs& a, int64_t tok, const CeToken& o) {
+  a.loss_tok[tok] = o.loss;
+  if (a.logp_tok) a.logp_tok[tok] = o.logp;
+  if (a.lse_tok) a.lse_tok[tok] = o.lse;
+}
+
 // A block takes 32 tokens (lane = token: a partial's load is one 128-byte line), its warps every 32nd
 // vocabulary tile in order; four warps join eight warps' each, warp 0 the four, in order.
 constexpr int kCeReduceWarps = 32;
@@ -157,33 +190,16 @@ __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduce
   bool bad = false;
   if (in) {
     const int64_t tok = a.idx ? (int64_t)a.idx[i] : i;
-    float loss = 0.f, logp = 0.f, lse = 0.f, l2 = 0.f, sw = 0.f, cp = 0.f;
+    CeToken o{};
     if (live) {
       join(0, 8, 4);
-      const MS tot = t;
-      const float nan = __int_as_float(0x7fc00000);
-      const int32_t y = a.target[tok];
-      const float zy = y >= 0 && (int64_t)y < a.V ? a.zy[tok] : nan;
-      const float l2s = log2f(tot.s);
-      l2 = tot.m + l2s;
-      // rows past the vouched range of logits count as non-finite, as in the policy loss
-      const bool ok = fabsf(l2) <= kLseMax * kLog2e;
-      lse = ok ? l2 * kLn2 : nan;
-      logp = ok ? (fmaf(zy, kLog2e, -tot.m) - l2s) * kLn2 : nan;  // without cancellation
-      loss = -(1.f - a.smoothing) * logp + a.z_loss * lse * lse;
-      // lse - mean z, from the shift too
-      if (a.part_z) loss += a.smoothing * ((tot.m - z / (float)a.V * kLog2e) + l2s) * kLn2;
-      sw = a.w_tok ? a.w_tok[tok] : 1.f;
-      cp = sw * fmaf(2.f * a.z_loss, lse, 1.f);
-      if (!isfinite(loss)) cp = nan;
-      bad = !isfinite(cp);
+      o = ce_token(a, tok, t, z);
+      bad = o.bad;
     }
-    a.loss_tok[tok] = loss;
-    if (a.logp_tok) a.logp_tok[tok] = logp;
-    if (a.lse_tok) a.lse_tok[tok] = lse;
-    a.lse2[tok] = l2;
-    a.coef[tok] = sw;
-    a.ea[tok] = cp;
+    ce_store_token(a, tok, o);
+    a.lse2[tok] = o.l2;
+    a.coef[tok] = o.sw;
+    a.ea[tok] = o.cp;
   }
   const unsigned n_tok = __popc(__ballot_sync(0xffffffffu, in)), n_live = __popc(__ballot_sync(0xffffffffu, live)),
                  n_bad = __popc(__ballot_sync(0xffffffffu, bad));
@@ -203,8 +219,26 @@ struct CeDzArgs {
   float cap, inv_cap, ce_hot, ce_smooth;
 };
 
-// The dlogits of the kept logits (the formula of epi_ce_dlogits, 8 columns a thread): a block takes 2048
-// columns of every gridDim.y-th row. The rows up to the padded count are zeros (dW reduces over them).
+// 8 columns of a row's dlogits from its kept logits (the formula of epi_ce_dlogits; k: the target's place).
+template <bool CAP>
+__device__ __forceinline__ uint4 ce_dz8(const CeDzArgs& a, const float* x, float sw, float l2, float cp, int64_t k) {
+  const float4 x0 = reinterpret_cast<const float4*>(x)[0], x1 = reinterpret_cast<const float4*>(x)[1];
+  const float ce = sw * a.ce_smooth, cy = sw * a.ce_hot;
+  float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float t = 0.f, d = 1.f;
+    if constexpr (CAP) {
+      tanh_pair(__fmul_rn(v[i], a.inv_cap), t, d);
+      v[i] = a.cap * t;
+    }
+    v[i] = (fmaf(cp, ex2(fmaf(v[i], kLog2e, -l2)), -ce) - (i == k ? cy : 0.f)) * d;
+  }
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// The dlogits of the kept logits: a block takes 2048 columns of every gridDim.y-th row. The rows up to the
+// padded count are zeros (dW reduces over them).
 template <bool CAP>
 __global__ void __launch_bounds__(256) ce_dz_kernel(CeDzArgs a) {
   pdl_launch();
@@ -217,25 +251,57 @@ __global__ void __launch_bounds__(256) ce_dz_kernel(CeDzArgs a) {
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     const int64_t tok = r < nl ? (a.idx ? (int64_t)a.idx[r] : r) : -1;
     const float sw = tok >= 0 ? a.coef[tok] : 0.f;
-    if (sw != 0.f) {
-      const float4* src = reinterpret_cast<const float4*>(a.x + r * a.ld + col);
-      const float4 x0 = src[0], x1 = src[1];
-      const float l2 = a.lse2[tok], cp = a.ea[tok], ce = sw * a.ce_smooth, cy = sw * a.ce_hot;
-      const int64_t k = a.target[tok] - col;
-      float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float t = 0.f, d = 1.f;
-        if constexpr (CAP) {
-          tanh_pair(__fmul_rn(v[i], a.inv_cap), t, d);
-          v[i] = a.cap * t;
-        }
-        v[i] = (fmaf(cp, ex2(fmaf(v[i], kLog2e, -l2)), -ce) - (i == k ? cy : 0.f)) * d;
-      }
-      w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    }
+    if (sw != 0.f) w = ce_dz8<CAP>(a, a.x + r * a.ld + col, sw, a.lse2[tok], a.ea[tok], a.target[tok] - col);
     *reinterpret_cast<uint4*>(a.dz + r * a.ld + col) = w;
   }
+}
+
+// ce_reduce_kernel and ce_dz_kernel in one, for few tokens: a block takes 2048 columns of one row, and joins
+// that row's partials for itself; the first column block writes the token's outputs.
+template <bool CAP>
+__global__ void __launch_bounds__(256) ce_reduce_dz_kernel(CeReduceArgs r, CeDzArgs a) {
+  const int lane = threadIdx.x & 31;
+  pdl_launch();
+  pdl_wait();
+  const int64_t i = blockIdx.y, nl = a.live_n ? (int64_t)*a.live_n : a.T, pad = a.live_n ? live_pad(nl, a.T) : a.T;
+  const int64_t tok = a.idx ? (int64_t)a.idx[i] : i;
+  CeToken o{};
+  if (i < nl) {  // (uniform)
+    // ce_reduce_kernel's order, its warps the lanes here: every 32nd tile, eight joined, then the four
+    MS t{-INFINITY, 0.f};
+    float z = 0.f;
+#pragma unroll 4
+    for (int c = lane; c < r.n_col_tiles; c += 32) {
+      const int64_t k = (int64_t)c * r.T + i;
+      t = ms2_combine(t, MS{r.part_m[k], r.part_s[k]});
+      if (r.part_z) z += r.part_z[k];
+    }
+    auto join = [&](int first, int step, int n) {
+      MS u{__shfl_sync(0xffffffffu, t.m, first), __shfl_sync(0xffffffffu, t.s, first)};
+      float s = __shfl_sync(0xffffffffu, z, first);
+#pragma unroll
+      for (int k = 1; k < n; ++k) {
+        u = ms2_combine(u, MS{__shfl_sync(0xffffffffu, t.m, first + k * step), __shfl_sync(0xffffffffu, t.s, first + k * step)});
+        s += __shfl_sync(0xffffffffu, z, first + k * step);
+      }
+      t = u;
+      z = s;
+    };
+    join(lane & 24, 1, 8);
+    join(0, 8, 4);
+    o = ce_token(r, tok, t, z);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    ce_store_token(r, tok, o);
+    atomicAdd(reinterpret_cast<unsigned long long*>(&r.acc->n_tokens), 1ull);
+    if (i < nl) atomicAdd(reinterpret_cast<unsigned long long*>(&r.acc->n_valid), 1ull);
+    if (o.bad) atomicAdd(reinterpret_cast<unsigned long long*>(&r.acc->n_nonfinite), 1ull);
+  }
+  const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= pad || col >= a.V) return;
+  uint4 w = make_uint4(0u, 0u, 0u, 0u);
+  if (o.sw != 0.f) w = ce_dz8<CAP>(a, a.x + i * a.ld + col, o.sw, o.l2, o.cp, a.target[tok] - col);
+  *reinterpret_cast<uint4*>(a.dz + i * a.ld + col) = w;
 }
 
 // d_h = scale (the runs' float sums, joined in an order that goes by `split`), rounded once; compact row r to
@@ -311,9 +377,14 @@ int ce_split(int64_t T, int64_t H, int chunk_tiles) {
   return (int)std::max<int64_t>(1, std::min<int64_t>((3 * kb1 + load - 1) / std::max<int64_t>(load, 1), kb1 / 8));
 }
 
-// Whether pass A keeps its logits, as float, for the dlogits: where the vocabulary is one piece and they take
-// 256 MB at most (the bound of a piece). Otherwise they are formed again.
-bool ce_keep(int64_t T, int64_t vchunk, int n_chunks) { return n_chunks == 1 && T * vchunk <= ((int64_t)64 << 20); }
+// Whether pass A keeps its logits, as float, for the dlogits: where the vocabulary is one piece and they stay
+// in L2 (48 MB) or take less memory traffic than forming them again costs (T <= H / 2), 256 MB at most.
+// Kept and formed again, us of a call: 16 x 32000 x 768 50 and 56, 400 x 50257 x 1000 178 and 192, 999 x 10000 x
+// 1000 93 and 99; the other way 300 x 50257 x 512 96 and 89, 999 x 30000 x 256 115 and 100.
+bool ce_keep(int64_t T, int64_t H, int64_t vchunk, int n_chunks) {
+  const int64_t bytes = T * vchunk * 4;
+  return n_chunks == 1 && (bytes <= ((int64_t)48 << 20) || (2 * T <= H && bytes <= ((int64_t)256 << 20)));
+}
 
 CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
   CeLayout w{};
@@ -344,11 +415,16 @@ CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
   w.dz[0] = take((size_t)T * w.vchunk * 2);
   w.dz[1] = w.n_chunks > 1 ? take((size_t)T * w.vchunk * 2) : w.dz[0];
   w.part = take((size_t)w.split * T * H * 4);  // d_h's float sums, of each run
-  w.keep = ce_keep(T, w.vchunk, w.n_chunks);
+  w.keep = ce_keep(T, H, w.vchunk, w.n_chunks);
   w.x = w.keep ? take((size_t)T * w.vchunk * 4) : 0;
   w.total = off;
   return w;
 }
+
+// Whether the reduce and the kept logits' dlogits are one launch: every column block of a row then joins the
+// row's partials again, which is worth a launch while that is little to read (64 x 9000: 28.1 us of a call and
+// 29.2 by two launches; 16 x 32000 x 768, above the limit: 50.2 and 48.7).
+bool ce_joint(int64_t T, int64_t col_blocks, int n_col_tiles) { return T * col_blocks * n_col_tiles <= (1 << 14); }
 
 struct CeCall {
   const void *h, *W;
@@ -363,6 +439,9 @@ struct CeCall {
   const void* h_src;      // h, or the compact hidden states
   const int32_t *idx, *live_n;
   cudaStream_t st;
+  // Rows of A that a CTA loads of the tokens' operands: all 128 of the tile, or with fewer tokens theirs (the
+  // others' accumulator rows are then whatever the stage held, and nothing reads them).
+  int a_rows() const { return cg == 1 && T < BM ? (int)((T + 7) / 8 * 8) : BM; }
   float* f(size_t off) const { return reinterpret_cast<float*>(base + off); }
 };
 
@@ -398,7 +477,7 @@ bool map_out(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64
 template <int PLAIN, int CAP>
 int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc, bool pdl) {
   CUtensorMap ma, mb, mc = {};
-  if (!map_k(&ma, c.h_src, c.T, c.H, c.H, BM) || !map_k(&mb, c.W, c.V, c.H, c.H, BN / c.cg)) return GRPO_ERR_UNSUPPORTED;
+  if (!map_k(&ma, c.h_src, c.T, c.H, c.H, c.a_rows()) || !map_k(&mb, c.W, c.V, c.H, c.H, BN / c.cg)) return GRPO_ERR_UNSUPPORTED;
   if (epi_is_dlogits(PLAIN) && !map_dz_store(&mc, g.dz, c.T, vc, g.ldz)) return GRPO_ERR_UNSUPPORTED;
   if (g.keep && !map_out(&mc, c.f(c.ws.x), c.V, c.T, 1, c.ws.vchunk, false)) return GRPO_ERR_UNSUPPORTED;
   g.M = c.T;
@@ -410,6 +489,7 @@ int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc, bool pdl
   g.live_n = c.live_n;
   g.acc = c.acc;
   g.zy = c.f(c.ws.zy);
+  g.a_rows = c.a_rows();
   g.cap = c.cap;
   g.inv_cap = 1.f / c.cap;
   return c.cap > 0.f ? launch<CAP, false, false>(c.cg, ma, mb, mc, g, st, pdl)
@@ -420,7 +500,7 @@ int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc, bool pdl
 template <int CG>
 int ce_products(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0, int64_t vc, cudaStream_t st, bool pdl) {
   CUtensorMap dz_k = {}, w = {}, part = {}, dz_mn = {}, h = {}, dw = {};
-  if (c.d_h && (!map_k(&dz_k, dz, c.T, vc, c.ws.vchunk, BM) ||
+  if (c.d_h && (!map_k(&dz_k, dz, c.T, vc, c.ws.vchunk, c.a_rows()) ||
                 !map_mn(&w, static_cast<const __nv_bfloat16*>(c.W) + v0 * c.H, vc, c.H, c.H) ||
                 !map_out(&part, c.f(c.ws.part), c.H, c.T, c.ws.split, c.H, false)))
     return GRPO_ERR_UNSUPPORTED;
@@ -429,6 +509,7 @@ int ce_products(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0,
     return GRPO_ERR_UNSUPPORTED;
   BwdArgs g{};
   g.T = c.T;
+  g.a_rows = c.a_rows();
   g.H = c.H;
   g.vc = vc;
   g.with_dh = c.d_h != nullptr;
@@ -445,7 +526,7 @@ int ce_products(const CeCall& c, const __nv_bfloat16* dz, int chunk, int64_t v0,
   return launch_units<CG, Shape<CG, EPI_CE_STORE>, &bwd_kernel<CG>>(units, st, pdl, dz_k, w, part, dz_mn, h, dw, g);
 }
 
-int ce_backward(const CeCall& c) {
+int ce_backward(const CeCall& c, const CeDzArgs& kept, bool kept_done) {
   std::unique_lock<std::mutex> lock;
   Overlap* ov = overlap_on() && c.ws.n_chunks > 1 ? overlap_state(lock, c.st) : nullptr;
   const cudaStream_t bst = ov ? ov->aux : c.st;
@@ -457,10 +538,10 @@ int ce_backward(const CeCall& c) {
       if (ov && i >= 2) GRPO_CUDA_TRY(cudaStreamWaitEvent(c.st, ov->buf_free[i & 1], 0));
       int rc;
       if (c.ws.keep) {
-        CeDzArgs a{c.T, c.V, c.ws.vchunk, c.f(c.ws.x), dz, c.target, c.idx, c.live_n, c.f(c.ws.lse2), c.f(c.ws.coef),
-                   c.f(c.ws.ea), c.cap, 1.f / c.cap, 1.f - c.smoothing, c.smoothing / (float)c.V};
         const int64_t gx = (c.V + 2047) / 2048, gy = std::min<int64_t>(c.T, std::max<int64_t>(1, (int64_t)sm_count() * 16 / gx));
-        rc = launch_dep(c.cap > 0.f ? ce_dz_kernel<true> : ce_dz_kernel<false>, dim3((unsigned)gx, (unsigned)gy), 256, c.st, a);
+        rc = kept_done ? GRPO_OK
+                       : launch_dep(c.cap > 0.f ? ce_dz_kernel<true> : ce_dz_kernel<false>,
+                                    dim3((unsigned)gx, (unsigned)gy), 256, c.st, kept);
       } else {
         GemmArgs g{};
         g.lse2 = c.f(c.ws.lse2);
@@ -560,6 +641,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   c.acc = acc;
   c.base = static_cast<uint8_t*>(workspace);
   c.st = as_stream(stream);
+  bool pdl = false;  // whether a kernel of this call comes before
   if (mask) {
     int32_t* idx = reinterpret_cast<int32_t*>(c.base + c.ws.idx);
     int32_t* live_n = reinterpret_cast<int32_t*>(c.base + c.ws.live_n);
@@ -573,6 +655,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
     c.h_src = h_live;
     c.idx = idx;
     c.live_n = live_n;
+    pdl = true;
   }
   GemmArgs g{};
   g.part_m = c.f(c.ws.part_m);
@@ -581,7 +664,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   g.n_n = c.ws.n_col_tiles;
   g.live_mode = c.live_n ? LIVE_ROWS : LIVE_NONE;
   g.keep = c.ws.keep && (d_h || dW);
-  int rc = ce_logits<EPI_CE_PARTIALS, EPI_CE_PARTIALS_CAP>(c, g, c.st, 0, mask != nullptr);
+  int rc = ce_logits<EPI_CE_PARTIALS, EPI_CE_PARTIALS_CAP>(c, g, c.st, 0, pdl);
   if (rc != GRPO_OK) return rc;
   CeReduceArgs r{};
   r.T = T;
@@ -604,7 +687,14 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   r.acc = acc;
   r.idx = c.idx;
   r.live_n = c.live_n;
-  rc = launch_dep(ce_reduce_kernel, dim3((unsigned)((T + 31) / 32)), kCeReduceWarps * 32, c.st, r);
-  if (rc != GRPO_OK) return rc;
-  return d_h || dW ? ce_backward(c) : GRPO_OK;
+  const bool grads = d_h || dW;
+  const CeDzArgs kept{T, V, c.ws.vchunk, c.f(c.ws.x), reinterpret_cast<__nv_bfloat16*>(c.base + c.ws.dz[0]), target, c.idx,
+                      c.live_n, r.lse2, r.coef, r.ea, c.cap, 1.f / c.cap, 1.f - c.smoothing, c.smoothing / (float)V};
+  const int64_t gx = (V + 2047) / 2048;
+  const bool joint = grads && c.ws.keep && ce_joint(T, gx, c.ws.n_col_tiles);
+  rc = joint ? launch_dep(c.cap > 0.f ? ce_reduce_dz_kernel<true> : ce_reduce_dz_kernel<false>,
+                          dim3((unsigned)gx, (unsigned)T), 256, c.st, r, kept)
+             : launch_dep(ce_reduce_kernel, dim3((unsigned)((T + 31) / 32)), kCeReduceWarps * 32, c.st, r);
+  if (rc != GRPO_OK || !grads) return rc;
+  return ce_backward(c, kept, joint);
 }

@@ -16,6 +16,7 @@ namespace lmhead {
 struct BwdArgs {
   int64_t T, H, vc;
   int with_dh, with_dw, split;
+  int a_rows;  // rows of dz that a d_h unit loads (see CeCall)
   int dh_accumulate, dw_accumulate, dw_bf16;
   float dw_scale;
   const int32_t* live_n;  // the unmasked tokens' count (compact rows), or NULL: T
@@ -126,7 +127,8 @@ bwd_kernel(const __grid_constant__ CUtensorMap dz_k, const __grid_constant__ CUt
         const int a_row = u.mu * BM * CG + (int)rank * BM, b_row = u.nu * BN + (int)rank * S::B_ROWS;
         for (int kb = u.k0; kb < u.k1; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, s_abort)) break;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * S::STAGE_BYTES);
+          if (rank == 0)
+            mbar_arrive_expect_tx(&full[stage], u.dw ? CG * S::STAGE_BYTES : CG * (g.a_rows * BK * 2 + S::B_BYTES));
           const uint32_t sa = sbase + stage * S::STAGE_BYTES, bar = full0 + stage * 8u;
           if (u.dw) {
             load_operand<CG, true, BM>(sa, &dz_mn, bar, kb * BK, a_row);

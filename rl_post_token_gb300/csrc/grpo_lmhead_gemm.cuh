@@ -283,6 +283,7 @@ struct GemmArgs {
   // ea: [T] s w (1 + 2 lambda lse); coef: [T] s w)
   float cap, inv_cap;      // the soft cap c and 1 / c (_CAP)
   float ce_hot, ce_smooth; // 1 - eps, eps / V
+  int a_rows;              // rows of the A tile that are loaded (the map's box)
   int keep;                // EPI_CE_PARTIALS: also store the products (float [T][ldz], map_c)
 };
 
@@ -626,7 +627,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const int b_row = (g.col_tile0 + nu) * BN + (int)rank * S::B_ROWS;
         for (int kb = k0; kb < k1; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, s_abort)) break;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * S::STAGE_BYTES);
+          if (rank == 0)
+            mbar_arrive_expect_tx(&full[stage], epi_is_ce(EPI) ? CG * (g.a_rows * BK * 2 + S::B_BYTES) : CG * S::STAGE_BYTES);
           const uint32_t sa = sbase + stage * S::STAGE_BYTES;
           const uint32_t bar = full0 + stage * 8u;
           load_operand<CG, A_MN, BM>(sa, &map_a, bar, kb * BK, a_row);
