@@ -126,13 +126,89 @@ def test_parity(cta_group, terms, T, V, H, masked):
     _check(a, 1.0 / T, _call(*a, 1.0 / T, w=w, dt=(BF16, BF16), **terms), w=w, **terms)
 
 
-@pytest.mark.parametrize("T, masked", [(700, 0.4), (1100, None)])
-def test_several_vocabulary_pieces(cta_group, T, masked):
-    # more than 66 tiles: over 32 MB of dlogits from T = 993 on
-    a = _inputs(T, 35000, 64, 3, masked)
+@pytest.mark.parametrize("T, V, masked", [(700, 35000, 0.4), (1100, 35000, None), (150, 6000, 0.4)])
+def test_logits_kept_and_formed_again(cta_group, T, V, masked):
+    # (the kept ones take 48 MB at most; few of them are joined and turned into dlogits by one kernel)
+    a = _inputs(T, V, 64, 3, masked)
     kw = dict(label_smoothing=0.1, z_loss=1e-3)
     _check(a, 1.0, _call(*a, 1.0, **kw), **kw)
     _check(a, 1.0, _call(*a, 1.0, dt=(BF16, F32), **kw), **kw)
+
+
+def _check64(args, scale, out, w=None, label_smoothing=0.0, z_loss=0.0, soft_cap=0.0):
+    """_check on the GPU in float64, all tokens at once (for calls too large for the row oracle)."""
+    h, Wt, y, mask = args
+    live = torch.ones(len(y), dtype=torch.bool, device=DEV) if mask is None else _t(mask) != 0
+    hd, wd, at = h.double()[live], Wt.double(), _t(y).long()[live][:, None]
+    V = wd.shape[0]
+    x = hd @ wd.T
+    z = soft_cap * torch.tanh(x / soft_cap) if soft_cap else x
+    d = 1 / torch.cosh(x / soft_cap) ** 2 if soft_cap else 1.0
+    lse = torch.logsumexp(z, 1, keepdim=True)
+    lp = z - lse
+    logp, mean = lp.gather(1, at), lp.mean(1, keepdim=True)
+    loss = -(1 - label_smoothing) * logp - label_smoothing * mean + z_loss * lse ** 2
+    rel = lambda v: 1e-5 * v.abs().clamp(min=1.0)
+    bar = (1 - label_smoothing) * rel(logp) + label_smoothing * rel(mean) + 2 * z_loss * lse.abs() * rel(lse) + 2.0 ** -22 * loss.abs()
+    for k, want, tol in (("logp", logp, rel(logp)), ("lse", lse, rel(lse)), ("loss", loss, bar)):
+        assert torch.all((out[k].double()[live] - want[:, 0]).abs() <= tol[:, 0]), k
+        assert torch.all(out[k][~live] == 0), k
+    g = torch.full_like(lse, abs(scale)) if w is None else abs(scale) * _t(w).double()[live][:, None]
+    p, hot = lp.exp(), torch.zeros_like(lp).scatter_(1, at, 1 - label_smoothing)
+    dx = g * d * ((1 + 2 * z_loss * lse) * p - hot - label_smoothing / V)
+    m = (2.0 ** -8 + 2.0 ** -10) * dx.abs() + 1.01 * g * d * (
+        (1 + 2 * z_loss * lse).abs() * p * (rel(lp) + 2.0 ** -21) + 2 * z_loss * rel(lse) * p
+        + 2.0 ** -21 * (hot + label_smoothing / V)) + (1e-5 * dx.abs() if soft_cap else 0.0)
+    full = torch.zeros(h.shape, dtype=torch.float64, device=DEV)
+    d_h, tol_h = full.clone(), full
+    d_h[live], tol_h[live] = dx @ wd, m @ wd.abs()
+    for k, want, tol in (("d_h", d_h, tol_h), ("dW", dx.T @ hd, m.T @ hd.abs())):
+        if out[k].dtype == BF16:
+            tol = tol + 2.0 ** -8 * (want.abs() + tol)
+        e = (out[k].double() - want).abs()
+        assert torch.all(e <= tol + 1e-30), (k, float(e.max()), float((e - tol).max()))
+
+
+@pytest.mark.parametrize("terms", [dict(), dict(label_smoothing=0.1, z_loss=1e-3, soft_cap=5.0)])
+@pytest.mark.parametrize("masked", [None, 0.5])
+def test_several_vocabulary_pieces(cta_group, masked, terms):
+    # a piece has 256 MB of dlogits: 124 tiles of 256 columns at 4200 tokens; two pieces, the second's last
+    # tile and K block ragged
+    a = _inputs(4200, 35001, 72, 3, masked)
+    w = np.random.default_rng(1).random(4200).astype(np.float32)
+    _check64(a, 0.3, _call(*a, 0.3, **terms), **terms)
+    _check64(a, 0.3, _call(*a, 0.3, w=w, dt=(BF16, BF16), **terms), w=w, **terms)
+    base = torch.randn((35001, 72), device=DEV)
+    one, buf = _call(*a, 1.0, **terms), base.clone()
+    two = _call(*a, 1.0, dW=buf, dw_accumulate=True, dt=(BF16, F32), **terms)
+    assert torch.equal(buf, base + one["dW"]) and torch.equal(two["d_h"], one["d_h"].to(BF16))
+
+
+def test_offsets_past_2_to_the_31():
+    # W and dW of 2.2e9 elements, targets among the last rows
+    T, V, H = 64, 1_100_000, 2048
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    Wt = torch.empty((V, H), dtype=BF16, device=DEV)
+    for a in range(0, V, 100_000):
+        Wt[a:a + 100_000] = (torch.randn((100_000, H), generator=g, device=DEV) / math.sqrt(H)).to(BF16)
+    h = torch.randn((T, H), generator=g, device=DEV).to(BF16)
+    y = (V - 1 - np.arange(T) * 331).astype(np.int32)
+    out = _call(h, Wt, y, None, 1.0, dt=(BF16, BF16))
+    x = torch.cat([h.double() @ Wt[a:a + 100_000].double().T for a in range(0, V, 100_000)], 1)
+    lse = torch.logsumexp(x, 1, keepdim=True)
+    logp = (x - lse).gather(1, _t(y).long()[:, None])[:, 0]
+    assert torch.all((out["logp"].double() - logp).abs() <= 1e-5 * logp.abs())
+    dx = (x - lse).exp()
+    dx[torch.arange(T, device=DEV), _t(y).long()] -= 1
+    rows = torch.tensor([0, 1, V // 2, 1_048_575, 1_048_576, V - 332, V - 2, V - 1], device=DEV)
+    hd = h.double()
+    want, tol = dx[:, rows].T @ hd, dx[:, rows].abs().T @ hd.abs()
+    e = (out["dW"][rows].double() - want).abs()
+    assert torch.all(e <= (2.0 ** -8 + 2.0 ** -9) * tol + 2.0 ** -8 * want.abs())
+    want = sum(dx[:, a:a + 100_000] @ Wt[a:a + 100_000].double() for a in range(0, V, 100_000))
+    size = sum(dx[:, a:a + 100_000].abs() @ Wt[a:a + 100_000].double().abs() for a in range(0, V, 100_000))
+    assert torch.all((out["d_h"].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -9) * size + 2.0 ** -8 * want.abs())
 
 
 def test_masked_tokens_may_hold_anything(cta_group):
@@ -232,7 +308,7 @@ def test_large_and_peaked_logits():
 
 
 def test_streams_and_graph_replay_give_the_bits():
-    T, V, H = 1100, 35000, 64  # several pieces: both streams
+    T, V, H = 4200, 35000, 64  # two pieces: both streams
     a, b = _inputs(T, V, H, 11, 0.3), _inputs(T, V, H, 12, 0.6)
     wa, wb = _call(*a, 1.0, dt=(BF16, BF16)), _call(*b, 1.0, dt=(BF16, BF16))
     h, Wt, y, mask = (x.clone() if torch.is_tensor(x) else _t(x) for x in a)
@@ -254,6 +330,38 @@ def test_streams_and_graph_replay_give_the_bits():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(loss, want["loss"]) and torch.equal(d_h, want["d_h"]) and torch.equal(dW, want["dW"])
+
+
+def test_an_eager_call_during_another_streams_capture():
+    # the capture holds the second stream until it ends; the eager call keeps to its own
+    T, V, H = 4200, 35000, 64
+    a, b = _inputs(T, V, H, 11, 0.3), _inputs(T, V, H, 12, 0.6)
+    wa, wb = _call(*a, 1.0), _call(*b, 1.0)
+
+    def buffers(x):
+        h, Wt, y, mask = x
+        return [h, Wt, _t(y), _t(mask), torch.zeros((T, H), device=DEV), torch.zeros((V, H), device=DEV),
+                torch.zeros(T, device=DEV), _lib.new_step_acc(DEV),
+                torch.empty(_lib.grpo_lmhead_ce_workspace_size(T, V, H), dtype=torch.uint8, device=DEV)]
+
+    def call(z):
+        _lib.grpo_lmhead_ce_fwd_bwd(*z[:4], 1.0, *z[4:])
+
+    za, zb = buffers(a), buffers(b)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, capture_error_mode="relaxed"):
+        call(za)
+        with torch.cuda.stream(side):
+            call(zb)
+    side.synchronize()
+    assert torch.equal(zb[6], wb["loss"]) and torch.equal(zb[4], wb["d_h"]) and torch.equal(zb[5], wb["dW"])
+    assert torch.all(za[6] == 0)
+    g.replay()
+    call(zb)
+    torch.cuda.synchronize()
+    for z, want in ((za, wa), (zb, wb)):
+        assert torch.equal(z[6], want["loss"]) and torch.equal(z[4], want["d_h"]) and torch.equal(z[5], want["dW"])
 
 
 def test_micro_batches_sum_to_the_whole_step():
