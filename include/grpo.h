@@ -39,8 +39,8 @@
  *       GRPO_ROWPASS_FWD=0        forward-only calls take the general cluster kernel instead of
  *                                 the streaming forward kernel;
  *       GRPO_LMHEAD_CTA_GROUP=1   fused LM-head: one-CTA 128 x 256 tiles instead of paired
- *                                 2-CTA 256 x 256 tiles (unset, the distillation's form chooses
- *                                 by its number of tokens);
+ *                                 2-CTA 256 x 256 tiles (unset, the distillation's form and the
+ *                                 cross entropy choose by their number of tokens);
  *       GRPO_LMHEAD_OVERLAP=0     fused LM-head: the backward's launches all on the caller's
  *                                 stream instead of two streams.
  */
@@ -693,8 +693,10 @@ GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const void* W, int6
  *   L = (1 - eps) (lse - z_y) + eps (lse - mean_v z_v) + lambda lse^2
  *   dL/dz_v = (1 + 2 lambda lse) p_v - (1 - eps) [v = y] - eps / V,  dL/dx = dL/dz (1 - (z / soft_cap)^2)
  *   d_h_t = grad_scale w_t m_t dL/dx W,  dW = sum_t grad_scale w_t m_t dL/dx_t h_t
- * x is formed tile by tile over pieces of the vocabulary and never stored, as in
- * grpo_lmhead_loss_fwd_bwd; the masked tokens cost no product (their hidden states are not read and may
+ * x is formed tile by tile over pieces of the vocabulary, as in grpo_lmhead_loss_fwd_bwd, first for the lse
+ * and once more for the gradient; no more than a piece is ever stored (256 MB of bf16 dlogits, 66 tiles of
+ * 256 columns at least; where the whole vocabulary is one piece its float32 logits, 256 MB at most, may be
+ * kept instead of formed again). The masked tokens cost no product (their hidden states are not read and may
  * hold anything). */
 typedef struct grpo_ce_terms {
   float label_smoothing;  /* eps in [0, 1]: the share of the uniform distribution in the target */
@@ -714,8 +716,9 @@ GRPO_API size_t grpo_lmhead_ce_workspace_size(int64_t T, int64_t V, int64_t H);
  *  terms      host, or NULL: none
  *  grad_scale 1/max(N, 1) (or 1 with a deferred finish or clip)
  *  d_h        device [T, H] of d_h_dtype, or NULL; dW device [V, H] of dW_dtype, or NULL (both NULL: loss
- *             only); GRPO_DTYPE_*, 16-byte aligned. dlogits go into the products as bf16, the sums are
- *             float32, a bf16 gradient is their one rounding
+ *             only); GRPO_DTYPE_*, 16-byte aligned, overlapping neither h nor W nor each other. dlogits
+ *             (without grad_scale) go into the products as bf16, the sums are float32, a bf16 gradient is
+ *             their one rounding
  *  flags      0, or GRPO_LMHEAD_DW_ACCUMULATE: dW += (float32 only)
  *  loss_tok   device float [T]; logp_tok (log p_y) and lse_tok device float [T] or NULL
  *  acc        device grpo_step_acc; loss_tok and acc go to grpo_finish_step (no token counts as clipped)
@@ -725,7 +728,7 @@ GRPO_API size_t grpo_lmhead_ce_workspace_size(int64_t T, int64_t V, int64_t H);
  * non-finite, and its gradient is NaN. T = 0 writes dW as zeros (or leaves it, accumulating).
  * Results of a token do not depend on the masked ones; dW sums the unmasked tokens in order; d_h's order of
  * sums depends on T, V and H. Environment: as grpo_lmhead_loss_fwd_bwd.
- * Errors: GRPO_ERR_INVALID (sizes, terms, a non-finite grad_scale, NULL required pointer, alignment,
+ * Errors: GRPO_ERR_INVALID (sizes, terms, a non-finite grad_scale, NULL required pointer, alignment, overlap,
  * DW_ACCUMULATE on a bf16 dW, unknown flags), GRPO_ERR_CAPACITY (workspace too small),
  * GRPO_ERR_UNSUPPORTED (dtype, tensor-map creation), GRPO_ERR_CUDA. */
 GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int64_t T, int64_t V, int64_t H,

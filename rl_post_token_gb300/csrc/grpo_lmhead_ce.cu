@@ -585,6 +585,12 @@ int ce_backward(const CeCall& c, const CeDzArgs& kept, bool kept_done) {
   return rc;
 }
 
+// Whether [a, a + n) and [b, b + m) meet (NULL meets nothing).
+bool meet(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + m && y < x + n;
+}
+
 bool known_dtype(int32_t d) { return d == GRPO_DTYPE_F32 || d == GRPO_DTYPE_BF16; }
 
 }  // namespace
@@ -619,6 +625,11 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   }
   if (!h || !W || !target || !loss_tok || !workspace) return GRPO_ERR_INVALID;
   if (((uintptr_t)h | (uintptr_t)W | (uintptr_t)d_h | (uintptr_t)dW) & 15u || ((uintptr_t)workspace & 255u))
+    return GRPO_ERR_INVALID;
+  const size_t nh = (size_t)T * H, nw = (size_t)V * H;
+  const size_t bh = nh * (d_h_dtype == GRPO_DTYPE_BF16 ? 2 : 4), bw = nw * (dW_dtype == GRPO_DTYPE_BF16 ? 2 : 4);
+  if (meet(d_h, bh, h, nh * 2) || meet(d_h, bh, W, nw * 2) || meet(d_h, bh, dW, bw) || meet(dW, bw, h, nh * 2) ||
+      meet(dW, bw, W, nw * 2))
     return GRPO_ERR_INVALID;
   CeCall c{};
   c.ws = ce_layout(T, V, H);

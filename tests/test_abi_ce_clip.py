@@ -7,6 +7,7 @@ import pytest
 from rl_post_token_gb300 import _lib
 
 P = 1 << 20  # a placeholder address
+Q = 1 << 16  # the matrices' distance
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -21,6 +22,7 @@ def _ce(T=4, V=10, H=64, h=P, W=P, target=P, mask=P, eps=0.0, lam=0.0, cap=0.0, 
         flags=0, loss=P, acc=P, ws=P, size=None):
     need = _lib.lib().grpo_lmhead_ce_workspace_size(max(T, 1), max(V, 1), max(H, 8))
     tm = _lib.grpo_ce_terms(eps, lam, cap, None)
+    h, W, d_h, dW = (x + k * Q if x == P else x for k, x in enumerate((h, W, d_h, dW)))
     return _lib.lib().grpo_lmhead_ce_fwd_bwd(h, W, T, V, H, target, mask, C.byref(tm), scale, d_h, dh, dW, dw, flags, loss,
                                              None, None, acc, ws, need if size is None else size, None)
 
@@ -45,6 +47,12 @@ def test_cross_entropy_types_sizes_and_capacity():
     for bad in ((0, 10, 64), (4, 0, 64), (4, 10, 0), (-1, 10, 64), (1 << 31, 10, 64), (4, 1 << 31, 64)):
         assert _lib.grpo_lmhead_ce_workspace_size(*bad) == 0
     assert _ce(T=0, dW=None) == _lib.OK  # nothing to launch
+
+
+@pytest.mark.parametrize("kw", [dict(d_h=P + 16), dict(d_h=P + Q + 16), dict(dW=P + 4 * 64 * 2 - 16), dict(dW=P + Q + 16),
+                                dict(dW=P + 2 * Q + 4 * 64 * 4 - 16), dict(d_h=P + Q - 16, dh=1)])
+def test_cross_entropy_refuses_overlaps(kw):
+    assert _ce(**kw) == _lib.ERR_INVALID
 
 
 def _list(n, ptr=P, numel=8, dtype=0, gap=1 << 12):
