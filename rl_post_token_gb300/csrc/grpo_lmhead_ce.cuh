@@ -6,7 +6,7 @@
 //   dL/dx_v   = ((1 + 2 lambda lse) p_v - (1 - eps) [v = y] - eps / V) (1 - (z_v / c)^2)
 //
 // A tile's epilogue must end before the next tile's products (256 x 256 x H on a pair of SMs: about 9 H
-// clocks); per element it takes one exponential and, with the cap, another and a reciprocal. Eight warps
+// clocks; with the cap the epilogue is the longer one below H = 2000 or so); per element it takes one exponential and, with the cap, another and a reciprocal. Eight warps
 // share it, two to each quarter of the accumulator's lanes: `half` is the columns' half that is a warp's.
 
 namespace grpo {
@@ -19,7 +19,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // t = tanh(u) and d = 1 - t^2. For |u| <= 1 the fifth convergent of Lambert's continued fraction,
-// u (945 + 105 u^2 + u^4) / (945 + 420 u^2 + 15 u^4), off by less than 6e-8 of its value there (the
+// u (945 + 105 u^2 + u^4) / (945 + 420 u^2 + 15 u^4), off by less than 7e-8 of its value there (the
 // exponential's form would lose the leading bits of a small u to cancellation); above it
 // e = exp(2 |u|), t = 1 - 2 / (1 + e), d = 4 e / (1 + e)^2. The exponent stops at 127: the reciprocal is
 // flushed to 0 there, so that t is 1 and d is 0 (they are within 2^-124 of it).
@@ -162,11 +162,11 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, const CUtenso
       float none[1];
       soft_cap32<false>(v, none, g.cap, g.inv_cap);
     }
-    const int k = y - cb;
-    if (y >= cb && k < 32) {
+    const uint32_t k = (uint32_t)y - (uint32_t)cb;  // (a target outside the vocabulary meets no column below V)
+    if (k < 32) {
       got = true;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (uint32_t i = 0; i < 32; ++i)
         if (i == k) zy = v[i];
     }
     if (cb + 32 > V) {  // warp-uniform
@@ -231,8 +231,7 @@ __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensor
     if (cb >= V || warp_row0 >= rows_store) continue;
     uint32_t w[16];
     if (__any_sync(0xffffffffu, live)) {
-      const int k = y - cb;
-      const bool hit = y >= cb && k < 32;
+      const uint32_t k = (uint32_t)y - (uint32_t)cb;
       float d[CAP ? 32 : 1];
       if constexpr (CAP) soft_cap32<true>(v, d, g.cap, g.inv_cap);
 #pragma unroll
@@ -241,9 +240,9 @@ __device__ __forceinline__ void epi_ce_dlogits(const GemmArgs& g, const CUtensor
         v[i] = p.x;
         v[i + 1] = p.y;
       }
-      if (hit) {
+      if (k < 32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (uint32_t i = 0; i < 32; ++i)
           if (i == k) v[i] -= cy;
       }
       if constexpr (CAP) {

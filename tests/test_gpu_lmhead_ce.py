@@ -277,7 +277,7 @@ def test_a_non_finite_token_skips_the_step(what):
     if what == "target":
         y[3] = 900
     elif what == "negative":
-        y[3] = -1
+        y[3] = -2 ** 31
     elif what == "nan":
         h[3, 5] = float("nan")
     elif what == "inf":
@@ -297,6 +297,23 @@ def test_saturated_caps(cap):
     a = _inputs(40, 600, 64, 9, None, std=30.0)
     kw = dict(soft_cap=cap, z_loss=1e-4)
     _check(a, 1.0, _call(*a, 1.0, **kw), **kw)
+
+
+@pytest.mark.parametrize("T", [64, 600])
+def test_a_token_does_not_see_its_neighbours_logits(T):
+    # (the cap's short form is taken where a warp's rows allow it: the same bits as the long one's)
+    h, Wt, y, _ = _inputs(T, 3000, 128, 15, None)
+    kw = dict(soft_cap=30.0, z_loss=1e-4, label_smoothing=0.1)
+    a = _call(h, Wt, y, None, 1.0, **kw)
+    h2 = h.clone()
+    h2[5] *= 200
+    h2[40, 3] = float("nan")
+    b = _call(h2, Wt, y, None, 1.0, **kw)
+    same = torch.ones(T, dtype=torch.bool, device=DEV)
+    same[[5, 40]] = False
+    assert b["loss"][5] != a["loss"][5] and torch.isnan(b["loss"][40])
+    for k in ("loss", "logp", "lse", "d_h"):
+        assert torch.equal(a[k][same], b[k][same]), k
 
 
 def test_large_and_peaked_logits():
