@@ -464,6 +464,25 @@ def _device_args(logits, *tensors) -> None:
             raise ValueError(f"{name} must be contiguous with at least {n} elements")
 
 
+def _flat_ptrs(first, specs):
+    """_device_args's checks of the flat tensors in `specs` and their addresses (None for None), in one
+    pass: half of a small call's time would go into them."""
+    import torch
+
+    dev = torch._C._cuda_getDevice()
+    out = []
+    for spec in specs:
+        _, t, dtype, n = spec
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+            _device_args(first, spec)
+            raise ValueError(f"the tensors must be on the current CUDA device, not on {t.device}")
+        out.append(t.data_ptr())
+    return out
+
+
 def _rows2d(t, name: str, cols: int, rows: int) -> int:
     """Row stride in elements of a 2-D tensor with unit inner stride and the given extent."""
     shape = t.shape
@@ -775,22 +794,20 @@ def grpo_lmhead_ce_fwd_bwd(h, W, target, mask, grad_scale: float, d_h, dW, loss_
     bf16, or None); see grpo.h."""
     import torch
 
-    if h.dim() != 2 or W.dim() != 2 or h.shape[1] != W.shape[1] or not (h.is_contiguous() and W.is_contiguous()):
+    hs, ws = h.shape, W.shape
+    if len(hs) != 2 or len(ws) != 2 or hs[1] != ws[1] or not (h.is_contiguous() and W.is_contiguous()):
         raise ValueError("h [T, H] and W [V, H] must be contiguous with one H")
-    T, H = h.shape
-    V = W.shape[0]
+    (T, H), V = hs, ws[0]
     f32, bf16, u8 = torch.float32, torch.bfloat16, torch.uint8
     dt_h, dt_w = _grad_dtype(d_h, "d_h"), _grad_dtype(dW, "dW")
-    _device_args(h, ("h", h, bf16, None), ("W", W, bf16, None), ("target", target, torch.int32, T), ("mask", mask, u8, T),
-                 ("w_tok", w_tok, f32, T), ("d_h", d_h, d_h.dtype if d_h is not None else None, T * H),
-                 ("dW", dW, dW.dtype if dW is not None else None, V * H), ("loss_tok", loss_tok, f32, T),
-                 ("logp_tok", logp_tok, f32, T), ("lse_tok", lse_tok, f32, T), ("acc", acc, u8, ACC_BYTES),
-                 ("workspace", workspace, workspace.dtype, 0))
-    tm = grpo_ce_terms(float(label_smoothing), float(z_loss), float(soft_cap), _ptr(w_tok))
-    rc = _lib().grpo_lmhead_ce_fwd_bwd(_ptr(h), _ptr(W), T, V, H, _ptr(target), _ptr(mask), C.byref(tm),
-                                       float(grad_scale), _ptr(d_h), dt_h, _ptr(dW), dt_w,
-                                       LMHEAD_DW_ACCUMULATE if dw_accumulate else 0, _ptr(loss_tok), _ptr(logp_tok),
-                                       _ptr(lse_tok), _ptr(acc), _ptr(workspace),
+    p = _flat_ptrs(h, (("h", h, bf16, 0), ("W", W, bf16, 0), ("target", target, torch.int32, T), ("mask", mask, u8, T),
+                       ("w_tok", w_tok, f32, T), ("d_h", d_h, bf16 if dt_h else f32, T * H),
+                       ("dW", dW, bf16 if dt_w else f32, V * H), ("loss_tok", loss_tok, f32, T),
+                       ("logp_tok", logp_tok, f32, T), ("lse_tok", lse_tok, f32, T), ("acc", acc, u8, ACC_BYTES),
+                       ("workspace", workspace, workspace.dtype, 0)))
+    tm = grpo_ce_terms(label_smoothing, z_loss, soft_cap, p[4])
+    rc = _lib().grpo_lmhead_ce_fwd_bwd(p[0], p[1], T, V, H, p[2], p[3], C.byref(tm), grad_scale, p[5], dt_h, p[6], dt_w,
+                                       LMHEAD_DW_ACCUMULATE if dw_accumulate else 0, p[7], p[8], p[9], p[10], p[11],
                                        workspace.numel() * workspace.element_size(), _stream(stream))
     if rc != OK:
         raise GrpoError(rc, "grpo_lmhead_ce_fwd_bwd")

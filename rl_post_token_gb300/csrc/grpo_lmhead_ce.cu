@@ -3,7 +3,7 @@
 // is stored than a piece of the vocabulary.
 //
 //  compact    the unmasked tokens first, in token order, and their hidden states gathered: every GEMM
-//             below runs over them only (a fine-tuning batch masks its prompts). mask NULL: none of it
+//             below runs over them only (a fine-tuning batch masks its prompts). Not with mask NULL
 //  pass A     per (token, 256 vocabulary entries) the softmax's (shift, sum), the target logit and, with
 //             label smoothing, the sum of the logits
 //  reduce     per token the tiles joined in a fixed order: loss, log-prob, lse and the gradient's factors
@@ -28,77 +28,79 @@
 namespace grpo {
 namespace lmhead {
 
-// The unmasked tokens' indices first, in token order, then the masked ones', and the unmasked count. One
-// block: each thread counts a run of tokens, one scan over the threads, then each writes its run.
-constexpr int kCompactThreads = 1024;
+constexpr int kCompactThreads = 256;
 
-__global__ void __launch_bounds__(kCompactThreads) ce_compact_kernel(int64_t T, const uint8_t* mask, int32_t* idx,
-                                                                     int32_t* live_n) {
+// The unmasked tokens' indices first, in token order, then the masked ones', and the unmasked count; their
+// hidden states gathered in that order, zeros behind them up to the padded count (dW reduces over those rows);
+// the masked tokens' d_h rows zeroed (dh_vec 16-byte vectors; no GEMM writes them). Every block counts the whole
+// mask for itself, which is less than a launch of its own for that: block b then takes the tokens
+// [b per, (b + 1) per), 256 at a time, a thread for each one's place and a warp for each row.
+__global__ void __launch_bounds__(kCompactThreads) ce_compact_kernel(int64_t T, int64_t per, int H, const uint8_t* mask,
+                                                                     const __nv_bfloat16* h, int32_t* idx,
+                                                                     int32_t* live_n, __nv_bfloat16* h_live, void* d_h,
+                                                                     int dh_vec) {
   pdl_launch();
-  pdl_wait();
-  __shared__ int32_t warp_sum[kCompactThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int64_t per = (T + kCompactThreads - 1) / kCompactThreads;
-  const int64_t b = (int64_t)tid * per < T ? (int64_t)tid * per : T, e = b + per < T ? b + per : T;
-  int32_t c = 0;
-  for (int64_t t = b; t < e; ++t) c += mask[t] != 0;
-  int32_t x = c;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t v = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += v;
-  }
-  if (lane == 31) warp_sum[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    int32_t v = warp_sum[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    warp_sum[lane] = v;
-  }
-  __syncthreads();
-  const int32_t total = warp_sum[kCompactThreads / 32 - 1];
-  int32_t pos = (w > 0 ? warp_sum[w - 1] : 0) + x - c;  // unmasked tokens before this thread's run
-  for (int64_t t = b; t < e; ++t) {
-    if (mask[t] != 0)
-      idx[pos++] = (int32_t)t;
-    else
-      idx[total + (t - pos)] = (int32_t)t;  // t - pos = masked tokens before t
-  }
-  if (tid == 0) *live_n = total;
-}
-
-// Row i of the compact order, one warp per row: an unmasked token's hidden state is copied; the rows up to
-// the padded count are zeroed (dW reduces over them); a masked token's d_h row is zeroed (dh_vec 16-byte
-// vectors; no GEMM writes it).
-__global__ void __launch_bounds__(256) ce_gather_kernel(int64_t T, int H, const __nv_bfloat16* h, const int32_t* idx,
-                                                        const int32_t* live_n, __nv_bfloat16* h_live, void* d_h,
-                                                        int dh_vec) {
-  pdl_launch();
-  pdl_wait();
-  const int64_t nl = *live_n;
-  const int64_t pad = live_pad(nl, T) < T ? live_pad(nl, T) : T;
-  const int lane = threadIdx.x & 31, nvec = H >> 3;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  constexpr int kWarps = kCompactThreads / 32;
+  __shared__ int32_t sums[2][kWarps], live_of[kWarps], place[kCompactThreads];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nvec = H >> 3;
   const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
-  for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < T; i += warps) {
-    const int64_t tok = idx[i];
-    uint4* dst = reinterpret_cast<uint4*>(h_live) + i * nvec;
-    if (i < nl) {
-      const uint4* src = reinterpret_cast<const uint4*>(h) + tok * nvec;
+  const int64_t t0 = (int64_t)blockIdx.x * per, t1 = t0 + per < T ? t0 + per : T;
+  int32_t before = 0, total = 0;
+#pragma unroll 8
+  for (int64_t t = tid; t < T; t += kCompactThreads) {
+    const int32_t on = mask[t] != 0;
+    total += on;
+    before += t < t0 ? on : 0;
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) {
+    sums[0][w] = total;
+    sums[1][w] = before;
+  }
+  __syncthreads();
+  total = before = 0;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) {
+    total += sums[0][k];
+    before += sums[1][k];
+  }
+  if (blockIdx.x == 0) {
+    if (tid == 0) *live_n = total;
+    const int64_t pad = live_pad(total, T) < T ? live_pad(total, T) : T;
+    for (int64_t i = total + w; i < pad; i += kWarps)
+      for (int k = lane; k < nvec; k += 32) reinterpret_cast<uint4*>(h_live)[i * nvec + k] = z4;
+  }
+  for (int64_t b = t0; b < t1; b += kCompactThreads) {
+    const int64_t t = b + tid;
+    const bool in = t < t1, on = in && mask[t] != 0;
+    const unsigned m = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) live_of[w] = __popc(m);
+    __syncthreads();
+    int32_t rank = before + __popc(m & ((1u << lane) - 1u)), all = 0;  // unmasked tokens before t
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      rank += k < w ? live_of[k] : 0;
+      all += live_of[k];
+    }
+    if (in) idx[on ? rank : total + (t - rank)] = (int32_t)t;  // t - rank: masked tokens before t
+    place[tid] = on ? rank : -1;
+    __syncthreads();
+    const int rows = (int)(t1 - b < kCompactThreads ? t1 - b : kCompactThreads);
+    for (int r = w; r < rows; r += kWarps) {
+      const int32_t to = place[r];
+      if (to >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(h) + (b + r) * nvec;
+        uint4* dst = reinterpret_cast<uint4*>(h_live) + (int64_t)to * nvec;
 #pragma unroll 4
-      for (int k = lane; k < nvec; k += 32) dst[k] = src[k];
-      continue;
+        for (int k = lane; k < nvec; k += 32) dst[k] = src[k];
+      } else if (d_h) {
+        uint4* row = reinterpret_cast<uint4*>(d_h) + (b + r) * dh_vec;
+        for (int k = lane; k < dh_vec; k += 32) row[k] = z4;
+      }
     }
-    if (i < pad)
-      for (int k = lane; k < nvec; k += 32) dst[k] = z4;
-    if (d_h) {
-      uint4* row = reinterpret_cast<uint4*>(d_h) + tok * dh_vec;
-      for (int k = lane; k < dh_vec; k += 32) row[k] = z4;
-    }
+    before += all;
+    __syncthreads();  // (live_of and place are written again)
   }
 }
 
@@ -662,12 +664,11 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
     int32_t* idx = reinterpret_cast<int32_t*>(c.base + c.ws.idx);
     int32_t* live_n = reinterpret_cast<int32_t*>(c.base + c.ws.live_n);
     __nv_bfloat16* h_live = reinterpret_cast<__nv_bfloat16*>(c.base + c.ws.h_live);
-    ce_compact_kernel<<<1, kCompactThreads, 0, c.st>>>(T, mask, idx, live_n);  // (not before the caller's own work ends)
+    // 16 tokens a block or more, no more blocks than 8 to an SM
+    const int64_t per = std::max<int64_t>(16, (T + (int64_t)sm_count() * 8 - 1) / ((int64_t)sm_count() * 8));
+    ce_compact_kernel<<<(unsigned)((T + per - 1) / per), kCompactThreads, 0, c.st>>>(
+        T, per, (int)H, mask, static_cast<const __nv_bfloat16*>(h), idx, live_n, h_live, d_h, (int)(H / (c.dh_bf16 ? 8 : 4)));
     GRPO_CUDA_TRY(cudaGetLastError());
-    const int64_t blocks = std::min<int64_t>((T + 7) / 8, (int64_t)sm_count() * 16);
-    const int rc = launch_dep(ce_gather_kernel, dim3((unsigned)blocks), 256, c.st, T, (int)H,
-                              static_cast<const __nv_bfloat16*>(h), idx, live_n, h_live, d_h, (int)(H / (c.dh_bf16 ? 8 : 4)));
-    if (rc != GRPO_OK) return rc;
     c.h_src = h_live;
     c.idx = idx;
     c.live_n = live_n;
