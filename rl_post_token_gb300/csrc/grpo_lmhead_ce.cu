@@ -20,6 +20,7 @@
 // reading): 44 us of five dependent launches.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 
 #include "grpo_lmhead_ce_bwd.cuh"
@@ -384,13 +385,28 @@ int ce_split(int64_t T, int64_t H, int chunk_tiles) {
   return (int)std::max<int64_t>(1, std::min<int64_t>((3 * kb1 + load - 1) / std::max<int64_t>(load, 1), kb1 / 8));
 }
 
-// Whether pass A keeps its logits, as float, for the dlogits: where the vocabulary is one piece and they stay
-// in L2 (48 MB) or take less memory traffic than forming them again costs (T <= H / 2), 256 MB at most.
-// Kept and formed again, us of a call: 16 x 32000 x 768 50 and 56, 400 x 50257 x 1000 178 and 192, 999 x 10000 x
-// 1000 93 and 99; the other way 300 x 50257 x 512 96 and 89, 999 x 30000 x 256 115 and 100.
+// Whether pass A keeps its logits, as float, for the dlogits: where the vocabulary is one piece and they take
+// 256 MB at most, and 8 bytes an entry (a store, a reading) cost less than 2 H flops. That goes by H: from 1088 on,
+// or from 768 where rows that are no multiple of 128 bytes slow the products; with few tokens (T <= H / 4)
+// forming them again is a reading of W; and a few MB stay in L2. Kept and formed again, us of a call:
+// 800 x 50257 with H = 768, 1024, 1280, 2048: 225 and 217, 266 and 272, 310 and 335, 442 and 509; 250 x 50257 x
+// 512 82 and 76, 100 x 151936 x 512 142 and 148, 16 x 32000 x 768 50 and 56, 500 x 9000 x 512 40 and 41,
+// 999 x 50257 x 1000 325 and 339.
 bool ce_keep(int64_t T, int64_t H, int64_t vchunk, int n_chunks) {
   const int64_t bytes = T * vchunk * 4;
-  return n_chunks == 1 && (bytes <= ((int64_t)48 << 20) || (2 * T <= H && bytes <= ((int64_t)256 << 20)));
+  return n_chunks == 1 && (bytes <= ((int64_t)20 << 20) ||
+                           (bytes <= ((int64_t)256 << 20) && (4 * T <= H || H >= (H % BK ? 768 : 1088))));
+}
+
+// CTAs per tile: 1 where tiles of 128 tokens come to less than 3/4 of the rounds over the SMs in pass A that the
+// pairs' of 256 take. (A CTA by itself loads half as much again for a tile: 800 x 50257 x 1000, 10 rounds and 11,
+// 390 us of a call against 318; 600 x 1024, 7 and 8, 222 and 204; 300 x 512, 4 and 6, 90 and 95; 64 x 151936 x 2048,
+// 4 and 8, 354 and 407.) GRPO_LMHEAD_CTA_GROUP decides where it is set.
+int ce_cta_group(int64_t T, int n_col_tiles) {
+  if (getenv("GRPO_LMHEAD_CTA_GROUP")) return cta_group();
+  auto rounds = [&](int64_t rows, int64_t slots) { return ((T + rows - 1) / rows * n_col_tiles + slots - 1) / slots; };
+  const int64_t sms = sm_count();
+  return 4 * rounds(BM, sms) < 3 * rounds(2 * BM, std::max<int64_t>(sms / 2, 1)) ? 1 : 2;
 }
 
 CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
@@ -655,7 +671,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   c.dh_bf16 = d_h_dtype == GRPO_DTYPE_BF16;
   c.dw_bf16 = dW_dtype == GRPO_DTYPE_BF16;
   c.dw_accumulate = (flags & GRPO_LMHEAD_DW_ACCUMULATE) != 0;
-  c.cg = distill_cta_group(T, c.ws.n_col_tiles);
+  c.cg = ce_cta_group(T, c.ws.n_col_tiles);
   c.acc = acc;
   c.base = static_cast<uint8_t*>(workspace);
   c.st = as_stream(stream);
