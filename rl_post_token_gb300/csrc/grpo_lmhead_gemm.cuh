@@ -282,6 +282,7 @@ struct GemmArgs {
   // the cross entropy's epilogues (part_s2: [n_col_tiles_total][T] sum of the tile's logits, or NULL;
   // ea: [T] s w (1 + 2 lambda lse); coef: [T] s w)
   float cap, inv_cap;      // the soft cap c and 1 / c (_CAP)
+  float gain;              // see give_back
   float ce_hot, ce_smooth; // 1 - eps, eps / V
   int a_rows;              // rows of the A tile that are loaded (the map's box)
   int keep;                // EPI_CE_PARTIALS: also store the products (float [T][ldz], map_c)
