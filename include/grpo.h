@@ -12,6 +12,7 @@
  *   grpo_group_advantage       device: group-normalised advantage per rollout, broadcast to tokens
  *   grpo_logprob_loss_fwd_bwd  device: per chunk, log-softmax + clipped surrogate + dlogits
  *   grpo_finish_step           device: the step's loss sum / max(N,1), metrics, deferred scaling
+ *   grpo_grad_norm, _clip      device: the gradients' norm and the clip, before the optimizer
  *
  * Conventions shared by every entry point:
  *   - Status: every function returns int: GRPO_OK (0), a positive step status, or a negative
@@ -434,7 +435,7 @@ GRPO_API int grpo_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_
  *   valid tokens; counts are sums; if any valid token was non-finite the step is skipped:
  *   status GRPO_STEP_SKIPPED_NONFINITE and the registered gradient buffers are zeroed;
  *   otherwise, when deferred != 0, each buffer is scaled once by 1/max(N, 1) (scale, then
- *   the caller clips, then steps). expected_N >= 0 is checked against N
+ *   clip -- grpo_grad_norm, which can take the scaling over -- then step). expected_N >= 0 is checked against N
  *   (GRPO_ERR_N_MISMATCH in result.status).
  *  loss_tok    device float [n_tok]: the step's per-token losses (input order)
  *  grad_bufs   host array of n_bufs device pointers; grad_numels host int64 [n_bufs];
