@@ -113,7 +113,7 @@ def _check(args, scale, out, w=None, dw0=None, label_smoothing=0.0, z_loss=0.0, 
 
 
 TERMS = [dict(), dict(label_smoothing=0.1), dict(z_loss=1e-3, soft_cap=3.0),
-         dict(label_smoothing=0.25, z_loss=1e-2, soft_cap=30.0)]
+         dict(label_smoothing=0.25, z_loss=1e-2, soft_cap=30.0), dict(label_smoothing=1.0)]
 
 
 @pytest.mark.parametrize("terms", TERMS)
@@ -182,6 +182,19 @@ def test_several_vocabulary_pieces(cta_group, masked, terms):
     one, buf = _call(*a, 1.0, **terms), base.clone()
     two = _call(*a, 1.0, dW=buf, dw_accumulate=True, dt=(BF16, F32), **terms)
     assert torch.equal(buf, base + one["dW"]) and torch.equal(two["d_h"], one["d_h"].to(BF16))
+
+
+@pytest.mark.parametrize("T, V, H", [(70_001, 300, 24), (400_003, 70, 8)])
+def test_many_tokens(T, V, H):
+    # (several rounds of the compaction's blocks)
+    a = _inputs(T, V, H, 16, 0.3)
+    a[3][a[3] != 0] = np.random.default_rng(2).integers(1, 256, int(a[3].sum()))  # any value but 0 counts
+    w = (np.random.default_rng(1).random(T) - 0.3).astype(np.float32)
+    kw = dict(label_smoothing=0.1, z_loss=1e-3)
+    _check64(a, 1.0 / T, _call(*a, 1.0 / T, **kw), **kw)
+    _check64(a, 1.0 / T, _call(*a, 1.0 / T, w=np.abs(w), **kw), w=np.abs(w), **kw)
+    plus, minus = _call(*a, 1.0 / T, w=w, **kw), _call(*a, -1.0 / T, w=-w, **kw)
+    assert torch.equal(plus["d_h"], minus["d_h"]) and torch.equal(plus["dW"], minus["dW"])
 
 
 def test_offsets_past_2_to_the_31():
