@@ -630,6 +630,32 @@ struct DistillLayout {
   int split;
 };
 
+// Vocabulary tiles per chunk: with few tokens more than the loss's, as long as a chunk's dlogits take at
+// most 32 MB (they are read back from L2). 300 tokens, V = 50257, H = 1024: one chunk 206 us, three 294.
+int distill_chunk_tiles(int64_t T) {
+  return (int)std::max<int64_t>(kMaxChunkTiles, std::min<int64_t>(((int64_t)32 << 20) / (T * BN * 2), INT32_MAX / BN));
+}
+
+// CTAs per tile: 1 where tiles of 128 tokens come to fewer rounds over the SMs in pass A than the pairs'
+// of 256 (a round takes the same time). 300 tokens at V = 50257: 4 rounds, not 6, 206 us against 239 of the
+// whole call; 1000 at V = 32000: 7 and 7, 461 against 524 the other way. GRPO_LMHEAD_CTA_GROUP
+// decides where it is set.
+int distill_cta_group(int64_t T, int n_col_tiles) {
+  if (getenv("GRPO_LMHEAD_CTA_GROUP")) return cta_group();
+  auto rounds = [&](int64_t rows, int64_t slots) { return ((T + rows - 1) / rows * n_col_tiles + slots - 1) / slots; };
+  const int64_t sms = sm_count();
+  return rounds(BM, sms) < rounds(2 * BM, std::max<int64_t>(sms / 2, 1)) ? 1 : 2;
+}
+
+// Runs that d_h's reduction over a chunk is cut into: as many as fill 152 SMs (a constant: the workspace's
+// size and the order of the sums follow from it), each of 16 K blocks or more, and of kMaxChunkTiles
+// vocabulary tiles at most. At 300 tokens, V = 50257, H = 1024 d_h took 255 us
+// of 491 in one run per chunk of 66 tiles.
+int d_h_split(int64_t T, int64_t H, int chunk_tiles) {
+  const int64_t units = ((T + BM - 1) / BM) * ((H + BN - 1) / BN), blocks = (int64_t)chunk_tiles * (BN / BK);
+  return (int)std::max<int64_t>((chunk_tiles + kMaxChunkTiles - 1) / kMaxChunkTiles, std::min<int64_t>(152 / units, blocks / 16));
+}
+
 DistillLayout distill_layout(int64_t T, int64_t V, int64_t H, int64_t K) {
   DistillLayout d{};
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };

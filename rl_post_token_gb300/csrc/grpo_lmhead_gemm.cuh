@@ -280,7 +280,7 @@ struct GemmArgs {
   const int32_t* row_idx;
   int live_mode;
   // the cross entropy's epilogues (part_s2: [n_col_tiles_total][T] sum of the tile's logits, or NULL;
-  // ea: [T] s w (1 + 2 lambda lse); coef: [T] s w)
+  // ea: [T] w (1 + 2 lambda lse); coef: [T] w)
   float cap, inv_cap;      // the soft cap c and 1 / c (_CAP)
   float gain;              // see give_back
   float ce_hot, ce_smooth; // 1 - eps, eps / V

@@ -1,6 +1,6 @@
 #pragma once
 // Host side shared by the LM-head entry points: the operands' tensor maps, the persistent launch of a
-// GEMM instance, the backward's second stream, and the choices of tile, vocabulary piece and runs.
+// GEMM instance, and the backward's second stream.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -137,32 +137,6 @@ int launch(int cg, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorM
 // Vocabulary tiles per backward chunk: at most 66 (16896 columns), the chunks of equal width
 // (V = 151936 -> 594 tiles -> 9 chunks of 66).
 constexpr int kMaxChunkTiles = 66;
-
-// Vocabulary tiles per chunk: with few tokens more than the loss's, as long as a chunk's dlogits take at
-// most 32 MB (they are read back from L2). 300 tokens, V = 50257, H = 1024: one chunk 206 us, three 294.
-inline int distill_chunk_tiles(int64_t T) {
-  return (int)std::max<int64_t>(kMaxChunkTiles, std::min<int64_t>(((int64_t)32 << 20) / (T * BN * 2), INT32_MAX / BN));
-}
-
-// CTAs per tile: 1 where tiles of 128 tokens come to fewer rounds over the SMs in pass A than the pairs'
-// of 256 (a round takes the same time). 300 tokens at V = 50257: 4 rounds, not 6, 206 us against 239 of the
-// whole call; 1000 at V = 32000: 7 and 7, 461 against 524 the other way. GRPO_LMHEAD_CTA_GROUP
-// decides where it is set.
-inline int distill_cta_group(int64_t T, int n_col_tiles) {
-  if (getenv("GRPO_LMHEAD_CTA_GROUP")) return cta_group();
-  auto rounds = [&](int64_t rows, int64_t slots) { return ((T + rows - 1) / rows * n_col_tiles + slots - 1) / slots; };
-  const int64_t sms = sm_count();
-  return rounds(BM, sms) < rounds(2 * BM, std::max<int64_t>(sms / 2, 1)) ? 1 : 2;
-}
-
-// Runs that d_h's reduction over a chunk is cut into: as many as fill 152 SMs (a constant: the workspace's
-// size and the order of the sums follow from it), each of 16 K blocks or more, and of kMaxChunkTiles
-// vocabulary tiles at most. At 300 tokens, V = 50257, H = 1024 d_h took 255 us
-// of 491 in one run per chunk of 66 tiles.
-inline int d_h_split(int64_t T, int64_t H, int chunk_tiles) {
-  const int64_t units = ((T + BM - 1) / BM) * ((H + BN - 1) / BN), blocks = (int64_t)chunk_tiles * (BN / BK);
-  return (int)std::max<int64_t>((chunk_tiles + kMaxChunkTiles - 1) / kMaxChunkTiles, std::min<int64_t>(152 / units, blocks / 16));
-}
 
 // The backward's second stream and its events, one set per device, created by the first call
 // that needs them (with the device current) and kept for the process lifetime. A call holds
