@@ -480,7 +480,7 @@ typedef struct grpo_grad_norm_result {
   int64_t reserved1;
 } grpo_grad_norm_result;
 
-/* Bytes of device workspace grpo_grad_norm needs for n tensors of total_numel elements together (82 KB at
+/* Bytes of device workspace grpo_grad_norm needs for n tensors of total_numel elements together (48 KB at
  * most). 0 on bad sizes (more than 2^24 tensors or 2^38 elements). */
 GRPO_API size_t grpo_grad_norm_workspace_size(int64_t total_numel, int32_t n);
 

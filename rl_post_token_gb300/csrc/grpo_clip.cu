@@ -6,10 +6,12 @@
 //   out_ij = factor g_ij
 //
 // Bound by memory: every element is read once for the norm, and read and written once by the clip, which
-// cannot begin before the norm is known. The elements of all tensors are cut into equal shares, one to a
-// block; a block leaves a partial sum for each tensor of its share. The
-// tensors' addresses and sizes travel in the kernel's parameters: no table in device memory, nothing to keep
-// alive, and a captured call replays by itself.
+// cannot begin before the norm is known. 1.24e9 bf16 in 219 tensors: the norm 343 us, 7.2 TB/s of reads, and 8
+// to 12 for the last kernel; 311M float into bf16: 172 us, and the clip 258, 7.2 TB/s. The elements of all tensors
+// are cut into equal shares, one to a block; a block leaves a partial sum for each tensor of its share. (A chunk
+// of each tensor to a block, with a search and a joining of its own, took 133 us for the norm of 213M bf16; the
+// shares take 67.) The tensors' addresses and sizes travel in the kernel's parameters: no table in device memory,
+// nothing to keep alive, and a captured call replays by itself.
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
@@ -25,7 +27,7 @@ constexpr int kVec = 8;        // elements a thread takes at a time
 constexpr int kSlot = 256;     // shares and tensors begin at multiples of so many elements (a tensor is padded)
 constexpr int kWave = 912;     // 152 SMs x 6 blocks: a constant, the order of the sums follows from it
 constexpr int kMaxShares = 6 * kWave;
-constexpr int kShare = 32768;  // elements of a share where there are several waves (of larger ones: one)
+constexpr int kShare = 32768;  // elements of a share, at least, where there are several waves
 constexpr int kFold = 8;       // vectors a thread sums before it folds them into its compensated sum
 constexpr int kFinalThreads = 1024;
 constexpr int kSeg = 16;  // partials of a tensor that a thread of the last kernel sums
@@ -463,9 +465,10 @@ bool overlaps(const void* const* src, const int32_t* sd, void* const* dst, const
   return false;
 }
 
-// Slots of a share of the norm. One wave of blocks up to 131072 elements each (8 slots at least: a vector a
-// thread); above, as many waves of such shares as fill the last, up to 6: blocks that end early then make
-// room for others (2^31 elements of bf16: one wave 627 us, six 588), and the last kernel's partials stay few.
+// Slots of a share of the norm: one wave of blocks up to 32768 elements each (8 slots at least: a vector a
+// thread); above, as many full waves of shares no smaller, up to 6: blocks that end early then make room for
+// others (2^31 elements of bf16: one wave 627 us, six 588), what is read last lies together at the tensors' end
+// (where the clip begins), and the last kernel's partials stay few.
 int norm_share(int32_t slots) {
   const int waves = std::min(std::max(1, (int)((int64_t)slots * kSlot / ((int64_t)kWave * kShare))), kMaxShares / kWave);
   return std::max(8, (slots + waves * kWave - 1) / (waves * kWave));
