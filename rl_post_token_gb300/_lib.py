@@ -645,8 +645,8 @@ def _addr(a: array) -> int:
 
 
 def grpo_grad_norm_workspace_size(grads) -> int:
-    """Workspace bytes of grpo_grad_norm for these tensors."""
-    return int(_lib().grpo_grad_norm_workspace_size(sum(g.numel() for g in grads), len(grads)))
+    """Workspace bytes of grpo_grad_norm for so many tensors of any sizes (48 KB at most)."""
+    return int(_lib().grpo_grad_norm_workspace_size(1 << 38, len(grads)))
 
 
 def grpo_grad_norm(grads, max_norm: float, result, workspace, tensor_norms=None, acc=None, deferred: bool = False,

@@ -450,7 +450,7 @@ CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
 bool ce_joint(int64_t T, int64_t col_blocks, int n_col_tiles) { return T * col_blocks * n_col_tiles <= (1 << 14); }
 
 struct CeCall {
-  const void *h, *W;
+  const void* W;
   int64_t T, V, H;
   const int32_t* target;
   float smoothing, cap, scale;
@@ -658,7 +658,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   CeCall c{};
   c.ws = ce_layout(T, V, H);
   if (workspace_bytes < c.ws.total) return GRPO_ERR_CAPACITY;
-  c.h = c.h_src = h;
+  c.h_src = h;
   c.W = W;
   c.T = T;
   c.V = V;

@@ -224,6 +224,27 @@ def test_offsets_past_2_to_the_31():
     assert torch.all((out["d_h"].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -9) * size + 2.0 ** -8 * want.abs())
 
 
+def _random_case(seed):
+    rng = np.random.default_rng(1000 + seed)
+    log = lambda lo, hi: int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    T, V, H = log(1, 3000), log(1, 30000), 8 * log(1, 100)
+    kw = dict(label_smoothing=float(rng.choice([0, 0, 0.1, 0.6])), z_loss=float(rng.choice([0, 1e-4, 0.05])),
+              soft_cap=float(rng.choice([0, 0, 2.0, 30.0])))
+    dt = (F32, BF16)
+    return (T, V, H), kw, (dt[rng.integers(2)], dt[rng.integers(2)]), rng.choice([None, 0.0, 0.3, 0.9]), rng
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_calls(seed, monkeypatch):
+    (T, V, H), kw, dt, masked, rng = _random_case(seed)
+    if seed % 3:
+        monkeypatch.setenv("GRPO_LMHEAD_CTA_GROUP", str(seed % 3))
+    a = _inputs(T, V, H, seed, masked, std=float(rng.choice([0.3, 1.0, 4.0])))
+    w = rng.random(T).astype(np.float32) if rng.random() < 0.4 else None
+    scale = float(rng.choice([1.0, 1.0 / T, 3e-5]))
+    _check64(a, scale, _call(*a, scale, w=w, dt=dt, **kw), w=w, **kw)
+
+
 def test_masked_tokens_may_hold_anything(cta_group):
     h, Wt, y, mask = _inputs(150, 2000, 136, 5, 0.5)
     a = _call(h, Wt, y, mask, 1.0, label_smoothing=0.1)
