@@ -628,16 +628,18 @@ def _grad_list(grads, name: str):
     or bf16 on the current CUDA device."""
     import torch
 
-    T = torch.Tensor
-    dts = list(map({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}.get, map(_dtype_of, grads)))
-    if None in dts:
-        i = dts.index(None)
-        raise ValueError(f"{name}[{i}] must be float32 or bfloat16, not {grads[i].dtype}")
+    T, n = torch.Tensor, len(grads)
+    code = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+    kinds = list(map(_dtype_of, grads))
+    if not code.keys() >= set(kinds):
+        i = next(i for i, k in enumerate(kinds) if k not in code)
+        raise ValueError(f"{name}[{i}] must be float32 or bfloat16, not {kinds[i]}")
     dev = torch._C._cuda_getDevice()
-    if not all(map(T.is_contiguous, grads)) or any(map(dev.__ne__, map(T.get_device, grads))):
+    if n and (set(map(T.get_device, grads)) != {dev} or not all(map(T.is_contiguous, grads))):
         i = next(i for i, g in enumerate(grads) if not g.is_contiguous() or g.get_device() != dev)
         raise ValueError(f"{name}[{i}] must be contiguous on the current CUDA device, not on {grads[i].device}")
-    return array("Q", map(T.data_ptr, grads)), array("q", map(T.numel, grads)), array("i", dts)
+    dts = array("i", [code[kinds[0]]]) * n if n and kinds.count(kinds[0]) == n else array("i", map(code.get, kinds))
+    return array("Q", map(T.data_ptr, grads)), array("q", map(T.numel, grads)), dts
 
 
 def _addr(a: array) -> int:
