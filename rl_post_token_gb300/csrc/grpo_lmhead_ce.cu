@@ -31,27 +31,41 @@ namespace lmhead {
 
 constexpr int kCompactThreads = 256;
 
+// The count of bytes that are not 0.
+__device__ __forceinline__ int32_t nonzero_bytes(uint32_t w) { return __popc(__vsetne4(w, 0u)); }
+
 // The unmasked tokens' indices first, in token order, then the masked ones', and the unmasked count; their
 // hidden states gathered in that order, zeros behind them up to the padded count (dW reduces over those rows);
 // the masked tokens' d_h rows zeroed (dh_vec 16-byte vectors; no GEMM writes them). Every block counts the whole
 // mask for itself, which is less than a launch of its own for that: block b then takes the tokens
-// [b per, (b + 1) per), 256 at a time, a thread for each one's place and a warp for each row.
+// [b per, (b + 1) per), per a multiple of 16, 256 at a time; its rows' vectors are dealt to all its threads.
 __global__ void __launch_bounds__(kCompactThreads) ce_compact_kernel(int64_t T, int64_t per, int H, const uint8_t* mask,
                                                                      const __nv_bfloat16* h, int32_t* idx,
                                                                      int32_t* live_n, __nv_bfloat16* h_live, void* d_h,
                                                                      int dh_vec) {
   pdl_launch();
   constexpr int kWarps = kCompactThreads / 32;
-  __shared__ int32_t sums[2][kWarps], live_of[kWarps], place[kCompactThreads];
+  __shared__ int32_t sums[2][kWarps], live_of[kWarps], on_row[kCompactThreads], off_row[kCompactThreads];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nvec = H >> 3;
   const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
   const int64_t t0 = (int64_t)blockIdx.x * per, t1 = t0 + per < T ? t0 + per : T;
   int32_t before = 0, total = 0;
+  int64_t done = 0;
+  if ((reinterpret_cast<uintptr_t>(mask) & 15u) == 0) {
+    done = T / 16 * 16;
+#pragma unroll 4
+    for (int64_t t = (int64_t)tid * 16; t < done; t += kCompactThreads * 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(mask + t);
+      const int32_t n = nonzero_bytes(v.x) + nonzero_bytes(v.y) + nonzero_bytes(v.z) + nonzero_bytes(v.w);
+      total += n;
+      before += t < t0 ? n : 0;
+    }
+  }
 #pragma unroll 8
-  for (int64_t t = tid; t < T; t += kCompactThreads) {
-    const int32_t on = mask[t] != 0;
-    total += on;
-    before += t < t0 ? on : 0;
+  for (int64_t t = done + tid; t < T; t += kCompactThreads) {
+    const int32_t n = mask[t] != 0;
+    total += n;
+    before += t < t0 ? n : 0;
   }
   total = __reduce_add_sync(0xffffffffu, total);
   before = __reduce_add_sync(0xffffffffu, before);
@@ -66,11 +80,11 @@ __global__ void __launch_bounds__(kCompactThreads) ce_compact_kernel(int64_t T, 
     total += sums[0][k];
     before += sums[1][k];
   }
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == gridDim.x - 1) {
     if (tid == 0) *live_n = total;
     const int64_t pad = live_pad(total, T) < T ? live_pad(total, T) : T;
-    for (int64_t i = total + w; i < pad; i += kWarps)
-      for (int k = lane; k < nvec; k += 32) reinterpret_cast<uint4*>(h_live)[i * nvec + k] = z4;
+    uint4* rest = reinterpret_cast<uint4*>(h_live) + (int64_t)total * nvec;
+    for (int64_t k = tid; k < (pad - total) * nvec; k += kCompactThreads) rest[k] = z4;
   }
   for (int64_t b = t0; b < t1; b += kCompactThreads) {
     const int64_t t = b + tid;
@@ -78,30 +92,36 @@ __global__ void __launch_bounds__(kCompactThreads) ce_compact_kernel(int64_t T, 
     const unsigned m = __ballot_sync(0xffffffffu, on);
     if (lane == 0) live_of[w] = __popc(m);
     __syncthreads();
-    int32_t rank = before + __popc(m & ((1u << lane) - 1u)), all = 0;  // unmasked tokens before t
+    int32_t rank = __popc(m & ((1u << lane) - 1u)), all = 0;  // unmasked tokens of [b, t)
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
       rank += k < w ? live_of[k] : 0;
       all += live_of[k];
     }
-    if (in) idx[on ? rank : total + (t - rank)] = (int32_t)t;  // t - rank: masked tokens before t
-    place[tid] = on ? rank : -1;
+    if (in) {
+      const int64_t masked = t - (before + rank);  // masked tokens before t
+      idx[on ? before + rank : total + masked] = (int32_t)t;
+      (on ? on_row[rank] : off_row[tid - rank]) = tid;
+    }
     __syncthreads();
-    const int rows = (int)(t1 - b < kCompactThreads ? t1 - b : kCompactThreads);
-    for (int r = w; r < rows; r += kWarps) {
-      const int32_t to = place[r];
-      if (to >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(h) + (b + r) * nvec;
-        uint4* dst = reinterpret_cast<uint4*>(h_live) + (int64_t)to * nvec;
+    // the block's unmasked rows lie side by side in the compact order
+    uint4* dst = reinterpret_cast<uint4*>(h_live) + (int64_t)before * nvec;
+    const uint4* src = reinterpret_cast<const uint4*>(h) + b * nvec;
 #pragma unroll 4
-        for (int k = lane; k < nvec; k += 32) dst[k] = src[k];
-      } else if (d_h) {
-        uint4* row = reinterpret_cast<uint4*>(d_h) + (b + r) * dh_vec;
-        for (int k = lane; k < dh_vec; k += 32) row[k] = z4;
+    for (int k = tid; k < all * nvec; k += kCompactThreads) {
+      const int r = k / nvec;
+      dst[k] = src[(int64_t)on_row[r] * nvec + (k - r * nvec)];
+    }
+    if (d_h) {
+      const int off = (int)(t1 - b < kCompactThreads ? t1 - b : kCompactThreads) - all;
+      uint4* rows = reinterpret_cast<uint4*>(d_h) + b * dh_vec;
+      for (int k = tid; k < off * dh_vec; k += kCompactThreads) {
+        const int r = k / dh_vec;
+        rows[(int64_t)off_row[r] * dh_vec + (k - r * dh_vec)] = z4;
       }
     }
     before += all;
-    __syncthreads();  // (live_of and place are written again)
+    __syncthreads();  // (live_of and the rows are written again)
   }
 }
 
@@ -124,11 +144,22 @@ struct CeToken {
   bool bad;
 };
 
-__device__ __forceinline__ CeToken ce_token(const CeReduceArgs& a, int64_t tok, MS t, float z) {
+// A token's target logit (NaN for a bad target) and weight: loaded before the partials are joined, which hides
+// the loads' latency.
+struct CeInputs {
+  float zy, w;
+};
+
+__device__ __forceinline__ CeInputs ce_inputs(const CeReduceArgs& a, int64_t tok) {
+  const float zy = a.zy[tok];  // (whatever it holds where no column is the target)
+  const int32_t y = a.target[tok];
+  return {y >= 0 && (int64_t)y < a.V ? zy : __int_as_float(0x7fc00000), a.w_tok ? a.w_tok[tok] : 1.f};
+}
+
+__device__ __forceinline__ CeToken ce_token(const CeReduceArgs& a, const CeInputs& in, MS t, float z) {
   CeToken o;
   const float nan = __int_as_float(0x7fc00000);
-  const int32_t y = a.target[tok];
-  const float zy = y >= 0 && (int64_t)y < a.V ? a.zy[tok] : nan;
+  const float zy = in.zy;
   const float l2s = log2f(t.s);
   o.l2 = t.m + l2s;
   // rows past the vouched range of logits count as non-finite, as in the policy loss
@@ -138,7 +169,7 @@ __device__ __forceinline__ CeToken ce_token(const CeReduceArgs& a, int64_t tok, 
   o.loss = -(1.f - a.smoothing) * o.logp + a.z_loss * o.lse * o.lse;
   // lse - mean z, from the shift too
   if (a.part_z) o.loss += a.smoothing * ((t.m - z / (float)a.V * kLog2e) + l2s) * kLn2;
-  o.sw = a.w_tok ? a.w_tok[tok] : 1.f;
+  o.sw = in.w;
   o.cp = o.sw * fmaf(2.f * a.z_loss, o.lse, 1.f);
   if (!isfinite(o.loss)) o.cp = nan;
   o.bad = !isfinite(o.cp);
@@ -151,10 +182,31 @@ __device__ __forceinline__ void ce_store_token(const CeReduceArgs& a, int64_t to
   if (a.lse_tok) a.lse_tok[tok] = o.lse;
 }
 
-// A block takes 32 tokens (lane = token: a partial's load is one 128-byte line), its warps every 32nd
-// vocabulary tile in order; four warps join eight warps' each, warp 0 the four, in order.
 constexpr int kCeReduceWarps = 32;
 
+// Every 32nd tile's partials of row i from `first` on, folded in order; four tiles' loads at a time.
+__device__ __forceinline__ void ce_fold(const CeReduceArgs& a, int64_t i, int first, MS& t, float& z) {
+  for (int c0 = first; c0 < a.n_col_tiles; c0 += 4 * kCeReduceWarps) {
+    MS u[4];
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + k * kCeReduceWarps;
+      const int64_t at = (int64_t)c * a.T + i;
+      const bool in = c < a.n_col_tiles;
+      u[k] = in ? MS{a.part_m[at], a.part_s[at]} : MS{-INFINITY, 0.f};
+      v[k] = in && a.part_z ? a.part_z[at] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      t = ms2_combine(t, u[k]);
+      z += v[k];
+    }
+  }
+}
+
+// A block takes 32 tokens (lane = token: a partial's load is one 128-byte line), its warps every 32nd
+// vocabulary tile in order; four warps join eight warps' each, warp 0 the four, in order.
 __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduceArgs a) {
   pdl_launch();
   pdl_wait();
@@ -162,16 +214,12 @@ __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduce
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t i = (int64_t)blockIdx.x * 32 + lane;
   const bool in = i < a.T, live = in && (!a.idx || i < (int64_t)*a.live_n);
+  const int64_t tok = in && a.idx ? (int64_t)a.idx[i] : i;
+  CeInputs given{};
+  if (w == 0 && live) given = ce_inputs(a, tok);
   MS t{-INFINITY, 0.f};
   float z = 0.f;
-  if (live) {
-#pragma unroll 8
-    for (int c = w; c < a.n_col_tiles; c += kCeReduceWarps) {
-      const int64_t k = (int64_t)c * a.T + i;
-      t = ms2_combine(t, MS{a.part_m[k], a.part_s[k]});
-      if (a.part_z) z += a.part_z[k];
-    }
-  }
+  if (live) ce_fold(a, i, w, t, z);
   wm[w][lane] = t.m;
   ws[w][lane] = t.s;
   wz[w][lane] = z;
@@ -197,11 +245,10 @@ __global__ void __launch_bounds__(kCeReduceWarps * 32) ce_reduce_kernel(CeReduce
   if (w != 0) return;
   bool bad = false;
   if (in) {
-    const int64_t tok = a.idx ? (int64_t)a.idx[i] : i;
     CeToken o{};
     if (live) {
       join(0, 8, 4);
-      o = ce_token(a, tok, t, z);
+      o = ce_token(a, given, t, z);
       bad = o.bad;
     }
     ce_store_token(a, tok, o);
@@ -275,15 +322,11 @@ __global__ void __launch_bounds__(256) ce_reduce_dz_kernel(CeReduceArgs r, CeDzA
   const int64_t tok = a.idx ? (int64_t)a.idx[i] : i;
   CeToken o{};
   if (i < nl) {  // (uniform)
+    const CeInputs given = ce_inputs(r, tok);
     // ce_reduce_kernel's order, its warps the lanes here: every 32nd tile, eight joined, then the four
     MS t{-INFINITY, 0.f};
     float z = 0.f;
-#pragma unroll 4
-    for (int c = lane; c < r.n_col_tiles; c += 32) {
-      const int64_t k = (int64_t)c * r.T + i;
-      t = ms2_combine(t, MS{r.part_m[k], r.part_s[k]});
-      if (r.part_z) z += r.part_z[k];
-    }
+    ce_fold(r, i, lane, t, z);
     auto join = [&](int first, int step, int n) {
       MS u{__shfl_sync(0xffffffffu, t.m, first), __shfl_sync(0xffffffffu, t.s, first)};
       float s = __shfl_sync(0xffffffffu, z, first);
@@ -297,7 +340,7 @@ __global__ void __launch_bounds__(256) ce_reduce_dz_kernel(CeReduceArgs r, CeDzA
     };
     join(lane & 24, 1, 8);
     join(0, 8, 4);
-    o = ce_token(r, tok, t, z);
+    o = ce_token(r, given, t, z);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     ce_store_token(r, tok, o);
@@ -328,7 +371,7 @@ __global__ void __launch_bounds__(256) ce_dh_kernel(const int32_t* live_n, const
     const int64_t i = i0 + x;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < n) {
-#pragma unroll 2
+#pragma unroll(G > 1 ? 2 : 8)
       for (int s = y; s < split; s += G) {
         const float4 o = p[s * stride + i];
         v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
@@ -592,8 +635,11 @@ int ce_backward(const CeCall& c, const CeDzArgs& kept, bool kept_done) {
     }
     if (c.d_h) {
       const int H4 = (int)(c.H / 4);
-      auto kern = c.ws.split > 4 ? ce_dh_kernel<8> : ce_dh_kernel<1>;
-      const int64_t per = c.ws.split > 4 ? 32 : 256, blocks = std::min<int64_t>((c.T * H4 + per - 1) / per, (int64_t)sm_count() * 16);
+      // Eight threads to a vector where the vectors alone are too few to fill the SMs; one where they do (999 x
+      // 1000: 9 us against 12 with eight). A constant, not the device's SMs: the order of the sums follows from it.
+      const bool wide = c.ws.split > 4 && c.T * H4 < 152 * 1024;
+      auto kern = wide ? ce_dh_kernel<8> : ce_dh_kernel<1>;
+      const int64_t per = wide ? 32 : 256, blocks = std::min<int64_t>((c.T * H4 + per - 1) / per, (int64_t)sm_count() * 16);
       const int rc = launch_dep(kern, dim3((unsigned)blocks), 256, bst, c.live_n, c.idx, c.T, H4, c.f(c.ws.part), c.ws.split,
                                 c.scale, c.d_h, c.dh_bf16);
       if (rc != GRPO_OK) return rc;
@@ -682,7 +728,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
     int32_t* live_n = reinterpret_cast<int32_t*>(c.base + c.ws.live_n);
     __nv_bfloat16* h_live = reinterpret_cast<__nv_bfloat16*>(c.base + c.ws.h_live);
     // 16 tokens a block or more, no more blocks than 8 to an SM
-    const int64_t per = std::max<int64_t>(16, (T + (int64_t)sm_count() * 8 - 1) / ((int64_t)sm_count() * 8));
+    const int64_t per = ((T + (int64_t)sm_count() * 8 - 1) / ((int64_t)sm_count() * 8) + 15) / 16 * 16;
     ce_compact_kernel<<<(unsigned)((T + per - 1) / per), kCompactThreads, 0, c.st>>>(
         T, per, (int)H, mask, static_cast<const __nv_bfloat16*>(h), idx, live_n, h_live, d_h, (int)(H / (c.dh_bf16 ? 8 : 4)));
     GRPO_CUDA_TRY(cudaGetLastError());
