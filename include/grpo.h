@@ -498,8 +498,8 @@ GRPO_API size_t grpo_grad_norm_workspace_size(int64_t total_numel, int32_t n);
  *  workspace  device, 8-byte aligned
  * Squares are summed in float32 chains of 16 (a part's sum is right to 2^-19 of itself), the parts in
  * float64, and all of it in float64 where float32's range does not hold them (any finite gradients have a
- * finite sum). The result depends on the values and sizes alone. Host arrays may be freed when the call returns; a captured call
- * keeps the pointers. n = 0: norm 0, coef s.
+ * finite sum). The result depends on the values and sizes alone. Host arrays may be freed when the call
+ * returns; a captured call keeps the pointers. n = 0: norm 0, coef s.
  * Errors: GRPO_ERR_INVALID (sizes, NULL, alignment, a negative or NaN max_norm, deferred without acc),
  * GRPO_ERR_UNSUPPORTED (dtype), GRPO_ERR_CAPACITY (workspace too small), GRPO_ERR_CUDA. */
 GRPO_API int grpo_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n,
@@ -710,7 +710,7 @@ typedef struct grpo_ce_terms {
 /* Bytes of device workspace grpo_lmhead_ce_fwd_bwd needs. 0 on bad sizes. */
 GRPO_API size_t grpo_lmhead_ce_workspace_size(int64_t T, int64_t V, int64_t H);
 
-/*  h, W       device bf16 [T, H], [V, H] row-major, 16-byte aligned; H a multiple of 8
+/*  h, W       device bf16 [T, H], [V, H] row-major, 16-byte aligned; H a multiple of 8, 2^24 at most
  *  target     device int32 [T]; outside [0, V) on an unmasked token: its loss is NaN
  *  mask       device uint8 [T] or NULL (every token counts); masked tokens get 0 in loss_tok, logp_tok and
  *             lse_tok and a zero d_h row, and their target may be anything

@@ -30,6 +30,7 @@ namespace grpo {
 namespace lmhead {
 
 constexpr int kCompactThreads = 256;
+constexpr int64_t kCeMaxH = (int64_t)1 << 24;  // (256 rows' vectors are counted in 32 bits)
 
 // The count of bytes that are not 0.
 __device__ __forceinline__ int32_t nonzero_bytes(uint32_t w) { return __popc(__vsetne4(w, 0u)); }
@@ -666,7 +667,7 @@ bool known_dtype(int32_t d) { return d == GRPO_DTYPE_F32 || d == GRPO_DTYPE_BF16
 }  // namespace
 
 extern "C" GRPO_API size_t grpo_lmhead_ce_workspace_size(int64_t T, int64_t V, int64_t H) {
-  if (T <= 0 || V <= 0 || H <= 0 || T > INT32_MAX / 2 || V > INT32_MAX / 2 || H > INT32_MAX / 2) return 0;
+  if (T <= 0 || V <= 0 || H <= 0 || T > INT32_MAX / 2 || V > INT32_MAX / 2 || H > kCeMaxH) return 0;
   return ce_layout(T, V, H).total;
 }
 
@@ -683,7 +684,7 @@ extern "C" GRPO_API int grpo_lmhead_ce_fwd_bwd(const void* h, const void* W, int
   if (tm.soft_cap != 0.f && !(tm.soft_cap >= 1e-6f && tm.soft_cap <= 1e6f)) return GRPO_ERR_INVALID;
   if (!std::isfinite(grad_scale)) return GRPO_ERR_INVALID;
   if (T < 0 || V < 1 || H < 8 || H % 8 != 0 || !acc || (uintptr_t)acc % alignof(grpo_step_acc)) return GRPO_ERR_INVALID;
-  if (T > INT32_MAX / 2 || V > INT32_MAX / 2 || H > INT32_MAX / 2) return GRPO_ERR_INVALID;
+  if (T > INT32_MAX / 2 || V > INT32_MAX / 2 || H > kCeMaxH) return GRPO_ERR_INVALID;
   if (flags & ~(uint32_t)GRPO_LMHEAD_DW_ACCUMULATE) return GRPO_ERR_INVALID;
   if ((d_h && !known_dtype(d_h_dtype)) || (dW && !known_dtype(dW_dtype))) return GRPO_ERR_UNSUPPORTED;
   // (a bf16 sum would be rounded at every call)

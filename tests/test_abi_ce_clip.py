@@ -27,7 +27,7 @@ def _ce(T=4, V=10, H=64, h=P, W=P, target=P, mask=P, eps=0.0, lam=0.0, cap=0.0, 
                                              None, None, acc, ws, need if size is None else size, None)
 
 
-INV = dict(T=[-1, 1 << 31], V=[0, -3, 1 << 31], H=[0, 4, 60, 66, -8], h=[None, P + 2, P + 8], W=[None, P + 8],
+INV = dict(T=[-1, 1 << 31], V=[0, -3, 1 << 31], H=[0, 4, 60, 66, -8, (1 << 24) + 8], h=[None, P + 2, P + 8], W=[None, P + 8],
            target=[None], eps=[-0.1, 1.01, float("nan")], lam=[-1.0, float("nan"), float("inf")],
            cap=[-1.0, 1e-7, 1e7, float("nan"), float("inf")], scale=[float("nan"), float("inf")], d_h=[P + 4], dW=[P + 8],
            flags=[2, 4, 1 << 31], loss=[None], acc=[None, P + 4], ws=[None, P + 128])
@@ -44,7 +44,8 @@ def test_cross_entropy_types_sizes_and_capacity():
     assert _ce(dw=1, flags=1) == _lib.ERR_INVALID  # bf16 sums
     need = _lib.grpo_lmhead_ce_workspace_size(4, 10, 64)
     assert need > 0 and _ce(size=need - 1) == _lib.ERR_CAPACITY
-    for bad in ((0, 10, 64), (4, 0, 64), (4, 10, 0), (-1, 10, 64), (1 << 31, 10, 64), (4, 1 << 31, 64)):
+    for bad in ((0, 10, 64), (4, 0, 64), (4, 10, 0), (-1, 10, 64), (1 << 31, 10, 64), (4, 1 << 31, 64),
+                (4, 10, (1 << 24) + 8)):
         assert _lib.grpo_lmhead_ce_workspace_size(*bad) == 0
     assert _ce(T=0, dW=None) == _lib.OK  # nothing to launch
 
