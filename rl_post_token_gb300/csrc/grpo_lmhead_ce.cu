@@ -489,8 +489,8 @@ CeLayout ce_layout(int64_t T, int64_t V, int64_t H) {
 }
 
 // Whether the reduce and the kept logits' dlogits are one launch: every column block of a row then joins the
-// row's partials again, which is worth a launch while that is little to read (64 x 9000: 28.1 us of a call and
-// 29.2 by two launches; 16 x 32000 x 768, above the limit: 50.2 and 48.7).
+// row's partials again, which is worth a launch while that is little to read (64 x 9000 x 128: 27.7 us of a call and
+// 31.6 by two launches; above the limit, 16 x 32000 x 768: 48.2 and 47.2, 64 x 32000 x 768: 56 and 51).
 bool ce_joint(int64_t T, int64_t col_blocks, int n_col_tiles) { return T * col_blocks * n_col_tiles <= (1 << 14); }
 
 struct CeCall {
