@@ -87,8 +87,8 @@ __device__ __forceinline__ void give_back(float (&v)[32], float gain) {
 }
 
 // Gives a tile's accumulator back to the MMA issuer, once a warp has loaded its last columns: before it
-// computes on them and stores. (The loads have completed; nothing else is published, so that the arrive at
-// the other CTA need not wait for the tile's global stores.)
+// computes on them and stores. Both arrives release, as the other epilogues' do: the issuer's acquire then has
+// all 32 lanes' accumulator loads before it, the other lanes' by way of __syncwarp.
 struct AccRelease {
   uint32_t remote;  // the even CTA's barrier as a cluster address, or 0: `local`
   uint64_t* local;
@@ -98,7 +98,7 @@ struct AccRelease {
     __syncwarp();
     if (lane == 0) {
       if (remote)
-        mbar_arrive_remote_relaxed(remote);
+        mbar_arrive_remote(remote);
       else
         mbar_arrive(local);
     }
