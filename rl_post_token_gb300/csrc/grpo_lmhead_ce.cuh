@@ -37,7 +37,8 @@ __device__ __forceinline__ void tanh_pair(float u, float& t, float& d) {
 }
 
 // tanh_pair of 32 logits x / c: z = c t in v, d in dz. Where no |x / c| of the warp's rows is above 1 -- the
-// cap's ordinary range -- by the convergent alone, two at a time.
+// cap's ordinary range -- by the convergent alone, two at a time. An infinite x, which the cap would make an
+// ordinary c, becomes NaN (x - x): its token counts as non-finite.
 template <bool DERIV>
 __device__ __forceinline__ void soft_cap32(float (&v)[32], float (&dz)[DERIV ? 32 : 1], float cap, float inv_cap) {
   float top = 0.f;
@@ -65,7 +66,7 @@ __device__ __forceinline__ void soft_cap32(float (&v)[32], float (&dz)[DERIV ? 3
       float t, d;
       tanh_pair(__fmul_rn(v[i], inv_cap), t, d);
       if constexpr (DERIV) dz[i] = d;
-      v[i] = cap * t;
+      v[i] = fmaf(cap, t, v[i] - v[i]);
     }
   }
 }
@@ -156,6 +157,7 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, const CUtenso
   const int y = rok ? g.target[tok] : -1;
   MS acc{-INFINITY, 0.f};
   float zy = 0.f, zsum = 0.f;
+  float2 odd = make_float2(0.f, 0.f);  // NaN once a logit is infinite: -inf would leave no trace in the sums
   bool got = false;
 #pragma unroll 1
   for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
@@ -178,6 +180,10 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, const CUtenso
     if constexpr (CAP) {
       float none[1];
       soft_cap32<false>(v, none, g.cap, g.inv_cap);
+    } else {
+      // (a column past the vocabulary is 0, or NaN with an infinite hidden state, whose logits are all non-finite)
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) odd = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(0.f, 0.f), odd);
     }
     const uint32_t k = (uint32_t)y - (uint32_t)cb;  // (a target outside the vocabulary meets no column below V)
     if (k < 32) {
@@ -204,6 +210,9 @@ __device__ __forceinline__ void epi_ce_partials(const GemmArgs& g, const CUtenso
     }
     lazy_online2<32>(acc, v);
   }
+  // (with an ordinary shift: the joining drops a sum whose shift is -inf, as that of a tile with nothing else is)
+  const float bad = acc.s + (odd.x + odd.y);
+  if (isnan(bad)) acc = MS{0.f, bad};
   if (got) g.zy[tok] = zy;
   if (half) {
     join[0] = acc.m;
