@@ -172,7 +172,7 @@ __device__ __forceinline__ CeToken ce_token(const CeReduceArgs& a, const CeInput
   if (a.part_z) o.loss += a.smoothing * ((t.m - z / (float)a.V * kLog2e) + l2s) * kLn2;
   o.sw = in.w;
   o.cp = o.sw * fmaf(2.f * a.z_loss, o.lse, 1.f);
-  if (!isfinite(o.loss)) o.cp = nan;
+  if (!isfinite(o.loss)) o.cp = o.sw = nan;  // (also with a weight of 0: the gradient is NaN)
   o.bad = !isfinite(o.cp);
   return o;
 }

@@ -1,5 +1,6 @@
 """GPU cross entropy from hidden states at its edges. Tolerances as in test_gpu_lmhead_ce.py where its checks are
 used; the others stand at their tests."""
+import numpy as np
 import pytest
 import torch
 
@@ -39,3 +40,16 @@ def test_a_logit_that_is_infinite_or_nan_counts_as_non_finite(path, column, what
     res = _lib.grpo_finish_step(out["acc"], out["loss"], expected_N=T, grad_bufs=[out["d_h"], out["dW"]])
     assert res["status"] == _lib.STEP_SKIPPED_NONFINITE and res["n_nonfinite"] == int(bad.sum())
     assert torch.all(out["d_h"] == 0) and torch.all(out["dW"] == 0)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_non_finite_token_of_weight_zero_has_a_nan_gradient(path):
+    T, V, H = PATHS[path]
+    h, Wt, y, _ = _inputs(T, V, H, 9, None)
+    y[3] = V
+    w = np.ones(T, np.float32)
+    w[3] = 0.0
+    out = _call(h, Wt, y, None, 1.0, w=w)
+    assert torch.isnan(out["loss"][3]) and torch.isnan(out["d_h"][3]).all() and torch.isnan(out["dW"]).all()
+    assert torch.isfinite(out["d_h"][4:]).all()
+    assert _lib.grpo_finish_step(out["acc"], out["loss"], expected_N=T)["n_nonfinite"] == 1
