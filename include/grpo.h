@@ -697,8 +697,10 @@ GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const void* W, int6
  * x is formed tile by tile over pieces of the vocabulary, as in grpo_lmhead_loss_fwd_bwd, first for the lse
  * and once more for the gradient; no more than a piece is ever stored (256 MB of bf16 dlogits, 66 tiles of
  * 256 columns at least; where the whole vocabulary is one piece its float32 logits, 256 MB at most, may be
- * kept instead of formed again). The masked tokens cost no product (their hidden states are not read and may
- * hold anything). */
+ * kept instead of formed again). x is the tensor cores' float32 sum times 1 + 2^-30 min(H, 8192), which stands
+ * for what their rounding towards zero takes of a dense product in the mean: an exact product (sparse hidden
+ * states, say) is off by that factor, and x of the policy's calls, which do not have it, differs by it. The masked
+ * tokens cost no product (their hidden states are not read and may hold anything). */
 typedef struct grpo_ce_terms {
   float label_smoothing;  /* eps in [0, 1]: the share of the uniform distribution in the target */
   float z_loss;           /* lambda >= 0, finite */

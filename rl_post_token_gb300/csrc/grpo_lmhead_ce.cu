@@ -558,7 +558,7 @@ int ce_logits(const CeCall& c, GemmArgs g, cudaStream_t st, int64_t vc, bool pdl
   g.zy = c.f(c.ws.zy);
   g.a_rows = c.a_rows();
   g.cap = c.cap;
-  g.gain = (float)c.H * 0x1p-30f;
+  g.gain = (float)std::min<int64_t>(c.H, kGainMaxH) * 0x1p-30f;
   g.inv_cap = 1.f / c.cap;
   return c.cap > 0.f ? launch<CAP, false, false>(c.cg, ma, mb, mc, g, st, pdl)
                      : launch<PLAIN, false, false>(c.cg, ma, mb, mc, g, st, pdl);

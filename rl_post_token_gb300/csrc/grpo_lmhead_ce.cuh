@@ -6,8 +6,9 @@
 //   dL/dx_v   = ((1 + 2 lambda lse) p_v - (1 - eps) [v = y] - eps / V) (1 - (z_v / c)^2)
 //
 // A tile's epilogue must end before the next tile's products (256 x 256 x H on a pair of SMs: about 9 H
-// clocks; with the cap the epilogue is the longer one below H = 2000 or so); per element it takes one exponential and, with the cap, another and a reciprocal. Eight warps
-// share it, two to each quarter of the accumulator's lanes: `half` is the columns' half that is a warp's.
+// clocks; with the cap the epilogue is the longer one below H = 2000 or so); per element it takes one exponential
+// and, with the cap, another and a reciprocal. Eight warps share it, two to each quarter of the accumulator's
+// lanes: `half` is the columns' half that is a warp's.
 
 namespace grpo {
 namespace lmhead {
@@ -73,10 +74,14 @@ __device__ __forceinline__ void soft_cap32(float (&v)[32], float (&dz)[DERIV ? 3
 
 // The tensor cores round a running sum towards zero at every accumulation (Fasi, Higham, Mikaitis, Pranesh,
 // "Numerical behavior of NVIDIA tensor cores", 2021), which takes a share of it each time, so of a product of
-// length K a share in proportion to K, whatever the order and the signs of its terms: 2^-30 K of it here, in
-// the mean over logits of three distributions with K from 256 to 4096. Given back, gain = 2^-30 K. The log-probs
-// of 512 tokens, V = 60000, K = 2048, are then 3.6e-7 of their size from 64 bits, 1.1e-6 without it. (Below H = 1000,
-// where the epilogue is the longer part of a tile, it costs 2%.)
+// length K a share in proportion to K: in the mean over dense normal operands, centred or not, 0.79 (K = 256), 0.87,
+// 0.93, 1.00 (4096), 1.03, 1.06 and 1.07 (32768) times 2^-30 K. Given back, gain = 2^-30 K: the log-probs of 512
+// tokens, V = 60000, K = 2048, are then 3.6e-7 of their size from 64 bits, 1.1e-6 without it. A product that is
+// exact (few entries that are not 0, or small integers) loses nothing, and the gain is then its error: it stops
+// at 2^-17 (K = 8192), where it stays below 1e-5 of a logit, the bar of the log-probs, for those, and what it
+// leaves of a dense one's share does up to K = 16384. (Below H = 1000, where the epilogue is the longer part of a
+// tile, it costs 2%.)
+constexpr int kGainMaxH = 8192;
 __device__ __forceinline__ void give_back(float (&v)[32], float gain) {
   const float2 g = make_float2(gain, gain);
 #pragma unroll

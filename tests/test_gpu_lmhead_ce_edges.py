@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from rl_post_token_gb300 import _lib
-from tests.test_gpu_lmhead_ce import DEV, _built, _call, _inputs  # noqa: F401
+from tests.test_gpu_lmhead_ce import BF16, DEV, _built, _call, _check64, _inputs, cta_group  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 # reduce and dlogits in one launch; logits kept; formed again; formed again in two pieces. The last column is alone
@@ -53,3 +53,46 @@ def test_a_non_finite_token_of_weight_zero_has_a_nan_gradient(path):
     assert torch.isnan(out["loss"][3]) and torch.isnan(out["d_h"][3]).all() and torch.isnan(out["dW"]).all()
     assert torch.isfinite(out["d_h"][4:]).all()
     assert _lib.grpo_finish_step(out["acc"], out["loss"], expected_N=T)["n_nonfinite"] == 1
+
+
+@pytest.mark.parametrize("H", [2048, 8192, 16384, 65536])
+def test_exact_products_of_large_hidden_sizes(H):
+    # Eight entries of a hidden state are not 0, and they and W are powers of two: no partial sum is rounded.
+    # The factor on the products is at most 1 + 2^-30 8192 = 1 + 2^-17, so lse is off by 2^-17 of the largest
+    # logit; exponentials, their sum and the logarithm add less than 2^-20 max(1, |lse|).
+    T, V = 300, 1000
+    rng = np.random.default_rng(H)
+    h = torch.zeros((T, H), device=DEV)
+    at = torch.from_numpy(np.stack([rng.choice(H, 8, replace=False) for _ in range(T)])).to(DEV)
+    h.scatter_(1, at, torch.from_numpy(2.0 ** rng.integers(0, 4, (T, 8))).float().to(DEV))
+    g = torch.Generator(device=DEV)
+    g.manual_seed(H)
+    Wt = torch.randint(0, 2, (V, H), generator=g, device=DEV) * 2.0 - 1.0
+    x = h.double() @ Wt.double().T
+    out = _call(h.to(BF16), Wt.to(BF16), rng.integers(0, V, T).astype(np.int32), None, 1.0, grads=False)
+    lse, top = torch.logsumexp(x, 1), x.abs().max(1).values
+    assert float(top.max()) > 24
+    assert torch.all((out["lse"].double() - lse).abs() <= 2.0 ** -17 * top + 2.0 ** -20 * lse.abs().clamp(min=1.0))
+
+
+@pytest.mark.parametrize("terms", [dict(), dict(label_smoothing=0.1, z_loss=1e-3, soft_cap=5.0)])
+@pytest.mark.parametrize("T, V, H", [(200, 3000, 4096), (300, 4000, 8192), (70, 4000, 16384)])
+def test_large_hidden_sizes(cta_group, T, V, H, terms):
+    # (at most 1e-5 of a logit is left of what the products lose; the logits are a few units, so that is below the
+    # bar, 1e-5 of log-probs and lse of 8 and more)
+    a = _inputs(T, V, H, 5, 0.2)
+    _check64(a, 1.0, _call(*a, 1.0, **terms), **terms)
+
+
+@pytest.mark.parametrize("H", [2048, 8192])
+def test_what_dense_products_lose_is_given_back(H):
+    # with one entry in the vocabulary lse is the logit: in the mean over many it loses 0.93 to 1.04 times 2^-30 H
+    # of its size, and less than half of that may be left
+    T, lost, size = 8192, 0.0, 0.0
+    for seed in range(8):
+        h, Wt, y, _ = _inputs(T, 1, H, seed, None, std=20.0)
+        x = (h.double() @ Wt.double().T)[:, 0]
+        out = _call(h, Wt, y, None, 1.0, grads=False)
+        lost += float(((out["lse"].double() - x) * x.sign()).sum())
+        size += float(x.abs().sum())
+    assert abs(lost) <= 0.5 * 2.0 ** -30 * H * size
