@@ -96,3 +96,25 @@ def test_what_dense_products_lose_is_given_back(H):
         lost += float(((out["lse"].double() - x) * x.sign()).sum())
         size += float(x.abs().sum())
     assert abs(lost) <= 0.5 * 2.0 ** -30 * H * size
+
+
+@pytest.mark.parametrize("terms", [dict(label_smoothing=0.1), dict(z_loss=1e-3, soft_cap=5.0)])
+@pytest.mark.parametrize("T, V, H, masked", [
+    (1000, 50257, 1000, 0.3), (1000, 50257, 1024, None), (1000, 50257, 1088, 0.3),  # by H, on and off 64
+    (250, 50257, 1000, None), (251, 50257, 1000, None), (250, 50257, 512, None),    # few tokens
+    (568, 9200, 64, None), (569, 9200, 64, 0.1),                                    # 20 MB
+    (1328, 50257, 1088, None), (1340, 50257, 1088, None),                           # 256 MB
+    (91, 9200, 64, None), (92, 9200, 64, None)])                                    # one launch for both
+def test_the_limits_of_keeping_the_logits(T, V, H, masked, terms):
+    a = _inputs(T, V, H, 6, masked)
+    _check64(a, 1.0 / T, _call(*a, 1.0 / T, **terms), **terms)
+
+
+def test_float32_gradients_over_micro_batches_at_a_large_hidden_size():
+    T, V, H = 300, 6000, 4096
+    a, b = _inputs(T, V, H, 21, 0.3), _inputs(T, V, H, 22, None)
+    b = (b[0], a[1], b[2], b[3])
+    one, two = _call(*a, 1.0), _call(*b, 1.0)
+    dW = _call(*a, 1.0)["dW"]
+    got = _call(*b, 1.0, dW=dW, dw_accumulate=True)["dW"]
+    assert got is dW and torch.equal(got, one["dW"] + two["dW"])
