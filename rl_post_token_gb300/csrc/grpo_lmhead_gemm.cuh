@@ -337,6 +337,7 @@ __device__ __forceinline__ void epi_partials(const GemmArgs& g, uint32_t taddr, 
     }
     lazy_online2<32>(acc, v);
   }
+  if (isnan(acc.s)) acc.m = 0.f;  // a NaN beside nothing but -inf: the joining drops a sum whose shift is -inf
   if (rok) {
     g.part_m[(int64_t)ct * g.M + row] = acc.m;
     g.part_s[(int64_t)ct * g.M + row] = acc.s;
@@ -371,6 +372,7 @@ __device__ __forceinline__ void epi_partials_ent(const GemmArgs& g, uint32_t tad
     }
     lazy_online3<32>(acc, v, guarded);
   }
+  if (isnan(acc.s)) acc.m = 0.f;  // (as above)
   if (rok) {
     g.part_m[(int64_t)ct * g.M + row] = acc.m;
     g.part_s[(int64_t)ct * g.M + row] = acc.s;
