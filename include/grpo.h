@@ -474,7 +474,8 @@ typedef struct grpo_grad_norm_result {
   double  sum_sq;    /* sum of the squares of every element, before the scale s (data-parallel ranks with
                         a part of the gradients each add theirs) */
   float   norm;      /* s sqrt(sum_sq), inf past float32's range (coef is formed in float64) */
-  float   coef;      /* s min(1, max_norm / norm); 0 when the step is skipped */
+  float   coef;      /* s min(1, max_norm / norm), rounded to float32 (with fewer bits below 2^-126); 0 when the
+                        step is skipped */
   int32_t status;    /* GRPO_OK; GRPO_STEP_SKIPPED_NONFINITE: sum_sq is not finite; else acc's status */
   int32_t reserved0;
   int64_t reserved1;
@@ -506,8 +507,8 @@ GRPO_API int grpo_grad_norm(const void* const* grads, const int64_t* numels, con
                             float max_norm, const grpo_step_acc* acc, int32_t deferred, float* tensor_norms,
                             grpo_grad_norm_result* result, void* workspace, size_t workspace_bytes, void* stream);
 
-/* dst_i = coef src_i for n tensors, rounded once to dst's type; zeros where the step is skipped (src is
- * then not read). dst_i may be src_i with the same dtype (in place: a coef of 1 writes nothing); otherwise
+/* dst_i = coef src_i for n tensors: the float32 product, rounded to bf16 where dst is; zeros where the
+ * step is skipped (src is then not read). dst_i may be src_i with the same dtype (in place: a coef of 1 writes nothing); otherwise
  * no tensor that is written may overlap any other of the call.
  *  src, dst   host arrays of n device pointers; src_dtypes, dst_dtypes, numels host arrays, as above
  *  result     device, from grpo_grad_norm earlier on this stream (or filled by the caller)
@@ -695,12 +696,13 @@ GRPO_API int grpo_lmhead_distill_topk_fwd_bwd(const void* h, const void* W, int6
  *   dL/dz_v = (1 + 2 lambda lse) p_v - (1 - eps) [v = y] - eps / V,  dL/dx = dL/dz (1 - (z / soft_cap)^2)
  *   d_h_t = grad_scale w_t m_t dL/dx W,  dW = sum_t grad_scale w_t m_t dL/dx_t h_t
  * x is formed tile by tile over pieces of the vocabulary, as in grpo_lmhead_loss_fwd_bwd, first for the lse
- * and once more for the gradient; no more than a piece is ever stored (256 MB of bf16 dlogits, 66 tiles of
- * 256 columns at least; where the whole vocabulary is one piece its float32 logits, 256 MB at most, may be
- * kept instead of formed again). x is the tensor cores' float32 sum times 1 + 2^-30 min(H, 8192), which stands
- * for what their rounding towards zero takes of a dense product in the mean: an exact product (sparse hidden
- * states, say) is off by that factor, and x of the policy's calls, which do not have it, differs by it. The masked
- * tokens cost no product (their hidden states are not read and may hold anything). */
+ * and once more for the gradient; no more is stored than the dlogits of two pieces, one read while the next is
+ * written (a piece: 256 MB of bf16, 66 tiles of 256 columns at least; where the whole vocabulary is one piece its
+ * float32 logits, 256 MB at most, may be kept instead of formed again). x is the tensor cores' float32 sum times
+ * 1 + 2^-30 min(H, 8192), which stands for what their rounding towards zero takes of a dense product in the mean:
+ * an exact product (sparse hidden states, say) is off by that factor, and x of the policy's calls, which do not
+ * have it, differs by it. The masked tokens cost no product (their hidden states are not read and may hold
+ * anything). */
 typedef struct grpo_ce_terms {
   float label_smoothing;  /* eps in [0, 1]: the share of the uniform distribution in the target */
   float z_loss;           /* lambda >= 0, finite */
@@ -709,7 +711,8 @@ typedef struct grpo_ce_terms {
                              loss_tok stays unweighted */
 } grpo_ce_terms;
 
-/* Bytes of device workspace grpo_lmhead_ce_fwd_bwd needs. 0 on bad sizes. */
+/* Bytes of device workspace grpo_lmhead_ce_fwd_bwd needs, the same with and without gradients. 0 on bad
+ * sizes. */
 GRPO_API size_t grpo_lmhead_ce_workspace_size(int64_t T, int64_t V, int64_t H);
 
 /*  h, W       device bf16 [T, H], [V, H] row-major, 16-byte aligned; H a multiple of 8, 2^24 at most
@@ -727,10 +730,10 @@ GRPO_API size_t grpo_lmhead_ce_workspace_size(int64_t T, int64_t V, int64_t H);
  *  acc        device grpo_step_acc; loss_tok and acc go to grpo_finish_step (no token counts as clipped)
  *  workspace  device, 256-byte aligned, grpo_lmhead_ce_workspace_size(T, V, H) bytes; overlapping calls
  *             need one each
- * A token with a non-finite loss (a bad target, a NaN or infinite logit, |lse| above 4096) counts as
- * non-finite, and its gradient is NaN. T = 0 writes dW as zeros (or leaves it, accumulating).
- * Results of a token do not depend on the masked ones; dW sums the unmasked tokens in order; d_h's order of
- * sums depends on T, V and H. Environment: as grpo_lmhead_loss_fwd_bwd.
+ * A token with a non-finite loss (a bad target, |lse| above 4096, a NaN or infinite logit: with a soft cap too,
+ * and -inf too) counts as non-finite, and its gradient is NaN, whatever its weight. T = 0 writes dW as zeros (or
+ * leaves it, accumulating). What the masked tokens hold changes no result; dW sums the unmasked tokens in order;
+ * d_h's order of sums goes by T (masked tokens counted), V and H. Environment: as grpo_lmhead_loss_fwd_bwd.
  * Errors: GRPO_ERR_INVALID (sizes, terms, a non-finite grad_scale, NULL required pointer, alignment, overlap,
  * DW_ACCUMULATE on a bf16 dW, unknown flags), GRPO_ERR_CAPACITY (workspace too small),
  * GRPO_ERR_UNSUPPORTED (dtype, tensor-map creation), GRPO_ERR_CUDA. */

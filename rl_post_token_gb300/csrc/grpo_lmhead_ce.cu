@@ -1,6 +1,6 @@
 // Softmax cross entropy from hidden states: z = h W^T is formed tile by tile on the tensor cores and
-// consumed in the GEMM's epilogue (formulas in grpo_lmhead_ce.cuh); no more of the [T, V] logits or dlogits
-// is stored than a piece of the vocabulary.
+// consumed in the GEMM's epilogue (formulas in grpo_lmhead_ce.cuh); no more of the [T, V] dlogits is stored
+// than two pieces of the vocabulary, and of the logits no more than 256 MB.
 //
 //  compact    the unmasked tokens first, in token order, and their hidden states gathered: every GEMM
 //             below runs over them only (a fine-tuning batch masks its prompts). Not with mask NULL
@@ -14,10 +14,10 @@
 //
 // Bound by the tensor cores with many tokens: 2 T V H flops of pass A and 6 T V H of the backward, of which
 // the 2 T V H of the logits' second forming stand for a store and two readings of the [T, V] logits. 4096
-// unmasked tokens of 8192, V = 151936, H = 2048 (1.02e13 flops): 5.4 ms serialised, 1.9 PFLOP/s; 6.15 ms among
-// others under the power cap, 1.66, where plain bf16 products of the same length reach 1.73. With few tokens
-// by the readings of W (two) and the writing of dW: 16 tokens, V = 32000, H = 768 (98 MB without the second
-// reading): 44 us of five dependent launches.
+// unmasked tokens of 8192, V = 151936, H = 2048 (1.02e13 flops): 5.4 ms serialised, 1.9 PFLOP/s; 5.8 to 6.35 ms
+// among others under the power cap, 1.6 to 1.77, where plain bf16 products of the same length reach 1.73. With
+// few tokens by the readings of W (two) and the writing of dW: 16 tokens, V = 32000, H = 768 (98 MB without the
+// second reading): 44 us of five dependent launches.
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
@@ -435,7 +435,7 @@ int ce_split(int64_t T, int64_t H, int chunk_tiles) {
 // forming them again is a reading of W; and a few MB stay in L2. Kept and formed again, us of a call:
 // 800 x 50257 with H = 768, 1024, 1280, 2048: 225 and 217, 266 and 272, 310 and 335, 442 and 509; 250 x 50257 x
 // 512 82 and 76, 100 x 151936 x 512 142 and 148, 16 x 32000 x 768 50 and 56, 500 x 9000 x 512 40 and 41,
-// 999 x 50257 x 1000 325 and 339.
+// 999 x 50257 x 1000 325 and 339 (the only size measured off 64 rows).
 bool ce_keep(int64_t T, int64_t H, int64_t vchunk, int n_chunks) {
   const int64_t bytes = T * vchunk * 4;
   return n_chunks == 1 && (bytes <= ((int64_t)20 << 20) ||
